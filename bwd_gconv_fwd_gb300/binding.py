@@ -39,7 +39,11 @@ EXPORTED = ("gconv_out_shape", "gconv_workspace_size", "gconv_plan", "gconv_fwd"
             "gconv_noalloc_scratch_bytes", "gconv_step_host", "gconv_step_device_bytes",
             "gconv_out_shape_ex", "gconv_workspace_size_ex", "gconv_plan_ex", "gconv_fwd_ex", "gconv_bwd_data_ex",
             "gconv_bwd_weight_ex", "gconv_bwd_bias_ex", "gconv_step_workspace_size_ex", "gconv_step_plan_ex", "gconv_step_ex",
-            "gconv_debug_set_step_events", "gconv_debug_set_wgrad_tma")
+            "gconv_debug_set_step_events", "gconv_debug_set_wgrad_tma",
+            "gconv_block_workspace_size", "gconv_norm_fwd", "gconv_norm_bwd", "gconv_join_fwd", "gconv_join_bwd")
+
+GATE_NONE, GATE_FULL, GATE_CHANNEL = range(3)
+ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 
 
 class Geometry(ctypes.Structure):
@@ -47,6 +51,12 @@ class Geometry(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("N", "C_in", "H", "W", "C_out", "kH", "kW", "stride_h", "stride_w",
                                              "pad_top", "pad_bottom", "pad_left", "pad_right", "dilation_h",
                                              "dilation_w", "groups")]
+
+
+class Block(ctypes.Structure):
+    """The gconv_block record of include/gconv.h."""
+    _fields_ = [("N", ctypes.c_int), ("C", ctypes.c_int), ("H", ctypes.c_int), ("W", ctypes.c_int),
+                ("groups", ctypes.c_int), ("eps", ctypes.c_float), ("gate", ctypes.c_int), ("act", ctypes.c_int)]
 
 
 def per_axis(geom):
@@ -149,6 +159,17 @@ def lib():
     L.gconv_step_plan_ex.restype = i
     L.gconv_debug_set_step_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), i]
     L.gconv_debug_set_step_events.restype = None
+    bp = ctypes.POINTER(Block)
+    L.gconv_block_workspace_size.argtypes = [bp, i]
+    L.gconv_block_workspace_size.restype = sz
+    L.gconv_norm_fwd.argtypes = [bp, i, vp, vp, vp, vp]
+    L.gconv_norm_fwd.restype = i
+    L.gconv_norm_bwd.argtypes = [bp, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.gconv_norm_bwd.restype = i
+    L.gconv_join_fwd.argtypes = [bp, i] + [vp] * 9
+    L.gconv_join_fwd.restype = i
+    L.gconv_join_bwd.argtypes = [bp, i] + [vp] * 15 + [sz, vp]
+    L.gconv_join_bwd.restype = i
     _lib = L
     return L
 
@@ -465,6 +486,115 @@ def gconv_bwd_bias(dy, db, *, geom=None, workspace=None, stream=None):
         _check(lib().gconv_bwd_bias_ex(ctypes.byref(rec), dt, _dev(dy, "dy"), _dev(db, "db"), ws, wsb,
                                        _stream_ptr(stream)), "gconv_bwd_bias_ex")
     return db
+
+
+# ---- block norm and block join ---------------------------------------------------
+
+def _like(t, ref, name):
+    """Pointer of an activation that must match ref's shape and dtype (None passes)."""
+    if t is None:
+        return None
+    if t.shape != ref.shape or t.dtype != ref.dtype:
+        raise ValueError(f"{name} must have shape {tuple(ref.shape)} and dtype {ref.dtype}")
+    return _dev(t, name)
+
+
+def _vector(t, c, name):
+    """Pointer of an fp32 [C] tensor (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != (c,):
+        raise ValueError(f"{name} must be float32 of shape ({c},)")
+    return _dev(t, name)
+
+
+def _block(x, groups, eps, gate=None, act="none"):
+    if x.dim() != 4:
+        raise ValueError("activations are [N, C, H, W]")
+    if act not in ACTS:
+        raise ValueError(f"act is one of {sorted(ACTS)}")
+    kind = GATE_NONE
+    if gate is not None:
+        if gate.dtype != x.dtype or gate.shape not in (x.shape, x.shape[:2]):
+            raise ValueError(f"gate must be {x.dtype}, [N, C, H, W] or [N, C]")
+        kind = GATE_FULL if gate.dim() == 4 else GATE_CHANNEL
+    N, C, H, W = x.shape
+    return Block(N, C, H, W, int(groups), float(eps), kind, ACTS[act])
+
+
+def _block_workspace(block, dt, workspace, device):
+    need = lib().gconv_block_workspace_size(ctypes.byref(block), dt)
+    if need == ctypes.c_size_t(-1).value:
+        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_block_workspace_size")
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is None:
+        return None, 0
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def gconv_block_workspace_size(x_shape, dtype: int, groups: int = 1) -> int:
+    """Workspace bytes gconv_norm_bwd and gconv_join_bwd need for activations of this shape."""
+    block = Block(*(int(v) for v in x_shape), int(groups), 0.0, 0, 0)
+    need = lib().gconv_block_workspace_size(ctypes.byref(block), int(dtype))
+    if need == ctypes.c_size_t(-1).value:
+        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_block_workspace_size")
+    return int(need)
+
+
+def gconv_norm_fwd(x, weight, y, *, groups=1, eps=1e-6, stream=None):
+    """y <- x / rms(x over each group's channels) * weight, at every position (weight: fp32 [C]
+    or None)."""
+    b, dt = _block(x, groups, eps), dtype_code(x.dtype)
+    _check(lib().gconv_norm_fwd(ctypes.byref(b), dt, _dev(x, "x"), _vector(weight, b.C, "weight"), _like(y, x, "y"),
+                                _stream_ptr(stream)), "gconv_norm_fwd")
+    return y
+
+
+def gconv_norm_bwd(x, weight, dy, dx, dweight=None, *, dres=None, groups=1, eps=1e-6, workspace=None, stream=None):
+    """dx <- dres + gradient of the norm w.r.t. x; dweight (fp32 [C]) <- gradient w.r.t. weight."""
+    b, dt = _block(x, groups, eps), dtype_code(x.dtype)
+    ws, wsb = _block_workspace(b, dt, workspace, x.device)
+    _check(lib().gconv_norm_bwd(ctypes.byref(b), dt, _dev(x, "x"), _vector(weight, b.C, "weight"), _like(dy, x, "dy"),
+                                _like(dres, x, "dres"), _like(dx, x, "dx"), _vector(dweight, b.C, "dweight"), ws, wsb,
+                                _stream_ptr(stream)), "gconv_norm_bwd")
+    return dx, dweight
+
+
+def gconv_join_fwd(res, h, out, *, gate=None, act="none", weight=None, scale=None, next=None, next_weight=None, groups=1,
+                   eps=1e-6, stream=None):
+    """out <- res + scale * act(gate) * (h / rms(h) * weight) and, with next, next <- out / rms(out) *
+    next_weight.  gate: None, [N, C, H, W] or [N, C]; weight, scale, next_weight: fp32 [C] or None."""
+    b, dt = _block(res, groups, eps, gate, act), dtype_code(res.dtype)
+    _check(lib().gconv_join_fwd(ctypes.byref(b), dt, _dev(res, "res"), _like(h, res, "h"), _dev(gate, "gate"),
+                                _vector(weight, b.C, "weight"), _vector(scale, b.C, "scale"),
+                                _vector(next_weight, b.C, "next_weight"), _like(out, res, "out"),
+                                _like(next, res, "next"), _stream_ptr(stream)), "gconv_join_fwd")
+    return out, next
+
+
+def gconv_join_bwd(h, dout, dh, *, gate=None, act="none", weight=None, scale=None, dgate=None, dweight=None, dscale=None,
+                   out=None, next_weight=None, dnext=None, dres=None, dnext_weight=None, groups=1, eps=1e-6,
+                   workspace=None, stream=None):
+    """Gradients of gconv_join_fwd.  Without dnext (the join had no next) dout is the gradient of
+    out; with it dres <- the whole gradient of out.  dgate: like gate for a full gate, fp32 [N, C]
+    for a channel gate; dweight, dscale, dnext_weight: fp32 [C] or None."""
+    b, dt = _block(h, groups, eps, gate, act), dtype_code(h.dtype)
+    if dgate is not None and b.gate == GATE_CHANNEL:
+        if dgate.dtype != torch.float32 or dgate.shape != gate.shape:
+            raise ValueError("dgate of a channel gate is float32 [N, C]")
+        dg = _dev(dgate, "dgate")
+    else:
+        dg = _like(dgate, h, "dgate")
+    ws, wsb = _block_workspace(b, dt, workspace, h.device)
+    _check(lib().gconv_join_bwd(ctypes.byref(b), dt, _like(out, h, "out"), _dev(h, "h"), _dev(gate, "gate"),
+                                _vector(weight, b.C, "weight"), _vector(scale, b.C, "scale"),
+                                _vector(next_weight, b.C, "next_weight"), _like(dout, h, "dout"),
+                                _like(dnext, h, "dnext"), _like(dres, h, "dres"), _like(dh, h, "dh"), dg,
+                                _vector(dweight, b.C, "dweight"), _vector(dscale, b.C, "dscale"),
+                                _vector(dnext_weight, b.C, "dnext_weight"), ws, wsb, _stream_ptr(stream)),
+           "gconv_join_bwd")
+    return dh, dres
 
 
 # ---- raw pointer level (same C signatures), for callers holding pointers ------

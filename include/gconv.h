@@ -226,6 +226,74 @@ gconv_status gconv_step_ex(const gconv_geometry *geometry, gconv_dtype dtype, gc
                            void *y, void *dx, float *dw, float *db,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Block norm and block join ---------------------------------------------------
+ *
+ * What stands between the convolutions of a residual block, in the same layout and with
+ * the same groups: activations [N][C][H][W], group g owning C/groups consecutive
+ * channels.  With r(t) = 1 / sqrt(mean over the group's channels of t^2 + eps), for every
+ * image, group and position:
+ *
+ *   norm   y    = x r(x) weight
+ *   join   out  = res + scale act(gate) (h r(h) weight)
+ *          next = out r(out) next_weight
+ *
+ * The join ends one block (h: its last convolution's result) and, when `next` is not NULL,
+ * opens the next one; next is the norm of the sum before it is rounded to out's dtype.
+ * Activations and their gradients are `dtype` (GCONV_F32 or GCONV_BF16), weight, scale and
+ * next_weight fp32 [C] (NULL: all ones), their gradients fp32.  All sums are fp32, each
+ * result is rounded once, and every reduction has a fixed order (bitwise reproducible).
+ * Inf and NaN spread through a position's group as the formulas say. */
+typedef enum { GCONV_ACT_NONE = 0, GCONV_ACT_SIGMOID = 1, GCONV_ACT_SILU = 2 } gconv_act;
+typedef enum {
+    GCONV_GATE_NONE = 0,      /* no gate: act(gate) is 1 */
+    GCONV_GATE_FULL = 1,      /* gate, dgate: dtype [N][C][H][W] */
+    GCONV_GATE_CHANNEL = 2    /* gate: dtype [N][C]; dgate: fp32 [N][C], the sum over positions */
+} gconv_gate;
+
+/* Requirements: C, H, W, groups >= 1, N >= 0, C divisible by groups, eps >= 0 and finite, tensors
+ * below 2^31 elements, device pointers 16-byte aligned; gate and act are read by the join
+ * only (act by a gated one).  The record is read during the call only. */
+typedef struct {
+    int N, C, H, W, groups;
+    float eps;
+    int gate, act;            /* gconv_gate, gconv_act */
+} gconv_block;
+
+/* Workspace bytes of gconv_norm_bwd and gconv_join_bwd ((size_t)-1: invalid record or dtype).
+ * The forward calls need none. */
+size_t gconv_block_workspace_size(const gconv_block *block, gconv_dtype dtype);
+
+/* y = norm(x).  N == 0 is a no-op.  Outputs of these four calls must not overlap their
+ * inputs or each other. */
+gconv_status gconv_norm_fwd(const gconv_block *block, gconv_dtype dtype, const void *x, const float *weight, void *y,
+                            void *stream);
+
+/* With g = dy weight and u = x r(x):
+ *   dx = dres + r(x) (g - u mean(g u))      dres: gradient reaching x along the residual branch, or NULL
+ *   dweight[c] = sum over n, positions of dy u                                     (may be NULL)
+ * N == 0 sets dweight to zero. */
+gconv_status gconv_norm_bwd(const gconv_block *block, gconv_dtype dtype, const void *x, const float *weight,
+                            const void *dy, const void *dres, void *dx, float *dweight, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* out, and next unless it is NULL (next_weight must then be NULL).  gate is NULL exactly when
+ * block->gate is GCONV_GATE_NONE. */
+gconv_status gconv_join_fwd(const gconv_block *block, gconv_dtype dtype, const void *res, const void *h,
+                            const void *gate, const float *weight, const float *scale, const float *next_weight,
+                            void *out, void *next, void *stream);
+
+/* Gradients of the join.  dout: gradient of out from its other readers (NULL: none; needed
+ * without dnext); dnext: gradient of next, or NULL when the join had no next (dres,
+ * next_weight and dnext_weight must then be NULL; out is not read).  With d the whole gradient of out,
+ *   dres = d = dout + norm gradient of (out, dnext)                 (required with dnext)
+ *   dh   = norm gradient of (h, d scale act(gate)),   dgate = d scale act'(gate) (h r(h) weight)
+ *   dweight[c] = sum d scale act(gate) h r(h),        dscale[c] = sum d act(gate) h r(h) weight
+ * The channel sums and dgate may be NULL.  N == 0 sets the channel sums to zero. */
+gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const void *out, const void *h,
+                            const void *gate, const float *weight, const float *scale, const float *next_weight,
+                            const void *dout, const void *dnext, void *dres, void *dh, void *dgate, float *dweight,
+                            float *dscale, float *dnext_weight, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Weight gradient that allocates nothing, for callers that cannot allocate device
  * memory themselves: code embedded in a host application that owns every
  * device allocation through its own pool or budget (plug-ins, engines with a
