@@ -40,7 +40,8 @@ EXPORTED = ("gconv_out_shape", "gconv_workspace_size", "gconv_plan", "gconv_fwd"
             "gconv_out_shape_ex", "gconv_workspace_size_ex", "gconv_plan_ex", "gconv_fwd_ex", "gconv_bwd_data_ex",
             "gconv_bwd_weight_ex", "gconv_bwd_bias_ex", "gconv_step_workspace_size_ex", "gconv_step_plan_ex", "gconv_step_ex",
             "gconv_debug_set_step_events", "gconv_debug_set_wgrad_tma",
-            "gconv_block_workspace_size", "gconv_norm_fwd", "gconv_norm_bwd", "gconv_join_fwd", "gconv_join_bwd")
+            "gconv_block_workspace_size", "gconv_norm_fwd", "gconv_norm_bwd", "gconv_join_fwd", "gconv_join_bwd",
+            "gconv_orthogonalize_workspace_size", "gconv_orthogonalize", "gconv_muon_step")
 
 GATE_NONE, GATE_FULL, GATE_CHANNEL = range(3)
 ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
@@ -57,6 +58,17 @@ class Block(ctypes.Structure):
     """The gconv_block record of include/gconv.h."""
     _fields_ = [("N", ctypes.c_int), ("C", ctypes.c_int), ("H", ctypes.c_int), ("W", ctypes.c_int),
                 ("groups", ctypes.c_int), ("eps", ctypes.c_float), ("gate", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+class Matrices(ctypes.Structure):
+    """The gconv_matrices record of include/gconv.h."""
+    _fields_ = [("count", ctypes.c_int), ("rows", ctypes.c_int), ("cols", ctypes.c_int)]
+
+
+class Muon(ctypes.Structure):
+    """The gconv_muon record of include/gconv.h."""
+    _fields_ = [(n, ctypes.c_float) for n in ("lr", "beta", "weight_decay", "scale", "eps")] + \
+        [("nesterov", ctypes.c_int), ("steps", ctypes.c_int), ("coeffs", ctypes.POINTER(ctypes.c_float))]
 
 
 def per_axis(geom):
@@ -170,6 +182,13 @@ def lib():
     L.gconv_join_fwd.restype = i
     L.gconv_join_bwd.argtypes = [bp, i] + [vp] * 15 + [sz, vp]
     L.gconv_join_bwd.restype = i
+    mp = ctypes.POINTER(Matrices)
+    L.gconv_orthogonalize_workspace_size.argtypes = [mp]
+    L.gconv_orthogonalize_workspace_size.restype = sz
+    L.gconv_orthogonalize.argtypes = [mp, i, i, vp, vp, i, ctypes.POINTER(ctypes.c_float), ctypes.c_float, vp, sz, vp]
+    L.gconv_orthogonalize.restype = i
+    L.gconv_muon_step.argtypes = [mp, ctypes.POINTER(Muon)] + [vp] * 7 + [sz, vp]
+    L.gconv_muon_step.restype = i
     _lib = L
     return L
 
@@ -595,6 +614,82 @@ def gconv_join_bwd(h, dout, dh, *, gate=None, act="none", weight=None, scale=Non
                                 _vector(dnext_weight, b.C, "dnext_weight"), ws, wsb, _stream_ptr(stream)),
            "gconv_join_bwd")
     return dh, dres
+
+
+# ---- orthogonalised updates ------------------------------------------------------
+
+def _matrices(w, groups):
+    rows = int(w.shape[0])
+    if w.dim() < 2 or int(groups) < 1 or rows % int(groups):
+        raise GconvError(GCONV_ERR_INVALID_ARG, f"{tuple(w.shape)} is not {groups} groups of matrices")
+    rows //= int(groups)
+    per = rows * int(groups)
+    return Matrices(int(groups), rows, w.numel() // per if per else 0)
+
+
+def _coeffs(coeffs, steps):
+    """(a, b, c) for every step, or one triple a step, as a float array (None: the library's)."""
+    if coeffs is None:
+        return None
+    flat = [float(v) for v in coeffs] if not hasattr(coeffs[0], "__len__") else [float(v) for t in coeffs for v in t]
+    if len(flat) == 3:
+        flat = flat * steps
+    if len(flat) != 3 * steps:
+        raise ValueError("coeffs is (a, b, c) or one such triple a step")
+    return (ctypes.c_float * len(flat))(*flat)
+
+
+def _orth_workspace(m, workspace, device):
+    need = lib().gconv_orthogonalize_workspace_size(ctypes.byref(m))
+    if need == ctypes.c_size_t(-1).value:
+        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_orthogonalize_workspace_size")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def gconv_orthogonalize_workspace_size(w_shape, groups: int = 1) -> int:
+    """Workspace bytes of gconv_orthogonalize and gconv_muon_step for weights of this shape."""
+    rows, cols = int(w_shape[0]) // int(groups), 1
+    for v in w_shape[1:]:
+        cols *= int(v)
+    need = lib().gconv_orthogonalize_workspace_size(ctypes.byref(Matrices(int(groups), rows, cols)))
+    if need == ctypes.c_size_t(-1).value:
+        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_orthogonalize_workspace_size")
+    return int(need)
+
+
+def gconv_orthogonalize(g, out, *, groups=1, steps=5, coeffs=None, eps=1e-7, workspace=None, stream=None):
+    """out <- each group's matrix of g ([C_out, ...]: C_out/groups rows) orthogonalised by `steps`
+    Newton-Schulz steps.  g, out: fp32 or bf16; coeffs: (a, b, c), or one triple a step."""
+    if out.shape != g.shape:
+        raise ValueError(f"out must have shape {tuple(g.shape)}")
+    m, dt, odt = _matrices(g, groups), dtype_code(g.dtype), _out_code(out)
+    c = _coeffs(coeffs, steps)
+    ws, wsb = _orth_workspace(m, workspace, g.device)
+    _check(lib().gconv_orthogonalize(ctypes.byref(m), dt, odt, _dev(g, "g"), _dev(out, "out"), int(steps), c, float(eps),
+                                     ws, wsb, _stream_ptr(stream)), "gconv_orthogonalize")
+    return out
+
+
+def gconv_muon_step(w, grad, momentum, *, w_out=None, m_out=None, w_bf16=None, groups=1, lr=0.02, beta=0.95,
+                    weight_decay=0.0, scale=0.0, nesterov=True, steps=5, coeffs=None, eps=1e-7, workspace=None,
+                    stream=None):
+    """One Muon step: fp32 w and momentum are updated (in place unless w_out, m_out are given) from
+    the fp32 weight gradient; w_bf16, when given, gets the new weights rounded to bf16."""
+    w_out, m_out = w if w_out is None else w_out, momentum if m_out is None else m_out
+    for name, t in (("w", w), ("grad", grad), ("momentum", momentum), ("w_out", w_out), ("m_out", m_out)):
+        if t.dtype != torch.float32 or t.shape != w.shape:
+            raise ValueError(f"{name} must be float32 of shape {tuple(w.shape)}")
+    if w_bf16 is not None and (w_bf16.dtype != torch.bfloat16 or w_bf16.shape != w.shape):
+        raise ValueError(f"w_bf16 must be bfloat16 of shape {tuple(w.shape)}")
+    m, c = _matrices(w, groups), _coeffs(coeffs, steps)
+    opt = Muon(float(lr), float(beta), float(weight_decay), float(scale), float(eps), int(bool(nesterov)), int(steps), c)
+    ws, wsb = _orth_workspace(m, workspace, w.device)
+    _check(lib().gconv_muon_step(ctypes.byref(m), ctypes.byref(opt), _dev(w, "w"), _dev(grad, "grad"),
+                                 _dev(momentum, "momentum"), _dev(w_out, "w_out"), _dev(m_out, "m_out"),
+                                 _dev(w_bf16, "w_bf16"), ws, wsb, _stream_ptr(stream)), "gconv_muon_step")
+    return w_out, m_out
 
 
 # ---- raw pointer level (same C signatures), for callers holding pointers ------

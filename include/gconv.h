@@ -294,6 +294,45 @@ gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const v
                             const void *dout, const void *dnext, void *dres, void *dh, void *dgate, float *dweight,
                             float *dscale, float *dnext_weight, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Orthogonalised updates ------------------------------------------------------
+ *
+ * A weight tensor [C_out][C_in/groups][kH][kW] is `count` = groups matrices of rows =
+ * C_out/groups and cols = (C_in/groups) kH kW, one after the other.  For each of them
+ *   X = g / (|g| + eps)                       (|g|: the root of the sum of squares)
+ *   `steps` times, with (a, b, c) = coeffs[3 k .. 3 k + 2]:   A = X X^T,  X <- a X + (b A + c A A) X
+ * on the shorter side (X^T X and products from the right where rows > cols), which drives
+ * the singular values towards one.  coeffs NULL: 3.4445, -4.7750, 2.0315 in every step.
+ * The iterates are kept in fp16 (11 bits) and products add in fp32: the result is about
+ * 1e-3 (relative, 2-norm) from exact arithmetic for well-conditioned matrices and up to 1e-2 where
+ * singular values span three decades.  Entries of an iterate must stay below 255 in magnitude,
+ * which holds for coefficients that converge.  A zero matrix gives zeros; an Inf or NaN
+ * makes its own matrix NaN.  Bitwise reproducible.
+ * Requirements: rows, cols >= 1, count >= 0, fewer than 2^31 elements in all, 1 <= steps <= 64,
+ * eps >= 0, finite numbers, 16-byte aligned pointers.  The records and coeffs (host memory) are
+ * read during the call only. */
+typedef struct { int count, rows, cols; } gconv_matrices;
+
+size_t gconv_orthogonalize_workspace_size(const gconv_matrices *matrices);   /* both calls; (size_t)-1: invalid */
+
+/* out (out_dtype) <- orthogonalised g (dtype).  out may be g when the dtypes are equal. */
+gconv_status gconv_orthogonalize(const gconv_matrices *matrices, gconv_dtype dtype, gconv_dtype out_dtype, const void *g,
+                                 void *out, int steps, const float *coeffs, float eps, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* One Muon step of fp32 weights from the fp32 gradient gconv_bwd_weight gives:
+ *   momentum' = beta momentum + grad,   u = nesterov ? grad + beta momentum' : momentum'
+ *   w' = (1 - lr weight_decay) w - lr scale orthogonalised(u)
+ * scale <= 0 stands for sqrt(max(1, rows / cols)).  w_out and momentum_out may be w and
+ * momentum; w_bf16 (bf16, or NULL) gets w' rounded, as the convolutions read it. */
+typedef struct {
+    float lr, beta, weight_decay, scale, eps;
+    int nesterov, steps;
+    const float *coeffs;
+} gconv_muon;
+gconv_status gconv_muon_step(const gconv_matrices *matrices, const gconv_muon *opt, const float *w, const float *grad,
+                             const float *momentum, float *w_out, float *momentum_out, void *w_bf16, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* Weight gradient that allocates nothing, for callers that cannot allocate device
  * memory themselves: code embedded in a host application that owns every
  * device allocation through its own pool or budget (plug-ins, engines with a
