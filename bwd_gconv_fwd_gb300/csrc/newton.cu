@@ -14,10 +14,8 @@
 // from the exact iteration (bf16's 8 bits: 1e-2), below the rounding of a bf16 result.
 // Keeping a I inside P rather than adding a X afterwards rounds the difference a - |b| + c
 // instead of its large terms.
-#include "internal.h"
-#include "ptx.cuh"
+#include "newton.cuh"
 
-#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <algorithm>
 #include <climits>
@@ -27,36 +25,12 @@ namespace gconv {
 
 namespace {
 
-constexpr float kScale = 256.f;   // 2^8, the scale of X, A and P in fp16
+constexpr float kScale = kNewtonScale;
 constexpr int kThreads = 352;     // warps 0, 6-10: TMA producers; 1: MMA; 2-5: epilogue
 constexpr int kProducers = 6;
 constexpr int kBM = 128, kBK = 64;
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kNormBlocks = 64;   // partial sums of a matrix's squares, at most
-
-// What the last product of a call writes.
-struct NewtonOut {
-    void *out;                   // orthogonalise: the result
-    int out_bf16;
-    const float *w;              // Muon: weights read and written
-    float *w_out;
-    __nv_bfloat16 *w_bf16;
-    float keep, rate;            // w' = keep w - rate o
-    int muon, tall;
-};
-
-// What the first kernels read.
-struct NewtonIn {
-    const void *g;
-    int g_bf16;
-    const float *m;              // Muon momentum, or nullptr
-    float *m_out;
-    float beta;
-    int nesterov, tall;
-    int64_t elems;               // of one matrix
-    int rows, cols;              // of one matrix as it lies in memory
-    float eps;
-};
 
 enum { kGram = 0, kPoly = 1, kApply = 2 };
 
@@ -71,18 +45,6 @@ struct NewtonParams {
     unsigned int *err;
     uint64_t wait_ns;
 };
-
-__device__ __forceinline__ float load_g(const NewtonIn &p, int64_t i)
-{
-    return p.g_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.g)[i]) : static_cast<const float *>(p.g)[i];
-}
-
-// The matrix that is orthogonalised, at one element: g, or the momentum's lookahead.  m is
-// the updated momentum at the element.
-__device__ __forceinline__ float lookahead(const NewtonIn &p, float g, float m)
-{
-    return p.nesterov ? fmaf(p.beta, m, g) : m;
-}
 
 // Sum over a block of 256 threads, in a fixed order; the result is in thread 0.
 __device__ __forceinline__ float block_sum(float v, float *sh)
@@ -161,27 +123,6 @@ __global__ void __launch_bounds__(256) newton_scale_kernel(const NewtonIn p, con
         if (row < p.cols && col < p.rows)
             x[((int64_t)blockIdx.z * m_rows + row) * ldx + col] = __float2half_rn(tile[tx][r]);
     }
-}
-
-// One result element of the last step: row i, column j of X of matrix b.
-__device__ __forceinline__ void store_result(const NewtonOut &o, int b, int M, int N, int i, int j, float v)
-{
-    const int64_t at = (int64_t)b * M * N + (o.tall ? (int64_t)j * M + i : (int64_t)i * N + j);
-    if (o.muon) {
-        v = o.keep * o.w[at] - o.rate * v;
-        o.w_out[at] = v;
-        if (o.w_bf16) o.w_bf16[at] = __float2bfloat16_rn(v);
-    } else if (o.out_bf16) {
-        static_cast<__nv_bfloat16 *>(o.out)[at] = __float2bfloat16_rn(v);
-    } else {
-        static_cast<float *>(o.out)[at] = v;
-    }
-}
-
-// fp16 instruction descriptor: f16 A and B, f32 accumulator
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major)
-{
-    return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // Tile t of the lower triangle, row by row: (row block, column block).
@@ -353,7 +294,8 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                         #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             if (col0 + j < p.N)
-                                store_result(p.o, bt, p.M, p.N, row, col0 + j,
+                                store_result(p.o, (int64_t)bt * p.M * p.N + (p.o.tall ? (int64_t)(col0 + j) * p.M + row
+                                                                                  : (int64_t)row * p.N + col0 + j),
                                              __uint_as_float(acc[j]) * (1.f / (kScale * kScale)));
                     } else {
                         __half2 h[8];
@@ -427,11 +369,6 @@ bool half_tmap(CUtensorMap *m, const void *base, int cols, int rows, int ld, int
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-struct NewtonShape {
-    int G, rows, cols, m, n, tall, ldx, lda;
-    size_t x_bytes, a_bytes, ws;
-};
-
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 bool newton_shape(const gconv_matrices *t, NewtonShape *s)
@@ -477,17 +414,15 @@ gconv_status launch_gemm(const CUtensorMap &tA, const CUtensorMap &tB, NewtonPar
     return GCONV_OK;
 }
 
-// The library's default: the quintic whose slope at zero is the largest that keeps every
-// singular value within about 0.7 to 1.2 after five steps.
-constexpr float kCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
-
 gconv_status run_newton(const NewtonShape &s, NewtonIn in, const NewtonOut &out, int steps, const float *coeffs,
                         void *workspace, cudaStream_t st)
 {
     unsigned int *err = device_error_word();
     if (!err) return GCONV_ERR_CUDA;
     cudaGetLastError();   // clear a stale error: the check after the launches is about this call
-    in.tall = s.tall; in.rows = s.rows; in.cols = s.cols; in.elems = (int64_t)s.rows * s.cols;
+    NewtonOut o = out;
+    o.tall = in.tall = s.tall; in.rows = s.rows; in.cols = s.cols; in.elems = (int64_t)s.rows * s.cols;
+    if (newton_small_fits(s)) return newton_small_launch(s, in, o, steps, coeffs, err, st);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *part = reinterpret_cast<float *>(ws);
     ws += up256((size_t)s.G * kNormBlocks * 4);
@@ -510,7 +445,7 @@ gconv_status run_newton(const NewtonShape &s, NewtonIn in, const NewtonOut &out,
             part_in, part + (size_t)g0 * kNormBlocks, parts, x[0] + (int64_t)g0 * s.m * s.ldx, s.ldx);
     }
     for (int k = 0; k < steps; ++k) {
-        const float *c = coeffs ? coeffs + 3 * k : kCoeffs;
+        const float *c = coeffs ? coeffs + 3 * k : kNewtonCoeffs;
         NewtonParams p{};
         p.batch = s.G; p.err = err; p.wait_ns = (uint64_t)wait_limit();
         p.M = s.m; p.N = s.m; p.K = s.n; p.ldc = s.lda; p.C = A;
@@ -522,8 +457,7 @@ gconv_status run_newton(const NewtonShape &s, NewtonIn in, const NewtonOut &out,
         if (r != GCONV_OK) return r;
         p.N = s.n; p.ldc = s.ldx; p.C = x[(k + 1) & 1];
         p.last = k + 1 == steps;
-        p.o = out;
-        p.o.tall = s.tall;
+        p.o = o;
         r = launch_gemm<256, kApply>(tP, tX[k & 1], p, st);
         if (r != GCONV_OK) return r;
     }
@@ -534,7 +468,7 @@ bool good(float v) { return v == v && v <= 3e38f && v >= -3e38f; }
 
 bool good_steps(int steps, const float *coeffs, float eps)
 {
-    if (steps < 1 || steps > 64 || !good(eps) || eps < 0.f) return false;
+    if (steps < 1 || steps > kNewtonSteps || !good(eps) || eps < 0.f) return false;
     for (int i = 0; coeffs && i < 3 * steps; ++i)
         if (!good(coeffs[i])) return false;
     return true;
