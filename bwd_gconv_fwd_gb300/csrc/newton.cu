@@ -26,19 +26,27 @@ namespace gconv {
 namespace {
 
 constexpr float kScale = kNewtonScale;
-constexpr int kThreads = 352;     // warps 0, 6-10: TMA producers; 1: MMA; 2-5: epilogue
-constexpr int kProducers = 6;
-constexpr int kBM = 128, kBK = 64;
+constexpr int kTile = 256;         // a pair of CTAs computes 256 x 256, 128 rows each
+constexpr int kBK = 64;
+constexpr int kStages = 6;
+constexpr uint32_t kOperand = 128 * kBK * 2, kStageBytes = 2 * kOperand;   // one CTA's half of A and of B
+constexpr int kProducers = 4, kDrainers = 8;
+constexpr int kThreads = 32 * (1 + kProducers + kDrainers);
+constexpr int kStagePitch = 33;    // floats of a staged row
+constexpr uint32_t kWarpStage = 32 * kStagePitch * 4;
+constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kDrainers * kWarpStage;
 constexpr uint64_t kDrainNs = 1000000000ull;
-constexpr int kNormBlocks = 64;   // partial sums of a matrix's squares, at most
+constexpr int kNormBlocks = 1024;  // partial sums of a matrix's squares, at most
+constexpr int kNormShare = 8192;   // elements of one
 
 enum { kGram = 0, kPoly = 1, kApply = 2 };
 
 struct NewtonParams {
     int batch, M, N, K, ldc;
-    int n_mblk, n_nblk, n_kblk, tiles_per, stages;
+    int n_mblk, n_kblk, tiles_per, splits, k_per;
     __half *C;                   // gram: A, poly: P, apply: the next X (not the last step)
     const __half *A;             // poly: A
+    float *part;                 // gram in several splits: their sums
     float a, b, c;               // poly
     int last;
     NewtonOut o;
@@ -46,84 +54,175 @@ struct NewtonParams {
     uint64_t wait_ns;
 };
 
-// Sum over a block of 256 threads, in a fixed order; the result is in thread 0.
-__device__ __forceinline__ float block_sum(float v, float *sh)
+// ---- norm and scale -------------------------------------------------------------
+
+template <int V>
+__device__ __forceinline__ void load_v(const float *p, int64_t i, float (&v)[V])
 {
     #pragma unroll
-    for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.f;
-    if (threadIdx.x < 32) {
-        t = threadIdx.x < 8 ? sh[threadIdx.x] : 0.f;
-        #pragma unroll
-        for (int m = 4; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+    for (int k = 0; k < V; k += 4) {
+        if constexpr (V >= 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p + i + k);
+            v[k] = q.x; v[k + 1] = q.y; v[k + 2] = q.z; v[k + 3] = q.w;
+        } else {
+            v[k] = p[i + k];
+        }
     }
-    return t;
+}
+
+template <int V>
+__device__ __forceinline__ void load_gv(const NewtonIn &p, int64_t i, float (&v)[V])
+{
+    if constexpr (V == 8) {
+        if (p.g_bf16) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.g) + i);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+            return;
+        }
+        load_v<V>(static_cast<const float *>(p.g), i, v);
+    } else {
+        v[0] = load_g(p, i);
+    }
 }
 
 // Updates the momentum and adds the squares of one share of one matrix.  grid (shares, G).
-__global__ void __launch_bounds__(256) newton_norm_kernel(const NewtonIn p, float *part)
+// V = 8 where a matrix is a multiple of eight elements.
+template <int V>
+__global__ void __launch_bounds__(256) newton_norm_kernel(const NewtonIn p, float *part, int64_t share)
 {
     __shared__ float sh[8];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int64_t base = (int64_t)blockIdx.y * p.elems;
+    const int64_t i0 = (int64_t)blockIdx.x * share, i1 = min(i0 + share, p.elems);
     float s = 0.f;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.elems; i += (int64_t)gridDim.x * 256) {
-        float u = load_g(p, base + i);
+    #pragma unroll 4
+    for (int64_t i = i0 + (int64_t)threadIdx.x * V; i < i1; i += 256 * V) {
+        float u[V];
+        load_gv<V>(p, base + i, u);
         if (p.m) {
-            const float m = fmaf(p.beta, p.m[base + i], u);
-            p.m_out[base + i] = m;
-            u = lookahead(p, u, m);
+            float m[V];
+            load_v<V>(p.m, base + i, m);
+            #pragma unroll
+            for (int k = 0; k < V; ++k) {
+                m[k] = fmaf(p.beta, m[k], u[k]);
+                u[k] = lookahead(p, u[k], m[k]);
+            }
+            #pragma unroll
+            for (int k = 0; k < V; k += 4) {
+                if constexpr (V == 8) *reinterpret_cast<float4 *>(p.m_out + base + i + k) = make_float4(m[k], m[k + 1], m[k + 2], m[k + 3]);
+                else p.m_out[base + i] = m[0];
+            }
         }
-        s = fmaf(u, u, s);
+        #pragma unroll
+        for (int k = 0; k < V; ++k) s = fmaf(u[k], u[k], s);
     }
-    s = block_sum(s, sh);
-    if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = s;
+    #pragma unroll
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float t = 0.f;
+        for (int k = 0; k < 8; ++k) t += sh[k];
+        part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
+    }
 }
 
-// X = 2^8 u / (|u| + eps) in fp16, rows = the shorter side; 32 x 32 tiles of the matrix as it
-// lies, through shared memory when it is transposed.  grid (column tiles, row tiles, G).
-__global__ void __launch_bounds__(256) newton_scale_kernel(const NewtonIn p, const float *part, int parts, __half *x, int ldx)
+// 2^8 / (|u| + eps) from a matrix's shares, in a fixed order, for a block of 256 threads.
+__device__ __forceinline__ float inverse_norm(const float *part, int parts, float eps, float *sh)
 {
-    __shared__ float tile[32][33];
-    __shared__ float inv_sh;
+    float s = 0.f;
+    for (int i = threadIdx.x; i < parts; i += 256) s += part[i];
+    #pragma unroll
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+    __syncthreads();
+    float t = 0.f;
+    for (int k = 0; k < 8; ++k) t += sh[k];
+    return kScale / (sqrtf(t) + eps);
+}
+
+// X = 2^8 u / (|u| + eps) in fp16 for matrices as wide as X and a multiple of eight columns:
+// grid (shares, G), eight elements a thread.
+__global__ void __launch_bounds__(256) newton_scale_flat_kernel(const NewtonIn p, const float *part, int parts, __half *x)
+{
+    __shared__ float sh[8];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const int64_t base = (int64_t)blockIdx.z * p.elems;
-    if (threadIdx.x < 32) {
-        float s = 0.f;
-        for (int i = threadIdx.x; i < parts; i += 32) s += part[blockIdx.z * kNormBlocks + i];
-        #pragma unroll
-        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-        if (threadIdx.x == 0) inv_sh = kScale / (sqrtf(s) + p.eps);
-    }
-    __syncthreads();
-    const float inv = inv_sh;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int c0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
-    const int m_rows = p.tall ? p.cols : p.rows;
-    for (int r = ty; r < 32; r += 8) {
-        const int row = r0 + r, col = c0 + tx;
-        float v = 0.f;
-        if (row < p.rows && col < p.cols) {
-            const int64_t i = base + (int64_t)row * p.cols + col;
-            v = load_g(p, i);
-            if (p.m) v = lookahead(p, v, p.m_out[i]);
-            v *= inv;
-            if (!p.tall) x[((int64_t)blockIdx.z * m_rows + row) * ldx + col] = __float2half_rn(v);
+    const float inv = inverse_norm(part + (int64_t)blockIdx.y * parts, parts, p.eps, sh);
+    const int64_t base = (int64_t)blockIdx.y * p.elems;
+    const int64_t i0 = (int64_t)blockIdx.x * kNormShare, i1 = min(i0 + kNormShare, p.elems);
+    #pragma unroll 4
+    for (int64_t i = i0 + (int64_t)threadIdx.x * 8; i < i1; i += 256 * 8) {
+        float u[8];
+        load_gv<8>(p, base + i, u);
+        if (p.m) {
+            float m[8];
+            load_v<8>(p.m_out, base + i, m);
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = lookahead(p, u[k], m[k]);
         }
-        tile[r][tx] = v;
-    }
-    if (!p.tall) return;
-    __syncthreads();
-    for (int r = ty; r < 32; r += 8) {
-        const int row = c0 + r, col = r0 + tx;   // of X
-        if (row < p.cols && col < p.rows)
-            x[((int64_t)blockIdx.z * m_rows + row) * ldx + col] = __float2half_rn(tile[tx][r]);
+        uint32_t h[4];
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = half2_bits(u[2 * k] * inv, u[2 * k + 1] * inv);
+        *reinterpret_cast<uint4 *>(x + base + i) = make_uint4(h[0], h[1], h[2], h[3]);
     }
 }
+
+// The same for any matrix: 64 x 32 tiles of the matrix as it lies, through shared memory when
+// X is its transpose.  grid (column tiles x row tiles, G).
+__global__ void __launch_bounds__(256) newton_scale_kernel(const NewtonIn p, const float *part, int parts, __half *x, int ldx,
+                                                           int col_tiles)
+{
+    __shared__ float tile[64][33];
+    __shared__ float sh[8];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const float inv = inverse_norm(part + (int64_t)blockIdx.y * parts, parts, p.eps, sh);
+    const int64_t base = (int64_t)blockIdx.y * p.elems;
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int c0 = (int)(blockIdx.x % col_tiles) * 32, r0 = (int)(blockIdx.x / col_tiles) * 64;
+    const int m_rows = p.tall ? p.cols : p.rows;
+    __half *xb = x + (int64_t)blockIdx.y * m_rows * ldx;
+    float v[8];
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int row = r0 + ty + 8 * k, col = c0 + tx;
+        v[k] = 0.f;
+        if (row < p.rows && col < p.cols) {
+            const int64_t i = base + (int64_t)row * p.cols + col;
+            v[k] = load_g(p, i);
+            if (p.m) v[k] = lookahead(p, v[k], p.m_out[i]);
+            v[k] *= inv;
+        }
+    }
+    if (!p.tall) {
+        #pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int row = r0 + ty + 8 * k, col = c0 + tx;
+            if (row < p.rows && col < p.cols) xb[(int64_t)row * ldx + col] = __float2half_rn(v[k]);
+        }
+        return;
+    }
+    #pragma unroll
+    for (int k = 0; k < 8; ++k) tile[ty + 8 * k][tx] = v[k];
+    __syncthreads();
+    // two neighbouring columns of X a thread: ldx is a multiple of eight, so the second is in bounds
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int row = c0 + ty + 8 * k, col = r0 + 2 * tx;
+        if (row < p.cols && col < p.rows)
+            *reinterpret_cast<uint32_t *>(xb + (int64_t)row * ldx + col) =
+                half2_bits(tile[2 * tx][ty + 8 * k], tile[2 * tx + 1][ty + 8 * k]);
+    }
+}
+
+// ---- products ---------------------------------------------------------------------
 
 // Tile t of the lower triangle, row by row: (row block, column block).
 __device__ __forceinline__ void triangle(int t, int *mb, int *nb)
@@ -135,131 +234,166 @@ __device__ __forceinline__ void triangle(int t, int *mb, int *nb)
     *nb = t - r * (r + 1) / 2;
 }
 
-// D = A B^T on 128 x BN tiles (gram, poly: both operands K-major, lower-triangle tiles only;
-// apply: B = X is N-major).  Persistent CTAs; a ring of 64-deep stages filled by six TMA
-// threads, one MMA thread, two accumulators so that four warps drain one while the other fills.
-template <int BN, int MODE>
+// A 32 x 32 block of a symmetric result: lane = row r0 + lane, v its 32 columns from c0.
+// Rows are ldc (a multiple of eight) elements; columns M..ldc get zeros.
+__device__ __forceinline__ void store_symmetric(__half *C, int M, int ldc, int r0, int c0, const float (&v)[32],
+                                                bool mirror, __half *stage, int lane)
+{
+    uint32_t h[16];
+    #pragma unroll
+    for (int j = 0; j < 16; ++j) h[j] = half2_bits(v[2 * j], v[2 * j + 1]);
+    const int row = r0 + lane;
+    if (row < M) {
+        #pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c0 + 8 * j < M)
+                *reinterpret_cast<uint4 *>(C + (int64_t)row * ldc + c0 + 8 * j) =
+                    make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+    }
+    if (!mirror) return;
+    constexpr int pitch = 40;   // halves: 16-byte rows, lanes of one column on neighbouring banks
+    #pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const __half2 hh = *reinterpret_cast<const __half2 *>(&h[j]);
+        stage[(2 * j) * pitch + lane] = __low2half(hh);
+        stage[(2 * j + 1) * pitch + lane] = __high2half(hh);
+    }
+    __syncwarp();
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int col = j * 8 + (lane >> 2), part = (lane & 3) * 8;
+        if (c0 + col < M && r0 + part < M)
+            *reinterpret_cast<uint4 *>(C + (int64_t)(c0 + col) * ldc + r0 + part) =
+                *reinterpret_cast<const uint4 *>(stage + col * pitch + part);
+    }
+    __syncwarp();
+}
+
+// D = A B^T on 256 x 256 tiles by pairs of CTAs (gram, poly: both operands K-major, lower
+// triangle only; apply: B = X is N-major).  Each CTA holds 128 rows of A and 128 columns of
+// B, so a stage is 32 KB a CTA for 2 x 2^21 products: a CTA alone with a 128 x 256 tile loads
+// half as much again, and the loads, not the tensor cores, were its limit.  Persistent pairs; a
+// ring of 64-deep stages filled by four TMA threads a CTA, one MMA thread a pair, two
+// accumulators so that eight warps a CTA drain one while the other fills.
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ NewtonParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_full[8], bar_empty[8], bar_acc_full[2], bar_acc_empty[2], bar_drain;
+    __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages], bar_acc_full[2], bar_acc_empty[2], bar_drain;
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
     constexpr int b_mn = MODE == kApply ? 1 : 0;
-    constexpr uint32_t tmem_cols = 2 * BN <= 256 ? 256u : 512u;
-    constexpr uint32_t a_bytes = kBM * kBK * 2, b_bytes = BN * kBK * 2, stage_bytes = a_bytes + b_bytes;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     const uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int n_tiles = p.batch * p.tiles_per;
-    auto where = [&](int tile, int *bt, int *mb, int *nb) {
+    const int units = p.batch * p.tiles_per * p.splits;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    auto where = [&](int u, int *bt, int *mb, int *nb, int *k0, int *k1) {
+        const int sp = u % p.splits, tile = u / p.splits;
         *bt = tile / p.tiles_per;
         const int t = tile - *bt * p.tiles_per;
         if (MODE == kApply) { *mb = t % p.n_mblk; *nb = t / p.n_mblk; }
         else triangle(t, mb, nb);
+        *k0 = sp * p.k_per;
+        *k1 = min(p.n_kblk, *k0 + p.k_per);
     };
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        for (int i = 0; i < p.stages; ++i) {
-            ptx::mbar_init(ptx::smem_u32(&bar_full[i]), kProducers);
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&bar_full[i]), 1);
             ptx::mbar_init(ptx::smem_u32(&bar_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_u32(&bar_acc_full[i]), 1);
-            ptx::mbar_init(ptx::smem_u32(&bar_acc_empty[i]), 128);
+            ptx::mbar_init(ptx::smem_u32(&bar_acc_empty[i]), 2 * kDrainers);
         }
         ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tmA);
         ptx::prefetch_tmap(&tmB);
     }
-    if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_u32(&tmem_base_sh), tmem_cols);
-        ptx::tmem_relinquish();
+    if (warp == 0) {
+        tmem_alloc_pair(ptx::smem_u32(&tmem_base_sh), 512);
+        tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
-    __syncthreads();
+    cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
     ptx::griddep_wait();
     if (threadIdx.x == 0) ptx::griddep_launch_dependents();
 
-    if (warp == 0 || warp >= 6) {
-        // ---------------- TMA producers ----------------
+    if (warp >= 1 && warp <= kProducers) {
+        // ---------------- TMA producers: one 8 KB box a stage each ----------------
         if (lane == 0) {
-            const int pi = warp == 0 ? 0 : warp - 5;
-            constexpr int nA = 2, nB = BN / 64;
-            uint32_t my_bytes = 0;
-            for (int i = pi; i < nA + nB; i += kProducers) my_bytes += 8192u;
+            const int pi = warp - 1;                        // 0, 1: halves of A; 2, 3: halves of B
             int it = 0;
-            for (int tile = blockIdx.x; tile < n_tiles && !abort_flag; tile += gridDim.x) {
-                int bt, mb, nb;
-                where(tile, &bt, &mb, &nb);
-                for (int kb = 0; kb < p.n_kblk && !abort_flag; ++kb, ++it) {
-                    const int slot = it % p.stages;
-                    if (it >= p.stages &&
-                        !ptx::mbar_wait(ptx::smem_u32(&bar_empty[slot]), ((it / p.stages) - 1) & 1, p.wait_ns)) {
+            for (int u = pair; u < units && !abort_flag; u += pairs) {
+                int bt, mb, nb, k0, k1;
+                where(u, &bt, &mb, &nb, &k0, &k1);
+                const int r = (pi < 2 ? mb : nb) * kTile + (int)rank * 128 + (pi & 1) * 64;
+                for (int kb = k0; kb < k1 && !abort_flag; ++kb, ++it) {
+                    const int slot = it % kStages;
+                    if (it >= kStages &&
+                        !ptx::mbar_wait(ptx::smem_u32(&bar_empty[slot]), ((it / kStages) - 1) & 1, p.wait_ns)) {
                         abort_flag = 1;
                         raise_device_error(p.err, DEVERR_WAIT_TIMEOUT);
                         break;
                     }
-                    const uint32_t fb = ptx::smem_u32(&bar_full[slot]);
-                    const uint32_t sa = sbase + slot * stage_bytes, sb = sa + a_bytes;
-                    ptx::mbar_arrive_expect_tx(fb, my_bytes);
-                    for (int i = pi; i < nA + nB; i += kProducers) {
-                        if (i < nA) {
-                            ptx::tma_load_3d(sa + i * 8192, &tmA, kb * kBK, mb * kBM + i * 64, bt, fb);
-                        } else {
-                            const int c = i - nA;
-                            const int x = b_mn ? nb * BN + c * 64 : kb * kBK, y = b_mn ? kb * kBK : nb * BN + c * 64;
-                            ptx::tma_load_3d(sb + c * 8192, &tmB, x, y, bt, fb);
-                        }
-                    }
+                    // the pair's stage is one barrier in the first CTA
+                    const uint32_t local = ptx::smem_u32(&bar_full[slot]);
+                    if (rank == 0 && pi == 0) ptx::mbar_arrive_expect_tx(local, 2 * kStageBytes);
+                    const uint32_t fb = map_to(local, 0);
+                    const uint32_t dst = sbase + slot * kStageBytes + pi * 8192;
+                    if (pi >= 2 && b_mn) tma_load_pair(dst, &tmB, r, kb * kBK, bt, fb);
+                    else tma_load_pair(dst, pi < 2 ? &tmA : &tmB, kb * kBK, r, bt, fb);
                 }
             }
-            // drain: this thread's copies have landed once its last stages are full (bounded; after
-            // an abort a stage may never fill, and the copies, issued long before, have landed)
-            for (int j = max(0, it - p.stages); j < it; ++j)
-                if (!ptx::mbar_wait(ptx::smem_u32(&bar_full[j % p.stages]), (j / p.stages) & 1, kDrainNs)) {
+            // drain: the copies of the last stages have been consumed once their slots are free
+            for (int j = max(0, it - kStages); j < it; ++j)
+                if (!ptx::mbar_wait(ptx::smem_u32(&bar_empty[j % kStages]), (j / kStages) & 1, kDrainNs)) {
                     raise_device_error(p.err, DEVERR_WAIT_TIMEOUT);
                     break;
                 }
         }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            const uint32_t idesc = idesc_f16(kBM, BN, b_mn);
+    } else if (warp == 0) {
+        // ---------------- MMA issuer of the pair ----------------
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_f16(kTile, kTile, b_mn);
             const uint64_t a0 = ptx::smem_desc(sbase, 16, 1024, 2);
-            const uint64_t b0 = b_mn ? ptx::smem_desc(sbase + a_bytes, 8192, 1024, 2)
-                                     : ptx::smem_desc(sbase + a_bytes, 16, 1024, 2);
+            const uint64_t b0 = b_mn ? ptx::smem_desc(sbase + kOperand, 8192, 1024, 2)
+                                     : ptx::smem_desc(sbase + kOperand, 16, 1024, 2);
             constexpr uint64_t ak = 32 >> 4, bk = b_mn ? 2048 >> 4 : 32 >> 4;
             int local = 0, slot = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x, ++local) {
+            for (int u = pair; u < units && ok; u += pairs, ++local) {
+                int bt, mb, nb, k0, k1;
+                where(u, &bt, &mb, &nb, &k0, &k1);
                 const int buf = local & 1;
                 if (local >= 2 && !ptx::mbar_test_wait(ptx::smem_u32(&bar_acc_empty[buf]), ((local >> 1) - 1) & 1))
                     ok = ptx::mbar_wait_ool(ptx::smem_u32(&bar_acc_empty[buf]), ((local >> 1) - 1) & 1, p.wait_ns, nullptr);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t dt = tmem + (uint32_t)(buf * BN);
-                for (int kb = 0; kb < p.n_kblk; ++kb) {
+                const uint32_t dt = tmem + (uint32_t)(buf * kTile);
+                for (int kb = k0; kb < k1; ++kb) {
                     const uint32_t fb = ptx::smem_u32(&bar_full[slot]);
                     if (!ptx::mbar_test_wait(fb, phase) && ok) ok = ptx::mbar_wait_ool(fb, phase, p.wait_ns, nullptr);
                     ptx::tc_fence_after();
-                    const uint64_t so = (uint64_t)((slot * stage_bytes) >> 4);
+                    const uint64_t so = (uint64_t)((slot * kStageBytes) >> 4);
                     const uint64_t ad = a0 + so, bd = b0 + so;
                     #pragma unroll
                     for (int k = 0; k < kBK / 16; ++k)
-                        ptx::mma_f16(dt, ad + k * ak, bd + k * bk, idesc, (kb > 0 || k > 0) ? 1u : 0u);
-                    ptx::mma_commit(ptx::smem_u32(&bar_empty[slot]));
-                    if (++slot == p.stages) { slot = 0; phase ^= 1u; }
+                        mma_f16_pair(dt, ad + k * ak, bd + k * bk, idesc, (kb > k0 || k > 0) ? 1u : 0u);
+                    mma_commit_pair(ptx::smem_u32(&bar_empty[slot]));
+                    if (++slot == kStages) { slot = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
-                ptx::mma_commit(ptx::smem_u32(&bar_acc_full[buf]));
+                mma_commit_pair(ptx::smem_u32(&bar_acc_full[buf]));
                 if (abort_flag) ok = false;
             }
             if (!ok) {
@@ -268,74 +402,143 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             }
         }
     } else {
-        // ---------------- epilogue (warps 2-5 -> TMEM lane groups 2,3,0,1) ----------------
-        const int lg = warp & 3;
+        // ---------------- drain: lanes 32 lg.. of tensor memory, 128 columns a warp ----------------
+        const int lg = warp & 3, dw = warp - 1 - kProducers;
+        const int half = dw >> 2;
+        uint8_t *stage8 = smem_raw + (sbase - ptx::smem_u32(smem_raw)) + kStages * kStageBytes + dw * kWarpStage;
+        float *stage = reinterpret_cast<float *>(stage8);
         int local = 0;
-        for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++local) {
+        for (int u = pair; u < units; u += pairs, ++local) {
             const int buf = local & 1;
             bool ready = ptx::mbar_wait(ptx::smem_u32(&bar_acc_full[buf]), (local >> 1) & 1, p.wait_ns);
             if (!ready) raise_device_error(p.err, DEVERR_WAIT_TIMEOUT);
             ready = __all_sync(0xffffffffu, ready && !abort_flag);
             if (!ready) break;
             ptx::tc_fence_after();
-            int bt, mb, nb;
-            where(tile, &bt, &mb, &nb);
-            const int row = mb * kBM + lg * 32 + lane;
+            int bt, mb, nb, k0, k1;
+            where(u, &bt, &mb, &nb, &k0, &k1);
+            const int r0 = mb * kTile + (int)rank * 128 + lg * 32, row = r0 + lane;
             __half *C = p.C + (int64_t)bt * p.M * p.ldc;
-            const __half *A = MODE == kPoly ? p.A + (int64_t)bt * p.M * p.ldc : nullptr;
-            for (int c0 = 0; c0 < BN; c0 += 16) {
-                uint32_t acc[16];
-                ptx::tmem_ld16(tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * BN + c0), acc);
+            for (int blk = half * 4; blk < half * 4 + 4; ++blk) {
+                uint32_t raw[2][16];
+                const uint32_t at = tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * kTile + blk * 32);
+                ptx::tmem_ld16(at, raw[0]);
+                ptx::tmem_ld16(at + 16, raw[1]);
                 ptx::tmem_ld_wait();
-                const int col0 = nb * BN + c0;
-                if (row >= p.M || col0 >= p.N) continue;
-                if (MODE == kApply) {
-                    if (p.last) {
+                const int c0 = nb * kTile + blk * 32;
+                if (r0 >= p.M || c0 >= p.N) continue;
+                float v[32];
+                #pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j >> 4][j & 15]);
+                if (MODE == kGram && p.splits > 1) {
+                    // [unit][CTA][drain warp][block][4 columns][lane]: newton_sum_kernel reads it the same way
+                    float4 *dst = reinterpret_cast<float4 *>(p.part) +
+                                  ((((int64_t)u * 2 + rank) * kDrainers + dw) * 4 + (blk & 3)) * 256 + lane;
+                    #pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dst[j * 32] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                } else if (MODE == kGram) {
+                    #pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= 1.f / kScale;
+                    store_symmetric(C, p.M, p.ldc, r0, c0, v, mb != nb, reinterpret_cast<__half *>(stage8), lane);
+                } else if (MODE == kPoly) {
+                    const __half *A = p.A + (int64_t)bt * p.M * p.ldc + (int64_t)row * p.ldc + c0;
+                    #pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint4 lin = make_uint4(0, 0, 0, 0);
+                        if (row < p.M && c0 + 8 * j < p.M) lin = *reinterpret_cast<const uint4 *>(A + 8 * j);
+                        const uint32_t w[4] = {lin.x, lin.y, lin.z, lin.w};
                         #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (col0 + j < p.N)
-                                store_result(p.o, (int64_t)bt * p.M * p.N + (p.o.tall ? (int64_t)(col0 + j) * p.M + row
-                                                                                  : (int64_t)row * p.N + col0 + j),
-                                             __uint_as_float(acc[j]) * (1.f / (kScale * kScale)));
-                    } else {
-                        __half2 h[8];
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                            v[8 * j + 2 * k] = fmaf(p.c * (1.f / kScale), v[8 * j + 2 * k], p.b * l.x);
+                            v[8 * j + 2 * k + 1] = fmaf(p.c * (1.f / kScale), v[8 * j + 2 * k + 1], p.b * l.y);
+                        }
+                    }
+                    if (r0 == c0) {
                         #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            h[j] = __floats2half2_rn(__uint_as_float(acc[2 * j]) * (1.f / kScale),
-                                                     __uint_as_float(acc[2 * j + 1]) * (1.f / kScale));
-                        // rows are padded to 8 columns, which no product reads past N
-                        uint4 *dst = reinterpret_cast<uint4 *>(C + (int64_t)row * p.ldc + col0);
-                        dst[0] = *reinterpret_cast<uint4 *>(&h[0]);
-                        if (col0 + 8 < p.N) dst[1] = *reinterpret_cast<uint4 *>(&h[4]);
+                        for (int j = 0; j < 32; ++j)
+                            if (j == lane && row < p.M) v[j] += p.a * kScale;
+                    }
+                    store_symmetric(C, p.M, p.ldc, r0, c0, v, mb != nb, reinterpret_cast<__half *>(stage8), lane);
+                } else if (!p.last) {
+                    if (row < p.M) {
+                        #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t h[4];
+                            #pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                h[k] = half2_bits(v[8 * j + 2 * k] * (1.f / kScale), v[8 * j + 2 * k + 1] * (1.f / kScale));
+                            // rows are padded to eight columns, which no product reads past N
+                            if (c0 + 8 * j < p.N)
+                                *reinterpret_cast<uint4 *>(C + (int64_t)row * p.ldc + c0 + 8 * j) =
+                                    make_uint4(h[0], h[1], h[2], h[3]);
+                        }
                     }
                 } else {
-                    #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int col = col0 + j;
-                        float v = __uint_as_float(acc[j]) * (1.f / kScale);
-                        if (col > row) continue;
-                        if (MODE == kPoly) {
-                            const float lin = __half2float(A[(int64_t)row * p.ldc + col]);
-                            v = fmaf(p.c * (1.f), v, p.b * lin);
-                            if (col == row) v += p.a * kScale;
-                        }
-                        const __half hv = __float2half_rn(v);
-                        C[(int64_t)row * p.ldc + col] = hv;
-                        if (col != row) C[(int64_t)col * p.ldc + row] = hv;
+                    constexpr float back = 1.f / (kScale * kScale);
+                    const int64_t out0 = (int64_t)bt * p.M * p.N;
+                    if (p.o.tall) {
+                        #pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (row < p.M && c0 + j < p.N) store_result(p.o, out0 + (int64_t)(c0 + j) * p.M + row, v[j] * back);
+                    } else {
+                        #pragma unroll
+                        for (int j = 0; j < 32; ++j) stage[lane * kStagePitch + j] = v[j] * back;
+                        __syncwarp();
+                        store_rows(p.o, out0 + (int64_t)r0 * p.N + c0, p.N, min(32, p.M - r0), min(32, p.N - c0), stage, lane);
+                        __syncwarp();
                     }
                 }
             }
             ptx::tc_fence_before();
-            ptx::mbar_arrive(ptx::smem_u32(&bar_acc_empty[buf]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(ptx::smem_u32(&bar_acc_empty[buf]), 0);
         }
     }
-    if (warp == 1 && lane == 0) {
-        ptx::mma_commit(ptx::smem_u32(&bar_drain));
+    if (warp == 0 && lane == 0 && rank == 0) {
+        // every issued MMA ends before tensor memory is released
+        mma_commit_pair_here(ptx::smem_u32(&bar_drain));
         if (!ptx::mbar_wait(ptx::smem_u32(&bar_drain), 0, kDrainNs)) raise_device_error(p.err, DEVERR_WAIT_TIMEOUT);
     }
+    __syncwarp();
     ptx::tc_fence_before();
-    __syncthreads();
-    if (warp == 1) ptx::tmem_dealloc(tmem, tmem_cols);
+    cluster_sync();   // no CTA leaves while the other may signal it or use its operands
+    if (warp == 0) tmem_dealloc_pair(tmem, 512);
+}
+
+// A = the sum of the splits of a gram, in split order, scaled, rounded and mirrored.  A warp a
+// 32 x 32 block of a tile.
+__global__ void __launch_bounds__(256) newton_sum_kernel(const __grid_constant__ NewtonParams p)
+{
+    __shared__ __align__(16) __half stage[8][32 * 40];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = blockIdx.x * 8 + warp;
+    const int tile = w >> 6, rank = (w >> 5) & 1, dw = (w >> 2) & 7, b = w & 3;
+    if (tile >= p.batch * p.tiles_per) return;
+    const int bt = tile / p.tiles_per;
+    int mb, nb;
+    triangle(tile - bt * p.tiles_per, &mb, &nb);
+    const int lg = (dw + 1 + kProducers) & 3, blk = (dw >> 2) * 4 + b;
+    const int r0 = mb * kTile + rank * 128 + lg * 32, c0 = nb * kTile + blk * 32;
+    if (r0 >= p.M || c0 >= p.N) return;
+    float v[32];
+    #pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+    for (int s = 0; s < p.splits; ++s) {
+        const float4 *src = reinterpret_cast<const float4 *>(p.part) +
+                            ((((int64_t)(tile * p.splits + s) * 2 + rank) * kDrainers + dw) * 4 + b) * 256 + lane;
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 q = src[j * 32];
+            v[4 * j] += q.x; v[4 * j + 1] += q.y; v[4 * j + 2] += q.z; v[4 * j + 3] += q.w;
+        }
+    }
+    #pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= 1.f / kScale;
+    store_symmetric(p.C + (int64_t)bt * p.M * p.ldc, p.M, p.ldc, r0, c0, v, mb != nb, stage[warp], lane);
 }
 
 // ---- host side ----------------------------------------------------------------
@@ -371,6 +574,16 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// Splits of a gram's K: as many as give every pair of CTAs a unit, of at least four stages each.
+int gram_splits(const NewtonShape &s, int *k_per)
+{
+    const int mb = (s.m + kTile - 1) / kTile, kblk = (s.n + kBK - 1) / kBK;
+    const int64_t tiles = (int64_t)s.G * mb * (mb + 1) / 2;
+    const int want = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / tiles, kblk / 4));
+    *k_per = (kblk + want - 1) / want;
+    return (kblk + *k_per - 1) / *k_per;
+}
+
 bool newton_shape(const gconv_matrices *t, NewtonShape *s)
 {
     if (!t || t->rows < 1 || t->cols < 1 || t->count < 0) return false;
@@ -382,35 +595,49 @@ bool newton_shape(const gconv_matrices *t, NewtonShape *s)
     s->n = s->tall ? t->rows : t->cols;
     s->ldx = (s->n + 7) & ~7;
     s->lda = (s->m + 7) & ~7;
+    s->parts = (int)std::min<int64_t>(kNormBlocks, (e + kNormShare - 1) / kNormShare);
     s->x_bytes = up256((size_t)s->G * s->m * s->ldx * 2);
     s->a_bytes = up256((size_t)s->G * s->m * s->lda * 2);
-    s->ws = up256((size_t)s->G * kNormBlocks * 4) + 2 * s->x_bytes + 2 * s->a_bytes;
+    s->ws = 0;
+    if (s->G == 0 || newton_small_fits(*s)) return true;
+    int k_per;
+    const int splits = gram_splits(*s, &k_per), mb = (s->m + kTile - 1) / kTile;
+    s->part_bytes = splits > 1 ? (size_t)s->G * mb * (mb + 1) / 2 * splits * kTile * kTile * 4 : 0;
+    s->ws = up256((size_t)s->G * s->parts * 4) + 2 * s->x_bytes + 2 * s->a_bytes + s->part_bytes;
     return true;
 }
 
-constexpr size_t kMaxSmem = 220 * 1024;
-
-template <int BN, int MODE>
-gconv_status launch_gemm(const CUtensorMap &tA, const CUtensorMap &tB, NewtonParams p, cudaStream_t st)
+template <int MODE>
+gconv_status launch_gemm(const CUtensorMap &tA, const CUtensorMap &tB, NewtonParams &p, cudaStream_t st)
 {
-    p.n_mblk = (p.M + kBM - 1) / kBM;
-    p.n_nblk = (p.N + BN - 1) / BN;
+    p.n_mblk = (p.M + kTile - 1) / kTile;
     p.n_kblk = (p.K + kBK - 1) / kBK;
-    p.tiles_per = MODE == kApply ? p.n_mblk * p.n_nblk : p.n_mblk * (p.n_mblk + 1) / 2;
-    const size_t stage = (size_t)(kBM + BN) * kBK * 2;
-    p.stages = (int)std::min<size_t>(8, (kMaxSmem - 1024) / stage);
+    p.tiles_per = MODE == kApply ? p.n_mblk * ((p.N + kTile - 1) / kTile) : p.n_mblk * (p.n_mblk + 1) / 2;
+    if (MODE != kGram) { p.splits = 1; p.k_per = p.n_kblk; }
     static bool attr[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GCONV_ERR_CUDA;
     if (!attr[dev]) {
-        if (cudaFuncSetAttribute(newton_gemm_kernel<BN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kMaxSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(newton_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
+            cudaSuccess)
             return GCONV_ERR_CUDA;
         attr[dev] = true;
     }
-    const int64_t tiles = (int64_t)p.batch * p.tiles_per;
-    launch_dependent(newton_gemm_kernel<BN, MODE>, (unsigned)std::min<int64_t>(tiles, num_sms()), kThreads,
-                     p.stages * stage + 1024, st, tA, tB, p);
+    const int64_t units = (int64_t)p.batch * p.tiles_per * p.splits;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(units, num_sms() / 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, newton_gemm_kernel<MODE>, tA, tB, p);
     return GCONV_OK;
 }
 
@@ -421,44 +648,60 @@ gconv_status run_newton(const NewtonShape &s, NewtonIn in, const NewtonOut &out,
     if (!err) return GCONV_ERR_CUDA;
     cudaGetLastError();   // clear a stale error: the check after the launches is about this call
     NewtonOut o = out;
-    o.tall = in.tall = s.tall; in.rows = s.rows; in.cols = s.cols; in.elems = (int64_t)s.rows * s.cols;
+    o.tall = in.tall = s.tall;
+    in.rows = s.rows; in.cols = s.cols; in.elems = (int64_t)s.rows * s.cols;
     if (newton_small_fits(s)) return newton_small_launch(s, in, o, steps, coeffs, err, st);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *part = reinterpret_cast<float *>(ws);
-    ws += up256((size_t)s.G * kNormBlocks * 4);
+    ws += up256((size_t)s.G * s.parts * 4);
     __half *x[2] = {reinterpret_cast<__half *>(ws), reinterpret_cast<__half *>(ws + s.x_bytes)};
     ws += 2 * s.x_bytes;
     __half *A = reinterpret_cast<__half *>(ws), *P = reinterpret_cast<__half *>(ws + s.a_bytes);
+    ws += 2 * s.a_bytes;
     CUtensorMap tX[2], tA, tP;
     if (!half_tmap(&tX[0], x[0], s.n, s.m, s.ldx, s.G) || !half_tmap(&tX[1], x[1], s.n, s.m, s.ldx, s.G) ||
         !half_tmap(&tA, A, s.m, s.m, s.lda, s.G) || !half_tmap(&tP, P, s.m, s.m, s.lda, s.G))
         return GCONV_ERR_CUDA;
-    const int parts = (int)std::min<int64_t>(kNormBlocks, (in.elems + 1023) / 1024);
-    for (int g0 = 0; g0 < s.G; g0 += 65535) {   // grid y and z are 16 bits
-        const int g = std::min(65535, s.G - g0);
-        NewtonIn part_in = in;
+    const int64_t share = ((in.elems + s.parts - 1) / s.parts + 7) & ~(int64_t)7;
+    const bool v8 = in.elems % 8 == 0;
+    const int col_tiles = (s.cols + 31) / 32, row_tiles = (s.rows + 63) / 64;
+    for (int g0 = 0; g0 < s.G; g0 += 65535) {   // a grid's y is 16 bits
+        const unsigned g = (unsigned)std::min(65535, s.G - g0);
+        NewtonIn q = in;
         const int64_t off = (int64_t)g0 * in.elems;
-        part_in.g = static_cast<const uint8_t *>(in.g) + off * (in.g_bf16 ? 2 : 4);
-        if (in.m) { part_in.m = in.m + off; part_in.m_out = in.m_out + off; }
-        newton_norm_kernel<<<dim3(parts, g), 256, 0, st>>>(part_in, part + (size_t)g0 * kNormBlocks);
-        newton_scale_kernel<<<dim3((s.cols + 31) / 32, (s.rows + 31) / 32, g), 256, 0, st>>>(
-            part_in, part + (size_t)g0 * kNormBlocks, parts, x[0] + (int64_t)g0 * s.m * s.ldx, s.ldx);
+        q.g = static_cast<const uint8_t *>(in.g) + off * (in.g_bf16 ? 2 : 4);
+        if (in.m) { q.m = in.m + off; q.m_out = in.m_out + off; }
+        float *pg = part + (size_t)g0 * s.parts;
+        __half *xg = x[0] + (int64_t)g0 * s.m * s.ldx;
+        if (v8) newton_norm_kernel<8><<<dim3(s.parts, g), 256, 0, st>>>(q, pg, share);
+        else newton_norm_kernel<1><<<dim3(s.parts, g), 256, 0, st>>>(q, pg, share);
+        if (!s.tall && s.n % 8 == 0)
+            newton_scale_flat_kernel<<<dim3((unsigned)((in.elems + kNormShare - 1) / kNormShare), g), 256, 0, st>>>(
+                q, pg, s.parts, xg);
+        else
+            newton_scale_kernel<<<dim3((unsigned)(col_tiles * row_tiles), g), 256, 0, st>>>(q, pg, s.parts, xg, s.ldx,
+                                                                                            col_tiles);
     }
+    NewtonParams p{};
+    p.batch = s.G; p.err = err; p.wait_ns = (uint64_t)wait_limit();
+    p.part = reinterpret_cast<float *>(ws);
+    p.M = s.m;
+    p.o = o;
     for (int k = 0; k < steps; ++k) {
         const float *c = coeffs ? coeffs + 3 * k : kNewtonCoeffs;
-        NewtonParams p{};
-        p.batch = s.G; p.err = err; p.wait_ns = (uint64_t)wait_limit();
-        p.M = s.m; p.N = s.m; p.K = s.n; p.ldc = s.lda; p.C = A;
-        gconv_status r = launch_gemm<128, kGram>(tX[k & 1], tX[k & 1], p, st);
+        p.N = s.m; p.K = s.n; p.ldc = s.lda; p.C = A;
+        p.splits = gram_splits(s, &p.k_per);
+        gconv_status r = launch_gemm<kGram>(tX[k & 1], tX[k & 1], p, st);
         if (r != GCONV_OK) return r;
+        if (p.splits > 1)
+            launch_dependent(newton_sum_kernel, (unsigned)(p.batch * p.tiles_per * 8), 256, 0, st, p);
         p.K = s.m; p.C = P; p.A = A;
         p.a = c[0]; p.b = c[1]; p.c = c[2];
-        r = launch_gemm<128, kPoly>(tA, tA, p, st);
+        r = launch_gemm<kPoly>(tA, tA, p, st);
         if (r != GCONV_OK) return r;
         p.N = s.n; p.ldc = s.ldx; p.C = x[(k + 1) & 1];
         p.last = k + 1 == steps;
-        p.o = o;
-        r = launch_gemm<256, kApply>(tP, tX[k & 1], p, st);
+        r = launch_gemm<kApply>(tP, tX[k & 1], p, st);
         if (r != GCONV_OK) return r;
     }
     return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA;
@@ -485,7 +728,7 @@ extern "C" {
 size_t gconv_orthogonalize_workspace_size(const gconv_matrices *matrices)
 {
     NewtonShape s;
-    return newton_shape(matrices, &s) ? (s.G ? s.ws : 0) : (size_t)-1;
+    return newton_shape(matrices, &s) ? s.ws : (size_t)-1;
 }
 
 gconv_status gconv_orthogonalize(const gconv_matrices *matrices, gconv_dtype dtype, gconv_dtype out_dtype, const void *g,
@@ -498,7 +741,7 @@ gconv_status gconv_orthogonalize(const gconv_matrices *matrices, gconv_dtype dty
         return GCONV_ERR_INVALID_ARG;
     if (s.G == 0) return GCONV_OK;
     if (!g || !out || !aligned16(g) || !aligned16(out) || !aligned16(workspace)) return GCONV_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < s.ws) return GCONV_ERR_WORKSPACE;
+    if (s.ws && (!workspace || workspace_bytes < s.ws)) return GCONV_ERR_WORKSPACE;
     NewtonIn in{};
     in.g = g; in.g_bf16 = dtype == GCONV_BF16; in.eps = eps;
     NewtonOut o{};
@@ -518,7 +761,7 @@ gconv_status gconv_muon_step(const gconv_matrices *matrices, const gconv_muon *o
     for (const void *q : {(const void *)w, (const void *)grad, (const void *)momentum, (const void *)w_out,
                           (const void *)momentum_out, (const void *)w_bf16, (const void *)workspace})
         if (!aligned16(q)) return GCONV_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < s.ws) return GCONV_ERR_WORKSPACE;
+    if (s.ws && (!workspace || workspace_bytes < s.ws)) return GCONV_ERR_WORKSPACE;
     NewtonIn in{};
     in.g = grad; in.m = momentum; in.m_out = momentum_out; in.beta = opt->beta; in.nesterov = opt->nesterov != 0;
     in.eps = opt->eps;

@@ -66,6 +66,114 @@ __device__ __forceinline__ void store_result(const NewtonOut &o, int64_t at, flo
     }
 }
 
+// A staged 32 x 32 block (rows of 33 floats) of the result: `rows` rows of `cols` columns, n
+// elements apart from element `at`, a row a store so that a warp writes consecutive elements.
+// Reads of the weights are issued eight rows ahead of the writes, which may alias them.
+__device__ __forceinline__ void store_rows(const NewtonOut &o, int64_t at, int n, int rows, int cols, const float *stage,
+                                           int lane)
+{
+    if (lane >= cols) return;
+    at += lane;
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        float v[8];
+        #pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (r0 + k < rows) {
+                v[k] = stage[(r0 + k) * 33 + lane];
+                if (o.muon) v[k] = fmaf(-o.rate, v[k], o.keep * o.w[at + (int64_t)(r0 + k) * n]);
+            }
+        #pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (r0 + k < rows) {
+                const int64_t i = at + (int64_t)(r0 + k) * n;
+                if (o.muon) {
+                    o.w_out[i] = v[k];
+                    if (o.w_bf16) o.w_bf16[i] = __float2bfloat16_rn(v[k]);
+                } else if (o.out_bf16) {
+                    static_cast<__nv_bfloat16 *>(o.out)[i] = __float2bfloat16_rn(v[k]);
+                } else {
+                    static_cast<float *>(o.out)[i] = v[k];
+                }
+            }
+    }
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// Arrives at the barrier that stands at this block's offset `bar` in block `rank` of the cluster.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t rank)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to(bar, rank)) : "memory");
+}
+
+// A 3D tensor-map load into this block's shared memory that signals a barrier of its pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *tmap, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+}
+
+// Tensor memory of both blocks of a pair; one warp of each calls these.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void tmem_relinquish_pair()
+{
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// The pair's product: 128 rows of D and A and half of B's columns in each block, at the same offsets.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Arrives at `bar` of both blocks once the products issued so far have ended.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+
+// The same for `bar` of this block alone.
+__device__ __forceinline__ void mma_commit_pair_here(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // fp16 instruction descriptor: f16 A and B, f32 accumulator
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major)
 {
@@ -74,8 +182,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major)
 
 // The matrices of a call: m <= n, X is m x n.
 struct NewtonShape {
-    int G, rows, cols, m, n, tall, ldx, lda;
-    size_t x_bytes, a_bytes, ws;
+    int G, rows, cols, m, n, tall, ldx, lda, parts;
+    size_t x_bytes, a_bytes, part_bytes, ws;
 };
 
 // Matrices whose shorter side fits one tile, in one launch each call (newton_small.cu).

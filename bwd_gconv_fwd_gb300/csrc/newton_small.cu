@@ -38,25 +38,6 @@ struct SmallParams {
     float coeffs[3 * kNewtonSteps];
 };
 
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr)
 {
     float4 v;
@@ -83,12 +64,6 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;
 __device__ __forceinline__ uint32_t piece(int row, int col)
 {
     return (uint32_t)(col >> 6) * kChunkBytes + (uint32_t)row * 128u + (uint32_t)((((col & 63) >> 3) ^ (row & 7)) << 4);
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float a, float b)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // V elements of the matrix to orthogonalise, at element i of the caller's tensors.  FIRST:
@@ -415,11 +390,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
             #pragma unroll
             for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = f[j] * back;
             __syncwarp();
-            const int col = blk * 32 + lane;
-            #pragma unroll 8
-            for (int r = 0; r < 32; ++r)
-                if (q * 32 + r < p.m && col < width)
-                    store_result(p.out, out0 + (int64_t)(q * 32 + r) * p.n + c0 + col, stage[r * 33 + lane]);
+            store_rows(p.out, out0 + (int64_t)(q * 32) * p.n + c0 + blk * 32, p.n, min(32, p.m - q * 32),
+                       min(32, width - blk * 32), stage, lane);
             __syncwarp();
         }
     }
@@ -463,8 +435,10 @@ gconv_status newton_small_launch(const NewtonShape &s, const NewtonIn &in, const
     p.cluster = small_cluster(s, &p.slice);
     p.err = err; p.wait_ns = (uint64_t)wait_limit();
     for (int k = 0; k < 3 * steps; ++k) p.coeffs[k] = coeffs ? coeffs[k] : kNewtonCoeffs[k % 3];
-    // X, A, then P or (several blocks) 64 KB of partial sums; the result is staged over them
-    const size_t smem = 1024 + (size_t)(p.slice / 64) * kChunkBytes + 2 * kChunkBytes + (p.cluster > 1 ? 4 : 2) * kChunkBytes;
+    // X, A, then P or (several blocks) 64 KB of partial sums; the result is staged over them.
+    // More than half an SM's shared memory: two blocks on one SM would wait for each other's
+    // tensor memory, and two clusters that each hold what the other waits for would never end.
+    const size_t smem = std::max<size_t>(1024 + (size_t)(p.slice / 64 + 2 + (p.cluster > 1 ? 4 : 2)) * kChunkBytes, 120 * 1024);
     const bool vec = s.cols % 4 == 0;
     static bool attr[64][2] = {};
     int dev = 0;
