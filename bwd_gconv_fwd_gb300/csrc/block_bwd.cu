@@ -1,30 +1,58 @@
 // block_bwd.cu -- the block norm / join backward kernels' instances and launches.
 #include "block_internal.h"
+#include "block_stage.cuh"
 
 namespace gconv {
 
 namespace {
 
-template <typename T, int VEC, bool ONE>
+template <typename T, int VEC>
 void launch(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
 {
     constexpr int NCH = block_nch(VEC);
     if (kind == kBlockNorm)
-        launch_dependent(block_bwd_kernel<T, VEC, NCH, false, true, ONE>, s.grid, s.threads, s.smem, st, a);
+        launch_dependent(block_bwd_kernel<T, VEC, NCH, false, true>, s.grid, s.threads, s.smem, st, a);
     else if (kind == kBlockJoin)
-        launch_dependent(block_bwd_kernel<T, VEC, NCH, true, false, ONE>, s.grid, s.threads, s.smem, st, a);
+        launch_dependent(block_bwd_kernel<T, VEC, NCH, true, false>, s.grid, s.threads, s.smem, st, a);
     else
-        launch_dependent(block_bwd_kernel<T, VEC, NCH, true, true, ONE>, s.grid, s.threads, s.smem, st, a);
+        launch_dependent(block_bwd_kernel<T, VEC, NCH, true, true>, s.grid, s.threads, s.smem, st, a);
+}
+
+template <void (*Kernel)(BlockArgs)>
+void launch_staged(const BlockShape &s, const BlockArgs &a, cudaStream_t st)
+{
+    static bool attr[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return;   // the error stays for the caller's check
+    if (!attr[dev]) {
+        if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem) != cudaSuccess) return;
+        attr[dev] = true;
+    }
+    launch_dependent(Kernel, s.grid, s.threads, s.smem, st, a);
+}
+
+template <typename T, bool PAIR>
+void staged(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
+{
+    if (kind == kBlockNorm) launch_staged<block_bwd_stage_kernel<T, PAIR, false, true>>(s, a, st);
+    else if (kind == kBlockJoin) launch_staged<block_bwd_stage_kernel<T, PAIR, true, false>>(s, a, st);
+    else launch_staged<block_bwd_stage_kernel<T, PAIR, true, true>>(s, a, st);
 }
 
 template <typename T>
 void launch_t(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
 {
-    if (!s.one) launch<T, 1, false>(kind, s, a, st);
-    else if (s.vec == 1) launch<T, 1, true>(kind, s, a, st);
-    else if (s.vec == 2) launch<T, 2, true>(kind, s, a, st);
-    else if (s.vec == 4) launch<T, 4, true>(kind, s, a, st);
-    else if constexpr (sizeof(T) == 2) launch<T, 8, true>(kind, s, a, st);
+    if (s.staged && a.P % 2 == 0) staged<T, true>(kind, s, a, st);
+    else if (s.staged) staged<T, false>(kind, s, a, st);
+    else if (s.one && s.vec == 1) launch<T, 1>(kind, s, a, st);
+    else if (s.one && s.vec == 2) launch<T, 2>(kind, s, a, st);
+    else if (s.one) launch<T, 4>(kind, s, a, st);
+    else if (kind == kBlockNorm)
+        launch_dependent(block_bwd_walk_kernel<T, false, true>, s.grid, s.threads, s.smem, st, a);
+    else if (kind == kBlockJoin)
+        launch_dependent(block_bwd_walk_kernel<T, true, false>, s.grid, s.threads, s.smem, st, a);
+    else
+        launch_dependent(block_bwd_walk_kernel<T, true, true>, s.grid, s.threads, s.smem, st, a);
 }
 
 }  // namespace

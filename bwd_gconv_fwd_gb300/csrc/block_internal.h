@@ -7,7 +7,9 @@ namespace gconv {
 
 // The shape of one launch (block_norm.cu, block_shape).
 struct BlockShape {
-    int vec, one;             // positions a thread holds at once; a thread's channels fit in registers
+    int staged;               // the kernels of block_stage.cuh, with:
+    int PT, flat, per, total, nch, pitch, tensor, pieces, lanes2;
+    int vec, one;             // else: positions a thread holds at once; its channels fit in registers
     int TX, TY, Z, PV, tiles, splits;
     int threads;
     unsigned grid;
@@ -16,7 +18,9 @@ struct BlockShape {
 
 enum { kBlockNorm = 0, kBlockJoin = 1, kBlockJoinNext = 2 };
 
-// Channels a thread holds: four where it holds 4 or 8 positions of each, eight where 1 or 2.
+constexpr size_t kBlockSmem = 227 * 1024;
+
+// Channels a thread holds: four where it holds 4 positions of each, eight where 1 or 2.
 constexpr int block_nch(int vec) { return vec >= 4 ? 4 : 8; }
 
 void block_fwd_launch(int kind, gconv_dtype dt, const BlockShape &s, const BlockArgs &a, cudaStream_t st);

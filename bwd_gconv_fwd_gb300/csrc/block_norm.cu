@@ -1,6 +1,7 @@
 // block_norm.cu -- extern "C" entry points of the block norm and block join: checks,
 // launch shapes, the channel-gradient finish.  The kernels are in block_norm.cuh.
 #include "block_internal.h"
+#include "block_stage.cuh"
 
 #include <algorithm>
 #include <climits>
@@ -18,10 +19,18 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // few, so the reads' latency, not their bytes, is what the launch costs.
 constexpr int kFinChannels = 8, kFinLanes = 32;
 
+struct FinishArgs {
+    const float *part;
+    int N, C, G, Cg, Z, splits;   // part: [2][splits][N][C], splits the most blocks that share rows
+    int tiles, per;               // Z rows' tiles from (row / Z) tiles on were walked `per` to a block
+    int next, post, gate, act;
+    const void *z;
+    const float *w, *s;
+    float *dw2, *dw, *ds, *dzc;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kFinChannels * kFinLanes)
-block_finish_kernel(const float *part, int N, int C, int splits, int next, int post, int gate, int act, const T *zg,
-                    const float *w, const float *s, float *dw2, float *dw, float *ds, float *dzc)
+__global__ void __launch_bounds__(kFinChannels * kFinLanes) block_finish_kernel(const FinishArgs a)
 {
     __shared__ float sh[2][kFinLanes][kFinChannels];
     const int cl = threadIdx.x % kFinChannels, ln = threadIdx.x / kFinChannels;
@@ -29,35 +38,38 @@ block_finish_kernel(const float *part, int N, int C, int splits, int next, int p
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     float t2 = 0.f, tk = 0.f;
-    if (c < C) {
-        const int64_t NC = (int64_t)N * C;
-        const float *p0 = part, *p1 = part + splits * NC;
-        const bool per_image = post && gate == GCONV_GATE_CHANNEL;
-        const float kc = (w ? w[c] : 1.f) * (s ? s[c] : 1.f);
-        if (next && dw2)
-            for (int64_t i = ln; i < (int64_t)N * splits; i += kFinLanes) t2 += p0[i * C + c];   // [splits][N][C]
-        if (per_image) {
-            for (int n = ln; n < N; n += kFinLanes) {
-                float q = 0.f;
-                for (int i = 0; i < splits; ++i) q += p1[i * NC + (int64_t)n * C + c];
-                float g;
-                const float dg = gate_grad(to_f(zg[(int64_t)n * C + c]), act, &g);
-                if (dzc) dzc[(int64_t)n * C + c] = q * kc * dg;
-                tk += q * g;
+    if (c < a.C) {
+        const int64_t NC = (int64_t)a.N * a.C;
+        const float kc = (a.w ? a.w[c] : 1.f) * (a.s ? a.s[c] : 1.f);
+        #pragma unroll 2
+        for (int n = ln; n < a.N; n += kFinLanes) {
+            const int64_t rb = (n * a.G + c / a.Cg) / a.Z;
+            const int shares = (int)(((rb + 1) * a.tiles - 1) / a.per - rb * a.tiles / a.per) + 1;
+            const float *p = a.part + (int64_t)n * a.C + c;
+            float q = 0.f;
+            #pragma unroll 4
+            for (int i = 0; i < shares; ++i) {
+                if (a.next) t2 += p[i * NC];
+                if (a.post) q += p[(a.splits + i) * NC];
             }
-        } else if (post) {
-            for (int64_t i = ln; i < (int64_t)N * splits; i += kFinLanes) tk += p1[i * C + c];
+            if (a.post && a.gate == GCONV_GATE_CHANNEL) {
+                float g;
+                const float dg = gate_grad(to_f(static_cast<const T *>(a.z)[(int64_t)n * a.C + c]), a.act, &g);
+                if (a.dzc) a.dzc[(int64_t)n * a.C + c] = q * kc * dg;
+                q *= g;
+            }
+            tk += q;
         }
     }
     sh[0][ln][cl] = t2;
     sh[1][ln][cl] = tk;
     __syncthreads();
-    if (ln == 0 && c < C) {
+    if (ln == 0 && c < a.C) {
         float u2 = 0.f, uk = 0.f;
         for (int i = 0; i < kFinLanes; ++i) { u2 += sh[0][i][cl]; uk += sh[1][i][cl]; }
-        if (next && dw2) dw2[c] = u2;
-        if (post && dw) dw[c] = uk * (s ? s[c] : 1.f);
-        if (post && ds) ds[c] = uk * (w ? w[c] : 1.f);
+        if (a.next && a.dw2) a.dw2[c] = u2;
+        if (a.post && a.dw) a.dw[c] = uk * (a.s ? a.s[c] : 1.f);
+        if (a.post && a.ds) a.ds[c] = uk * (a.w ? a.w[c] : 1.f);
     }
 }
 
@@ -80,14 +92,66 @@ int pow2_up(int v)
     return p;
 }
 
-// Launch shape.  The widest vector that divides the plane (rows are then aligned for it);
-// TX such that a channel's positions in a block are 64 bytes or more where 512 threads
-// allow it.
-void block_shape(const gconv_block &b, gconv_dtype dt, bool bwd, BlockShape *s)
+// Launch shape of the staged kernels: a group's channels at eight a thread, as many lanes a
+// channel as then fit in `most` threads.
+bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int tensors, int most, BlockShape *s)
 {
     const int P = b.H * b.W, Cg = b.C / b.groups, rows = b.N * b.groups;
+    const int es = dt == GCONV_BF16 ? 2 : 4;
+    int TY = (Cg + kStageChannels - 1) / kStageChannels;
+    s->flat = P <= 64;
+    int TX = s->flat ? pow2_up((P + 1) / 2) : 32;
+    while (TX > 1 && (TX * TY > most)) { TX >>= 1; s->flat = s->flat && 2 * TX >= P; }
+    if (TX * TY > most || (!s->flat && 2 * TX * es < 16)) return false;
+    // whole warps a row, or a power of two of rows a warp
+    if (TX * TY >= 32) TY = (TY + 32 / TX - 1) / (32 / TX) * (32 / TX);
+    else TY = pow2_up(TY);
+    int Z = 1;
+    while (TX * TY * Z < 32 || (TX * TY * Z * 2 <= most && Z < rows)) Z *= 2;
+    s->PT = 2 * TX;
+    const size_t limit = kBlockSmem;
+    const int sums = bwd ? 2 : 1;
+    while (true) {
+        if (s->flat) {
+            s->pitch = P * es;
+            s->tensor = ((Z * Cg * P * es + 15 + 16 + 2 * TX * es) & ~15);
+        } else {
+            const bool aligned = (int64_t)P * es % 16 == 0 && s->PT * es % 16 == 0;
+            s->pieces = (s->PT * es + 15) / 16 + (aligned ? 0 : 1);
+            s->pitch = s->pieces * 16;
+            s->tensor = Z * Cg * s->pitch + 16;
+        }
+        s->smem = (size_t)2 * tensors * s->tensor + (TY > 1 ? (size_t)Z * (TY + column_shares(TY)) * TX * 2 * sums * 4 : 0);
+        if (s->smem <= limit) break;
+        if (Z > 1 && TX * TY * Z >= 64) Z /= 2;
+        else return false;
+    }
+    s->lanes2 = pow2_up(s->pieces);
+    s->staged = 1;
+    s->TX = TX; s->TY = TY; s->Z = Z; s->nch = (Cg + TY - 1) / TY;
+    s->threads = TX * TY * Z;
+    s->tiles = s->flat ? 1 : (P + s->PT - 1) / s->PT;
+    s->total = (rows + Z - 1) / Z * s->tiles;
+    const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(kBlockSmem / (s->smem + 1024), 1024 / s->threads));
+    s->per = (s->total + num_sms() * per_sm - 1) / (num_sms() * per_sm);
+    s->grid = (unsigned)((s->total + s->per - 1) / s->per);
+    s->splits = (s->tiles + s->per - 1) / s->per + 1;   // blocks that may share a row
+    return true;
+}
+
+// Launch shape.  The widest vector of at most four positions that divides the plane (rows are
+// then aligned for it);
+// TX such that a channel's positions in a block are 64 bytes or more where 512 threads
+// allow it.
+void block_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
+{
+    *s = BlockShape{};
+    const int tensors = bwd ? (kind == kBlockJoinNext ? 5 : 3) : (kind == kBlockNorm ? 1 : 3);
+    if (stage_shape(b, dt, bwd, tensors, 512, s)) return;
+    *s = BlockShape{};
+    const int P = b.H * b.W, Cg = b.C / b.groups, rows = b.N * b.groups;
     const int esize = dt == GCONV_BF16 ? 2 : 4;
-    int vec = 16 / esize;
+    int vec = 4;
     while (P % vec) vec >>= 1;
     int nch = block_nch(vec);
     int one = 1;
@@ -102,7 +166,7 @@ void block_shape(const gconv_block &b, gconv_dtype dt, bool bwd, BlockShape *s)
         TY = ty;
     } else {
         TX = std::min(32, pow2_up(PV));
-        TY = 256 / TX;
+        TY = 512 / TX;
     }
     // a row's threads: whole warps, or a power of two of them in one warp
     if (TX * TY >= 32) TY = (TY + 32 / TX - 1) / (32 / TX) * (32 / TX);
@@ -112,6 +176,7 @@ void block_shape(const gconv_block &b, gconv_dtype dt, bool bwd, BlockShape *s)
     s->vec = vec; s->one = one; s->TX = TX; s->TY = TY; s->Z = Z; s->PV = PV;
     s->threads = TX * TY * Z;
     s->tiles = (PV + TX - 1) / TX;
+    s->per = 1;
     const int64_t row_blocks = (rows + Z - 1) / Z;
     s->splits = s->tiles;
     if (bwd && one) {
@@ -121,15 +186,18 @@ void block_shape(const gconv_block &b, gconv_dtype dt, bool bwd, BlockShape *s)
         s->splits = (s->tiles + per - 1) / per;
     }
     s->grid = (unsigned)(row_blocks * (bwd ? s->splits : s->tiles));
-    const int per_row = TX * TY;
-    s->smem = per_row > 32 ? (size_t)Z * (per_row / 32 + 1) * TX * vec * (bwd ? 2 : 1) * sizeof(float) : 0;
+    const int sums = bwd ? 2 : 1;
+    s->smem = TY > 1 ? (size_t)Z * (TY + column_shares(TY)) * TX * vec * sums * sizeof(float) : 0;
 }
 
-void block_args(const gconv_block &b, const BlockShape &s, BlockArgs *a)
+void block_args(const gconv_block &b, gconv_dtype dt, const BlockShape &s, BlockArgs *a)
 {
     a->G = b.groups; a->Cg = b.C / b.groups; a->rows = b.N * b.groups;
     a->P = b.H * b.W; a->PV = s.PV;
     a->TX = s.TX; a->TY = s.TY; a->Z = s.Z; a->tiles = s.tiles; a->splits = s.splits;
+    a->PT = s.PT; a->flat = s.flat; a->per = s.per; a->total = s.total; a->nch = s.nch; a->shares = column_shares(s.TY);
+    a->pitch = s.pitch; a->tensor = s.tensor; a->pieces = s.pieces; a->lanes2 = s.lanes2;
+    a->bytes = (int64_t)b.N * b.C * a->P * (dt == GCONV_BF16 ? 2 : 4);
     a->eps = b.eps; a->inv_cg = 1.f / (float)a->Cg;
     cudaGetLastError();   // clear a stale error: the check after the launches is about this call
 }
@@ -137,9 +205,13 @@ void block_args(const gconv_block &b, const BlockShape &s, BlockArgs *a)
 size_t block_ws(const gconv_block &b, gconv_dtype dt)
 {
     if (b.N == 0) return 0;
-    BlockShape s;
-    block_shape(b, dt, true, &s);
-    return (size_t)2 * s.splits * b.N * b.C * sizeof(float);
+    size_t most = 0;   // over the backward calls this record may be used with
+    for (int kind : {kBlockNorm, kBlockJoin, kBlockJoinNext}) {
+        BlockShape s;
+        block_shape(b, dt, true, kind, &s);
+        most = std::max(most, (size_t)2 * s.splits * b.N * b.C * sizeof(float));
+    }
+    return most;
 }
 
 gconv_status done() { return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA; }
@@ -171,9 +243,9 @@ gconv_status gconv_norm_fwd(const gconv_block *block, gconv_dtype dtype, const v
     if (block->N == 0) return GCONV_OK;
     if (!x || !y || !aligned16(x) || !aligned16(y) || !aligned16(weight)) return GCONV_ERR_INVALID_ARG;
     BlockShape s;
-    block_shape(*block, dtype, false, &s);
+    block_shape(*block, dtype, false, kBlockNorm, &s);
     BlockArgs a{};
-    block_args(*block, s, &a);
+    block_args(*block, dtype, s, &a);
     a.x = x; a.w2 = weight; a.next = y;
     block_fwd_launch(kBlockNorm, dtype, s, a, static_cast<cudaStream_t>(stream));
     return done();
@@ -191,27 +263,28 @@ gconv_status gconv_join_fwd(const gconv_block *block, gconv_dtype dtype, const v
                           (const void *)out, (const void *)next})
         if (!aligned16(p)) return GCONV_ERR_INVALID_ARG;
     BlockShape s;
-    block_shape(*block, dtype, false, &s);
+    const int kind = next ? kBlockJoinNext : kBlockJoin;
+    block_shape(*block, dtype, false, kind, &s);
     BlockArgs a{};
-    block_args(*block, s, &a);
+    block_args(*block, dtype, s, &a);
     a.gate = block->gate; a.act = block->act;
     a.x = res; a.h = h; a.z = gate; a.w = weight; a.s = scale; a.w2 = next_weight; a.out = out; a.next = next;
-    block_fwd_launch(next ? kBlockJoinNext : kBlockJoin, dtype, s, a, static_cast<cudaStream_t>(stream));
+    block_fwd_launch(kind, dtype, s, a, static_cast<cudaStream_t>(stream));
     return done();
 }
 
-static gconv_status finish(const gconv_block &b, gconv_dtype dt, const BlockArgs &a, int next, int post, float *dw2,
-                           float *dw, float *ds, float *dzc, cudaStream_t st)
+static gconv_status finish(const gconv_block &b, gconv_dtype dt, const BlockShape &s, const BlockArgs &a, int next, int post,
+                           float *dw2, float *dw, float *ds, float *dzc, cudaStream_t st)
 {
+    FinishArgs f{};
+    f.part = a.part; f.N = b.N; f.C = b.C; f.G = b.groups; f.Cg = a.Cg; f.Z = a.Z; f.splits = s.splits;
+    f.tiles = s.staged ? s.tiles : s.splits;
+    f.per = s.per;
+    f.next = next; f.post = post; f.gate = a.gate; f.act = a.act; f.z = a.z; f.w = a.w; f.s = a.s;
+    f.dw2 = dw2; f.dw = dw; f.ds = ds; f.dzc = dzc;
     const unsigned grid = (unsigned)((b.C + kFinChannels - 1) / kFinChannels);
-    const int threads = kFinChannels * kFinLanes;
-    if (dt == GCONV_BF16)
-        launch_dependent(block_finish_kernel<__nv_bfloat16>, grid, threads, 0, st, (const float *)a.part, b.N, b.C,
-                         a.splits, next, post, a.gate, a.act, static_cast<const __nv_bfloat16 *>(a.z), a.w, a.s, dw2,
-                         dw, ds, dzc);
-    else
-        launch_dependent(block_finish_kernel<float>, grid, threads, 0, st, (const float *)a.part, b.N, b.C, a.splits,
-                         next, post, a.gate, a.act, static_cast<const float *>(a.z), a.w, a.s, dw2, dw, ds, dzc);
+    if (dt == GCONV_BF16) launch_dependent(block_finish_kernel<__nv_bfloat16>, grid, kFinChannels * kFinLanes, 0, st, f);
+    else launch_dependent(block_finish_kernel<float>, grid, kFinChannels * kFinLanes, 0, st, f);
     return done();
 }
 
@@ -228,14 +301,14 @@ gconv_status gconv_norm_bwd(const gconv_block *block, gconv_dtype dtype, const v
         if (!aligned16(p)) return GCONV_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < block_ws(*block, dtype)) return GCONV_ERR_WORKSPACE;
     BlockShape s;
-    block_shape(*block, dtype, true, &s);
+    block_shape(*block, dtype, true, kBlockNorm, &s);
     BlockArgs a{};
-    block_args(*block, s, &a);
+    block_args(*block, dtype, s, &a);
     a.x = x; a.w2 = weight; a.dnext = dy; a.dout = dres; a.dx = dx;
     a.part = static_cast<float *>(workspace);
     block_bwd_launch(kBlockNorm, dtype, s, a, st);
     if (!dweight) return done();
-    return finish(*block, dtype, a, 1, 0, dweight, nullptr, nullptr, nullptr, st);
+    return finish(*block, dtype, s, a, 1, 0, dweight, nullptr, nullptr, nullptr, st);
 }
 
 gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const void *out, const void *h,
@@ -258,18 +331,19 @@ gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const v
         if (!aligned16(p)) return GCONV_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < block_ws(*block, dtype)) return GCONV_ERR_WORKSPACE;
     BlockShape s;
-    block_shape(*block, dtype, true, &s);
+    const int kind = dnext ? kBlockJoinNext : kBlockJoin;
+    block_shape(*block, dtype, true, kind, &s);
     BlockArgs a{};
-    block_args(*block, s, &a);
+    block_args(*block, dtype, s, &a);
     a.gate = block->gate; a.act = block->act;
     a.x = out; a.h = h; a.z = gate; a.w = weight; a.s = scale; a.w2 = next_weight;
     a.dout = dout; a.dnext = dnext; a.dx = dres; a.dh = dh;
     a.dz = block->gate == GCONV_GATE_FULL ? dgate : nullptr;
     a.part = static_cast<float *>(workspace);
-    block_bwd_launch(dnext ? kBlockJoinNext : kBlockJoin, dtype, s, a, st);
+    block_bwd_launch(kind, dtype, s, a, st);
     float *dzc = block->gate == GCONV_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr;
     if (!dweight && !dscale && !dnext_weight && !dzc) return done();
-    return finish(*block, dtype, a, dnext != nullptr, 1, dnext_weight, dweight, dscale, dzc, st);
+    return finish(*block, dtype, s, a, dnext != nullptr, 1, dnext_weight, dweight, dscale, dzc, st);
 }
 
 }  // extern "C"
