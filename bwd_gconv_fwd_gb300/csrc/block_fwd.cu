@@ -31,20 +31,23 @@ void launch_staged(const BlockShape &s, const BlockArgs &a, cudaStream_t st)
     launch_dependent(Kernel, s.grid, s.threads, s.smem, st, a);
 }
 
-template <typename T, bool PAIR>
+template <typename T, int VEC>
 void staged(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
 {
-    if (kind == kBlockNorm) launch_staged<block_fwd_stage_kernel<T, PAIR, false, true>>(s, a, st);
-    else if (kind == kBlockJoin) launch_staged<block_fwd_stage_kernel<T, PAIR, true, false>>(s, a, st);
-    else launch_staged<block_fwd_stage_kernel<T, PAIR, true, true>>(s, a, st);
+    if (kind == kBlockNorm) launch_staged<block_fwd_stage_kernel<T, VEC, false, true>>(s, a, st);
+    else if (kind == kBlockJoin) launch_staged<block_fwd_stage_kernel<T, VEC, true, false>>(s, a, st);
+    else launch_staged<block_fwd_stage_kernel<T, VEC, true, true>>(s, a, st);
 }
 
 template <typename T>
 void launch_t(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
 {
-    if (s.staged && a.P % 2 == 0) staged<T, true>(kind, s, a, st);
-    else if (s.staged) staged<T, false>(kind, s, a, st);
-    else if (s.one && s.vec == 1) launch<T, 1>(kind, s, a, st);
+    if (s.staged) {
+        if (s.vec == 1) staged<T, 1>(kind, s, a, st);
+        else if (s.vec == 2) staged<T, 2>(kind, s, a, st);
+        else if (s.vec == 4) staged<T, 4>(kind, s, a, st);
+        else if constexpr (sizeof(T) == 2) staged<T, 8>(kind, s, a, st);
+    } else if (s.one && s.vec == 1) launch<T, 1>(kind, s, a, st);
     else if (s.one && s.vec == 2) launch<T, 2>(kind, s, a, st);
     else if (s.one) launch<T, 4>(kind, s, a, st);
     else if (kind == kBlockNorm)

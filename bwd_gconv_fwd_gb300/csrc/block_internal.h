@@ -8,8 +8,9 @@ namespace gconv {
 // The shape of one launch (block_norm.cu, block_shape).
 struct BlockShape {
     int staged;               // the kernels of block_stage.cuh, with:
-    int PT, flat, per, total, nch, pitch, tensor, pieces, lanes2;
-    int vec, one;             // else: positions a thread holds at once; its channels fit in registers
+    int PT, flat, per, total, pitch, tensor, pieces, lanes2;
+    int vec;                  // positions a thread holds at once
+    int one;                  // not staged: a thread's channels fit in its registers
     int TX, TY, Z, PV, tiles, splits;
     int threads;
     unsigned grid;

@@ -92,43 +92,47 @@ int pow2_up(int v)
     return p;
 }
 
-// Launch shape of the staged kernels: a group's channels at eight a thread, as many lanes a
-// channel as then fit in `most` threads.
+// Launch shape of the staged kernels: 16 elements a thread, at most `most` threads, as many lanes
+// a channel as that leaves.
 bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int tensors, int most, BlockShape *s)
 {
     const int P = b.H * b.W, Cg = b.C / b.groups, rows = b.N * b.groups;
     const int es = dt == GCONV_BF16 ? 2 : 4;
-    int TY = (Cg + kStageChannels - 1) / kStageChannels;
+    int vec = 16 / es;
+    while (P % vec) vec >>= 1;
+    const int held = vec > 1 ? vec : 2;   // positions a lane holds
+    int TY = (Cg + stage_nch(vec) - 1) / stage_nch(vec);
+    s->vec = vec;
     s->flat = P <= 64;
-    int TX = s->flat ? pow2_up((P + 1) / 2) : 32;
-    while (TX > 1 && (TX * TY > most)) { TX >>= 1; s->flat = s->flat && 2 * TX >= P; }
-    if (TX * TY > most || (!s->flat && 2 * TX * es < 16)) return false;
+    int TX = s->flat ? pow2_up((P + held - 1) / held) : 32;
+    while (TX > 1 && TX * TY > most) { TX >>= 1; s->flat = s->flat && held * TX >= P; }
+    if (TX * TY > most || (!s->flat && held * TX * es < 16)) return false;
     // whole warps a row, or a power of two of rows a warp
     if (TX * TY >= 32) TY = (TY + 32 / TX - 1) / (32 / TX) * (32 / TX);
     else TY = pow2_up(TY);
     int Z = 1;
     while (TX * TY * Z < 32 || (TX * TY * Z * 2 <= most && Z < rows)) Z *= 2;
-    s->PT = 2 * TX;
+    s->PT = held * TX;
     const size_t limit = kBlockSmem;
     const int sums = bwd ? 2 : 1;
     while (true) {
         if (s->flat) {
             s->pitch = P * es;
-            s->tensor = ((Z * Cg * P * es + 15 + 16 + 2 * TX * es) & ~15);
+            s->tensor = ((Z * Cg * P * es + 15 + 16 + held * TX * es) & ~15);
         } else {
             const bool aligned = (int64_t)P * es % 16 == 0 && s->PT * es % 16 == 0;
             s->pieces = (s->PT * es + 15) / 16 + (aligned ? 0 : 1);
             s->pitch = s->pieces * 16;
             s->tensor = Z * Cg * s->pitch + 16;
         }
-        s->smem = (size_t)2 * tensors * s->tensor + (TY > 1 ? (size_t)Z * (TY + column_shares(TY)) * TX * 2 * sums * 4 : 0);
+        s->smem = (size_t)2 * tensors * s->tensor + (TX * TY > 32 ? (size_t)Z * (TX * TY / 32 + 1) * TX * stage_pairs(vec) * sums * 8 : 0);
         if (s->smem <= limit) break;
         if (Z > 1 && TX * TY * Z >= 64) Z /= 2;
         else return false;
     }
     s->lanes2 = pow2_up(s->pieces);
     s->staged = 1;
-    s->TX = TX; s->TY = TY; s->Z = Z; s->nch = (Cg + TY - 1) / TY;
+    s->TX = TX; s->TY = TY; s->Z = Z; 
     s->threads = TX * TY * Z;
     s->tiles = s->flat ? 1 : (P + s->PT - 1) / s->PT;
     s->total = (rows + Z - 1) / Z * s->tiles;
@@ -195,7 +199,7 @@ void block_args(const gconv_block &b, gconv_dtype dt, const BlockShape &s, Block
     a->G = b.groups; a->Cg = b.C / b.groups; a->rows = b.N * b.groups;
     a->P = b.H * b.W; a->PV = s.PV;
     a->TX = s.TX; a->TY = s.TY; a->Z = s.Z; a->tiles = s.tiles; a->splits = s.splits;
-    a->PT = s.PT; a->flat = s.flat; a->per = s.per; a->total = s.total; a->nch = s.nch; a->shares = column_shares(s.TY);
+    a->PT = s.PT; a->flat = s.flat; a->per = s.per; a->total = s.total; 
     a->pitch = s.pitch; a->tensor = s.tensor; a->pieces = s.pieces; a->lanes2 = s.lanes2;
     a->bytes = (int64_t)b.N * b.C * a->P * (dt == GCONV_BF16 ? 2 : 4);
     a->eps = b.eps; a->inv_cg = 1.f / (float)a->Cg;

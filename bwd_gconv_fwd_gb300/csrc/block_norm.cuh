@@ -27,7 +27,6 @@ struct BlockArgs {
     int tiles, splits;        // tiles of TX vectors in a plane; blocks that share a row (backward)
     // staged kernels: a tile is PT positions of Z rows (flat: Z whole rows, tiles = 1)
     int PT, flat, per, total; // tiles a block walks, tiles in all
-    int nch, shares;          // channels a thread holds; column_shares(TY)
     int pitch, tensor;        // bytes of a staged channel, of a staged tensor
     int pieces, lanes2;       // 16-byte pieces of a channel, and the power of two threads for them
     int64_t bytes;            // of a whole tensor

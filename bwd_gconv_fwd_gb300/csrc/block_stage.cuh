@@ -10,15 +10,19 @@
 // instruction (packed fp32 pairs) and every index is 32 bits and steps by constants.
 //
 // Two forms of a tile: PT positions of every channel of Z rows, or (flat) Z whole rows, which are
-// one run of memory, for planes of at most 64 positions.  A lane holds two positions of nch
-// channels: neighbours where P is even (one access for both), else TX apart.
+// one run of memory, for planes of at most 64 positions.  A thread holds 16 elements: VEC
+// neighbouring positions (as many as divide P, at most 16 bytes) of 16 / VEC channels, so that an
+// address, a predicate and a channel's weight serve VEC elements; where P is odd, two positions TX
+// apart of 8 channels (VEC = 1).
 #pragma once
 
 #include "block_norm.cuh"
 
 namespace gconv {
 
-constexpr int kStageChannels = 8;
+constexpr int stage_pairs(int vec) { return vec > 1 ? vec / 2 : 1; }      // pairs of positions a thread holds
+constexpr int stage_nch(int vec) { return 8 / stage_pairs(vec); }         // channels
+
 
 // ---- pairs of fp32 ------------------------------------------------------------------
 
@@ -115,61 +119,100 @@ __device__ __forceinline__ void stage_tile(const BlockArgs &a, const Tile &w, co
     }
 }
 
-// Two positions of a staged channel, as they lie next to each other (PAIR) or `apart` bytes apart.
-template <typename T, bool PAIR>
-__device__ __forceinline__ F2 read_two(const uint8_t *at, int apart)
+// A thread's positions of a staged channel, and their store to a tensor.
+template <typename T, int VEC>
+__device__ __forceinline__ void read_vec(const uint8_t *at, int apart, F2 (&v)[stage_pairs(VEC)])
 {
-    if constexpr (PAIR && sizeof(T) == 2) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(at);
-        return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    } else if constexpr (PAIR) {
-        F2 r;
-        r.v = *reinterpret_cast<const uint64_t *>(at);
-        return r;
+    if constexpr (VEC == 1) {
+        v[0] = f2(to_f(*reinterpret_cast<const T *>(at)), to_f(*reinterpret_cast<const T *>(at + apart)));
     } else {
-        return f2(to_f(*reinterpret_cast<const T *>(at)), to_f(*reinterpret_cast<const T *>(at + apart)));
+        const Pack<T, VEC> p = *reinterpret_cast<const Pack<T, VEC> *>(at);
+        #pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) v[k] = f2(to_f(p.v[2 * k]), to_f(p.v[2 * k + 1]));
     }
 }
 
-template <typename T, bool PAIR>
-__device__ __forceinline__ void write_two(void *p, uint32_t i, int apart, F2 v, bool ok0, bool ok1)
+template <typename T, int VEC>
+__device__ __forceinline__ void write_vec(void *p, uint32_t i, int apart, const F2 (&v)[stage_pairs(VEC)], bool ok0, bool ok1)
 {
-    const float2 f = parts(v);
-    if constexpr (PAIR) {
-        const float o[2] = {f.x, f.y};
-        if (ok0) store_pack<T, 2>(p, i, o);
-    } else {
+    if constexpr (VEC == 1) {
+        const float2 f = parts(v[0]);
         T *q = static_cast<T *>(p) + i;
         if (ok0) from_f(f.x, q);
         if (ok1) from_f(f.y, q + apart);
+    } else {
+        Pack<T, VEC> o;
+        #pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+            const float2 f = parts(v[k]);
+            if constexpr (sizeof(T) == 2) reinterpret_cast<__nv_bfloat162 *>(&o)[k] = __floats2bfloat162_rn(f.x, f.y);
+            else { o.v[2 * k] = f.x; o.v[2 * k + 1] = f.y; }
+        }
+        if (ok0) *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(p) + i) = o;
     }
 }
 
-// column_sum for pairs; the widths are powers of two.
-template <int NS>
-__device__ __forceinline__ void column_sum2(F2 (&v)[NS], float *red, const BlockArgs &a, int tx, int ty, int z)
+__device__ __forceinline__ F2 shfl_xor2(F2 v, int m)
 {
-    if (a.TY == 1) return;
-    const int pairs = a.TX * NS, lg = 31 - __clz(pairs);
-    uint64_t *mine = reinterpret_cast<uint64_t *>(red) + z * (a.TY + a.shares) * pairs;
-    #pragma unroll
-    for (int q = 0; q < NS; ++q) mine[ty * pairs + q * a.TX + tx] = v[q].v;
+    const float2 f = parts(v);
+    return f2(__shfl_xor_sync(0xffffffffu, f.x, m), __shfl_xor_sync(0xffffffffu, f.y, m));
+}
+
+// Adds N values over the lanes that differ in the bits M, M / 2, ..., TX: a lane keeps half of
+// its values at each level while it has two, and stores what it ends with as values base.. of its
+// vector tx.
+template <int N, int M>
+__device__ __forceinline__ void scatter_sum(const F2 (&v)[N], uint64_t *to, int TX, int tx, int base)
+{
+    if (M < TX || M == 0) {
+        #pragma unroll
+        for (int i = 0; i < N; ++i) to[(base + i) * TX + tx] = v[i].v;
+        return;
+    }
+    if constexpr (M > 0 && N > 1) {
+        const bool high = threadIdx.x & M;
+        F2 keep[N / 2];
+        #pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const F2 mine = high ? v[N / 2 + i] : v[i], theirs = high ? v[i] : v[N / 2 + i];
+            keep[i] = add2(mine, shfl_xor2(theirs, M));
+        }
+        scatter_sum<N / 2, M / 2>(keep, to, TX, tx, base + (high ? N / 2 : 0));
+    } else if constexpr (M > 0) {
+        const F2 sum[1] = {add2(v[0], shfl_xor2(v[0], M))};
+        scatter_sum<1, M / 2>(sum, to, TX, tx, base);
+    }
+}
+
+// Adds v over the TY threads that share a row and a vector; every one of them gets the sum, by
+// the same additions in the same order: within a warp by shuffles that split the values among
+// its lanes, then over a row's warps through shared memory.  `red`: for each row, a row of N TX
+// pairs a warp and one more.  The next call may follow at once: it writes what this one reads
+// last only behind its own first barrier.
+template <int N>
+__device__ __forceinline__ void column_sum2(F2 (&v)[N], float *red, const BlockArgs &a, int tx, int ty, int z)
+{
+    const int per_row = a.TX * a.TY;
+    if (per_row <= 32) {
+        for (int m = a.TX; m < per_row; m <<= 1) {
+            #pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = add2(v[i], shfl_xor2(v[i], m));
+        }
+        return;
+    }
+    const int warps = per_row >> 5, width = N * a.TX, in_row = ty * a.TX + tx;
+    uint64_t *mine = reinterpret_cast<uint64_t *>(red) + z * (warps + 1) * width;
+    scatter_sum<N, 16>(v, mine + (in_row >> 5) * width, a.TX, tx, 0);
     __syncthreads();
-    uint64_t *sums = mine + a.TY * pairs;
-    for (int i = ty * a.TX + tx; i < a.shares << lg; i += a.TY * a.TX) {
-        const uint64_t *p = mine + (i & (pairs - 1));
-        F2 t = f2(0.f);
-        #pragma unroll 4
-        for (int k = i >> lg; k < a.TY; k += a.shares) t = add2(t, F2{p[k << lg]});
-        sums[i] = t.v;
+    for (int i = in_row; i < width; i += per_row) {
+        F2 t{mine[i]};
+        #pragma unroll 8
+        for (int w = 1; w < warps; ++w) t = add2(t, F2{mine[w * width + i]});
+        mine[warps * width + i] = t.v;
     }
     __syncthreads();
     #pragma unroll
-    for (int q = 0; q < NS; ++q) {
-        F2 t{sums[q * a.TX + tx]};
-        for (int s = 1; s < a.shares; ++s) t = add2(t, F2{sums[(s << lg) + q * a.TX + tx]});
-        v[q] = t;
-    }
+    for (int i = 0; i < N; ++i) v[i].v = mine[warps * width + i * a.TX + tx];
 }
 
 // r = 1 / sqrt(mean + eps) of both positions; 0 at a dead one, where eps = 0 would make it infinite.
@@ -189,7 +232,7 @@ struct Seat {
     uint32_t e_step;
 };
 
-template <typename T, bool PAIR>
+template <typename T, int VEC>
 __device__ __forceinline__ Seat seat(const BlockArgs &a)
 {
     constexpr int es = (int)sizeof(T);
@@ -198,9 +241,9 @@ __device__ __forceinline__ Seat seat(const BlockArgs &a)
     const int ry = threadIdx.x / a.TX;
     s.ty = ry % a.TY;
     s.z = ry / a.TY;
-    s.pos = PAIR ? 2 * s.tx : s.tx;
+    s.pos = VEC * s.tx;
     s.c0 = s.z * a.Cg + s.ty;
-    s.apart = PAIR ? 1 : a.TX;
+    s.apart = VEC > 1 ? VEC - 1 : a.TX;
     s.s_first = s.c0 * a.pitch + s.pos * es;
     s.s_step = a.TY * a.pitch;
     s.m_step = a.flat ? 0 : a.TY * a.P * es;
@@ -222,13 +265,13 @@ __device__ __forceinline__ uint32_t misfit(const BlockArgs &a, const Seat &s, co
     return (first + (a.flat ? 0u : (uint32_t)s.c0 * (uint32_t)a.P + (uint32_t)w.p0)) * (uint32_t)sizeof(T);
 }
 
-template <typename T, bool PAIR, bool POST, bool NEXT>
+template <typename T, int VEC, bool POST, bool NEXT>
 __global__ void __launch_bounds__(512) block_fwd_stage_kernel(const BlockArgs a)
 {
-    constexpr int NT = POST ? 3 : 1, NCH = kStageChannels;
+    constexpr int NT = POST ? 3 : 1, NP = stage_pairs(VEC), NCH = stage_nch(VEC);
     extern __shared__ __align__(128) uint8_t smem[];
     float *red = reinterpret_cast<float *>(smem + 2 * NT * a.tensor);
-    const Seat s = seat<T, PAIR>(a);
+    const Seat s = seat<T, VEC>(a);
     const int apart = s.apart * (int)sizeof(T);
     const bool full = POST && a.gate == GCONV_GATE_FULL;
     const char *src[NT];
@@ -246,6 +289,9 @@ __global__ void __launch_bounds__(512) block_fwd_stage_kernel(const BlockArgs a)
 
     int at_row = -1;
     float kb[NCH], wn[NCH];
+    bool has[NCH];
+    #pragma unroll
+    for (int j = 0; j < NCH; ++j) has[j] = s.ty + j * a.TY < a.Cg;
     for (int t = t0; t < t1; ++t, w.next(a)) {
         const int buf = (t - t0) & 1;
         ptx::cp_async_wait_group<0>();
@@ -264,7 +310,7 @@ __global__ void __launch_bounds__(512) block_fwd_stage_kernel(const BlockArgs a)
             #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 kb[j] = wn[j] = 0.f;
-                if (in_row && s.ty + j * a.TY < a.Cg) {
+                if (in_row && has[j]) {
                     if (NEXT) wn[j] = a.w2 ? a.w2[ch0 + j * a.TY] : 1.f;
                     if (POST) {
                         kb[j] = branch_coeff(a, ch0 + j * a.TY);
@@ -277,57 +323,80 @@ __global__ void __launch_bounds__(512) block_fwd_stage_kernel(const BlockArgs a)
         const uint32_t m0 = misfit<T>(a, s, w);
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)s.c0) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
         int at[NCH];
-        F2 sum[1] = {f2(0.f)};
-        F2 o[NCH];
+        F2 sum[NP], r[NP], o[NCH][NP];
+        #pragma unroll
+        for (int k = 0; k < NP; ++k) sum[k] = f2(0.f);
         #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             at[j] = staged_at<T>(s, m0, j);
-            if (s.ty + j * a.TY < a.Cg) {
-                o[j] = read_two<T, PAIR>(st + (POST ? a.tensor : 0) + at[j], apart);
-                sum[0] = fma2(o[j], o[j], sum[0]);
+            if (has[j]) {
+                read_vec<T, VEC>(st + (POST ? a.tensor : 0) + at[j], apart, o[j]);
+                #pragma unroll
+                for (int k = 0; k < NP; ++k) sum[k] = fma2(o[j][k], o[j][k], sum[k]);
             }
         }
-        column_sum2<1>(sum, red, a, s.tx, s.ty, s.z);
-        F2 r = root2(a, sum[0], true, true);
+        column_sum2<NP>(sum, red, a, s.tx, s.ty, s.z);
+        #pragma unroll
+        for (int k = 0; k < NP; ++k) r[k] = root2(a, sum[k], true, true);
         if (POST) {
-            sum[0] = f2(0.f);
+            #pragma unroll
+            for (int k = 0; k < NP; ++k) sum[k] = f2(0.f);
             #pragma unroll
             for (int j = 0; j < NCH; ++j)
-                if (s.ty + j * a.TY < a.Cg) {
-                    const F2 x = read_two<T, PAIR>(st + at[j], apart);
-                    F2 g = f2(kb[j]);
-                    if (full) {
-                        const F2 z = read_two<T, PAIR>(st + 2 * a.tensor + at[j], apart);
-                        const F2 sg = sigmoid2(z);
-                        const F2 v = a.act == GCONV_ACT_NONE ? z : a.act == GCONV_ACT_SIGMOID ? sg : mul2(z, sg);
-                        g = mul2(g, v);
+                if (has[j]) {
+                    F2 x[NP], z[NP];
+                    read_vec<T, VEC>(st + at[j], apart, x);
+                    if (full) read_vec<T, VEC>(st + 2 * a.tensor + at[j], apart, z);
+                    #pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        F2 g = f2(kb[j]);
+                        if (full) {
+                            if (a.act != GCONV_ACT_NONE) {
+                                const F2 sg = sigmoid2(z[k]);
+                                z[k] = a.act == GCONV_ACT_SILU ? mul2(z[k], sg) : sg;
+                            }
+                            g = mul2(g, z[k]);
+                        }
+                        o[j][k] = fma2(g, mul2(o[j][k], r[k]), x[k]);
+                        sum[k] = fma2(o[j][k], o[j][k], sum[k]);
                     }
-                    o[j] = fma2(g, mul2(o[j], r), x);
-                    write_two<T, PAIR>(a.out, e0 + j * s.e_step, s.apart, o[j], ok0, ok1);
-                    sum[0] = fma2(o[j], o[j], sum[0]);
+                    write_vec<T, VEC>(a.out, e0 + j * s.e_step, s.apart, o[j], ok0, ok1);
                 }
             if (!NEXT) continue;
-            column_sum2<1>(sum, red, a, s.tx, s.ty, s.z);
-            r = root2(a, sum[0], true, true);
+            column_sum2<NP>(sum, red, a, s.tx, s.ty, s.z);
+            #pragma unroll
+            for (int k = 0; k < NP; ++k) r[k] = root2(a, sum[k], true, true);
         }
         #pragma unroll
         for (int j = 0; j < NCH; ++j)
-            if (s.ty + j * a.TY < a.Cg)
-                write_two<T, PAIR>(a.next, e0 + j * s.e_step, s.apart, mul2(o[j], mul2(r, f2(wn[j]))), ok0, ok1);
+            if (has[j]) {
+                #pragma unroll
+                for (int k = 0; k < NP; ++k) o[j][k] = mul2(o[j][k], mul2(r[k], f2(wn[j])));
+                write_vec<T, VEC>(a.next, e0 + j * s.e_step, s.apart, o[j], ok0, ok1);
+            }
     }
+}
+
+// A pair's sum, without what stands at a dead position.
+template <int VEC>
+__device__ __forceinline__ F2 live_only(F2 v, bool ok0, bool ok1)
+{
+    if constexpr (VEC > 1) return ok0 ? v : f2(0.f);
+    const float2 f = parts(v);
+    return f2(ok0 ? f.x : 0.f, ok1 ? f.y : 0.f);
 }
 
 // Backward.  A block walks consecutive tiles; its channel sums of a block of rows stay in
 // registers and go to part[i][row][channel] when the rows change, i counting the blocks that
 // share those rows.  Dead positions hold what an earlier tile left: they meet no live one but in
 // the channel sums, which leave them out.
-template <typename T, bool PAIR, bool POST, bool NEXT>
+template <typename T, int VEC, bool POST, bool NEXT>
 __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
 {
-    constexpr int NT = POST && NEXT ? 5 : 3, NCH = kStageChannels;
+    constexpr int NT = POST && NEXT ? 5 : 3, NP = stage_pairs(VEC), NCH = stage_nch(VEC);
     extern __shared__ __align__(128) uint8_t smem[];
     float *red = reinterpret_cast<float *>(smem + 2 * NT * a.tensor);
-    const Seat s = seat<T, PAIR>(a);
+    const Seat s = seat<T, VEC>(a);
     const int apart = s.apart * (int)sizeof(T);
     const bool full = POST && a.gate == GCONV_GATE_FULL;
     const char *src[NT];
@@ -348,19 +417,24 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
 
     int at_row = -1;
     bool in_row = false;
-    float acc2[NCH], acck[NCH], wn[NCH], kb[NCH];
+    F2 acc2[NCH], acck[NCH];
+    float wn[NCH], kb[NCH];
+    bool has[NCH];
+    #pragma unroll
+    for (int j = 0; j < NCH; ++j) has[j] = s.ty + j * a.TY < a.Cg;
     auto flush = [&] {
         const int share = blockIdx.x - (int)((int64_t)(at_row / a.Z) * a.tiles / a.per);
         float *p0 = a.part + share * NC + (int64_t)(at_row + s.z) * a.Cg + s.ty;
         #pragma unroll
         for (int j = 0; j < NCH; ++j)
-            if (j < a.nch) {
-                float s2 = acc2[j], sk = acck[j];
+            if (j * a.TY < a.Cg) {
+                const float2 f2v = parts(acc2[j]), fkv = parts(acck[j]);
+                float s2 = f2v.x + f2v.y, sk = fkv.x + fkv.y;
                 for (int m = 1; m < a.TX; m <<= 1) {
                     if (NEXT) s2 += __shfl_xor_sync(0xffffffffu, s2, m);
                     if (POST) sk += __shfl_xor_sync(0xffffffffu, sk, m);
                 }
-                if (s.tx == 0 && in_row && s.ty + j * a.TY < a.Cg) {
+                if (s.tx == 0 && in_row && has[j]) {
                     if (NEXT) p0[j * a.TY] = s2;
                     if (POST) p0[a.splits * NC + j * a.TY] = sk;
                 }
@@ -383,8 +457,9 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
             const int row = w.row0 + s.z, ch0 = (row % a.G) * a.Cg + s.ty;
             #pragma unroll
             for (int j = 0; j < NCH; ++j) {
-                acc2[j] = acck[j] = wn[j] = kb[j] = 0.f;
-                if (in_row && s.ty + j * a.TY < a.Cg) {
+                acc2[j] = acck[j] = f2(0.f);
+                wn[j] = kb[j] = 0.f;
+                if (in_row && has[j]) {
                     if (NEXT) wn[j] = a.w2 ? a.w2[ch0 + j * a.TY] : 1.f;
                     if (POST) kb[j] = branch_coeff(a, ch0 + j * a.TY);
                     if (POST && a.gate == GCONV_GATE_CHANNEL)
@@ -398,81 +473,105 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
         int at[NCH];
         #pragma unroll
         for (int j = 0; j < NCH; ++j) at[j] = staged_at<T>(s, m0, j);
-        F2 d[NCH], sum[2] = {f2(0.f), f2(0.f)};
-        F2 r = f2(0.f), m = f2(0.f);   // r, and -mean(g w t) r^3
+        F2 d[NCH][NP], sum[2 * NP];
+        F2 r[NP], m[NP];   // r, and -mean(g w t) r^3
+        auto roots = [&] {
+            #pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                r[k] = root2(a, sum[k], ok0, ok1);
+                m[k] = mul2(mul2(sum[NP + k], f2(-a.inv_cg)), mul2(r[k], mul2(r[k], r[k])));
+            }
+        };
+        #pragma unroll
+        for (int k = 0; k < 2 * NP; ++k) sum[k] = f2(0.f);
         if (NEXT) {
             #pragma unroll
             for (int j = 0; j < NCH; ++j)
-                if (s.ty + j * a.TY < a.Cg) {
-                    const F2 x = read_two<T, PAIR>(st + iX * a.tensor + at[j], apart);
-                    const F2 g = read_two<T, PAIR>(st + iG * a.tensor + at[j], apart);
-                    sum[0] = fma2(x, x, sum[0]);
-                    sum[1] = fma2(x, mul2(g, f2(wn[j])), sum[1]);
+                if (has[j]) {
+                    F2 x[NP], g[NP];
+                    read_vec<T, VEC>(st + iX * a.tensor + at[j], apart, x);
+                    read_vec<T, VEC>(st + iG * a.tensor + at[j], apart, g);
+                    #pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        sum[k] = fma2(x[k], x[k], sum[k]);
+                        sum[NP + k] = fma2(x[k], mul2(g[k], f2(wn[j])), sum[NP + k]);
+                    }
                 }
-            column_sum2<2>(sum, red, a, s.tx, s.ty, s.z);
-            r = root2(a, sum[0], ok0, ok1);
-            m = mul2(mul2(sum[1], f2(-a.inv_cg)), mul2(r, mul2(r, r)));
+            column_sum2<2 * NP>(sum, red, a, s.tx, s.ty, s.z);
+            roots();
+            #pragma unroll
+            for (int k = 0; k < 2 * NP; ++k) sum[k] = f2(0.f);
         }
-        sum[0] = sum[1] = f2(0.f);
-        F2 sg[NCH];   // the gate's sigmoid, or its value without one
+        F2 sg[NCH][NP];   // the gate's sigmoid, or its value without one
         #pragma unroll
         for (int j = 0; j < NCH; ++j)
-            if (s.ty + j * a.TY < a.Cg) {
-                d[j] = f2(0.f);
-                if (a.dout) d[j] = read_two<T, PAIR>(st + at[j], apart);
+            if (has[j]) {
+                #pragma unroll
+                for (int k = 0; k < NP; ++k) d[j][k] = f2(0.f);
+                if (a.dout) read_vec<T, VEC>(st + at[j], apart, d[j]);
                 if (NEXT) {
-                    const F2 x = read_two<T, PAIR>(st + iX * a.tensor + at[j], apart);
-                    const F2 g = mul2(read_two<T, PAIR>(st + iG * a.tensor + at[j], apart), r);
-                    d[j] = fma2(x, m, fma2(g, f2(wn[j]), d[j]));
-                    const float2 u = parts(mul2(g, x));
-                    if (ok0) acc2[j] += u.x;
-                    if (ok1) acc2[j] += u.y;
-                    write_two<T, PAIR>(a.dx, e0 + j * s.e_step, s.apart, d[j], ok0, ok1);
+                    F2 x[NP], g[NP], u = f2(0.f);
+                    read_vec<T, VEC>(st + iX * a.tensor + at[j], apart, x);
+                    read_vec<T, VEC>(st + iG * a.tensor + at[j], apart, g);
+                    #pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        g[k] = mul2(g[k], r[k]);
+                        d[j][k] = fma2(x[k], m[k], fma2(g[k], f2(wn[j]), d[j][k]));
+                        u = fma2(g[k], x[k], u);
+                    }
+                    acc2[j] = add2(acc2[j], live_only<VEC>(u, ok0, ok1));
+                    write_vec<T, VEC>(a.dx, e0 + j * s.e_step, s.apart, d[j], ok0, ok1);
                 }
                 if (POST) {
-                    const F2 h = read_two<T, PAIR>(st + iH * a.tensor + at[j], apart);
-                    F2 v = mul2(d[j], f2(kb[j]));
-                    if (full) {
-                        const F2 z = read_two<T, PAIR>(st + iZ * a.tensor + at[j], apart);
-                        sg[j] = sigmoid2(z);
-                        if (a.act == GCONV_ACT_NONE) sg[j] = z;
-                        v = mul2(v, a.act == GCONV_ACT_SILU ? mul2(z, sg[j]) : sg[j]);
+                    F2 h[NP], z[NP];
+                    read_vec<T, VEC>(st + iH * a.tensor + at[j], apart, h);
+                    if (full) read_vec<T, VEC>(st + iZ * a.tensor + at[j], apart, z);
+                    #pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        F2 v = mul2(d[j][k], f2(kb[j]));
+                        if (full) {
+                            sg[j][k] = z[k];
+                            if (a.act != GCONV_ACT_NONE) sg[j][k] = sigmoid2(z[k]);
+                            v = mul2(v, a.act == GCONV_ACT_SILU ? mul2(z[k], sg[j][k]) : sg[j][k]);
+                        }
+                        sum[k] = fma2(h[k], h[k], sum[k]);
+                        sum[NP + k] = fma2(h[k], v, sum[NP + k]);
                     }
-                    sum[0] = fma2(h, h, sum[0]);
-                    sum[1] = fma2(h, v, sum[1]);
                 }
             }
         if (!POST) continue;
-        column_sum2<2>(sum, red, a, s.tx, s.ty, s.z);
-        r = root2(a, sum[0], ok0, ok1);
-        m = mul2(mul2(sum[1], f2(-a.inv_cg)), mul2(r, mul2(r, r)));
+        column_sum2<2 * NP>(sum, red, a, s.tx, s.ty, s.z);
+        roots();
         #pragma unroll
         for (int j = 0; j < NCH; ++j)
-            if (s.ty + j * a.TY < a.Cg) {
+            if (has[j]) {
                 const uint32_t e = e0 + j * s.e_step;
-                const F2 h = read_two<T, PAIR>(st + iH * a.tensor + at[j], apart);
-                const F2 dr = mul2(d[j], r), dk = mul2(dr, f2(kb[j]));
-                F2 u = mul2(dr, h), dh = dk;   // the channel gate is in kb; its own gradient needs u without it
-                if (full) {
-                    // act'(z): 1; s (1 - s); s (1 + z (1 - s)) = s + g (1 - s)
-                    F2 g = sg[j], dg = f2(1.f);
-                    if (a.act != GCONV_ACT_NONE) {
-                        const F2 rest = fma2(sg[j], f2(-1.f), f2(1.f));
-                        if (a.act == GCONV_ACT_SILU) {
-                            g = mul2(read_two<T, PAIR>(st + iZ * a.tensor + at[j], apart), sg[j]);
-                            dg = fma2(g, rest, sg[j]);
-                        } else {
-                            dg = mul2(g, rest);
+                F2 h[NP], z[NP], u = f2(0.f);
+                read_vec<T, VEC>(st + iH * a.tensor + at[j], apart, h);
+                if (full && a.act == GCONV_ACT_SILU) read_vec<T, VEC>(st + iZ * a.tensor + at[j], apart, z);
+                #pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    const F2 dr = mul2(d[j][k], r[k]), dk = mul2(dr, f2(kb[j]));
+                    F2 dh = dk;   // the channel gate is in kb; its own gradient needs the sum without it
+                    if (full) {
+                        // act'(z): 1; s (1 - s); s (1 + z (1 - s)) = s + g (1 - s)
+                        F2 g = sg[j][k], dg = f2(1.f);
+                        if (a.act != GCONV_ACT_NONE) {
+                            const F2 rest = fma2(sg[j][k], f2(-1.f), f2(1.f));
+                            if (a.act == GCONV_ACT_SILU) g = mul2(z[k], sg[j][k]);
+                            dg = a.act == GCONV_ACT_SILU ? fma2(g, rest, sg[j][k]) : mul2(g, rest);
                         }
+                        sg[j][k] = mul2(mul2(dk, h[k]), dg);   // dz
+                        u = fma2(mul2(dr, h[k]), g, u);
+                        dh = mul2(dk, g);
+                    } else {
+                        u = fma2(dr, h[k], u);
                     }
-                    if (a.dz) write_two<T, PAIR>(a.dz, e, s.apart, mul2(mul2(dk, h), dg), ok0, ok1);
-                    u = mul2(u, g);
-                    dh = mul2(dk, g);
+                    d[j][k] = fma2(h[k], m[k], dh);
                 }
-                const float2 q = parts(u);
-                if (ok0) acck[j] += q.x;
-                if (ok1) acck[j] += q.y;
-                write_two<T, PAIR>(a.dh, e, s.apart, fma2(h, m, dh), ok0, ok1);
+                acck[j] = add2(acck[j], live_only<VEC>(u, ok0, ok1));
+                write_vec<T, VEC>(a.dh, e, s.apart, d[j], ok0, ok1);
+                if (full && a.dz) write_vec<T, VEC>(a.dz, e, s.apart, sg[j], ok0, ok1);
             }
     }
     if (at_row >= 0) flush();
