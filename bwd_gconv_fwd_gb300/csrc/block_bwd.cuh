@@ -1,4 +1,4 @@
-// block_bwd.cu -- the block norm / join backward kernels' instances and launches.
+// block_bwd.cuh -- the block norm / join backward kernels' instances and launches.
 #include "block_internal.h"
 #include "block_stage.cuh"
 
@@ -34,9 +34,14 @@ void launch_staged(const BlockShape &s, const BlockArgs &a, cudaStream_t st)
 template <typename T, int VEC>
 void staged(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
 {
-    if (kind == kBlockNorm) launch_staged<block_bwd_stage_kernel<T, VEC, false, true>>(s, a, st);
-    else if (kind == kBlockJoin) launch_staged<block_bwd_stage_kernel<T, VEC, true, false>>(s, a, st);
-    else launch_staged<block_bwd_stage_kernel<T, VEC, true, true>>(s, a, st);
+    const int gate = a.gate != GCONV_GATE_FULL ? kGateOff : a.act == GCONV_ACT_SILU ? kGateSilu : kGateOther;
+    if (kind == kBlockNorm) launch_staged<block_bwd_stage_kernel<T, VEC, false, true, kGateOff>>(s, a, st);
+    else if (kind == kBlockJoin && gate == kGateOff) launch_staged<block_bwd_stage_kernel<T, VEC, true, false, kGateOff>>(s, a, st);
+    else if (kind == kBlockJoin && gate == kGateSilu) launch_staged<block_bwd_stage_kernel<T, VEC, true, false, kGateSilu>>(s, a, st);
+    else if (kind == kBlockJoin) launch_staged<block_bwd_stage_kernel<T, VEC, true, false, kGateOther>>(s, a, st);
+    else if (gate == kGateOff) launch_staged<block_bwd_stage_kernel<T, VEC, true, true, kGateOff>>(s, a, st);
+    else if (gate == kGateSilu) launch_staged<block_bwd_stage_kernel<T, VEC, true, true, kGateSilu>>(s, a, st);
+    else launch_staged<block_bwd_stage_kernel<T, VEC, true, true, kGateOther>>(s, a, st);
 }
 
 template <typename T>
@@ -59,11 +64,5 @@ void launch_t(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st
 }
 
 }  // namespace
-
-void block_bwd_launch(int kind, gconv_dtype dt, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
-{
-    if (dt == GCONV_BF16) launch_t<__nv_bfloat16>(kind, s, a, st);
-    else launch_t<float>(kind, s, a, st);
-}
 
 }  // namespace gconv

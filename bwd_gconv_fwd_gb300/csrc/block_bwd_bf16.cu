@@ -1,0 +1,8 @@
+// block_bwd_bf16.cu -- the instances of block_bwd.cuh for bf16 (a unit of its own for the build's sake).
+#include "block_bwd.cuh"
+
+namespace gconv {
+
+void block_bwd_bf16(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st) { launch_t<__nv_bfloat16>(kind, s, a, st); }
+
+}  // namespace gconv

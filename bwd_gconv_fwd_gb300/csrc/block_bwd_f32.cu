@@ -1,0 +1,8 @@
+// block_bwd_f32.cu -- the instances of block_bwd.cuh for f32 (a unit of its own for the build's sake).
+#include "block_bwd.cuh"
+
+namespace gconv {
+
+void block_bwd_f32(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st) { launch_t<float>(kind, s, a, st); }
+
+}  // namespace gconv

@@ -24,7 +24,9 @@ constexpr size_t kBlockSmem = 227 * 1024;
 // Channels a thread holds: four where it holds 4 positions of each, eight where 1 or 2.
 constexpr int block_nch(int vec) { return vec >= 4 ? 4 : 8; }
 
-void block_fwd_launch(int kind, gconv_dtype dt, const BlockShape &s, const BlockArgs &a, cudaStream_t st);
-void block_bwd_launch(int kind, gconv_dtype dt, const BlockShape &s, const BlockArgs &a, cudaStream_t st);
+void block_fwd_bf16(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st);
+void block_fwd_f32(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st);
+void block_bwd_bf16(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st);
+void block_bwd_f32(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st);
 
 }  // namespace gconv

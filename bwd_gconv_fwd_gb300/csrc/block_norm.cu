@@ -202,6 +202,7 @@ void block_args(const gconv_block &b, gconv_dtype dt, const BlockShape &s, Block
     a->PT = s.PT; a->flat = s.flat; a->per = s.per; a->total = s.total; 
     a->pitch = s.pitch; a->tensor = s.tensor; a->pieces = s.pieces; a->lanes2 = s.lanes2;
     a->bytes = (int64_t)b.N * b.C * a->P * (dt == GCONV_BF16 ? 2 : 4);
+    a->whole = a->bytes % 16 == 0;
     a->eps = b.eps; a->inv_cg = 1.f / (float)a->Cg;
     cudaGetLastError();   // clear a stale error: the check after the launches is about this call
 }
@@ -251,7 +252,7 @@ gconv_status gconv_norm_fwd(const gconv_block *block, gconv_dtype dtype, const v
     BlockArgs a{};
     block_args(*block, dtype, s, &a);
     a.x = x; a.w2 = weight; a.next = y;
-    block_fwd_launch(kBlockNorm, dtype, s, a, static_cast<cudaStream_t>(stream));
+    (dtype == GCONV_BF16 ? block_fwd_bf16 : block_fwd_f32)(kBlockNorm, s, a, static_cast<cudaStream_t>(stream));
     return done();
 }
 
@@ -273,7 +274,7 @@ gconv_status gconv_join_fwd(const gconv_block *block, gconv_dtype dtype, const v
     block_args(*block, dtype, s, &a);
     a.gate = block->gate; a.act = block->act;
     a.x = res; a.h = h; a.z = gate; a.w = weight; a.s = scale; a.w2 = next_weight; a.out = out; a.next = next;
-    block_fwd_launch(kind, dtype, s, a, static_cast<cudaStream_t>(stream));
+    (dtype == GCONV_BF16 ? block_fwd_bf16 : block_fwd_f32)(kind, s, a, static_cast<cudaStream_t>(stream));
     return done();
 }
 
@@ -310,7 +311,7 @@ gconv_status gconv_norm_bwd(const gconv_block *block, gconv_dtype dtype, const v
     block_args(*block, dtype, s, &a);
     a.x = x; a.w2 = weight; a.dnext = dy; a.dout = dres; a.dx = dx;
     a.part = static_cast<float *>(workspace);
-    block_bwd_launch(kBlockNorm, dtype, s, a, st);
+    (dtype == GCONV_BF16 ? block_bwd_bf16 : block_bwd_f32)(kBlockNorm, s, a, st);
     if (!dweight) return done();
     return finish(*block, dtype, s, a, 1, 0, dweight, nullptr, nullptr, nullptr, st);
 }
@@ -344,7 +345,7 @@ gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const v
     a.dout = dout; a.dnext = dnext; a.dx = dres; a.dh = dh;
     a.dz = block->gate == GCONV_GATE_FULL ? dgate : nullptr;
     a.part = static_cast<float *>(workspace);
-    block_bwd_launch(kind, dtype, s, a, st);
+    (dtype == GCONV_BF16 ? block_bwd_bf16 : block_bwd_f32)(kind, s, a, st);
     float *dzc = block->gate == GCONV_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr;
     if (!dweight && !dscale && !dnext_weight && !dzc) return done();
     return finish(*block, dtype, s, a, dnext != nullptr, 1, dnext_weight, dweight, dscale, dzc, st);

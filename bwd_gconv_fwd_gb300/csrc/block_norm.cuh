@@ -30,6 +30,7 @@ struct BlockArgs {
     int pitch, tensor;        // bytes of a staged channel, of a staged tensor
     int pieces, lanes2;       // 16-byte pieces of a channel, and the power of two threads for them
     int64_t bytes;            // of a whole tensor
+    int whole;                // bytes is a multiple of 16
     int gate, act;
     float eps, inv_cg;
     const void *x, *h, *z;    // x: norm input / join residual (forward), join `out` (backward)

@@ -74,6 +74,17 @@ __device__ __forceinline__ F2 sigmoid2(F2 z)
     return f2(e.x, e.y);
 }
 
+// What a full gate does: a template argument, so that the arithmetic is straight-line code.
+enum { kGateOff = 0, kGateSilu = 1, kGateOther = 2 };   // off: none, or one a channel
+
+// s, from which the gate's value and derivative follow: the sigmoid of z, or z where act is none.
+template <int GATE>
+__device__ __forceinline__ F2 gate_core(F2 z, bool plain)
+{
+    const F2 s = sigmoid2(z);
+    return GATE == kGateOther && plain ? z : s;
+}
+
 // ---- tiles --------------------------------------------------------------------------
 
 // A tile: Z rows from row0, PT positions from p0.
@@ -95,7 +106,8 @@ __device__ __forceinline__ void stage_tile(const BlockArgs &a, const Tile &w, co
     const int rows = min(a.Z, a.rows - w.row0) * a.Cg;         // channels
     const int64_t first = (int64_t)w.row0 * a.Cg * a.P * es;
     auto copy = [&](uint32_t to, int64_t from) {
-        const uint32_t n = (uint32_t)min((int64_t)16, a.bytes - from);
+        // a piece that a tensor's end cuts is read up to it
+        const uint32_t n = a.whole ? 16u : (uint32_t)min((int64_t)16, a.bytes - from);
         #pragma unroll
         for (int i = 0; i < NT; ++i)
             if (src[i]) ptx::cp_async16(to + i * a.tensor, src[i] + from, n);
@@ -184,43 +196,57 @@ __device__ __forceinline__ void scatter_sum(const F2 (&v)[N], uint64_t *to, int 
     }
 }
 
-// Adds v over the TY threads that share a row and a vector; every one of them gets the sum, by
-// the same additions in the same order: within a warp by shuffles that split the values among
-// its lanes, then over a row's warps through shared memory.  `red`: for each row, a row of N TX
-// pairs a warp and one more.  The next call may follow at once: it writes what this one reads
-// last only behind its own first barrier.
-template <int N>
-__device__ __forceinline__ void column_sum2(F2 (&v)[N], float *red, const BlockArgs &a, int tx, int ty, int z)
+// From the sum of squares of both positions r = 1 / sqrt(mean + eps), and from the sum of g w t
+// m = -mean(g w t) r^3.
+__device__ __forceinline__ F2 root2(const BlockArgs &a, F2 sum)
 {
+    const float2 s = parts(sum);
+    return f2(rsqrtf(fmaf(s.x, a.inv_cg, a.eps)), rsqrtf(fmaf(s.y, a.inv_cg, a.eps)));
+}
+__device__ __forceinline__ F2 pull2(const BlockArgs &a, F2 sum, F2 r) { return mul2(mul2(sum, f2(-a.inv_cg)), mul2(r, mul2(r, r))); }
+
+// Adds v over the TY threads that share a row and a vector and turns the sums into r (the first
+// NP) and m (the second NP, with TWO), the same bits in every thread: within a warp by shuffles
+// that split the values among its lanes, then over a row's warps through shared memory, where
+// one thread a pair of positions takes the roots.  `red`: for each row, N TX pairs a warp and
+// N TX more.  The next call may follow at once: it writes what this one reads last only behind its
+// own first barrier.
+template <int NP, bool TWO>
+__device__ __forceinline__ void column_roots(F2 (&v)[TWO ? 2 * NP : NP], float *red, const BlockArgs &a, int tx, int ty, int z)
+{
+    constexpr int N = TWO ? 2 * NP : NP;
     const int per_row = a.TX * a.TY;
     if (per_row <= 32) {
         for (int m = a.TX; m < per_row; m <<= 1) {
             #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = add2(v[i], shfl_xor2(v[i], m));
         }
+        #pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            v[i] = root2(a, v[i]);
+            if constexpr (TWO) v[NP + i] = pull2(a, v[NP + i], v[i]);
+        }
         return;
     }
-    const int warps = per_row >> 5, width = N * a.TX, in_row = ty * a.TX + tx;
+    const int warps = per_row >> 5, width = N * a.TX, half = NP * a.TX, in_row = ty * a.TX + tx;
     uint64_t *mine = reinterpret_cast<uint64_t *>(red) + z * (warps + 1) * width;
+    uint64_t *done = mine + warps * width;
     scatter_sum<N, 16>(v, mine + (in_row >> 5) * width, a.TX, tx, 0);
     __syncthreads();
-    for (int i = in_row; i < width; i += per_row) {
-        F2 t{mine[i]};
+    for (int i = in_row; i < half; i += per_row) {
+        F2 s{mine[i]}, u{TWO ? mine[half + i] : 0};
         #pragma unroll 8
-        for (int w = 1; w < warps; ++w) t = add2(t, F2{mine[w * width + i]});
-        mine[warps * width + i] = t.v;
+        for (int w = 1; w < warps; ++w) {
+            s = add2(s, F2{mine[w * width + i]});
+            if constexpr (TWO) u = add2(u, F2{mine[w * width + half + i]});
+        }
+        const F2 r = root2(a, s);
+        done[i] = r.v;
+        if constexpr (TWO) done[half + i] = pull2(a, u, r).v;
     }
     __syncthreads();
     #pragma unroll
-    for (int i = 0; i < N; ++i) v[i].v = mine[warps * width + i * a.TX + tx];
-}
-
-// r = 1 / sqrt(mean + eps) of both positions; 0 at a dead one, where eps = 0 would make it infinite.
-__device__ __forceinline__ F2 root2(const BlockArgs &a, F2 sum, bool ok0, bool ok1)
-{
-    const float2 s = parts(sum);
-    const float x = rsqrtf(fmaf(s.x, a.inv_cg, a.eps)), y = rsqrtf(fmaf(s.y, a.inv_cg, a.eps));
-    return f2(ok0 ? x : 0.f, ok1 ? y : 0.f);
+    for (int i = 0; i < N; ++i) v[i].v = done[i * a.TX + tx];
 }
 
 // A thread's place: vector tx, channels ty, ty + TY, ... of row z of the tile, and from it the
@@ -265,15 +291,16 @@ __device__ __forceinline__ uint32_t misfit(const BlockArgs &a, const Seat &s, co
     return (first + (a.flat ? 0u : (uint32_t)s.c0 * (uint32_t)a.P + (uint32_t)w.p0)) * (uint32_t)sizeof(T);
 }
 
-template <typename T, int VEC, bool POST, bool NEXT>
-__global__ void __launch_bounds__(512) block_fwd_stage_kernel(const BlockArgs a)
+template <typename T, int VEC, bool POST, bool NEXT, int GATE>
+__global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs a)
 {
     constexpr int NT = POST ? 3 : 1, NP = stage_pairs(VEC), NCH = stage_nch(VEC);
     extern __shared__ __align__(128) uint8_t smem[];
     float *red = reinterpret_cast<float *>(smem + 2 * NT * a.tensor);
     const Seat s = seat<T, VEC>(a);
     const int apart = s.apart * (int)sizeof(T);
-    const bool full = POST && a.gate == GCONV_GATE_FULL;
+    constexpr bool full = GATE != kGateOff;
+    const bool plain = a.act == GCONV_ACT_NONE;
     const char *src[NT];
     src[0] = static_cast<const char *>(a.x);
     if constexpr (POST) { src[1] = static_cast<const char *>(a.h); src[2] = full ? static_cast<const char *>(a.z) : nullptr; }
@@ -323,22 +350,21 @@ __global__ void __launch_bounds__(512) block_fwd_stage_kernel(const BlockArgs a)
         const uint32_t m0 = misfit<T>(a, s, w);
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)s.c0) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
         int at[NCH];
-        F2 sum[NP], r[NP], o[NCH][NP];
+        F2 r[NP], o[NCH][NP];
         #pragma unroll
-        for (int k = 0; k < NP; ++k) sum[k] = f2(0.f);
+        for (int k = 0; k < NP; ++k) r[k] = f2(0.f);
         #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             at[j] = staged_at<T>(s, m0, j);
             if (has[j]) {
                 read_vec<T, VEC>(st + (POST ? a.tensor : 0) + at[j], apart, o[j]);
                 #pragma unroll
-                for (int k = 0; k < NP; ++k) sum[k] = fma2(o[j][k], o[j][k], sum[k]);
+                for (int k = 0; k < NP; ++k) r[k] = fma2(o[j][k], o[j][k], r[k]);
             }
         }
-        column_sum2<NP>(sum, red, a, s.tx, s.ty, s.z);
-        #pragma unroll
-        for (int k = 0; k < NP; ++k) r[k] = root2(a, sum[k], true, true);
+        column_roots<NP, false>(r, red, a, s.tx, s.ty, s.z);
         if (POST) {
+            F2 sum[NP];
             #pragma unroll
             for (int k = 0; k < NP; ++k) sum[k] = f2(0.f);
             #pragma unroll
@@ -351,11 +377,8 @@ __global__ void __launch_bounds__(512) block_fwd_stage_kernel(const BlockArgs a)
                     for (int k = 0; k < NP; ++k) {
                         F2 g = f2(kb[j]);
                         if (full) {
-                            if (a.act != GCONV_ACT_NONE) {
-                                const F2 sg = sigmoid2(z[k]);
-                                z[k] = a.act == GCONV_ACT_SILU ? mul2(z[k], sg) : sg;
-                            }
-                            g = mul2(g, z[k]);
+                            const F2 sg = gate_core<GATE>(z[k], plain);
+                            g = mul2(g, GATE == kGateSilu ? mul2(z[k], sg) : sg);
                         }
                         o[j][k] = fma2(g, mul2(o[j][k], r[k]), x[k]);
                         sum[k] = fma2(o[j][k], o[j][k], sum[k]);
@@ -363,9 +386,9 @@ __global__ void __launch_bounds__(512) block_fwd_stage_kernel(const BlockArgs a)
                     write_vec<T, VEC>(a.out, e0 + j * s.e_step, s.apart, o[j], ok0, ok1);
                 }
             if (!NEXT) continue;
-            column_sum2<NP>(sum, red, a, s.tx, s.ty, s.z);
+            column_roots<NP, false>(sum, red, a, s.tx, s.ty, s.z);
             #pragma unroll
-            for (int k = 0; k < NP; ++k) r[k] = root2(a, sum[k], true, true);
+            for (int k = 0; k < NP; ++k) r[k] = sum[k];
         }
         #pragma unroll
         for (int j = 0; j < NCH; ++j)
@@ -390,7 +413,7 @@ __device__ __forceinline__ F2 live_only(F2 v, bool ok0, bool ok1)
 // registers and go to part[i][row][channel] when the rows change, i counting the blocks that
 // share those rows.  Dead positions hold what an earlier tile left: they meet no live one but in
 // the channel sums, which leave them out.
-template <typename T, int VEC, bool POST, bool NEXT>
+template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
 {
     constexpr int NT = POST && NEXT ? 5 : 3, NP = stage_pairs(VEC), NCH = stage_nch(VEC);
@@ -398,7 +421,8 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
     float *red = reinterpret_cast<float *>(smem + 2 * NT * a.tensor);
     const Seat s = seat<T, VEC>(a);
     const int apart = s.apart * (int)sizeof(T);
-    const bool full = POST && a.gate == GCONV_GATE_FULL;
+    constexpr bool full = GATE != kGateOff;
+    const bool plain = a.act == GCONV_ACT_NONE;
     const char *src[NT];
     src[0] = static_cast<const char *>(a.dout);
     constexpr int iX = 1, iG = 2, iH = NEXT ? 3 : 1, iZ = NEXT ? 4 : 2;
@@ -474,14 +498,7 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
         #pragma unroll
         for (int j = 0; j < NCH; ++j) at[j] = staged_at<T>(s, m0, j);
         F2 d[NCH][NP], sum[2 * NP];
-        F2 r[NP], m[NP];   // r, and -mean(g w t) r^3
-        auto roots = [&] {
-            #pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                r[k] = root2(a, sum[k], ok0, ok1);
-                m[k] = mul2(mul2(sum[NP + k], f2(-a.inv_cg)), mul2(r[k], mul2(r[k], r[k])));
-            }
-        };
+        F2 rm[2 * NP];   // r and m
         #pragma unroll
         for (int k = 0; k < 2 * NP; ++k) sum[k] = f2(0.f);
         if (NEXT) {
@@ -497,10 +514,9 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
                         sum[NP + k] = fma2(x[k], mul2(g[k], f2(wn[j])), sum[NP + k]);
                     }
                 }
-            column_sum2<2 * NP>(sum, red, a, s.tx, s.ty, s.z);
-            roots();
+            column_roots<NP, true>(sum, red, a, s.tx, s.ty, s.z);
             #pragma unroll
-            for (int k = 0; k < 2 * NP; ++k) sum[k] = f2(0.f);
+            for (int k = 0; k < 2 * NP; ++k) { rm[k] = sum[k]; sum[k] = f2(0.f); }
         }
         F2 sg[NCH][NP];   // the gate's sigmoid, or its value without one
         #pragma unroll
@@ -515,8 +531,8 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
                     read_vec<T, VEC>(st + iG * a.tensor + at[j], apart, g);
                     #pragma unroll
                     for (int k = 0; k < NP; ++k) {
-                        g[k] = mul2(g[k], r[k]);
-                        d[j][k] = fma2(x[k], m[k], fma2(g[k], f2(wn[j]), d[j][k]));
+                        g[k] = mul2(g[k], rm[k]);
+                        d[j][k] = fma2(x[k], rm[NP + k], fma2(g[k], f2(wn[j]), d[j][k]));
                         u = fma2(g[k], x[k], u);
                     }
                     acc2[j] = add2(acc2[j], live_only<VEC>(u, ok0, ok1));
@@ -530,9 +546,8 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
                     for (int k = 0; k < NP; ++k) {
                         F2 v = mul2(d[j][k], f2(kb[j]));
                         if (full) {
-                            sg[j][k] = z[k];
-                            if (a.act != GCONV_ACT_NONE) sg[j][k] = sigmoid2(z[k]);
-                            v = mul2(v, a.act == GCONV_ACT_SILU ? mul2(z[k], sg[j][k]) : sg[j][k]);
+                            sg[j][k] = gate_core<GATE>(z[k], plain);
+                            v = mul2(v, GATE == kGateSilu ? mul2(z[k], sg[j][k]) : sg[j][k]);
                         }
                         sum[k] = fma2(h[k], h[k], sum[k]);
                         sum[NP + k] = fma2(h[k], v, sum[NP + k]);
@@ -540,34 +555,30 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
                 }
             }
         if (!POST) continue;
-        column_sum2<2 * NP>(sum, red, a, s.tx, s.ty, s.z);
-        roots();
+        column_roots<NP, true>(sum, red, a, s.tx, s.ty, s.z);
         #pragma unroll
         for (int j = 0; j < NCH; ++j)
             if (has[j]) {
                 const uint32_t e = e0 + j * s.e_step;
                 F2 h[NP], z[NP], u = f2(0.f);
                 read_vec<T, VEC>(st + iH * a.tensor + at[j], apart, h);
-                if (full && a.act == GCONV_ACT_SILU) read_vec<T, VEC>(st + iZ * a.tensor + at[j], apart, z);
+                if (GATE == kGateSilu) read_vec<T, VEC>(st + iZ * a.tensor + at[j], apart, z);
                 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
-                    const F2 dr = mul2(d[j][k], r[k]), dk = mul2(dr, f2(kb[j]));
+                    const F2 dr = mul2(d[j][k], sum[k]), dk = mul2(dr, f2(kb[j]));
                     F2 dh = dk;   // the channel gate is in kb; its own gradient needs the sum without it
                     if (full) {
                         // act'(z): 1; s (1 - s); s (1 + z (1 - s)) = s + g (1 - s)
-                        F2 g = sg[j][k], dg = f2(1.f);
-                        if (a.act != GCONV_ACT_NONE) {
-                            const F2 rest = fma2(sg[j][k], f2(-1.f), f2(1.f));
-                            if (a.act == GCONV_ACT_SILU) g = mul2(z[k], sg[j][k]);
-                            dg = a.act == GCONV_ACT_SILU ? fma2(g, rest, sg[j][k]) : mul2(g, rest);
-                        }
+                        const F2 rest = fma2(sg[j][k], f2(-1.f), f2(1.f));
+                        const F2 g = GATE == kGateSilu ? mul2(z[k], sg[j][k]) : sg[j][k];
+                        const F2 dg = GATE == kGateSilu ? fma2(g, rest, sg[j][k]) : plain ? f2(1.f) : mul2(g, rest);
                         sg[j][k] = mul2(mul2(dk, h[k]), dg);   // dz
                         u = fma2(mul2(dr, h[k]), g, u);
                         dh = mul2(dk, g);
                     } else {
                         u = fma2(dr, h[k], u);
                     }
-                    d[j][k] = fma2(h[k], m[k], dh);
+                    d[j][k] = fma2(h[k], sum[NP + k], dh);
                 }
                 acck[j] = add2(acck[j], live_only<VEC>(u, ok0, ok1));
                 write_vec<T, VEC>(a.dh, e, s.apart, d[j], ok0, ok1);
