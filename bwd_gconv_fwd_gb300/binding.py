@@ -18,6 +18,7 @@ bias gradient) and the per-axis ``*_ex`` entry points otherwise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -508,75 +509,89 @@ def gconv_bwd_bias(dy, db, *, geom=None, workspace=None, stream=None):
 
 
 # ---- block norm and block join ---------------------------------------------------
+#
+# These calls take microseconds on the GPU for small layers, so their marshalling is lean: a
+# tensor's checks are five attribute reads, pointers pass as integers, and the records and
+# workspace sizes, which depend on sizes alone, are made once for each set of sizes.
 
-def _like(t, ref, name):
-    """Pointer of an activation that must match ref's shape and dtype (None passes)."""
+def _like(t, shape, dtype, name):
+    """Address of a contiguous CUDA tensor of this shape and dtype (0 for None)."""
     if t is None:
-        return None
-    if t.shape != ref.shape or t.dtype != ref.dtype:
-        raise ValueError(f"{name} must have shape {tuple(ref.shape)} and dtype {ref.dtype}")
-    return _dev(t, name)
+        return 0
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must have shape {tuple(shape)} and dtype {dtype}")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.data_ptr()
 
 
-def _vector(t, c, name):
-    """Pointer of an fp32 [C] tensor (None passes)."""
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or tuple(t.shape) != (c,):
-        raise ValueError(f"{name} must be float32 of shape ({c},)")
-    return _dev(t, name)
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _block(x, groups, eps, gate=None, act="none"):
-    if x.dim() != 4:
-        raise ValueError("activations are [N, C, H, W]")
+@functools.lru_cache(maxsize=1024)
+def _block_record(N, C, H, W, groups, eps, gate, act, dt):
+    """(record, its reference, workspace bytes of the backward calls, [C])."""
     if act not in ACTS:
         raise ValueError(f"act is one of {sorted(ACTS)}")
-    kind = GATE_NONE
-    if gate is not None:
-        if gate.dtype != x.dtype or gate.shape not in (x.shape, x.shape[:2]):
-            raise ValueError(f"gate must be {x.dtype}, [N, C, H, W] or [N, C]")
-        kind = GATE_FULL if gate.dim() == 4 else GATE_CHANNEL
-    N, C, H, W = x.shape
-    return Block(N, C, H, W, int(groups), float(eps), kind, ACTS[act])
-
-
-def _block_workspace(block, dt, workspace, device):
+    block = Block(N, C, H, W, groups, eps, gate, ACTS[act])
     need = lib().gconv_block_workspace_size(ctypes.byref(block), dt)
     if need == ctypes.c_size_t(-1).value:
         raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_block_workspace_size")
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return block, ctypes.byref(block), int(need), torch.Size((C,))
+
+
+def _block(x, name, groups, eps, gate=None, act="none"):
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 4:
+        raise ValueError(f"{name} is [N, C, H, W]")
+    kind = GATE_NONE
+    if gate is not None:
+        kind = GATE_FULL if gate.shape == shape else GATE_CHANNEL
+        if kind == GATE_CHANNEL and gate.shape != shape[:2]:
+            raise ValueError("gate is [N, C, H, W] or [N, C]")
+    dt = GCONV_BF16 if dtype is torch.bfloat16 else dtype_code(dtype)
+    record = _block_record(*shape, int(groups), float(eps), kind, act, dt)
+    return shape, dtype, dt, kind, *record
+
+
+def _block_workspace(need, workspace, device):
     if workspace is None:
-        return None, 0
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def gconv_block_workspace_size(x_shape, dtype: int, groups: int = 1) -> int:
     """Workspace bytes gconv_norm_bwd and gconv_join_bwd need for activations of this shape."""
-    block = Block(*(int(v) for v in x_shape), int(groups), 0.0, 0, 0)
-    need = lib().gconv_block_workspace_size(ctypes.byref(block), int(dtype))
-    if need == ctypes.c_size_t(-1).value:
-        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_block_workspace_size")
-    return int(need)
+    N, C, H, W = (int(v) for v in x_shape)
+    return _block_record(N, C, H, W, int(groups), 0.0, GATE_NONE, "none", int(dtype))[2]
 
 
 def gconv_norm_fwd(x, weight, y, *, groups=1, eps=1e-6, stream=None):
     """y <- x / rms(x over each group's channels) * weight, at every position (weight: fp32 [C]
     or None)."""
-    b, dt = _block(x, groups, eps), dtype_code(x.dtype)
-    _check(lib().gconv_norm_fwd(ctypes.byref(b), dt, _dev(x, "x"), _vector(weight, b.C, "weight"), _like(y, x, "y"),
-                                _stream_ptr(stream)), "gconv_norm_fwd")
+    s, d, dt, _, _, ref, _, c = _block(x, "x", groups, eps)
+    st = lib().gconv_norm_fwd(ref, dt, _like(x, s, d, "x"), _like(weight, c, torch.float32, "weight"),
+                              _like(y, s, d, "y"), _raw_stream(stream))
+    if st:
+        _check(st, "gconv_norm_fwd")
     return y
 
 
 def gconv_norm_bwd(x, weight, dy, dx, dweight=None, *, dres=None, groups=1, eps=1e-6, workspace=None, stream=None):
     """dx <- dres + gradient of the norm w.r.t. x; dweight (fp32 [C]) <- gradient w.r.t. weight."""
-    b, dt = _block(x, groups, eps), dtype_code(x.dtype)
-    ws, wsb = _block_workspace(b, dt, workspace, x.device)
-    _check(lib().gconv_norm_bwd(ctypes.byref(b), dt, _dev(x, "x"), _vector(weight, b.C, "weight"), _like(dy, x, "dy"),
-                                _like(dres, x, "dres"), _like(dx, x, "dx"), _vector(dweight, b.C, "dweight"), ws, wsb,
-                                _stream_ptr(stream)), "gconv_norm_bwd")
+    s, d, dt, _, _, ref, need, c = _block(x, "x", groups, eps)
+    f = torch.float32
+    ws, wp, wb = _block_workspace(need, workspace, x.device)
+    st = lib().gconv_norm_bwd(ref, dt, _like(x, s, d, "x"), _like(weight, c, f, "weight"), _like(dy, s, d, "dy"),
+                              _like(dres, s, d, "dres"), _like(dx, s, d, "dx"), _like(dweight, c, f, "dweight"), wp, wb,
+                              _raw_stream(stream))
+    if st:
+        _check(st, "gconv_norm_bwd")
     return dx, dweight
 
 
@@ -584,11 +599,14 @@ def gconv_join_fwd(res, h, out, *, gate=None, act="none", weight=None, scale=Non
                    eps=1e-6, stream=None):
     """out <- res + scale * act(gate) * (h / rms(h) * weight) and, with next, next <- out / rms(out) *
     next_weight.  gate: None, [N, C, H, W] or [N, C]; weight, scale, next_weight: fp32 [C] or None."""
-    b, dt = _block(res, groups, eps, gate, act), dtype_code(res.dtype)
-    _check(lib().gconv_join_fwd(ctypes.byref(b), dt, _dev(res, "res"), _like(h, res, "h"), _dev(gate, "gate"),
-                                _vector(weight, b.C, "weight"), _vector(scale, b.C, "scale"),
-                                _vector(next_weight, b.C, "next_weight"), _like(out, res, "out"),
-                                _like(next, res, "next"), _stream_ptr(stream)), "gconv_join_fwd")
+    s, d, dt, kind, _, ref, _, c = _block(res, "res", groups, eps, gate, act)
+    f = torch.float32
+    st = lib().gconv_join_fwd(ref, dt, _like(res, s, d, "res"), _like(h, s, d, "h"),
+                              _like(gate, s if kind != GATE_CHANNEL else s[:2], d, "gate"), _like(weight, c, f, "weight"),
+                              _like(scale, c, f, "scale"), _like(next_weight, c, f, "next_weight"),
+                              _like(out, s, d, "out"), _like(next, s, d, "next"), _raw_stream(stream))
+    if st:
+        _check(st, "gconv_join_fwd")
     return out, next
 
 
@@ -598,40 +616,43 @@ def gconv_join_bwd(h, dout, dh, *, gate=None, act="none", weight=None, scale=Non
     """Gradients of gconv_join_fwd.  Without dnext (the join had no next) dout is the gradient of
     out; with it dres <- the whole gradient of out.  dgate: like gate for a full gate, fp32 [N, C]
     for a channel gate; dweight, dscale, dnext_weight: fp32 [C] or None."""
-    b, dt = _block(h, groups, eps, gate, act), dtype_code(h.dtype)
-    if dgate is not None and b.gate == GATE_CHANNEL:
-        if dgate.dtype != torch.float32 or dgate.shape != gate.shape:
-            raise ValueError("dgate of a channel gate is float32 [N, C]")
-        dg = _dev(dgate, "dgate")
-    else:
-        dg = _like(dgate, h, "dgate")
-    ws, wsb = _block_workspace(b, dt, workspace, h.device)
-    _check(lib().gconv_join_bwd(ctypes.byref(b), dt, _like(out, h, "out"), _dev(h, "h"), _dev(gate, "gate"),
-                                _vector(weight, b.C, "weight"), _vector(scale, b.C, "scale"),
-                                _vector(next_weight, b.C, "next_weight"), _like(dout, h, "dout"),
-                                _like(dnext, h, "dnext"), _like(dres, h, "dres"), _like(dh, h, "dh"), dg,
-                                _vector(dweight, b.C, "dweight"), _vector(dscale, b.C, "dscale"),
-                                _vector(dnext_weight, b.C, "dnext_weight"), ws, wsb, _stream_ptr(stream)),
-           "gconv_join_bwd")
+    s, d, dt, kind, _, ref, need, c = _block(h, "h", groups, eps, gate, act)
+    f = torch.float32
+    by_channel = kind == GATE_CHANNEL
+    nc = s[:2] if by_channel else s
+    ws, wp, wb = _block_workspace(need, workspace, h.device)
+    st = lib().gconv_join_bwd(ref, dt, _like(out, s, d, "out"), _like(h, s, d, "h"), _like(gate, nc, d, "gate"),
+                              _like(weight, c, f, "weight"), _like(scale, c, f, "scale"),
+                              _like(next_weight, c, f, "next_weight"), _like(dout, s, d, "dout"),
+                              _like(dnext, s, d, "dnext"), _like(dres, s, d, "dres"), _like(dh, s, d, "dh"),
+                              _like(dgate, nc, f if by_channel else d, "dgate"), _like(dweight, c, f, "dweight"),
+                              _like(dscale, c, f, "dscale"), _like(dnext_weight, c, f, "dnext_weight"), wp, wb,
+                              _raw_stream(stream))
+    if st:
+        _check(st, "gconv_join_bwd")
     return dh, dres
 
 
 # ---- orthogonalised updates ------------------------------------------------------
 
-def _matrices(w, groups):
-    rows = int(w.shape[0])
-    if w.dim() < 2 or int(groups) < 1 or rows % int(groups):
-        raise GconvError(GCONV_ERR_INVALID_ARG, f"{tuple(w.shape)} is not {groups} groups of matrices")
-    rows //= int(groups)
-    per = rows * int(groups)
-    return Matrices(int(groups), rows, w.numel() // per if per else 0)
+@functools.lru_cache(maxsize=1024)
+def _matrices(shape, groups):
+    """(record, its reference, workspace bytes) of a weight shape."""
+    if len(shape) < 2 or groups < 1 or shape[0] % groups:
+        raise GconvError(GCONV_ERR_INVALID_ARG, f"{tuple(shape)} is not {groups} groups of matrices")
+    cols = 1
+    for v in shape[1:]:
+        cols *= int(v)
+    m = Matrices(groups, shape[0] // groups, cols)
+    need = lib().gconv_orthogonalize_workspace_size(ctypes.byref(m))
+    if need == ctypes.c_size_t(-1).value:
+        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_orthogonalize_workspace_size")
+    return m, ctypes.byref(m), int(need)
 
 
-def _coeffs(coeffs, steps):
-    """(a, b, c) for every step, or one triple a step, as a float array (None: the library's)."""
-    if coeffs is None:
-        return None
-    flat = [float(v) for v in coeffs] if not hasattr(coeffs[0], "__len__") else [float(v) for t in coeffs for v in t]
+@functools.lru_cache(maxsize=64)
+def _coeff_array(coeffs, steps):
+    flat = [float(v) for t in coeffs for v in (t if isinstance(t, tuple) else (t,))]
     if len(flat) == 3:
         flat = flat * steps
     if len(flat) != 3 * steps:
@@ -639,36 +660,40 @@ def _coeffs(coeffs, steps):
     return (ctypes.c_float * len(flat))(*flat)
 
 
-def _orth_workspace(m, workspace, device):
-    need = lib().gconv_orthogonalize_workspace_size(ctypes.byref(m))
-    if need == ctypes.c_size_t(-1).value:
-        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_orthogonalize_workspace_size")
+def _coeffs(coeffs, steps):
+    """(a, b, c) for every step, or one triple a step, as a float array (None: the library's)."""
+    if coeffs is None:
+        return None
+    return _coeff_array(tuple(tuple(c) if hasattr(c, "__len__") else c for c in coeffs), int(steps))
+
+
+def _orth_workspace(need, workspace, device):
     if workspace is None:
+        if need == 0:
+            return None, 0, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def gconv_orthogonalize_workspace_size(w_shape, groups: int = 1) -> int:
     """Workspace bytes of gconv_orthogonalize and gconv_muon_step for weights of this shape."""
-    rows, cols = int(w_shape[0]) // int(groups), 1
-    for v in w_shape[1:]:
-        cols *= int(v)
-    need = lib().gconv_orthogonalize_workspace_size(ctypes.byref(Matrices(int(groups), rows, cols)))
-    if need == ctypes.c_size_t(-1).value:
-        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_orthogonalize_workspace_size")
-    return int(need)
+    return _matrices(torch.Size(w_shape), int(groups))[2]
 
 
 def gconv_orthogonalize(g, out, *, groups=1, steps=5, coeffs=None, eps=1e-7, workspace=None, stream=None):
     """out <- each group's matrix of g ([C_out, ...]: C_out/groups rows) orthogonalised by `steps`
     Newton-Schulz steps.  g, out: fp32 or bf16; coeffs: (a, b, c), or one triple a step."""
-    if out.shape != g.shape:
-        raise ValueError(f"out must have shape {tuple(g.shape)}")
-    m, dt, odt = _matrices(g, groups), dtype_code(g.dtype), _out_code(out)
+    shape = g.shape
+    dt, odt = dtype_code(g.dtype), _out_code(out)
+    _, ref, need = _matrices(shape, int(groups))
     c = _coeffs(coeffs, steps)
-    ws, wsb = _orth_workspace(m, workspace, g.device)
-    _check(lib().gconv_orthogonalize(ctypes.byref(m), dt, odt, _dev(g, "g"), _dev(out, "out"), int(steps), c, float(eps),
-                                     ws, wsb, _stream_ptr(stream)), "gconv_orthogonalize")
+    ws, wp, wb = _orth_workspace(need, workspace, g.device)
+    st = lib().gconv_orthogonalize(ref, dt, odt, _like(g, shape, g.dtype, "g"), _like(out, shape, out.dtype, "out"),
+                                   int(steps), c, float(eps), wp, wb, _raw_stream(stream))
+    if st:
+        _check(st, "gconv_orthogonalize")
     return out
 
 
@@ -678,17 +703,16 @@ def gconv_muon_step(w, grad, momentum, *, w_out=None, m_out=None, w_bf16=None, g
     """One Muon step: fp32 w and momentum are updated (in place unless w_out, m_out are given) from
     the fp32 weight gradient; w_bf16, when given, gets the new weights rounded to bf16."""
     w_out, m_out = w if w_out is None else w_out, momentum if m_out is None else m_out
-    for name, t in (("w", w), ("grad", grad), ("momentum", momentum), ("w_out", w_out), ("m_out", m_out)):
-        if t.dtype != torch.float32 or t.shape != w.shape:
-            raise ValueError(f"{name} must be float32 of shape {tuple(w.shape)}")
-    if w_bf16 is not None and (w_bf16.dtype != torch.bfloat16 or w_bf16.shape != w.shape):
-        raise ValueError(f"w_bf16 must be bfloat16 of shape {tuple(w.shape)}")
-    m, c = _matrices(w, groups), _coeffs(coeffs, steps)
-    opt = Muon(float(lr), float(beta), float(weight_decay), float(scale), float(eps), int(bool(nesterov)), int(steps), c)
-    ws, wsb = _orth_workspace(m, workspace, w.device)
-    _check(lib().gconv_muon_step(ctypes.byref(m), ctypes.byref(opt), _dev(w, "w"), _dev(grad, "grad"),
-                                 _dev(momentum, "momentum"), _dev(w_out, "w_out"), _dev(m_out, "m_out"),
-                                 _dev(w_bf16, "w_bf16"), ws, wsb, _stream_ptr(stream)), "gconv_muon_step")
+    shape, f = w.shape, torch.float32
+    _, ref, need = _matrices(shape, int(groups))
+    opt = Muon(lr, beta, weight_decay, scale, eps, 1 if nesterov else 0, steps, _coeffs(coeffs, steps))
+    ws, wp, wb = _orth_workspace(need, workspace, w.device)
+    st = lib().gconv_muon_step(ref, ctypes.byref(opt), _like(w, shape, f, "w"), _like(grad, shape, f, "grad"),
+                               _like(momentum, shape, f, "momentum"), _like(w_out, shape, f, "w_out"),
+                               _like(m_out, shape, f, "m_out"), _like(w_bf16, shape, torch.bfloat16, "w_bf16"), wp, wb,
+                               _raw_stream(stream))
+    if st:
+        _check(st, "gconv_muon_step")
     return w_out, m_out
 
 
