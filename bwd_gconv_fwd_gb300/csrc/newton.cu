@@ -224,14 +224,17 @@ __global__ void __launch_bounds__(256) newton_scale_kernel(const NewtonIn p, con
 
 // ---- products ---------------------------------------------------------------------
 
-// Tile t of the lower triangle, row by row: (row block, column block).
+// Tile t of the lower triangle, row by row, of tiles of 256 rows and BN columns: (row block,
+// column block).  Row block r has (r + 1) 256 / BN tiles, those of its diagonal block included.
+template <int BN>
 __device__ __forceinline__ void triangle(int t, int *mb, int *nb)
 {
-    int r = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
-    while ((r + 1) * (r + 2) / 2 <= t) ++r;
-    while (r * (r + 1) / 2 > t) --r;
+    constexpr int per = kTile / BN;
+    int r = (int)((sqrtf(8.f * (float)(t / per) + 1.f) - 1.f) * 0.5f);
+    while (per * (r + 1) * (r + 2) / 2 <= t) ++r;
+    while (per * r * (r + 1) / 2 > t) --r;
     *mb = r;
-    *nb = t - r * (r + 1) / 2;
+    *nb = t - per * r * (r + 1) / 2;
 }
 
 // A 32 x 32 block of a symmetric result: lane = row r0 + lane, v its 32 columns from c0.
@@ -269,13 +272,14 @@ __device__ __forceinline__ void store_symmetric(__half *C, int M, int ldc, int r
     __syncwarp();
 }
 
-// D = A B^T on 256 x 256 tiles by pairs of CTAs (gram, poly: both operands K-major, lower
+// D = A B^T on 256 x BN tiles by pairs of CTAs (gram, poly: both operands K-major, lower
 // triangle only; apply: B = X is N-major).  Each CTA holds 128 rows of A and 128 columns of
 // B, so a stage is 32 KB a CTA for 2 x 2^21 products: a CTA alone with a 128 x 256 tile loads
 // half as much again, and the loads, not the tensor cores, were its limit.  Persistent pairs; a
 // ring of 64-deep stages filled by four TMA threads a CTA, one MMA thread a pair, two
-// accumulators so that eight warps a CTA drain one while the other fills.
-template <int MODE>
+// accumulators so that eight warps a CTA drain one while the other fills.  BN = 128 where 256
+// would leave half the pairs without a tile: the fill and the drain of one tile are then the time.
+template <int MODE, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
 newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ NewtonParams p)
@@ -285,6 +289,8 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
     constexpr int b_mn = MODE == kApply ? 1 : 0;
+    constexpr int boxes = 2 + BN / 128;                     // 8 KB boxes of a stage and CTA
+    constexpr int blocks = BN / 64;                         // 32-column blocks a drain warp
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -296,7 +302,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         *bt = tile / p.tiles_per;
         const int t = tile - *bt * p.tiles_per;
         if (MODE == kApply) { *mb = t % p.n_mblk; *nb = t / p.n_mblk; }
-        else triangle(t, mb, nb);
+        else triangle<BN>(t, mb, nb);
         *k0 = sp * p.k_per;
         *k1 = min(p.n_kblk, *k0 + p.k_per);
     };
@@ -329,13 +335,13 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 
     if (warp >= 1 && warp <= kProducers) {
         // ---------------- TMA producers: one 8 KB box a stage each ----------------
-        if (lane == 0) {
-            const int pi = warp - 1;                        // 0, 1: halves of A; 2, 3: halves of B
+        if (lane == 0 && warp - 1 < boxes) {
+            const int pi = warp - 1;                        // 0, 1: halves of A; 2, 3: B
             int it = 0;
             for (int u = pair; u < units && !abort_flag; u += pairs) {
                 int bt, mb, nb, k0, k1;
                 where(u, &bt, &mb, &nb, &k0, &k1);
-                const int r = (pi < 2 ? mb : nb) * kTile + (int)rank * 128 + (pi & 1) * 64;
+                const int r = pi < 2 ? mb * kTile + (int)rank * 128 + pi * 64 : nb * BN + (int)rank * (BN / 2) + (pi - 2) * 64;
                 for (int kb = k0; kb < k1 && !abort_flag; ++kb, ++it) {
                     const int slot = it % kStages;
                     if (it >= kStages &&
@@ -346,7 +352,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     }
                     // the pair's stage is one barrier in the first CTA
                     const uint32_t local = ptx::smem_u32(&bar_full[slot]);
-                    if (rank == 0 && pi == 0) ptx::mbar_arrive_expect_tx(local, 2 * kStageBytes);
+                    if (rank == 0 && pi == 0) ptx::mbar_arrive_expect_tx(local, 2 * boxes * 8192);
                     const uint32_t fb = map_to(local, 0);
                     const uint32_t dst = sbase + slot * kStageBytes + pi * 8192;
                     if (pi >= 2 && b_mn) tma_load_pair(dst, &tmB, r, kb * kBK, bt, fb);
@@ -363,7 +369,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     } else if (warp == 0) {
         // ---------------- MMA issuer of the pair ----------------
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = idesc_f16(kTile, kTile, b_mn);
+            const uint32_t idesc = idesc_f16(kTile, BN, b_mn);
             const uint64_t a0 = ptx::smem_desc(sbase, 16, 1024, 2);
             const uint64_t b0 = b_mn ? ptx::smem_desc(sbase + kOperand, 8192, 1024, 2)
                                      : ptx::smem_desc(sbase + kOperand, 16, 1024, 2);
@@ -379,7 +385,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     ok = ptx::mbar_wait_ool(ptx::smem_u32(&bar_acc_empty[buf]), ((local >> 1) - 1) & 1, p.wait_ns, nullptr);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t dt = tmem + (uint32_t)(buf * kTile);
+                const uint32_t dt = tmem + (uint32_t)(buf * BN);
                 for (int kb = k0; kb < k1; ++kb) {
                     const uint32_t fb = ptx::smem_u32(&bar_full[slot]);
                     if (!ptx::mbar_test_wait(fb, phase) && ok) ok = ptx::mbar_wait_ool(fb, phase, p.wait_ns, nullptr);
@@ -402,7 +408,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             }
         }
     } else {
-        // ---------------- drain: lanes 32 lg.. of tensor memory, 128 columns a warp ----------------
+        // ---------------- drain: lanes 32 lg.. of tensor memory, half the columns a warp ----------------
         const int lg = warp & 3, dw = warp - 1 - kProducers;
         const int half = dw >> 2;
         uint8_t *stage8 = smem_raw + (sbase - ptx::smem_u32(smem_raw)) + kStages * kStageBytes + dw * kWarpStage;
@@ -410,22 +416,47 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         int local = 0;
         for (int u = pair; u < units; u += pairs, ++local) {
             const int buf = local & 1;
+            int bt, mb, nb, k0, k1;
+            where(u, &bt, &mb, &nb, &k0, &k1);
+            const int r0 = mb * kTile + (int)rank * 128 + lg * 32, row = r0 + lane;
+            __half *C = p.C + (int64_t)bt * p.M * p.ldc;
+            const int64_t out0 = (int64_t)bt * p.M * p.N;
+            // What a block needs from memory beside the product is read a block ahead, the first
+            // before the product is done: A's elements (poly), the weights (Muon's last step).
+            uint4 lin[4];
+            float wv[32];
+            const bool weights = MODE == kApply && p.last && p.o.muon && !p.o.tall;
+            auto ahead = [&](int blk) {
+                const int c0 = nb * BN + blk * 32;
+                if constexpr (MODE == kPoly) {
+                    const __half *A = p.A + (int64_t)bt * p.M * p.ldc + (int64_t)row * p.ldc + c0;
+                    #pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        lin[j] = make_uint4(0, 0, 0, 0);
+                        if (row < p.M && c0 + 8 * j < p.M) lin[j] = *reinterpret_cast<const uint4 *>(A + 8 * j);
+                    }
+                }
+                if constexpr (MODE == kApply) {
+                    if (weights) {
+                        #pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (r0 + j < p.M && c0 + lane < p.N) wv[j] = p.o.w[out0 + (int64_t)(r0 + j) * p.N + c0 + lane];
+                    }
+                }
+            };
+            ahead(half * blocks);
             bool ready = ptx::mbar_wait(ptx::smem_u32(&bar_acc_full[buf]), (local >> 1) & 1, p.wait_ns);
             if (!ready) raise_device_error(p.err, DEVERR_WAIT_TIMEOUT);
             ready = __all_sync(0xffffffffu, ready && !abort_flag);
             if (!ready) break;
             ptx::tc_fence_after();
-            int bt, mb, nb, k0, k1;
-            where(u, &bt, &mb, &nb, &k0, &k1);
-            const int r0 = mb * kTile + (int)rank * 128 + lg * 32, row = r0 + lane;
-            __half *C = p.C + (int64_t)bt * p.M * p.ldc;
-            for (int blk = half * 4; blk < half * 4 + 4; ++blk) {
+            for (int blk = half * blocks; blk < half * blocks + blocks; ++blk) {
                 uint32_t raw[2][16];
-                const uint32_t at = tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * kTile + blk * 32);
+                const uint32_t at = tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(buf * BN + blk * 32);
                 ptx::tmem_ld16(at, raw[0]);
                 ptx::tmem_ld16(at + 16, raw[1]);
                 ptx::tmem_ld_wait();
-                const int c0 = nb * kTile + blk * 32;
+                const int c0 = nb * BN + blk * 32;
                 if (r0 >= p.M || c0 >= p.N) continue;
                 float v[32];
                 #pragma unroll
@@ -433,21 +464,18 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 if (MODE == kGram && p.splits > 1) {
                     // [unit][CTA][drain warp][block][4 columns][lane]: newton_sum_kernel reads it the same way
                     float4 *dst = reinterpret_cast<float4 *>(p.part) +
-                                  ((((int64_t)u * 2 + rank) * kDrainers + dw) * 4 + (blk & 3)) * 256 + lane;
+                                  ((((int64_t)u * 2 + rank) * kDrainers + dw) * blocks + (blk - half * blocks)) * 256 + lane;
                     #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         dst[j * 32] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 } else if (MODE == kGram) {
                     #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] *= 1.f / kScale;
-                    store_symmetric(C, p.M, p.ldc, r0, c0, v, mb != nb, reinterpret_cast<__half *>(stage8), lane);
+                    store_symmetric(C, p.M, p.ldc, r0, c0, v, mb != nb * BN / kTile, reinterpret_cast<__half *>(stage8), lane);
                 } else if (MODE == kPoly) {
-                    const __half *A = p.A + (int64_t)bt * p.M * p.ldc + (int64_t)row * p.ldc + c0;
                     #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint4 lin = make_uint4(0, 0, 0, 0);
-                        if (row < p.M && c0 + 8 * j < p.M) lin = *reinterpret_cast<const uint4 *>(A + 8 * j);
-                        const uint32_t w[4] = {lin.x, lin.y, lin.z, lin.w};
+                        const uint32_t w[4] = {lin[j].x, lin[j].y, lin[j].z, lin[j].w};
                         #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
@@ -455,12 +483,13 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                             v[8 * j + 2 * k + 1] = fmaf(p.c * (1.f / kScale), v[8 * j + 2 * k + 1], p.b * l.y);
                         }
                     }
+                    if (blk + 1 < half * blocks + blocks) ahead(blk + 1);
                     if (r0 == c0) {
                         #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (j == lane && row < p.M) v[j] += p.a * kScale;
                     }
-                    store_symmetric(C, p.M, p.ldc, r0, c0, v, mb != nb, reinterpret_cast<__half *>(stage8), lane);
+                    store_symmetric(C, p.M, p.ldc, r0, c0, v, mb != nb * BN / kTile, reinterpret_cast<__half *>(stage8), lane);
                 } else if (!p.last) {
                     if (row < p.M) {
                         #pragma unroll
@@ -477,7 +506,6 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     }
                 } else {
                     constexpr float back = 1.f / (kScale * kScale);
-                    const int64_t out0 = (int64_t)bt * p.M * p.N;
                     if (p.o.tall) {
                         #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -486,7 +514,17 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                         #pragma unroll
                         for (int j = 0; j < 32; ++j) stage[lane * kStagePitch + j] = v[j] * back;
                         __syncwarp();
-                        store_rows(p.o, out0 + (int64_t)r0 * p.N + c0, p.N, min(32, p.M - r0), min(32, p.N - c0), stage, lane);
+                        const int64_t at0 = out0 + (int64_t)r0 * p.N + c0 + lane;
+                        float res[32];
+                        #pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            res[j] = stage[j * kStagePitch + lane];
+                            if (weights) res[j] = fmaf(-p.o.rate, res[j], p.o.keep * wv[j]);
+                        }
+                        if (blk + 1 < half * blocks + blocks) ahead(blk + 1);
+                        #pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (r0 + j < p.M && c0 + lane < p.N) put_result(p.o, at0 + (int64_t)j * p.N, res[j]);
                         __syncwarp();
                     }
                 }
@@ -507,38 +545,54 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
 
-// A = the sum of the splits of a gram, in split order, scaled, rounded and mirrored.  A warp a
-// 32 x 32 block of a tile.
+// A = the sum of the splits of a gram, in split order, scaled, rounded and mirrored.  A warp
+// takes 32 rows x 8 columns of a tile, so that all its loads are in flight at once.
+template <int BN>
 __global__ void __launch_bounds__(256) newton_sum_kernel(const __grid_constant__ NewtonParams p)
 {
-    __shared__ __align__(16) __half stage[8][32 * 40];
+    constexpr int pitch = 40;
+    __shared__ __align__(16) __half stage[8][8 * pitch];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    constexpr int blocks = BN / 64;                        // of 32 columns a drain warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.x * 8 + warp;
-    const int tile = w >> 6, rank = (w >> 5) & 1, dw = (w >> 2) & 7, b = w & 3;
+    const int quarter = w & 3, b = (w >> 2) % blocks, dw = (w >> 2) / blocks & 7, rank = (w >> 2) / (blocks * 8) & 1;
+    const int tile = (w >> 2) / (blocks * 16);
     if (tile >= p.batch * p.tiles_per) return;
     const int bt = tile / p.tiles_per;
     int mb, nb;
-    triangle(tile - bt * p.tiles_per, &mb, &nb);
-    const int lg = (dw + 1 + kProducers) & 3, blk = (dw >> 2) * 4 + b;
-    const int r0 = mb * kTile + rank * 128 + lg * 32, c0 = nb * kTile + blk * 32;
+    triangle<BN>(tile - bt * p.tiles_per, &mb, &nb);
+    const int lg = (dw + 1 + kProducers) & 3, blk = (dw >> 2) * blocks + b;
+    const int r0 = mb * kTile + rank * 128 + lg * 32, c0 = nb * BN + blk * 32 + quarter * 8;
     if (r0 >= p.M || c0 >= p.N) return;
-    float v[32];
-    #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+    float v[8] = {};
+    const float4 *src = reinterpret_cast<const float4 *>(p.part) +
+                        ((((int64_t)tile * p.splits * 2 + rank) * kDrainers + dw) * blocks + b) * 256 + quarter * 64 + lane;
+    const int64_t hop = (int64_t)2 * kDrainers * blocks * 256;
+    #pragma unroll 8
     for (int s = 0; s < p.splits; ++s) {
-        const float4 *src = reinterpret_cast<const float4 *>(p.part) +
-                            ((((int64_t)(tile * p.splits + s) * 2 + rank) * kDrainers + dw) * 4 + b) * 256 + lane;
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float4 q = src[j * 32];
-            v[4 * j] += q.x; v[4 * j + 1] += q.y; v[4 * j + 2] += q.z; v[4 * j + 3] += q.w;
-        }
+        const float4 x = src[s * hop], y = src[s * hop + 32];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }
+    uint32_t h[4];
     #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= 1.f / kScale;
-    store_symmetric(p.C + (int64_t)bt * p.M * p.ldc, p.M, p.ldc, r0, c0, v, mb != nb, stage[warp], lane);
+    for (int j = 0; j < 4; ++j) h[j] = half2_bits(v[2 * j] * (1.f / kScale), v[2 * j + 1] * (1.f / kScale));
+    __half *C = p.C + (int64_t)bt * p.M * p.ldc;
+    if (r0 + lane < p.M) *reinterpret_cast<uint4 *>(C + (int64_t)(r0 + lane) * p.ldc + c0) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (mb == nb * BN / kTile) return;
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2 hh = *reinterpret_cast<const __half2 *>(&h[j]);
+        stage[warp][(2 * j) * pitch + lane] = __low2half(hh);
+        stage[warp][(2 * j + 1) * pitch + lane] = __high2half(hh);
+    }
+    __syncwarp();
+    const int col = lane >> 2, at = (lane & 3) * 8;
+    if (c0 + col < p.M && r0 + at < p.M)
+        *reinterpret_cast<uint4 *>(C + (int64_t)(c0 + col) * p.ldc + r0 + at) =
+            *reinterpret_cast<const uint4 *>(&stage[warp][col * pitch + at]);
 }
 
 // ---- host side ----------------------------------------------------------------
@@ -607,18 +661,18 @@ bool newton_shape(const gconv_matrices *t, NewtonShape *s)
     return true;
 }
 
-template <int MODE>
-gconv_status launch_gemm(const CUtensorMap &tA, const CUtensorMap &tB, NewtonParams &p, cudaStream_t st)
+// Columns of a product's tiles: 128 where tiles of 256 would leave half the pairs idle.
+int tile_columns(int64_t tiles256) { return tiles256 * 2 <= num_sms() / 2 ? 128 : 256; }
+
+template <int MODE, int BN>
+gconv_status launch_tiles(const CUtensorMap &tA, const CUtensorMap &tB, NewtonParams &p, cudaStream_t st)
 {
-    p.n_mblk = (p.M + kTile - 1) / kTile;
-    p.n_kblk = (p.K + kBK - 1) / kBK;
-    p.tiles_per = MODE == kApply ? p.n_mblk * ((p.N + kTile - 1) / kTile) : p.n_mblk * (p.n_mblk + 1) / 2;
-    if (MODE != kGram) { p.splits = 1; p.k_per = p.n_kblk; }
+    p.tiles_per = MODE == kApply ? p.n_mblk * ((p.N + BN - 1) / BN) : kTile / BN * p.n_mblk * (p.n_mblk + 1) / 2;
     static bool attr[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GCONV_ERR_CUDA;
     if (!attr[dev]) {
-        if (cudaFuncSetAttribute(newton_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
+        if (cudaFuncSetAttribute(newton_gemm_kernel<MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
             cudaSuccess)
             return GCONV_ERR_CUDA;
         attr[dev] = true;
@@ -637,8 +691,23 @@ gconv_status launch_gemm(const CUtensorMap &tA, const CUtensorMap &tB, NewtonPar
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    cudaLaunchKernelEx(&cfg, newton_gemm_kernel<MODE>, tA, tB, p);
+    cudaLaunchKernelEx(&cfg, newton_gemm_kernel<MODE, BN>, tA, tB, p);
+    if (MODE == kGram && p.splits > 1)   // 64 BN / 8 warps a tile
+        launch_dependent(newton_sum_kernel<BN>, (unsigned)(p.batch * p.tiles_per * (BN / 8)), 256, 0, st, p);
     return GCONV_OK;
+}
+
+template <int MODE>
+gconv_status launch_gemm(const CUtensorMap &tA, const CUtensorMap &tB, NewtonParams &p, cudaStream_t st)
+{
+    p.n_mblk = (p.M + kTile - 1) / kTile;
+    p.n_kblk = (p.K + kBK - 1) / kBK;
+    if (MODE != kGram) { p.splits = 1; p.k_per = p.n_kblk; }
+    const int64_t tiles = (int64_t)p.batch * (MODE == kApply ? p.n_mblk * ((p.N + kTile - 1) / kTile)
+                                                             : p.n_mblk * (p.n_mblk + 1) / 2);
+    // a gram in splits fills the pairs already
+    if (p.splits == 1 && tile_columns(tiles) == 128) return launch_tiles<MODE, 128>(tA, tB, p, st);
+    return launch_tiles<MODE, 256>(tA, tB, p, st);
 }
 
 gconv_status run_newton(const NewtonShape &s, NewtonIn in, const NewtonOut &out, int steps, const float *coeffs,
@@ -693,8 +762,6 @@ gconv_status run_newton(const NewtonShape &s, NewtonIn in, const NewtonOut &out,
         p.splits = gram_splits(s, &p.k_per);
         gconv_status r = launch_gemm<kGram>(tX[k & 1], tX[k & 1], p, st);
         if (r != GCONV_OK) return r;
-        if (p.splits > 1)
-            launch_dependent(newton_sum_kernel, (unsigned)(p.batch * p.tiles_per * 8), 256, 0, st, p);
         p.K = s.m; p.C = P; p.A = A;
         p.a = c[0]; p.b = c[1]; p.c = c[2];
         r = launch_gemm<kPoly>(tA, tA, p, st);

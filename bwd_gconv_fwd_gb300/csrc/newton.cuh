@@ -52,11 +52,10 @@ __device__ __forceinline__ float lookahead(const NewtonIn &p, float g, float m)
     return p.nesterov ? fmaf(p.beta, m, g) : m;
 }
 
-// One element (at, in the caller's layout) of the result.
-__device__ __forceinline__ void store_result(const NewtonOut &o, int64_t at, float v)
+// One element (at, in the caller's layout) of what a call writes: o, or the updated weight.
+__device__ __forceinline__ void put_result(const NewtonOut &o, int64_t at, float v)
 {
     if (o.muon) {
-        v = fmaf(-o.rate, v, o.keep * o.w[at]);
         o.w_out[at] = v;
         if (o.w_bf16) o.w_bf16[at] = __float2bfloat16_rn(v);
     } else if (o.out_bf16) {
@@ -64,6 +63,12 @@ __device__ __forceinline__ void store_result(const NewtonOut &o, int64_t at, flo
     } else {
         static_cast<float *>(o.out)[at] = v;
     }
+}
+
+// The same from the orthogonalised matrix.
+__device__ __forceinline__ void store_result(const NewtonOut &o, int64_t at, float v)
+{
+    put_result(o, at, o.muon ? fmaf(-o.rate, v, o.keep * o.w[at]) : v);
 }
 
 // A staged 32 x 32 block (rows of 33 floats) of the result: `rows` rows of `cols` columns, n
@@ -84,17 +89,7 @@ __device__ __forceinline__ void store_rows(const NewtonOut &o, int64_t at, int n
             }
         #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (r0 + k < rows) {
-                const int64_t i = at + (int64_t)(r0 + k) * n;
-                if (o.muon) {
-                    o.w_out[i] = v[k];
-                    if (o.w_bf16) o.w_bf16[i] = __float2bfloat16_rn(v[k]);
-                } else if (o.out_bf16) {
-                    static_cast<__nv_bfloat16 *>(o.out)[i] = __float2bfloat16_rn(v[k]);
-                } else {
-                    static_cast<float *>(o.out)[i] = v[k];
-                }
-            }
+            if (r0 + k < rows) put_result(o, at + (int64_t)(r0 + k) * n, v[k]);
     }
 }
 
