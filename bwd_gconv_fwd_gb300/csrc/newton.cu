@@ -653,7 +653,7 @@ bool newton_shape(const gconv_matrices *t, NewtonShape *s)
     s->x_bytes = up256((size_t)s->G * s->m * s->ldx * 2);
     s->a_bytes = up256((size_t)s->G * s->m * s->lda * 2);
     s->ws = 0;
-    if (s->G == 0 || newton_small_fits(*s)) return true;
+    if (s->G == 0 || newton_tiny_fits(*s) || newton_small_fits(*s)) return true;
     int k_per;
     const int splits = gram_splits(*s, &k_per), mb = (s->m + kTile - 1) / kTile;
     s->part_bytes = splits > 1 ? (size_t)s->G * mb * (mb + 1) / 2 * splits * kTile * kTile * 4 : 0;
@@ -719,6 +719,7 @@ gconv_status run_newton(const NewtonShape &s, NewtonIn in, const NewtonOut &out,
     NewtonOut o = out;
     o.tall = in.tall = s.tall;
     in.rows = s.rows; in.cols = s.cols; in.elems = (int64_t)s.rows * s.cols;
+    if (newton_tiny_fits(s)) return newton_tiny_launch(s, in, o, steps, coeffs, st);
     if (newton_small_fits(s)) return newton_small_launch(s, in, o, steps, coeffs, err, st);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *part = reinterpret_cast<float *>(ws);

@@ -1,5 +1,5 @@
 // newton.cuh -- what the orthogonalisation's translation units share (newton.cu,
-// newton_small.cu).
+// newton_small.cu, newton_tiny.cu).
 #pragma once
 
 #include "internal.h"
@@ -180,6 +180,11 @@ struct NewtonShape {
     int G, rows, cols, m, n, tall, ldx, lda, parts;
     size_t x_bytes, a_bytes, part_bytes, ws;
 };
+
+// Matrices of at most 16 x 1024 in fp32 (newton_tiny.cu).
+bool newton_tiny_fits(const NewtonShape &s);
+gconv_status newton_tiny_launch(const NewtonShape &s, const NewtonIn &in, const NewtonOut &out, int steps,
+                                const float *coeffs, cudaStream_t st);
 
 // Matrices whose shorter side fits one tile, in one launch each call (newton_small.cu).
 bool newton_small_fits(const NewtonShape &s);

@@ -56,8 +56,10 @@ __device__ __forceinline__ void st_cluster_f(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// generic writes (this block's and, after a cluster barrier, others') before tensor-core reads
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// Shared-memory writes of the threads behind the next barrier before tensor-core reads after it:
+// within the block, and into the others of the cluster.  (The fence over all memory takes some
+// hundred cycles more, three times a step.)
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.proxy.async.shared::cluster;" ::: "memory"); }
 
 // Byte offset of the 16-byte piece that holds column `col` of row `row`: 64-column chunks of
 // 128-byte rows, pieces exchanged by the row's last three bits (the 128-byte swizzle).
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
             *reinterpret_cast<__half *>(sgen + oX + piece(r, c) + (c & 7) * 2) = __float2half_rn(u[0] * inv);
         }
     });
-    fence_async();
+    ptx::fence_proxy_async_smem();
     __syncthreads();
 
     uint32_t phase = 0;
@@ -224,7 +226,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
         const float a = p.coeffs[3 * step], b = p.coeffs[3 * step + 1], c = p.coeffs[3 * step + 2];
         // ---- S = X X^T ----
         if (tid == 0) {
-            fence_async();
             const uint32_t idesc = idesc_f16(128, m16, 0);
             uint32_t acc = 0;
             for (int k = 0; k < max(live, 1); ++k)
@@ -263,15 +264,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
         }
         if (CS > 1) {
             cluster_sync();
-            const int share = 128 / (int)CS;                // rows of A this block adds up
-            for (int i = tid; i < share * 32; i += kSmallThreads) {
-                const int r = (int)rank * share + (i >> 5), pc = i & 31;
-                if (pc * 4 >= m16 || r >= m16) continue;   // rows m to m16 are sums of zeros
+            // This block adds rows rank, rank + CS, ... of the m16 (rows m to m16 are sums of zeros).
+            // It begins with its own part and goes round the others, so that at any time the
+            // blocks read from, and write to, different ones.
+            const int pieces = m16 / 4, mine = (m16 - (int)rank + (int)CS - 1) / (int)CS;
+            for (int i = tid; i < mine * pieces; i += kSmallThreads) {
+                const int k_row = i / pieces, pc = i - k_row * pieces, r = (int)rank + k_row * (int)CS;
                 const uint32_t at = sbase + oP + r * 512 + ((pc ^ (r & 7)) << 4);
                 float4 part[8];
                 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (k < (int)CS) part[k] = ld_cluster4(map_to(at, (uint32_t)k));
+                    if (k < (int)CS) part[k] = ld_cluster4(map_to(at, (rank + k) & (CS - 1)));
                 float4 t = part[0];
                 #pragma unroll
                 for (int k = 1; k < 8; ++k)
@@ -279,18 +282,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
                 const uint32_t lo = half2_bits(t.x * (1.f / kNewtonScale), t.y * (1.f / kNewtonScale));
                 const uint32_t hi = half2_bits(t.z * (1.f / kNewtonScale), t.w * (1.f / kNewtonScale));
                 const uint32_t to = sbase + oA + piece(r, pc * 4) + ((pc & 1) << 3);
-                for (uint32_t k = 0; k < CS; ++k) st_cluster2(map_to(to, k), lo, hi);
+                #pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < (int)CS) st_cluster2(map_to(to, (rank + k) & (CS - 1)), lo, hi);
             }
-            fence_async();
+            fence_cluster();
             cluster_sync();
         } else {
-            fence_async();
+            ptx::fence_proxy_async_smem();
             ptx::tc_fence_before();
             __syncthreads();
         }
         // ---- P = a I + b A + c A A ----
         if (tid == 0) {
-            fence_async();
+            if (CS > 1) fence_cluster();   // the others' writes
             ptx::tc_fence_after();
             const uint32_t idesc = idesc_f16(128, m16, 0);
             for (int k = 0; k < m16 / 16; ++k) {
@@ -325,12 +330,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
                 *reinterpret_cast<uint4 *>(sgen + oP + at) = make_uint4(h[0], h[1], h[2], h[3]);
             }
         }
-        fence_async();
+        ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncthreads();
         // ---- X = P X ----
         if (tid == 0) {
-            fence_async();
             ptx::tc_fence_after();
             for (int g = 0; g < max(live, 1); g += 4) {
                 const int n = min(4, max(live, 1) - g) * 64;
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
                     }
                 }
             }
-            fence_async();
+            ptx::fence_proxy_async_smem();
             ptx::tc_fence_before();
             __syncthreads();
             if (tid == 0) ptx::tc_fence_after();
