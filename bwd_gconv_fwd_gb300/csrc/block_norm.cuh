@@ -49,10 +49,6 @@ __host__ __device__ __forceinline__ int column_shares(int TY)
     return s;
 }
 
-// VEC elements of T as they lie in memory.
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack { T v[VEC]; };
-
 template <typename T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const void *p, int64_t i)
 {

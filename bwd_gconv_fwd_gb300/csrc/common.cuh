@@ -42,6 +42,10 @@ __device__ __forceinline__ void store_out4(float *base, int64_t i, float a, floa
     }
 }
 
+// VEC elements of T as they lie in memory.
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack { T v[VEC]; };
+
 // Codes OR-ed into the library's device error word (its address is passed to
 // kernels that have bounded waits; gconv_check_device_error reads and clears it).
 enum : unsigned int {

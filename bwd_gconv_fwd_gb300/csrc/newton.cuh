@@ -71,28 +71,6 @@ __device__ __forceinline__ void store_result(const NewtonOut &o, int64_t at, flo
     put_result(o, at, o.muon ? fmaf(-o.rate, v, o.keep * o.w[at]) : v);
 }
 
-// A staged 32 x 32 block (rows of 33 floats) of the result: `rows` rows of `cols` columns, n
-// elements apart from element `at`, a row a store so that a warp writes consecutive elements.
-// Reads of the weights are issued eight rows ahead of the writes, which may alias them.
-__device__ __forceinline__ void store_rows(const NewtonOut &o, int64_t at, int n, int rows, int cols, const float *stage,
-                                           int lane)
-{
-    if (lane >= cols) return;
-    at += lane;
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-        float v[8];
-        #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (r0 + k < rows) {
-                v[k] = stage[(r0 + k) * 33 + lane];
-                if (o.muon) v[k] = fmaf(-o.rate, v[k], o.keep * o.w[at + (int64_t)(r0 + k) * n]);
-            }
-        #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (r0 + k < rows) put_result(o, at + (int64_t)(r0 + k) * n, v[k]);
-    }
-}
-
 __device__ __forceinline__ uint32_t half2_bits(float a, float b)
 {
     const __half2 h = __floats2half2_rn(a, b);

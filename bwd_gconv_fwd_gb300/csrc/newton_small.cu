@@ -4,12 +4,14 @@
 //
 // A step of block r with its slice X_r (m x ns):
 //   S_r = X_r X_r^T                    tcgen05, 128 x 128 accumulator in tensor memory
-//   A   = sum over r of S_r            rows dealt over the blocks, read through distributed
-//                                      shared memory in rank order, A sent to every block
+//   A   = sum over r of S_r            each block sends every other its share of S_r's rows, adds the
+//                                      shares it gets in rank order, and sends its rows of A back
 //   P   = a I + b A + c A A            every block for itself
 //   X_r = P X_r                        in place
-// What a step costs is its chain of waits (three products, two cluster barriers), not its
-// bytes or operations, which is why a matrix stays on one cluster.
+// What a step costs is its chain of waits (three products, two exchanges), not its bytes or
+// operations, which is why a matrix stays on one cluster.  The exchanges are bulk copies between
+// the blocks' shared memory that signal the receiver's barrier: reading the others' memory between
+// two cluster barriers cost half of a step (128 x 1200: 7500 of 14700 cycles).
 //
 // The 128-byte swizzled tile of 64 columns x 128 rows that the first product reads with rows
 // as its outer side (K-major) is, with the roles of rows and columns exchanged, the tile
@@ -26,6 +28,9 @@ namespace {
 constexpr int kSmallThreads = 512, kSmallWarps = 16;
 constexpr uint32_t kChunkBytes = 16384;       // 64 columns x 128 rows of fp16
 constexpr int kMaxChunks = 8;                 // a slice of 512 columns: all of tensor memory
+constexpr int kMaxCluster = 16;
+constexpr int kSmallPitch = 36;               // floats of a staged row of the result
+constexpr size_t kSmallSmem = 1024 + 14 * (size_t)kChunkBytes;
 constexpr uint64_t kSmallDrainNs = 1000000000ull;
 
 struct SmallParams {
@@ -33,33 +38,25 @@ struct SmallParams {
     NewtonOut out;
     int m, n, steps, slice;                   // slice: columns a block holds, a multiple of 64
     int cluster;
+    int m16, pitch, keep;                     // m up to 16; bytes of a row of S_r, a power of two; see sweep
+    uint32_t oA, oS, oR, oOut;                // A; S_r, and P in its place; the shares received; the result's stage
     unsigned int *err;
     uint64_t wait_ns;
     float coeffs[3 * kNewtonSteps];
 };
-
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void st_cluster2(uint32_t addr, uint32_t a, uint32_t b)
-{
-    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
 
 __device__ __forceinline__ void st_cluster_f(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// Shared-memory writes of the threads behind the next barrier before tensor-core reads after it:
-// within the block, and into the others of the cluster.  (The fence over all memory takes some
-// hundred cycles more, three times a step.)
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.proxy.async.shared::cluster;" ::: "memory"); }
+// `bytes` (a multiple of 16) of this block's shared memory to the same or another offset of block
+// `rank`'s, counted on its barrier `bar` (an offset like the others).
+__device__ __forceinline__ void send(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar, uint32_t rank)
+{
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(map_to(to, rank)), "r"(from), "r"(bytes), "r"(map_to(bar, rank)) : "memory");
+}
 
 // Byte offset of the 16-byte piece that holds column `col` of row `row`: 64-column chunks of
 // 128-byte rows, pieces exchanged by the row's last three bits (the 128-byte swizzle).
@@ -105,14 +102,64 @@ __device__ __forceinline__ void read_u(const NewtonIn &p, int64_t i, float (&u)[
     for (int k = 0; k < V; ++k) u[k] = lookahead(p, u[k], m[k]);
 }
 
+// V elements of what a call writes.
+template <int V>
+__device__ __forceinline__ void put_results(const NewtonOut &o, int64_t at, const float (&v)[V])
+{
+    if constexpr (V == 4) {
+        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+        const float4 f = make_float4(v[0], v[1], v[2], v[3]);
+        if (o.muon) {
+            *reinterpret_cast<float4 *>(o.w_out + at) = f;
+            if (o.w_bf16) *reinterpret_cast<uint2 *>(o.w_bf16 + at) = *reinterpret_cast<uint2 *>(h);
+        } else if (o.out_bf16) {
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(o.out) + at) = *reinterpret_cast<uint2 *>(h);
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(o.out) + at) = f;
+        }
+    } else {
+        put_result(o, at, v[0]);
+    }
+}
+
+// A staged 32 x 32 block of the result to rows n elements apart from element `at`; `rows` and `cols`
+// of it exist.  32 / V lanes a row; the weights are read for the whole block before any is written.
+template <int V>
+__device__ __forceinline__ void store_block(const NewtonOut &o, int64_t at, int n, int rows, int cols, const float *stage, int lane)
+{
+    constexpr int per = V, rounds = 32 / per;               // rows a store, stores
+    const int r0 = lane / (32 / V), c = lane % (32 / V) * V;
+    if (c >= cols) return;
+    float w[rounds][V];
+    if (o.muon) {
+        #pragma unroll
+        for (int k = 0; k < rounds; ++k)
+            if (k * per + r0 < rows) {
+                const Pack<float, V> p = *reinterpret_cast<const Pack<float, V> *>(o.w + at + (int64_t)(k * per + r0) * n + c);
+                #pragma unroll
+                for (int e = 0; e < V; ++e) w[k][e] = p.v[e];
+            }
+    }
+    #pragma unroll
+    for (int k = 0; k < rounds; ++k) {
+        const int r = k * per + r0;
+        if (r >= rows) continue;
+        const Pack<float, V> p = *reinterpret_cast<const Pack<float, V> *>(stage + r * kSmallPitch + c);
+        float v[V];
+        #pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = o.muon ? fmaf(-o.rate, p.v[e], o.keep * w[k][e]) : p.v[e];
+        put_results<V>(o, at + (int64_t)r * n + c, v);
+    }
+}
+
 // grid: G clusters of p.cluster blocks.
 template <int V>
 __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __grid_constant__ SmallParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar, bar_drain;
+    __shared__ __align__(8) uint64_t bar, bar_drain, bar_shares, bar_rows;
     __shared__ uint32_t tmem_sh;
-    __shared__ float warp_sum[kSmallWarps], rank_sum[16];
+    __shared__ float warp_sum[kSmallWarps], rank_sum[kMaxCluster];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t CS = (uint32_t)p.cluster, rank = cluster_rank();
@@ -123,12 +170,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     const int live = (width + 63) >> 6;                     // chunks that hold columns
     const uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *sgen = smem_raw + (sbase - ptx::smem_u32(smem_raw));
-    const uint32_t oX = 0, oA = (uint32_t)chunks * kChunkBytes, oP = oA + 2 * kChunkBytes;   // P, or the 64 KB of sums
-    const int m16 = (p.m + 15) & ~15;
+    const uint32_t oX = 0, oA = p.oA, oP = p.oS;
+    const int m16 = p.m16;
 
     if (tid == 0) {
         ptx::mbar_init(ptx::smem_u32(&bar), 1);
         ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
+        ptx::mbar_init(ptx::smem_u32(&bar_shares), 1);
+        ptx::mbar_init(ptx::smem_u32(&bar_rows), 1);
         ptx::fence_mbar_init();
     }
     if (warp == 0) {
@@ -150,29 +199,42 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
 
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    constexpr int kBatch = V == 4 ? 4 : 8;                  // reads in flight
+    // The first sweep adds the squares, the second scales; between them the values wait in what
+    // A, S and the shares will use, where that is large enough, else they are read again.
+    constexpr int kBatch = 8;                               // reads in flight
+    float *kept = reinterpret_cast<float *>(sgen + p.oA) + tid * V;
     auto sweep = [&](auto first, auto use) {
-        int r = r_first, c = c_first;
+        int r = r_first, c = c_first, n = 0;
         while (r < rows) {
             float u[kBatch][V];
             int rr[kBatch], cc[kBatch];
             #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
+            for (int k = 0; k < kBatch; ++k, ++n) {
                 rr[k] = r; cc[k] = c;
-                if (r < rows && c < wide) read_u<V, decltype(first)::value>(p.in, base + (int64_t)r * pitch + c, u[k]);
+                if (r < rows && c < wide) {
+                    if (!decltype(first)::value && p.keep) {
+                        const Pack<float, V> v = *reinterpret_cast<const Pack<float, V> *>(kept + n * kSmallThreads * V);
+                        #pragma unroll
+                        for (int e = 0; e < V; ++e) u[k][e] = v.v[e];
+                    } else {
+                        read_u<V, decltype(first)::value>(p.in, base + (int64_t)r * pitch + c, u[k]);
+                    }
+                }
                 c += cstep;
                 if (c >= wide) { c = c_first; r += rstep; }
             }
             #pragma unroll
             for (int k = 0; k < kBatch; ++k)
-                if (rr[k] < rows && cc[k] < wide) use(rr[k], cc[k], u[k]);
+                if (rr[k] < rows && cc[k] < wide) use(rr[k], cc[k], n - kBatch + k, u[k]);
         }
     };
 
     float s = 0.f;
-    sweep(std::true_type{}, [&](int, int, const float (&u)[V]) {
+    sweep(std::true_type{}, [&](int, int, int n, const float (&u)[V]) {
+        Pack<float, V> v;
         #pragma unroll
-        for (int k = 0; k < V; ++k) s = fmaf(u[k], u[k], s);
+        for (int k = 0; k < V; ++k) { s = fmaf(u[k], u[k], s); v.v[k] = u[k]; }
+        if (p.keep) *reinterpret_cast<Pack<float, V> *>(kept + n * kSmallThreads * V) = v;
     });
     #pragma unroll
     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
@@ -191,7 +253,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     float total = 0.f;
     for (uint32_t k = 0; k < CS; ++k) total += rank_sum[k];
     const float inv = kNewtonScale / (sqrtf(total) + p.in.eps);
-    sweep(std::false_type{}, [&](int r, int c, const float (&u)[V]) {
+    sweep(std::false_type{}, [&](int r, int c, int, const float (&u)[V]) {
         if (p.in.tall) {
             #pragma unroll
             for (int k = 0; k < V; ++k)
@@ -208,16 +270,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
 
     uint32_t phase = 0;
     bool ok = true;
-    // waits for the products committed last; after a wait that gave up, none waits again
-    auto products_done = [&] {
-        if (ok && !ptx::mbar_wait(ptx::smem_u32(&bar), phase, p.wait_ns)) {
+    // Waits, every thread, for a barrier's phase; after a wait that gave up, none waits again.
+    auto wait_for = [&](uint64_t *b, uint32_t parity) {
+        if (ok && !ptx::mbar_wait(ptx::smem_u32(b), parity, p.wait_ns)) {
             ok = false;
             if (lane == 0) raise_device_error(p.err, DEVERR_WAIT_TIMEOUT);
         }
+    };
+    auto products_done = [&] {
+        wait_for(&bar, phase);
         phase ^= 1u;
         ptx::tc_fence_after();
         __syncwarp();
     };
+    const int share = m16 / (int)CS;                        // rows of A this block adds up, from share * rank
+    const uint32_t share_bytes = (uint32_t)share * (uint32_t)p.pitch;
+    const int swap = (p.pitch >> 4) < 8 ? (p.pitch >> 4) - 1 : 7;   // which pieces of a row of S change places
     const int q = warp & 3, cb = warp >> 2;                 // TMEM lane quarter, 32-column block
     const int row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
@@ -255,47 +323,55 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
                     *reinterpret_cast<uint4 *>(sgen + oA + piece(row, cb * 32 + 8 * j)) = h;
                 }
             } else {
-                // 512-byte rows of fp32, 16-byte pieces exchanged by the row's last three bits
+                // rows of fp32, 16-byte pieces exchanged by the row's last bits
                 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4 *>(sgen + oP + row * 512 + (((cb * 8 + j) ^ (row & 7)) << 4)) =
-                        make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                    if (row < m16 && cb * 32 + 4 * j < m16)
+                        *reinterpret_cast<float4 *>(sgen + p.oS + row * p.pitch + (((cb * 8 + j) ^ (row & swap)) << 4)) =
+                            make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
             }
         }
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncthreads();
         if (CS > 1) {
-            cluster_sync();
-            // This block adds rows rank, rank + CS, ... of the m16 (rows m to m16 are sums of zeros).
-            // It begins with its own part and goes round the others, so that at any time the
-            // blocks read from, and write to, different ones.
-            const int pieces = m16 / 4, mine = (m16 - (int)rank + (int)CS - 1) / (int)CS;
-            for (int i = tid; i < mine * pieces; i += kSmallThreads) {
-                const int k_row = i / pieces, pc = i - k_row * pieces, r = (int)rank + k_row * (int)CS;
-                const uint32_t at = sbase + oP + r * 512 + ((pc ^ (r & 7)) << 4);
-                float4 part[8];
-                #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < (int)CS) part[k] = ld_cluster4(map_to(at, (rank + k) & (CS - 1)));
-                float4 t = part[0];
-                #pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    if (k < (int)CS) { t.x += part[k].x; t.y += part[k].y; t.z += part[k].z; t.w += part[k].w; }
-                const uint32_t lo = half2_bits(t.x * (1.f / kNewtonScale), t.y * (1.f / kNewtonScale));
-                const uint32_t hi = half2_bits(t.z * (1.f / kNewtonScale), t.w * (1.f / kNewtonScale));
-                const uint32_t to = sbase + oA + piece(r, pc * 4) + ((pc & 1) << 3);
-                #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < (int)CS) st_cluster2(map_to(to, (rank + k) & (CS - 1)), lo, hi);
+            // What a block overwrites here has been read: S was received everywhere before A's rows came
+            // back last step; R was added up before its rows of A left; A's old rows were read before
+            // the sums that replace them were sent.
+            const uint32_t bar_s = ptx::smem_u32(&bar_shares), bar_r = ptx::smem_u32(&bar_rows);
+            const int a_chunks = (m16 + 63) >> 6;
+            if (tid == 0) {
+                ptx::mbar_arrive_expect_tx(bar_s, CS * share_bytes);
+                ptx::mbar_arrive_expect_tx(bar_r, (CS - 1) * (uint32_t)(a_chunks * share * 128));
             }
-            fence_cluster();
-            cluster_sync();
-        } else {
+            if (tid < (int)CS && ok)
+                send(sbase + p.oR + rank * share_bytes, sbase + p.oS + (uint32_t)tid * share_bytes, share_bytes, bar_s,
+                     (uint32_t)tid);
+            wait_for(&bar_shares, step & 1);
+            const int pieces = m16 / 4;
+            for (int i = tid; i < share * pieces; i += kSmallThreads) {
+                const int k_row = i / pieces, pc = i - k_row * pieces, r = (int)rank * share + k_row;
+                const uint8_t *from = sgen + p.oR + k_row * p.pitch + ((pc ^ (r & swap)) << 4);
+                float4 t = *reinterpret_cast<const float4 *>(from);
+                #pragma unroll 8
+                for (uint32_t k = 1; k < CS; ++k) {
+                    const float4 u = *reinterpret_cast<const float4 *>(from + k * share_bytes);
+                    t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+                }
+                *reinterpret_cast<uint2 *>(sgen + oA + piece(r, pc * 4) + ((pc & 1) << 3)) =
+                    make_uint2(half2_bits(t.x * (1.f / kNewtonScale), t.y * (1.f / kNewtonScale)),
+                               half2_bits(t.z * (1.f / kNewtonScale), t.w * (1.f / kNewtonScale)));
+            }
             ptx::fence_proxy_async_smem();
-            ptx::tc_fence_before();
             __syncthreads();
+            if (tid < (int)CS * a_chunks && ok) {
+                const uint32_t to = (uint32_t)tid % CS, at = sbase + oA + (uint32_t)tid / CS * kChunkBytes + rank * (uint32_t)share * 128u;
+                if (to != rank) send(at, at, (uint32_t)share * 128u, bar_r, to);
+            }
+            wait_for(&bar_rows, step & 1);
         }
         // ---- P = a I + b A + c A A ----
         if (tid == 0) {
-            if (CS > 1) fence_cluster();   // the others' writes
             ptx::tc_fence_after();
             const uint32_t idesc = idesc_f16(128, m16, 0);
             for (int k = 0; k < m16 / 16; ++k) {
@@ -376,8 +452,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     // ---- the result, through shared memory where a warp's lanes hold a column ----
     const float back = 1.f / (kNewtonScale * kNewtonScale);
     const int64_t out0 = (int64_t)mat * p.m * p.n;
-    __syncthreads();   // every warp past its last wait: X, A and P are free
-    float *stage = reinterpret_cast<float *>(sgen) + warp * 32 * 33;
+    __syncthreads();   // every warp past its last wait: X and P are free
+    float *stage = reinterpret_cast<float *>(sgen + p.oOut) + warp * 32 * kSmallPitch;
     for (int blk = cb; blk < live * 2; blk += 4) {
         uint32_t v[2][16];
         ptx::tmem_ld16(tmem + lanes + blk * 32, v[0]);
@@ -392,10 +468,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
             }
         } else {
             #pragma unroll
-            for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = f[j] * back;
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4 *>(stage + lane * kSmallPitch + 4 * j) =
+                    make_float4(f[4 * j] * back, f[4 * j + 1] * back, f[4 * j + 2] * back, f[4 * j + 3] * back);
             __syncwarp();
-            store_rows(p.out, out0 + (int64_t)(q * 32) * p.n + c0 + blk * 32, p.n, min(32, p.m - q * 32),
-                       min(32, width - blk * 32), stage, lane);
+            store_block<V>(p.out, out0 + (int64_t)(q * 32) * p.n + c0 + blk * 32, p.n, p.m - q * 32, width - blk * 32, stage, lane);
             __syncwarp();
         }
     }
@@ -404,19 +481,75 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
         ptx::mma_commit(ptx::smem_u32(&bar_drain));
         if (!ptx::mbar_wait(ptx::smem_u32(&bar_drain), 0, kSmallDrainNs)) raise_device_error(p.err, DEVERR_WAIT_TIMEOUT);
     }
+    // Copies to and from this block have ended: each was waited for where it arrived, or, after a wait
+    // that gave up, has the time to land.
+    if (CS > 1 && !ok && lane == 0) ptx::mbar_wait(ptx::smem_u32(&bar_rows), (p.steps - 1) & 1, kSmallDrainNs);
+    __syncwarp();
     ptx::tc_fence_before();
-    __syncthreads();
+    cluster_sync();
     if (warp == 0) ptx::tmem_dealloc(tmem, 512);
 }
 
-// Blocks a matrix: as few as keep a slice at kMaxChunks, more while they are idle and slices
-// are longer than two chunks.
+// Where a block keeps what (the kernel's oA, oS, oR), and the bytes in all.
+size_t small_layout(const NewtonShape &s, int cluster, int slice, SmallParams *p)
+{
+    const int m16 = (s.m + 15) & ~15, a_chunks = (m16 + 63) / 64;
+    int pitch = 64;
+    while (pitch < m16 * 4) pitch <<= 1;
+    p->m16 = m16;
+    p->pitch = pitch;
+    p->oA = (uint32_t)(slice / 64) * kChunkBytes;
+    p->oS = p->oA + a_chunks * kChunkBytes;
+    const uint32_t sums = cluster > 1 ? (uint32_t)(m16 * pitch) : 0;
+    p->oR = p->oS + std::max<uint32_t>(sums, a_chunks * kChunkBytes);
+    // the result is staged where nothing is read or sent any more: not over A
+    constexpr uint32_t stage = kSmallWarps * 32 * kSmallPitch * 4;
+    p->oOut = p->oA >= stage ? 0 : p->oS;
+    return 1024 + std::max(p->oR + sums, p->oOut + stage);
+}
+
+// Whether a cluster of sixteen blocks of this kernel fits the current device.
+bool sixteen_fit()
+{
+    static int cache[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return false;
+    }
+    if (!cache[dev]) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kMaxCluster);
+        cfg.blockDim = dim3(kSmallThreads);
+        cfg.dynamicSmemBytes = kSmallSmem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = kMaxCluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        auto fn = newton_small_kernel<4>;
+        const bool ok = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem) == cudaSuccess &&
+                        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
+        cudaGetLastError();
+        cache[dev] = ok ? 1 : -1;
+    }
+    return cache[dev] > 0;
+}
+
+// Blocks a matrix: as few as their shared memory allows, more while they are idle and a slice is
+// longer than one chunk.  Clusters of sixteen, which not every
+// part of the device can hold, only where eight do not fit.
 int small_cluster(const NewtonShape &s, int *slice)
 {
-    for (int cs = 1; cs <= 8; cs *= 2) {
+    for (int cs = 1; cs <= kMaxCluster; cs *= 2) {
         const int sl = ((s.n + cs - 1) / cs + 63) / 64 * 64;
-        if (sl > kMaxChunks * 64) continue;
-        if (cs < 8 && sl > 128 && (int64_t)s.G * cs * 2 <= num_sms()) continue;
+        SmallParams p;
+        if (sl > kMaxChunks * 64 || small_layout(s, cs, sl, &p) > kSmallSmem) continue;
+        if (cs == 16 && !sixteen_fit()) continue;
+        if (cs < 8 && sl > 64 && (int64_t)s.G * cs * 2 <= num_sms()) continue;
         *slice = sl;
         return cs;
     }
@@ -439,18 +572,24 @@ gconv_status newton_small_launch(const NewtonShape &s, const NewtonIn &in, const
     p.cluster = small_cluster(s, &p.slice);
     p.err = err; p.wait_ns = (uint64_t)wait_limit();
     for (int k = 0; k < 3 * steps; ++k) p.coeffs[k] = coeffs ? coeffs[k] : kNewtonCoeffs[k % 3];
-    // X, A, then P or (several blocks) 64 KB of partial sums; the result is staged over them.
     // More than half an SM's shared memory: two blocks on one SM would wait for each other's
     // tensor memory, and two clusters that each hold what the other waits for would never end.
-    const size_t smem = std::max<size_t>(1024 + (size_t)(p.slice / 64 + 2 + (p.cluster > 1 ? 4 : 2)) * kChunkBytes, 120 * 1024);
+    const size_t smem = std::max<size_t>(small_layout(s, p.cluster, p.slice, &p), 120 * 1024);
     const bool vec = s.cols % 4 == 0;
+    // items of the sweep a thread has, at most, against the room for them
+    const int V = vec ? 4 : 1, rows = s.tall ? p.slice : s.m, wide = s.tall ? s.m : std::min(p.slice, s.n);
+    int lpr = 1;
+    while (lpr < 32 && lpr * V < wide) lpr <<= 1;
+    const int64_t items = (int64_t)((rows + kSmallThreads / lpr - 1) / (kSmallThreads / lpr)) * ((wide + lpr * V - 1) / (lpr * V));
+    p.keep = items * kSmallThreads * V * 4 <= (int64_t)smem - 1024 - p.oA;
     static bool attr[64][2] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GCONV_ERR_CUDA;
     auto fn = vec ? newton_small_kernel<4> : newton_small_kernel<1>;
     if (!attr[dev][vec]) {
-        const int most = 1024 + (kMaxChunks + 6) * (int)kChunkBytes;
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return GCONV_ERR_CUDA;
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return GCONV_ERR_CUDA;
         attr[dev][vec] = true;
     }
     cudaLaunchConfig_t cfg = {};
