@@ -6,18 +6,6 @@ namespace gconv {
 
 namespace {
 
-template <typename T, int VEC>
-void launch(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
-{
-    constexpr int NCH = block_nch(VEC);
-    if (kind == kBlockNorm)
-        launch_dependent(block_bwd_kernel<T, VEC, NCH, false, true>, s.grid, s.threads, s.smem, st, a);
-    else if (kind == kBlockJoin)
-        launch_dependent(block_bwd_kernel<T, VEC, NCH, true, false>, s.grid, s.threads, s.smem, st, a);
-    else
-        launch_dependent(block_bwd_kernel<T, VEC, NCH, true, true>, s.grid, s.threads, s.smem, st, a);
-}
-
 template <void (*Kernel)(BlockArgs)>
 void launch_staged(const BlockShape &s, const BlockArgs &a, cudaStream_t st)
 {
@@ -28,7 +16,7 @@ void launch_staged(const BlockShape &s, const BlockArgs &a, cudaStream_t st)
         if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem) != cudaSuccess) return;
         attr[dev] = true;
     }
-    launch_dependent(Kernel, s.grid, s.threads, s.smem, st, a);
+    launch_dependent_clusters(Kernel, s.grid, s.threads, s.smem, s.cluster, st, a);
 }
 
 template <typename T, int VEC>
@@ -52,10 +40,7 @@ void launch_t(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st
         else if (s.vec == 2) staged<T, 2>(kind, s, a, st);
         else if (s.vec == 4) staged<T, 4>(kind, s, a, st);
         else if constexpr (sizeof(T) == 2) staged<T, 8>(kind, s, a, st);
-    } else if (s.one && s.vec == 1) launch<T, 1>(kind, s, a, st);
-    else if (s.one && s.vec == 2) launch<T, 2>(kind, s, a, st);
-    else if (s.one) launch<T, 4>(kind, s, a, st);
-    else if (kind == kBlockNorm)
+    } else if (kind == kBlockNorm)
         launch_dependent(block_bwd_walk_kernel<T, false, true>, s.grid, s.threads, s.smem, st, a);
     else if (kind == kBlockJoin)
         launch_dependent(block_bwd_walk_kernel<T, true, false>, s.grid, s.threads, s.smem, st, a);

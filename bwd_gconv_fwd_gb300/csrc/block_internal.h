@@ -8,10 +8,9 @@ namespace gconv {
 // The shape of one launch (block_norm.cu, block_shape).
 struct BlockShape {
     int staged;               // the kernels of block_stage.cuh, with:
-    int PT, flat, per, total, pitch, tensor, pieces, lanes2;
+    int PT, flat, per, total, stages, cluster, Cc, pitch, tensor, pieces, lanes2;
     int vec;                  // positions a thread holds at once
-    int one;                  // not staged: a thread's channels fit in its registers
-    int TX, TY, Z, PV, tiles, splits;
+    int TX, TY, Z, tiles, splits;
     int threads;
     unsigned grid;
     size_t smem;
@@ -20,9 +19,6 @@ struct BlockShape {
 enum { kBlockNorm = 0, kBlockJoin = 1, kBlockJoinNext = 2 };
 
 constexpr size_t kBlockSmem = 227 * 1024;
-
-// Channels a thread holds: four where it holds 4 positions of each, eight where 1 or 2.
-constexpr int block_nch(int vec) { return vec >= 4 ? 4 : 8; }
 
 void block_fwd_bf16(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st);
 void block_fwd_f32(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st);

@@ -41,24 +41,38 @@ __global__ void __launch_bounds__(kFinChannels * kFinLanes) block_finish_kernel(
     if (c < a.C) {
         const int64_t NC = (int64_t)a.N * a.C;
         const float kc = (a.w ? a.w[c] : 1.f) * (a.s ? a.s[c] : 1.f);
-        #pragma unroll 2
-        for (int n = ln; n < a.N; n += kFinLanes) {
-            const int64_t rb = (n * a.G + c / a.Cg) / a.Z;
-            const int shares = (int)(((rb + 1) * a.tiles - 1) / a.per - rb * a.tiles / a.per) + 1;
-            const float *p = a.part + (int64_t)n * a.C + c;
-            float q = 0.f;
-            #pragma unroll 4
-            for (int i = 0; i < shares; ++i) {
-                if (a.next) t2 += p[i * NC];
-                if (a.post) q += p[(a.splits + i) * NC];
+        // walkers that share the rows of image n and this channel's group
+        const int g = c / a.Cg;
+        auto shares = [&](int n) {
+            const int at = (n * a.G + g) / a.Z * a.tiles;
+            return (at + a.tiles - 1) / a.per - at / a.per + 1;
+        };
+        const float *p = a.part + c;
+        if (a.post && a.gate == GCONV_GATE_CHANNEL) {
+            for (int n = ln; n < a.N; n += kFinLanes) {
+                const int m = shares(n);
+                float q = 0.f;
+                #pragma unroll 4
+                for (int i = 0; i < m; ++i) {
+                    if (a.next) t2 += p[i * NC + (int64_t)n * a.C];
+                    q += p[(a.splits + i) * NC + (int64_t)n * a.C];
+                }
+                float v;
+                const float dv = gate_grad(to_f(static_cast<const T *>(a.z)[(int64_t)n * a.C + c]), a.act, &v);
+                if (a.dzc) a.dzc[(int64_t)n * a.C + c] = q * kc * dv;
+                tk = fmaf(q, v, tk);
             }
-            if (a.post && a.gate == GCONV_GATE_CHANNEL) {
-                float g;
-                const float dg = gate_grad(to_f(static_cast<const T *>(a.z)[(int64_t)n * a.C + c]), a.act, &g);
-                if (a.dzc) a.dzc[(int64_t)n * a.C + c] = q * kc * dg;
-                q *= g;
+        } else {
+            // images and walkers as one sum, so that its terms are all in flight
+            #pragma unroll 8
+            for (int i = ln; i < a.N * a.splits; i += kFinLanes) {
+                const int n = i / a.splits, m = i - n * a.splits;
+                if (m < shares(n)) {
+                    const int64_t at = (int64_t)n * a.C + m * NC;
+                    if (a.next) t2 += p[at];
+                    if (a.post) tk += p[at + a.splits * NC];
+                }
             }
-            tk += q;
         }
     }
     sh[0][ln][cl] = t2;
@@ -92,114 +106,102 @@ int pow2_up(int v)
     return p;
 }
 
-// Launch shape of the staged kernels: 16 elements a thread, at most `most` threads, as many lanes
-// a channel as that leaves.
-bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int tensors, int most, BlockShape *s)
+// Launch shape of the staged kernels: 16 elements a thread in at most 512 threads, as many lanes
+// a channel as that and shared memory leave.  Two tiles stand in shared memory; a channel's
+// positions in one are 32 bytes or more, or the whole plane, for which a group's channels go over
+// as few blocks of a cluster as needed.  Where a cluster of eight is not enough, one tile of 16
+// bytes a channel (its copies then wait for the tile before), or none (the walking kernels).
+bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
+    const int tensors = bwd ? (kind == kBlockJoinNext ? 5 : 3) : (kind == kBlockNorm ? 1 : 3), sums = bwd ? 2 : 1;
+    // threads an SM's registers hold: 128 a thread in the gradient of a join, 64 elsewhere
+    const int resident = bwd && kind != kBlockNorm ? 512 : 1024;
     const int P = b.H * b.W, Cg = b.C / b.groups, rows = b.N * b.groups;
     const int es = dt == GCONV_BF16 ? 2 : 4;
     int vec = 16 / es;
     while (P % vec) vec >>= 1;
     const int held = vec > 1 ? vec : 2;   // positions a lane holds
-    int TY = (Cg + stage_nch(vec) - 1) / stage_nch(vec);
-    s->vec = vec;
-    s->flat = P <= 64;
-    int TX = s->flat ? pow2_up((P + held - 1) / held) : 32;
-    while (TX > 1 && TX * TY > most) { TX >>= 1; s->flat = s->flat && held * TX >= P; }
-    if (TX * TY > most || (!s->flat && held * TX * es < 16)) return false;
-    // whole warps a row, or a power of two of rows a warp
-    if (TX * TY >= 32) TY = (TY + 32 / TX - 1) / (32 / TX) * (32 / TX);
-    else TY = pow2_up(TY);
-    int Z = 1;
-    while (TX * TY * Z < 32 || (TX * TY * Z * 2 <= most && Z < rows)) Z *= 2;
-    s->PT = held * TX;
-    const size_t limit = kBlockSmem;
-    const int sums = bwd ? 2 : 1;
-    while (true) {
+    const int widest = P <= 64 ? pow2_up((P + held - 1) / held) : 32;
+
+    auto fits = [&](int cluster, int TX, int Z, int stages) {
+        const int Cc = (Cg + cluster - 1) / cluster, share = (Cc + stage_nch(vec) - 1) / stage_nch(vec);
+        if ((cluster - 1) * Cc >= Cg) return false;            // a block without channels
+        // whole warps a row, or a power of two of rows a warp
+        const int TY = TX * share >= 32 || cluster > 1 ? (share + 32 / TX - 1) / (32 / TX) * (32 / TX) : pow2_up(share);
+        if (TX * TY * Z > 512) return false;
+        s->flat = P <= 64 && held * TX >= P;
+        s->PT = held * TX;
+        if (!s->flat && s->PT * es < (stages == 2 ? 32 : 16)) return false;
         if (s->flat) {
+            s->pieces = 1;
             s->pitch = P * es;
-            s->tensor = ((Z * Cg * P * es + 15 + 16 + held * TX * es) & ~15);
+            s->tensor = (Z * Cc * P * es + 15 + 16 + held * TX * es) & ~15;
         } else {
             const bool aligned = (int64_t)P * es % 16 == 0 && s->PT * es % 16 == 0;
             s->pieces = (s->PT * es + 15) / 16 + (aligned ? 0 : 1);
             s->pitch = s->pieces * 16;
-            s->tensor = Z * Cg * s->pitch + 16;
+            s->tensor = Z * Cc * s->pitch + 16;
         }
-        s->smem = (size_t)2 * tensors * s->tensor + (TX * TY > 32 ? (size_t)Z * (TX * TY / 32 + 1) * TX * stage_pairs(vec) * sums * 8 : 0);
-        if (s->smem <= limit) break;
-        if (Z > 1 && TX * TY * Z >= 64) Z /= 2;
-        else return false;
+        const size_t width = (size_t)TX * stage_pairs(vec) * sums * 8;
+        s->smem = (size_t)stages * tensors * s->tensor;
+        if (TX * TY > 32 || cluster > 1) s->smem += Z * (TX * TY / 32 + 1) * width + (cluster > 1 ? 2 * cluster * width : 0);
+        if (s->smem > kBlockSmem) return false;
+        s->TX = TX; s->TY = TY; s->Z = Z; s->stages = stages; s->cluster = cluster; s->Cc = Cc;
+        s->threads = TX * TY * Z;
+        return true;
+    };
+    bool found = false;
+    for (int stages = 2; stages >= 1 && !found; --stages)
+        for (int cluster = 1; cluster <= 8 && !found; cluster *= 2)
+            for (int TX = widest; TX >= 1 && !found; TX >>= 1) {
+                int Z = 1;
+                while (cluster == 1 && TX * pow2_up((Cg + stage_nch(vec) - 1) / stage_nch(vec)) * Z < 32) Z *= 2;
+                found = fits(cluster, TX, Z, stages);
+            }
+    if (!found) return false;
+    // several rows a block where one gives it few threads
+    while (s->cluster == 1 && s->threads * 2 <= 256 && s->Z < rows) {
+        const BlockShape kept = *s;
+        if (!fits(1, kept.TX, kept.Z * 2, kept.stages)) { *s = kept; break; }
     }
+    s->vec = vec;
     s->lanes2 = pow2_up(s->pieces);
     s->staged = 1;
-    s->TX = TX; s->TY = TY; s->Z = Z; 
-    s->threads = TX * TY * Z;
     s->tiles = s->flat ? 1 : (P + s->PT - 1) / s->PT;
-    s->total = (rows + Z - 1) / Z * s->tiles;
-    const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(kBlockSmem / (s->smem + 1024), 1024 / s->threads));
-    s->per = (s->total + num_sms() * per_sm - 1) / (num_sms() * per_sm);
-    s->grid = (unsigned)((s->total + s->per - 1) / s->per);
-    s->splits = (s->tiles + s->per - 1) / s->per + 1;   // blocks that may share a row
+    s->total = (rows + s->Z - 1) / s->Z * s->tiles;
+    const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(kBlockSmem / (s->smem + 1024), resident / s->threads));
+    const int walkers = std::max(1, num_sms() * per_sm / s->cluster);
+    s->per = (s->total + walkers - 1) / walkers;
+    s->grid = (unsigned)((s->total + s->per - 1) / s->per) * s->cluster;
+    s->splits = (s->tiles + s->per - 1) / s->per + 1;   // walkers that may share a row
     return true;
 }
 
-// Launch shape.  The widest vector of at most four positions that divides the plane (rows are
-// then aligned for it);
-// TX such that a channel's positions in a block are 64 bytes or more where 512 threads
-// allow it.
+// Launch shape of a call; of the walking kernels where the staged ones do not fit: 32 positions of
+// a row a block.
 void block_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
     *s = BlockShape{};
-    const int tensors = bwd ? (kind == kBlockJoinNext ? 5 : 3) : (kind == kBlockNorm ? 1 : 3);
-    if (stage_shape(b, dt, bwd, tensors, 512, s)) return;
+    if (stage_shape(b, dt, bwd, kind, s)) return;
     *s = BlockShape{};
-    const int P = b.H * b.W, Cg = b.C / b.groups, rows = b.N * b.groups;
-    const int esize = dt == GCONV_BF16 ? 2 : 4;
-    int vec = 4;
-    while (P % vec) vec >>= 1;
-    int nch = block_nch(vec);
-    int one = 1;
-    if ((Cg + nch - 1) / nch > 512) { one = 0; vec = 1; nch = block_nch(1); }
-    const int PV = P / vec;
-    int TX, TY;
-    if (one) {
-        const int ty = (Cg + nch - 1) / nch;
-        TX = std::min(32, pow2_up(PV));
-        while (TX > 1 && TX * ty > 512) TX >>= 1;
-        while (TX > 1 && TX * ty > 256 && TX * vec * esize > 64) TX >>= 1;
-        TY = ty;
-    } else {
-        TX = std::min(32, pow2_up(PV));
-        TY = 512 / TX;
-    }
-    // a row's threads: whole warps, or a power of two of them in one warp
-    if (TX * TY >= 32) TY = (TY + 32 / TX - 1) / (32 / TX) * (32 / TX);
-    else TY = pow2_up(TY);
-    int Z = 1;
-    while (TX * TY * Z < 32 || (TX * TY * Z < 256 && Z * 2 <= rows && TX * TY * Z * 2 <= 256)) Z *= 2;
-    s->vec = vec; s->one = one; s->TX = TX; s->TY = TY; s->Z = Z; s->PV = PV;
-    s->threads = TX * TY * Z;
-    s->tiles = (PV + TX - 1) / TX;
+    const int P = b.H * b.W, rows = b.N * b.groups;
+    s->TX = std::min(32, pow2_up(P));
+    s->TY = 512 / s->TX;
+    s->Z = 1;
+    s->cluster = 1;
+    s->threads = s->TX * s->TY;
+    s->tiles = s->splits = (P + s->TX - 1) / s->TX;
     s->per = 1;
-    const int64_t row_blocks = (rows + Z - 1) / Z;
-    s->splits = s->tiles;
-    if (bwd && one) {
-        const int64_t want = (int64_t)num_sms() * (2048 / s->threads);
-        s->splits = (int)std::max<int64_t>(1, std::min<int64_t>(s->tiles, want / std::max<int64_t>(1, row_blocks)));
-        const int per = (s->tiles + s->splits - 1) / s->splits;
-        s->splits = (s->tiles + per - 1) / per;
-    }
-    s->grid = (unsigned)(row_blocks * (bwd ? s->splits : s->tiles));
-    const int sums = bwd ? 2 : 1;
-    s->smem = TY > 1 ? (size_t)Z * (TY + column_shares(TY)) * TX * vec * sums * sizeof(float) : 0;
+    s->grid = (unsigned)(rows * s->tiles);
+    s->smem = (size_t)(s->TY + column_shares(s->TY)) * s->TX * (bwd ? 2 : 1) * sizeof(float);
 }
 
 void block_args(const gconv_block &b, gconv_dtype dt, const BlockShape &s, BlockArgs *a)
 {
     a->G = b.groups; a->Cg = b.C / b.groups; a->rows = b.N * b.groups;
-    a->P = b.H * b.W; a->PV = s.PV;
+    a->P = b.H * b.W;
     a->TX = s.TX; a->TY = s.TY; a->Z = s.Z; a->tiles = s.tiles; a->splits = s.splits;
-    a->PT = s.PT; a->flat = s.flat; a->per = s.per; a->total = s.total; 
+    a->PT = s.PT; a->flat = s.flat; a->per = s.per; a->total = s.total; a->stages = s.stages; a->cluster = s.cluster; a->Cc = s.Cc;
     a->pitch = s.pitch; a->tensor = s.tensor; a->pieces = s.pieces; a->lanes2 = s.lanes2;
     a->bytes = (int64_t)b.N * b.C * a->P * (dt == GCONV_BF16 ? 2 : 4);
     a->whole = a->bytes % 16 == 0;

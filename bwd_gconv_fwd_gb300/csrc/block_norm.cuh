@@ -22,11 +22,13 @@ namespace gconv {
 
 struct BlockArgs {
     int G, Cg, rows;          // rows = N G
-    int P, PV;                // positions of a plane, vectors of VEC positions in it
+    int P;                    // positions of a plane
     int TX, TY, Z;            // the block's shape; TX is a power of two
     int tiles, splits;        // tiles of TX vectors in a plane; blocks that share a row (backward)
     // staged kernels: a tile is PT positions of Z rows (flat: Z whole rows, tiles = 1)
     int PT, flat, per, total; // tiles a block walks, tiles in all
+    int stages;               // tiles in shared memory: 2, or 1
+    int cluster, Cc;          // blocks that share a group's channels, and how many each has
     int pitch, tensor;        // bytes of a staged channel, of a staged tensor
     int pieces, lanes2;       // 16-byte pieces of a channel, and the power of two threads for them
     int64_t bytes;            // of a whole tensor
@@ -135,242 +137,8 @@ __device__ __forceinline__ float join_sum(float res, float k, float g, float h, 
     return fmaf(__fmul_rn(k, g), __fmul_rn(h, r), res);
 }
 
-// ---- a group's channels in the registers of one thread block ----------------------
-
-// Forward.  POST: the join's branch; NEXT: the norm (of out, or of x alone without POST).
-// Every load of a tile is issued before its first use and its first store: the stores may
-// alias the loads as far as the compiler knows, and a load behind one would wait for it.
-template <typename T, int VEC, int NCH, bool POST, bool NEXT>
-__global__ void __launch_bounds__(512) block_fwd_kernel(const BlockArgs a)
-{
-    extern __shared__ __align__(16) float red[];
-    const int tx = threadIdx.x % a.TX, ry = threadIdx.x / a.TX;
-    const int ty = ry % a.TY, z = ry / a.TY;
-    const int tile = blockIdx.x % a.tiles;
-    const int row = (blockIdx.x / a.tiles) * a.Z + z;
-    const int v0 = tile * a.TX + tx;
-    const bool live = row < a.rows && v0 < a.PV;
-    const int64_t base = (int64_t)row * a.Cg * a.P + (int64_t)v0 * VEC + (int64_t)ty * a.P;
-    const int64_t hop = (int64_t)a.TY * a.P;                   // to the thread's next channel
-    const int ch0 = live ? (row % a.G) * a.Cg + ty : 0;
-    const int64_t nc0 = live ? (int64_t)row * a.Cg + ty : 0;   // in [N][C]
-    const int mine = live ? (a.Cg - ty + a.TY - 1) / a.TY : 0; // channels of this thread, at most NCH
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-
-    Pack<T, VEC> hk[NCH], xk[NCH], zk[NCH];
-    float kb[NCH], wn[NCH];
-    #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-        hk[j] = xk[j] = zk[j] = Pack<T, VEC>{};
-        if (j < mine) {
-            xk[j] = load_pack<T, VEC>(a.x, base + j * hop);
-            if (POST) hk[j] = load_pack<T, VEC>(a.h, base + j * hop);
-            if (POST && a.gate == GCONV_GATE_FULL) zk[j] = load_pack<T, VEC>(a.z, base + j * hop);
-        }
-    }
-    #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-        kb[j] = wn[j] = 0.f;
-        if (j < mine) {
-            if (NEXT) wn[j] = a.w2 ? a.w2[ch0 + j * a.TY] : 1.f;
-            if (POST) {
-                kb[j] = branch_coeff(a, ch0 + j * a.TY);
-                if (a.gate == GCONV_GATE_CHANNEL)
-                    kb[j] = __fmul_rn(kb[j], gate_value(to_f(static_cast<const T *>(a.z)[nc0 + j * a.TY]), a.act));
-            }
-        }
-    }
-    float sum[1][VEC];
-    float o[NCH][VEC];
-    if (POST) {
-        #pragma unroll
-        for (int k = 0; k < VEC; ++k) sum[0][k] = 0.f;
-        #pragma unroll
-        for (int j = 0; j < NCH; ++j)
-            #pragma unroll
-            for (int k = 0; k < VEC; ++k) { const float t = to_f(hk[j].v[k]); sum[0][k] = fmaf(t, t, sum[0][k]); }
-        column_sum<1, VEC>(sum, red, a, tx, ty, z);
-        #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const float r = rsqrtf(sum[0][k] * a.inv_cg + a.eps);
-            #pragma unroll
-            for (int j = 0; j < NCH; ++j) {
-                const float g = a.gate == GCONV_GATE_FULL ? __fmul_rn(kb[j], gate_value(to_f(zk[j].v[k]), a.act)) : kb[j];
-                o[j][k] = fmaf(g, __fmul_rn(to_f(hk[j].v[k]), r), to_f(xk[j].v[k]));
-            }
-        }
-        #pragma unroll
-        for (int j = 0; j < NCH; ++j)
-            if (j < mine) store_pack<T, VEC>(a.out, base + j * hop, o[j]);
-        if (!NEXT) return;
-    } else {
-        #pragma unroll
-        for (int j = 0; j < NCH; ++j)
-            #pragma unroll
-            for (int k = 0; k < VEC; ++k) o[j][k] = to_f(xk[j].v[k]);
-    }
-    #pragma unroll
-    for (int k = 0; k < VEC; ++k) sum[0][k] = 0.f;
-    #pragma unroll
-    for (int j = 0; j < NCH; ++j)
-        #pragma unroll
-        for (int k = 0; k < VEC; ++k) sum[0][k] = fmaf(o[j][k], o[j][k], sum[0][k]);
-    column_sum<1, VEC>(sum, red, a, tx, ty, z);
-    #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-        const float r = rsqrtf(sum[0][k] * a.inv_cg + a.eps);
-        #pragma unroll
-        for (int j = 0; j < NCH; ++j) o[j][k] *= r * wn[j];
-    }
-    #pragma unroll
-    for (int j = 0; j < NCH; ++j)
-        if (j < mine) store_pack<T, VEC>(a.next, base + j * hop, o[j]);
-}
-
-// Backward.  NEXT: dx = dout + gradient of the norm of x (= out); POST: the branch's dh, dz
-// from dx (= dout without NEXT).  A block walks the tiles split, split + splits, ... of its
-// rows and keeps its channel sums in registers; they go to `part` at the end.
-template <typename T, int VEC, int NCH, bool POST, bool NEXT>
-__global__ void __launch_bounds__(512) block_bwd_kernel(const BlockArgs a)
-{
-    extern __shared__ __align__(16) float red[];
-    const int tx = threadIdx.x % a.TX, ry = threadIdx.x / a.TX;
-    const int ty = ry % a.TY, z = ry / a.TY;
-    const int split = blockIdx.x % a.splits;
-    const int row = (blockIdx.x / a.splits) * a.Z + z;
-    const bool row_ok = row < a.rows;
-    const int64_t base0 = (int64_t)row * a.Cg * a.P + (int64_t)ty * a.P;
-    const int64_t hop = (int64_t)a.TY * a.P;
-    const int ch0 = row_ok ? (row % a.G) * a.Cg + ty : 0;
-    const int64_t nc0 = row_ok ? (int64_t)row * a.Cg + ty : 0;
-    const int mine_row = row_ok ? (a.Cg - ty + a.TY - 1) / a.TY : 0;
-    const bool full = POST && a.gate == GCONV_GATE_FULL;
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-
-    float acc2[NCH], acck[NCH], wn[NCH], kb[NCH], zc[NCH];
-    #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-        acc2[j] = acck[j] = wn[j] = kb[j] = 0.f;
-        zc[j] = 1.f;
-        if (j < mine_row) {
-            if (NEXT) wn[j] = a.w2 ? a.w2[ch0 + j * a.TY] : 1.f;
-            if (POST) kb[j] = branch_coeff(a, ch0 + j * a.TY);
-            if (POST && a.gate == GCONV_GATE_CHANNEL)
-                zc[j] = gate_value(to_f(static_cast<const T *>(a.z)[nc0 + j * a.TY]), a.act);
-        }
-    }
-    for (int tile = split; tile < a.tiles; tile += a.splits) {
-        const int v0 = tile * a.TX + tx;
-        const int mine = v0 < a.PV ? mine_row : 0;
-        const int64_t base = base0 + (int64_t)v0 * VEC;
-        Pack<T, VEC> xk[NCH], gk[NCH], dk[NCH], hk[NCH], zk[NCH];
-        #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-            xk[j] = gk[j] = dk[j] = hk[j] = zk[j] = Pack<T, VEC>{};
-            if (j < mine) {
-                const int64_t at = base + j * hop;
-                if (NEXT) {
-                    xk[j] = load_pack<T, VEC>(a.x, at);
-                    gk[j] = load_pack<T, VEC>(a.dnext, at);
-                }
-                if (a.dout) dk[j] = load_pack<T, VEC>(a.dout, at);
-                if (POST) hk[j] = load_pack<T, VEC>(a.h, at);
-                if (full) zk[j] = load_pack<T, VEC>(a.z, at);
-            }
-        }
-        float sum[2][VEC];
-        float d[NCH][VEC];
-        #pragma unroll
-        for (int j = 0; j < NCH; ++j)
-            #pragma unroll
-            for (int k = 0; k < VEC; ++k) d[j][k] = to_f(dk[j].v[k]);
-        if (NEXT) {
-            #pragma unroll
-            for (int k = 0; k < VEC; ++k) sum[0][k] = sum[1][k] = 0.f;
-            #pragma unroll
-            for (int j = 0; j < NCH; ++j)
-                #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    const float t = to_f(xk[j].v[k]);
-                    sum[0][k] = fmaf(t, t, sum[0][k]);
-                    sum[1][k] = fmaf(t, to_f(gk[j].v[k]) * wn[j], sum[1][k]);
-                }
-            column_sum<2, VEC>(sum, red, a, tx, ty, z);
-            #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                // r is 0 past the plane's end, where eps = 0 would make it infinite
-                const float r = v0 < a.PV ? rsqrtf(sum[0][k] * a.inv_cg + a.eps) : 0.f;
-                const float m = sum[1][k] * a.inv_cg * r * r * r;
-                #pragma unroll
-                for (int j = 0; j < NCH; ++j) {
-                    const float x = to_f(xk[j].v[k]), rg = to_f(gk[j].v[k]) * r;
-                    d[j][k] = fmaf(-x, m, fmaf(rg, wn[j], d[j][k]));
-                    acc2[j] = fmaf(rg, x, acc2[j]);
-                }
-            }
-            #pragma unroll
-            for (int j = 0; j < NCH; ++j)
-                if (j < mine) store_pack<T, VEC>(a.dx, base + j * hop, d[j]);
-        }
-        if (POST) {
-            #pragma unroll
-            for (int k = 0; k < VEC; ++k) sum[0][k] = sum[1][k] = 0.f;
-            float sg[NCH][VEC];   // the gate's sigmoid, or its value without one
-            #pragma unroll
-            for (int j = 0; j < NCH; ++j)
-                #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    const float h = to_f(hk[j].v[k]), zv = to_f(zk[j].v[k]);
-                    sg[j][k] = !full ? zc[j] : a.act == GCONV_ACT_NONE ? zv : sigmoid(zv);
-                    const float g = full && a.act == GCONV_ACT_SILU ? zv * sg[j][k] : sg[j][k];
-                    sum[0][k] = fmaf(h, h, sum[0][k]);
-                    sum[1][k] = fmaf(h, d[j][k] * (kb[j] * g), sum[1][k]);
-                }
-            column_sum<2, VEC>(sum, red, a, tx, ty, z);
-            #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                // r is 0 past the plane's end, where eps = 0 would make it infinite
-                const float r = v0 < a.PV ? rsqrtf(sum[0][k] * a.inv_cg + a.eps) : 0.f;
-                const float m = sum[1][k] * a.inv_cg * r * r * r;
-                #pragma unroll
-                for (int j = 0; j < NCH; ++j) {
-                    const float h = to_f(hk[j].v[k]), zv = to_f(zk[j].v[k]), s = sg[j][k];
-                    const float g = full && a.act == GCONV_ACT_SILU ? zv * s : s;
-                    const float dr = d[j][k] * r, dk_ = dr * kb[j];
-                    // act'(z): 1; s (1 - s); s (1 + z (1 - s)) = s + g (1 - s)
-                    const float dg = a.act == GCONV_ACT_NONE ? 1.f : a.act == GCONV_ACT_SIGMOID ? s - s * s : fmaf(g, 1.f - s, s);
-                    // the channel gate's own gradient needs the sum without the gate; the
-                    // finish kernel multiplies it in
-                    acck[j] = fmaf(dr * h, full ? g : 1.f, acck[j]);
-                    d[j][k] = fmaf(-h, m, dk_ * g);          // dh
-                    sg[j][k] = dk_ * h * dg;                 // dz
-                }
-            }
-            #pragma unroll
-            for (int j = 0; j < NCH; ++j)
-                if (j < mine) {
-                    store_pack<T, VEC>(a.dh, base + j * hop, d[j]);
-                    if (full && a.dz) store_pack<T, VEC>(a.dz, base + j * hop, sg[j]);
-                }
-        }
-    }
-    #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-        float s2 = acc2[j], sk = acck[j];
-        for (int m = 1; m < a.TX; m <<= 1) {
-            if (NEXT) s2 += __shfl_xor_sync(0xffffffffu, s2, m);
-            if (POST) sk += __shfl_xor_sync(0xffffffffu, sk, m);
-        }
-        if (tx == 0 && j < mine_row) {
-            if (NEXT) a.part[(int64_t)split * a.rows * a.Cg + nc0 + j * a.TY] = s2;
-            if (POST) a.part[(int64_t)(a.splits + split) * a.rows * a.Cg + nc0 + j * a.TY] = sk;
-        }
-    }
-}
-
-// ---- groups too wide for that: the channels walked in steps, inputs read again in each sweep ----
+// ---- groups too wide for the staged kernels: the channels walked in steps, inputs read again in
+// each sweep ----
 
 // out of the join at one element, from its three inputs
 template <typename T>

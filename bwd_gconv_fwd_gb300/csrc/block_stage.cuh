@@ -1,5 +1,5 @@
 // block_stage.cuh -- the block norm / join kernels for groups whose tiles fit in shared memory
-// twice: while a block computes one tile, the next lands by 16-byte asynchronous copies.
+// twice (or once): while a block computes one tile, the next lands by 16-byte asynchronous copies.
 //
 // These operators do 4 to 40 operations an element against 4 to 16 bytes, so the memory is the
 // limit as long as enough of it is in flight: a whole tile of every input here (40 to 100 KB an
@@ -87,6 +87,18 @@ __device__ __forceinline__ F2 gate_core(F2 z, bool plain)
 
 // ---- tiles --------------------------------------------------------------------------
 
+// A group too wide for one block's threads and shared memory is dealt over a cluster: block `rank`
+// has channels rank Cc, ... of every tile, and the blocks exchange their column sums.  (Z is 1 then.)
+struct Part {
+    int rank, c0, n;          // first channel of the group, how many
+    __device__ __forceinline__ explicit Part(const BlockArgs &a)
+    {
+        rank = a.cluster > 1 ? (int)ptx::cluster_rank() : 0;
+        c0 = rank * a.Cc;
+        n = min(a.Cc, a.Cg - c0);
+    }
+};
+
 // A tile: Z rows from row0, PT positions from p0.
 struct Tile {
     int row0, p0;
@@ -100,11 +112,12 @@ struct Tile {
 
 // Starts the copies of one tile of NT tensors to `dst` (a.tensor bytes each; a null tensor is skipped).
 template <typename T, int NT>
-__device__ __forceinline__ void stage_tile(const BlockArgs &a, const Tile &w, const char *const (&src)[NT], uint32_t dst)
+__device__ __forceinline__ void stage_tile(const BlockArgs &a, const Part &g, const Tile &w, const char *const (&src)[NT],
+                                           uint32_t dst)
 {
     constexpr int es = (int)sizeof(T);
-    const int rows = min(a.Z, a.rows - w.row0) * a.Cg;         // channels
-    const int64_t first = (int64_t)w.row0 * a.Cg * a.P * es;
+    const int rows = min(a.Z, a.rows - w.row0) * g.n;          // channels
+    const int64_t first = ((int64_t)w.row0 * a.Cg + g.c0) * a.P * es;
     auto copy = [&](uint32_t to, int64_t from) {
         // a piece that a tensor's end cuts is read up to it
         const uint32_t n = a.whole ? 16u : (uint32_t)min((int64_t)16, a.bytes - from);
@@ -208,15 +221,18 @@ __device__ __forceinline__ F2 pull2(const BlockArgs &a, F2 sum, F2 r) { return m
 // Adds v over the TY threads that share a row and a vector and turns the sums into r (the first
 // NP) and m (the second NP, with TWO), the same bits in every thread: within a warp by shuffles
 // that split the values among its lanes, then over a row's warps through shared memory, where
-// one thread a pair of positions takes the roots.  `red`: for each row, N TX pairs a warp and
-// N TX more.  The next call may follow at once: it writes what this one reads last only behind its
-// own first barrier.
+// one thread a pair of positions takes the roots; in a cluster that thread first sends its sums to
+// the other blocks and adds theirs to them in rank order.  `red`: for each row, N TX pairs a
+// warp and N TX more, then N TX a block of the cluster, twice (`turn` says which; a block writes into
+// another's half only after the barrier that follows the other's reading of it).  The next call may
+// follow at once: it writes what this one reads last only behind its own first barrier.
 template <int NP, bool TWO>
-__device__ __forceinline__ void column_roots(F2 (&v)[TWO ? 2 * NP : NP], float *red, const BlockArgs &a, int tx, int ty, int z)
+__device__ __forceinline__ void column_roots(F2 (&v)[TWO ? 2 * NP : NP], float *red, const BlockArgs &a, const Part &g, int &turn,
+                                             int tx, int ty, int z)
 {
     constexpr int N = TWO ? 2 * NP : NP;
     const int per_row = a.TX * a.TY;
-    if (per_row <= 32) {
+    if (per_row <= 32 && a.cluster == 1) {
         for (int m = a.TX; m < per_row; m <<= 1) {
             #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = add2(v[i], shfl_xor2(v[i], m));
@@ -233,6 +249,12 @@ __device__ __forceinline__ void column_roots(F2 (&v)[TWO ? 2 * NP : NP], float *
     uint64_t *done = mine + warps * width;
     scatter_sum<N, 16>(v, mine + (in_row >> 5) * width, a.TX, tx, 0);
     __syncthreads();
+    auto finish = [&](int i, F2 s, F2 u) {
+        const F2 r = root2(a, s);
+        done[i] = r.v;
+        if constexpr (TWO) done[half + i] = pull2(a, u, r).v;
+    };
+    uint64_t *others = mine + (warps + 1) * width + turn * a.cluster * width;
     for (int i = in_row; i < half; i += per_row) {
         F2 s{mine[i]}, u{TWO ? mine[half + i] : 0};
         #pragma unroll 8
@@ -240,9 +262,28 @@ __device__ __forceinline__ void column_roots(F2 (&v)[TWO ? 2 * NP : NP], float *
             s = add2(s, F2{mine[w * width + i]});
             if constexpr (TWO) u = add2(u, F2{mine[w * width + half + i]});
         }
-        const F2 r = root2(a, s);
-        done[i] = r.v;
-        if constexpr (TWO) done[half + i] = pull2(a, u, r).v;
+        if (a.cluster == 1) {
+            finish(i, s, u);
+        } else {
+            const uint32_t to = ptx::smem_u32(others + g.rank * width + i);
+            for (int k = 0; k < a.cluster; ++k) {
+                ptx::st_cluster64(ptx::map_to(to, (uint32_t)k), s.v);
+                if constexpr (TWO) ptx::st_cluster64(ptx::map_to(to + half * 8, (uint32_t)k), u.v);
+            }
+        }
+    }
+    if (a.cluster > 1) {
+        __syncwarp();
+        ptx::cluster_sync();
+        for (int i = in_row; i < half; i += per_row) {
+            F2 s{others[i]}, u{TWO ? others[half + i] : 0};
+            for (int k = 1; k < a.cluster; ++k) {
+                s = add2(s, F2{others[k * width + i]});
+                if constexpr (TWO) u = add2(u, F2{others[k * width + half + i]});
+            }
+            finish(i, s, u);
+        }
+        turn ^= 1;
     }
     __syncthreads();
     #pragma unroll
@@ -259,7 +300,7 @@ struct Seat {
 };
 
 template <typename T, int VEC>
-__device__ __forceinline__ Seat seat(const BlockArgs &a)
+__device__ __forceinline__ Seat seat(const BlockArgs &a, const Part &g)
 {
     constexpr int es = (int)sizeof(T);
     Seat s;
@@ -268,7 +309,7 @@ __device__ __forceinline__ Seat seat(const BlockArgs &a)
     s.ty = ry % a.TY;
     s.z = ry / a.TY;
     s.pos = VEC * s.tx;
-    s.c0 = s.z * a.Cg + s.ty;
+    s.c0 = s.z * g.n + s.ty;
     s.apart = VEC > 1 ? VEC - 1 : a.TX;
     s.s_first = s.c0 * a.pitch + s.pos * es;
     s.s_step = a.TY * a.pitch;
@@ -285,9 +326,9 @@ __device__ __forceinline__ int staged_at(const Seat &s, uint32_t m0, int j)
 
 // Byte offset, modulo 16, of the thread's first channel in this tile (flat: of the tile).
 template <typename T>
-__device__ __forceinline__ uint32_t misfit(const BlockArgs &a, const Seat &s, const Tile &w)
+__device__ __forceinline__ uint32_t misfit(const BlockArgs &a, const Part &g, const Seat &s, const Tile &w)
 {
-    const uint32_t first = (uint32_t)w.row0 * (uint32_t)a.Cg * (uint32_t)a.P;
+    const uint32_t first = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)g.c0) * (uint32_t)a.P;
     return (first + (a.flat ? 0u : (uint32_t)s.c0 * (uint32_t)a.P + (uint32_t)w.p0)) * (uint32_t)sizeof(T);
 }
 
@@ -296,8 +337,9 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
 {
     constexpr int NT = POST ? 3 : 1, NP = stage_pairs(VEC), NCH = stage_nch(VEC);
     extern __shared__ __align__(128) uint8_t smem[];
-    float *red = reinterpret_cast<float *>(smem + 2 * NT * a.tensor);
-    const Seat s = seat<T, VEC>(a);
+    float *red = reinterpret_cast<float *>(smem + a.stages * NT * a.tensor);
+    const Part g(a);
+    const Seat s = seat<T, VEC>(a, g);
     const int apart = s.apart * (int)sizeof(T);
     constexpr bool full = GATE != kGateOff;
     const bool plain = a.act == GCONV_ACT_NONE;
@@ -305,35 +347,40 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
     src[0] = static_cast<const char *>(a.x);
     if constexpr (POST) { src[1] = static_cast<const char *>(a.h); src[2] = full ? static_cast<const char *>(a.z) : nullptr; }
     const uint32_t stage0 = ptx::smem_u32(smem);
-    const int t0 = blockIdx.x * a.per, t1 = min(a.total, t0 + a.per);
+    const int walker = blockIdx.x / a.cluster;
+    const int t0 = walker * a.per, t1 = min(a.total, t0 + a.per);
     Tile w, ahead;
     w.set(a, t0);
     ahead = w;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    stage_tile<T, NT>(a, ahead, src, stage0);
-    ptx::cp_async_commit();
+    if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
+    stage_tile<T, NT>(a, g, ahead, src, stage0);
 
-    int at_row = -1;
+    int at_row = -1, turn = 0;
     float kb[NCH], wn[NCH];
     bool has[NCH];
     #pragma unroll
-    for (int j = 0; j < NCH; ++j) has[j] = s.ty + j * a.TY < a.Cg;
+    for (int j = 0; j < NCH; ++j) has[j] = s.ty + j * a.TY < g.n;
     for (int t = t0; t < t1; ++t, w.next(a)) {
-        const int buf = (t - t0) & 1;
-        ptx::cp_async_wait_group<0>();
-        __syncthreads();
-        if (t + 1 < t1) {
+        const int buf = (t - t0) & (a.stages - 1);
+        if (a.stages == 1 && t > t0) {
+            __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
-            ptx::cp_async_commit();
+            stage_tile<T, NT>(a, g, ahead, src, stage0);
+        }
+        ptx::cp_async_wait_all();
+        __syncthreads();
+        if (a.stages == 2 && t + 1 < t1) {
+            ahead.next(a);
+            stage_tile<T, NT>(a, g, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
         }
         const uint8_t *st = smem + buf * NT * a.tensor;
         const bool in_row = w.row0 + s.z < a.rows;
         const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + s.apart < a.P;
         if (at_row != w.row0) {
             at_row = w.row0;
-            const int row = w.row0 + s.z, ch0 = (row % a.G) * a.Cg + s.ty;
+            const int row = w.row0 + s.z, ch0 = (row % a.G) * a.Cg + g.c0 + s.ty;
             #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 kb[j] = wn[j] = 0.f;
@@ -342,13 +389,13 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
                     if (POST) {
                         kb[j] = branch_coeff(a, ch0 + j * a.TY);
                         if (a.gate == GCONV_GATE_CHANNEL)
-                            kb[j] = __fmul_rn(kb[j], gate_value(to_f(static_cast<const T *>(a.z)[(int64_t)row * a.Cg + s.ty + j * a.TY]), a.act));
+                            kb[j] = __fmul_rn(kb[j], gate_value(to_f(static_cast<const T *>(a.z)[(int64_t)row * a.Cg + g.c0 + s.ty + j * a.TY]), a.act));
                     }
                 }
             }
         }
-        const uint32_t m0 = misfit<T>(a, s, w);
-        const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)s.c0) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
+        const uint32_t m0 = misfit<T>(a, g, s, w);
+        const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
         int at[NCH];
         F2 r[NP], o[NCH][NP];
         #pragma unroll
@@ -362,7 +409,7 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
                 for (int k = 0; k < NP; ++k) r[k] = fma2(o[j][k], o[j][k], r[k]);
             }
         }
-        column_roots<NP, false>(r, red, a, s.tx, s.ty, s.z);
+        column_roots<NP, false>(r, red, a, g, turn, s.tx, s.ty, s.z);
         if (POST) {
             F2 sum[NP];
             #pragma unroll
@@ -375,18 +422,18 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
                     if (full) read_vec<T, VEC>(st + 2 * a.tensor + at[j], apart, z);
                     #pragma unroll
                     for (int k = 0; k < NP; ++k) {
-                        F2 g = f2(kb[j]);
+                        F2 kg = f2(kb[j]);
                         if (full) {
                             const F2 sg = gate_core<GATE>(z[k], plain);
-                            g = mul2(g, GATE == kGateSilu ? mul2(z[k], sg) : sg);
+                            kg = mul2(kg, GATE == kGateSilu ? mul2(z[k], sg) : sg);
                         }
-                        o[j][k] = fma2(g, mul2(o[j][k], r[k]), x[k]);
+                        o[j][k] = fma2(kg, mul2(o[j][k], r[k]), x[k]);
                         sum[k] = fma2(o[j][k], o[j][k], sum[k]);
                     }
                     write_vec<T, VEC>(a.out, e0 + j * s.e_step, s.apart, o[j], ok0, ok1);
                 }
             if (!NEXT) continue;
-            column_roots<NP, false>(sum, red, a, s.tx, s.ty, s.z);
+            column_roots<NP, false>(sum, red, a, g, turn, s.tx, s.ty, s.z);
             #pragma unroll
             for (int k = 0; k < NP; ++k) r[k] = sum[k];
         }
@@ -414,12 +461,13 @@ __device__ __forceinline__ F2 live_only(F2 v, bool ok0, bool ok1)
 // share those rows.  Dead positions hold what an earlier tile left: they meet no live one but in
 // the channel sums, which leave them out.
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
-__global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
+__global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(const BlockArgs a)
 {
     constexpr int NT = POST && NEXT ? 5 : 3, NP = stage_pairs(VEC), NCH = stage_nch(VEC);
     extern __shared__ __align__(128) uint8_t smem[];
-    float *red = reinterpret_cast<float *>(smem + 2 * NT * a.tensor);
-    const Seat s = seat<T, VEC>(a);
+    float *red = reinterpret_cast<float *>(smem + a.stages * NT * a.tensor);
+    const Part g(a);
+    const Seat s = seat<T, VEC>(a, g);
     const int apart = s.apart * (int)sizeof(T);
     constexpr bool full = GATE != kGateOff;
     const bool plain = a.act == GCONV_ACT_NONE;
@@ -429,29 +477,30 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
     if constexpr (NEXT) { src[iX] = static_cast<const char *>(a.x); src[iG] = static_cast<const char *>(a.dnext); }
     if constexpr (POST) { src[iH] = static_cast<const char *>(a.h); src[iZ] = full ? static_cast<const char *>(a.z) : nullptr; }
     const uint32_t stage0 = ptx::smem_u32(smem);
-    const int t0 = blockIdx.x * a.per, t1 = min(a.total, t0 + a.per);
+    const int walker = blockIdx.x / a.cluster;
+    const int t0 = walker * a.per, t1 = min(a.total, t0 + a.per);
     const int64_t NC = (int64_t)a.rows * a.Cg;
     Tile w, ahead;
     w.set(a, t0);
     ahead = w;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    stage_tile<T, NT>(a, ahead, src, stage0);
-    ptx::cp_async_commit();
+    if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
+    stage_tile<T, NT>(a, g, ahead, src, stage0);
 
-    int at_row = -1;
+    int at_row = -1, turn = 0;
     bool in_row = false;
     F2 acc2[NCH], acck[NCH];
     float wn[NCH], kb[NCH];
     bool has[NCH];
     #pragma unroll
-    for (int j = 0; j < NCH; ++j) has[j] = s.ty + j * a.TY < a.Cg;
+    for (int j = 0; j < NCH; ++j) has[j] = s.ty + j * a.TY < g.n;
     auto flush = [&] {
-        const int share = blockIdx.x - (int)((int64_t)(at_row / a.Z) * a.tiles / a.per);
-        float *p0 = a.part + share * NC + (int64_t)(at_row + s.z) * a.Cg + s.ty;
+        const int share = walker - (int)((int64_t)(at_row / a.Z) * a.tiles / a.per);
+        float *p0 = a.part + share * NC + (int64_t)(at_row + s.z) * a.Cg + g.c0 + s.ty;
         #pragma unroll
         for (int j = 0; j < NCH; ++j)
-            if (j * a.TY < a.Cg) {
+            if (j * a.TY < g.n) {
                 const float2 f2v = parts(acc2[j]), fkv = parts(acck[j]);
                 float s2 = f2v.x + f2v.y, sk = fkv.x + fkv.y;
                 for (int m = 1; m < a.TX; m <<= 1) {
@@ -465,20 +514,24 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
             }
     };
     for (int t = t0; t < t1; ++t, w.next(a)) {
-        const int buf = (t - t0) & 1;
-        ptx::cp_async_wait_group<0>();
-        __syncthreads();
-        if (t + 1 < t1) {
+        const int buf = (t - t0) & (a.stages - 1);
+        if (a.stages == 1 && t > t0) {
+            __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
-            ptx::cp_async_commit();
+            stage_tile<T, NT>(a, g, ahead, src, stage0);
+        }
+        ptx::cp_async_wait_all();
+        __syncthreads();
+        if (a.stages == 2 && t + 1 < t1) {
+            ahead.next(a);
+            stage_tile<T, NT>(a, g, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
         }
         const uint8_t *st = smem + buf * NT * a.tensor;
         if (at_row != w.row0) {
             if (at_row >= 0) flush();
             at_row = w.row0;
             in_row = w.row0 + s.z < a.rows;
-            const int row = w.row0 + s.z, ch0 = (row % a.G) * a.Cg + s.ty;
+            const int row = w.row0 + s.z, ch0 = (row % a.G) * a.Cg + g.c0 + s.ty;
             #pragma unroll
             for (int j = 0; j < NCH; ++j) {
                 acc2[j] = acck[j] = f2(0.f);
@@ -487,13 +540,13 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
                     if (NEXT) wn[j] = a.w2 ? a.w2[ch0 + j * a.TY] : 1.f;
                     if (POST) kb[j] = branch_coeff(a, ch0 + j * a.TY);
                     if (POST && a.gate == GCONV_GATE_CHANNEL)
-                        kb[j] *= gate_value(to_f(static_cast<const T *>(a.z)[(int64_t)row * a.Cg + s.ty + j * a.TY]), a.act);
+                        kb[j] *= gate_value(to_f(static_cast<const T *>(a.z)[(int64_t)row * a.Cg + g.c0 + s.ty + j * a.TY]), a.act);
                 }
             }
         }
         const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + s.apart < a.P;
-        const uint32_t m0 = misfit<T>(a, s, w);
-        const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)s.c0) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
+        const uint32_t m0 = misfit<T>(a, g, s, w);
+        const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
         int at[NCH];
         #pragma unroll
         for (int j = 0; j < NCH; ++j) at[j] = staged_at<T>(s, m0, j);
@@ -514,7 +567,7 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
                         sum[NP + k] = fma2(x[k], mul2(g[k], f2(wn[j])), sum[NP + k]);
                     }
                 }
-            column_roots<NP, true>(sum, red, a, s.tx, s.ty, s.z);
+            column_roots<NP, true>(sum, red, a, g, turn, s.tx, s.ty, s.z);
             #pragma unroll
             for (int k = 0; k < 2 * NP; ++k) { rm[k] = sum[k]; sum[k] = f2(0.f); }
         }
@@ -555,7 +608,7 @@ __global__ void __launch_bounds__(512) block_bwd_stage_kernel(const BlockArgs a)
                 }
             }
         if (!POST) continue;
-        column_roots<NP, true>(sum, red, a, s.tx, s.ty, s.z);
+        column_roots<NP, true>(sum, red, a, g, turn, s.tx, s.ty, s.z);
         #pragma unroll
         for (int j = 0; j < NCH; ++j)
             if (has[j]) {

@@ -52,6 +52,27 @@ void launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned block, s
     cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The same in clusters of `cluster` blocks.
+template <typename... KArgs, typename... Args>
+void launch_dependent_clusters(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, int cluster,
+                               cudaStream_t s, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 long long wait_limit();
 unsigned int *device_error_word();   // device address of the error word, nullptr on failure
 int forced_path();

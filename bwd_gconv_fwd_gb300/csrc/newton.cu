@@ -293,7 +293,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     constexpr int blocks = BN / 64;                         // 32-column blocks a drain warp
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = ptx::cluster_rank();
     const uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
     const int units = p.batch * p.tiles_per * p.splits;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -327,7 +327,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
-    cluster_sync();
+    ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
     ptx::griddep_wait();
@@ -353,7 +353,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     // the pair's stage is one barrier in the first CTA
                     const uint32_t local = ptx::smem_u32(&bar_full[slot]);
                     if (rank == 0 && pi == 0) ptx::mbar_arrive_expect_tx(local, 2 * boxes * 8192);
-                    const uint32_t fb = map_to(local, 0);
+                    const uint32_t fb = ptx::map_to(local, 0);
                     const uint32_t dst = sbase + slot * kStageBytes + pi * 8192;
                     if (pi >= 2 && b_mn) tma_load_pair(dst, &tmB, r, kb * kBK, bt, fb);
                     else tma_load_pair(dst, pi < 2 ? &tmA : &tmB, kb * kBK, r, bt, fb);
@@ -541,7 +541,7 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     }
     __syncwarp();
     ptx::tc_fence_before();
-    cluster_sync();   // no CTA leaves while the other may signal it or use its operands
+    ptx::cluster_sync();   // no CTA leaves while the other may signal it or use its operands
     if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
 
@@ -678,20 +678,8 @@ gconv_status launch_tiles(const CUtensorMap &tA, const CUtensorMap &tB, NewtonPa
         attr[dev] = true;
     }
     const int64_t units = (int64_t)p.batch * p.tiles_per * p.splits;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(units, num_sms() / 2));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = 2;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    cudaLaunchKernelEx(&cfg, newton_gemm_kernel<MODE, BN>, tA, tB, p);
+    launch_dependent_clusters(newton_gemm_kernel<MODE, BN>, 2 * (unsigned)std::min<int64_t>(units, num_sms() / 2), kThreads, kSmem,
+                              2, st, tA, tB, p);
     if (MODE == kGram && p.splits > 1)   // 64 BN / 8 warps a tile
         launch_dependent(newton_sum_kernel<BN>, (unsigned)(p.batch * p.tiles_per * (BN / 8)), 256, 0, st, p);
     return GCONV_OK;

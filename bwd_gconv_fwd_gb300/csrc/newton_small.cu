@@ -55,7 +55,7 @@ __device__ __forceinline__ void st_cluster_f(uint32_t addr, float v)
 __device__ __forceinline__ void send(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar, uint32_t rank)
 {
     asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(map_to(to, rank)), "r"(from), "r"(bytes), "r"(map_to(bar, rank)) : "memory");
+                 ::"r"(ptx::map_to(to, rank)), "r"(from), "r"(bytes), "r"(ptx::map_to(bar, rank)) : "memory");
 }
 
 // Byte offset of the 16-byte piece that holds column `col` of row `row`: 64-column chunks of
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     __shared__ float warp_sum[kSmallWarps], rank_sum[kMaxCluster];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t CS = (uint32_t)p.cluster, rank = cluster_rank();
+    const uint32_t CS = (uint32_t)p.cluster, rank = ptx::cluster_rank();
     const int mat = blockIdx.x / p.cluster;
     const int c0 = (int)rank * p.slice;
     const int width = min(p.slice, max(0, p.n - c0));       // columns of X here
@@ -243,13 +243,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_sh;
-    cluster_sync();   // the others' shared memory may be written from here on
+    ptx::cluster_sync();   // the others' shared memory may be written from here on
     if (tid < (int)CS) {
         float t = 0.f;
         for (int k = 0; k < kSmallWarps; ++k) t += warp_sum[k];
-        st_cluster_f(map_to(ptx::smem_u32(&rank_sum[rank]), (uint32_t)tid), t);
+        st_cluster_f(ptx::map_to(ptx::smem_u32(&rank_sum[rank]), (uint32_t)tid), t);
     }
-    cluster_sync();
+    ptx::cluster_sync();
     float total = 0.f;
     for (uint32_t k = 0; k < CS; ++k) total += rank_sum[k];
     const float inv = kNewtonScale / (sqrtf(total) + p.in.eps);
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     if (CS > 1 && !ok && lane == 0) ptx::mbar_wait(ptx::smem_u32(&bar_rows), (p.steps - 1) & 1, kSmallDrainNs);
     __syncwarp();
     ptx::tc_fence_before();
-    cluster_sync();
+    ptx::cluster_sync();
     if (warp == 0) ptx::tmem_dealloc(tmem, 512);
 }
 

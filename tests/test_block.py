@@ -101,12 +101,12 @@ def up(v):
 
 
 # (N, C, H, W, groups): one position, odd planes, planes of 2, 4 and 8 times an odd number, thin and
-# wide groups, groups past what a thread block holds at once, several rows a block
+# wide groups, groups that take several thread blocks or are walked, several rows a block
 SHAPES = [
     (1, 1, 1, 1, 1), (3, 8, 1, 1, 1), (2, 1000, 1, 1, 1), (5, 96, 1, 1, 2), (2, 5, 3, 3, 5), (2, 12, 1, 7, 4),
     (2, 100, 28, 28, 5), (3, 96, 27, 27, 2), (2, 48, 13, 13, 1), (1, 512, 7, 7, 1), (4, 128, 6, 4, 32), (2, 64, 14, 14, 1),
     (1, 256, 56, 56, 1), (2, 33, 2, 5, 1), (1, 2050, 4, 4, 1), (2, 4200, 1, 3, 1), (1, 9, 1, 4097, 3), (130, 16, 1, 2, 2),
-    (1, 1536, 3, 8, 1), (2, 20, 5, 8, 1),
+    (1, 1536, 3, 8, 1), (2, 20, 5, 8, 1), (3, 1024, 7, 7, 1), (2, 2048, 7, 7, 1), (1, 3001, 5, 5, 1), (1, 40000, 1, 2, 1),
 ]
 
 
