@@ -332,6 +332,47 @@ __device__ __forceinline__ uint32_t misfit(const BlockArgs &a, const Part &g, co
     return (first + (a.flat ? 0u : (uint32_t)s.c0 * (uint32_t)a.P + (uint32_t)w.p0)) * (uint32_t)sizeof(T);
 }
 
+// The channel numbers of the thread's row: the next norm's weight and the branch's coefficient (times
+// the channel gate), 0 where there is no channel.  Every load is issued before the first use, none
+// behind a branch of its own.
+template <typename T, int NCH, bool POST, bool NEXT>
+__device__ __forceinline__ void row_numbers(const BlockArgs &a, const Part &g, const Seat &s, int row, bool in_row,
+                                            const bool (&has)[NCH], float (&wn)[NCH], float (&kb)[NCH])
+{
+    const int ch0 = in_row ? (row % a.G) * a.Cg + g.c0 : 0;
+    const int64_t nc0 = in_row ? (int64_t)row * a.Cg + g.c0 : 0;
+    int at[NCH];
+    float sc[NCH], zc[NCH];
+    #pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        at[j] = in_row && has[j] ? s.ty + j * a.TY : 0;
+        wn[j] = kb[j] = sc[j] = 1.f;
+        zc[j] = 0.f;
+    }
+    if (NEXT && a.w2) {
+        #pragma unroll
+        for (int j = 0; j < NCH; ++j) wn[j] = a.w2[ch0 + at[j]];
+    }
+    if (POST && a.w) {
+        #pragma unroll
+        for (int j = 0; j < NCH; ++j) kb[j] = a.w[ch0 + at[j]];
+    }
+    if (POST && a.s) {
+        #pragma unroll
+        for (int j = 0; j < NCH; ++j) sc[j] = a.s[ch0 + at[j]];
+    }
+    if (POST && a.gate == GCONV_GATE_CHANNEL) {
+        #pragma unroll
+        for (int j = 0; j < NCH; ++j) zc[j] = to_f(static_cast<const T *>(a.z)[nc0 + at[j]]);
+    }
+    #pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        if (POST) kb[j] = __fmul_rn(kb[j], sc[j]);
+        if (POST && a.gate == GCONV_GATE_CHANNEL) kb[j] = __fmul_rn(kb[j], gate_value(zc[j], a.act));
+        if (!(in_row && has[j])) wn[j] = kb[j] = 0.f;
+    }
+}
+
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs a)
 {
@@ -369,6 +410,11 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
             ahead.next(a);
             stage_tile<T, NT>(a, g, ahead, src, stage0);
         }
+        const bool in_row = w.row0 + s.z < a.rows;
+        if (at_row != w.row0) {
+            at_row = w.row0;
+            row_numbers<T, NCH, POST, NEXT>(a, g, s, at_row + s.z, in_row, has, wn, kb);
+        }
         ptx::cp_async_wait_all();
         __syncthreads();
         if (a.stages == 2 && t + 1 < t1) {
@@ -376,24 +422,7 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
             stage_tile<T, NT>(a, g, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
         }
         const uint8_t *st = smem + buf * NT * a.tensor;
-        const bool in_row = w.row0 + s.z < a.rows;
         const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + s.apart < a.P;
-        if (at_row != w.row0) {
-            at_row = w.row0;
-            const int row = w.row0 + s.z, ch0 = (row % a.G) * a.Cg + g.c0 + s.ty;
-            #pragma unroll
-            for (int j = 0; j < NCH; ++j) {
-                kb[j] = wn[j] = 0.f;
-                if (in_row && has[j]) {
-                    if (NEXT) wn[j] = a.w2 ? a.w2[ch0 + j * a.TY] : 1.f;
-                    if (POST) {
-                        kb[j] = branch_coeff(a, ch0 + j * a.TY);
-                        if (a.gate == GCONV_GATE_CHANNEL)
-                            kb[j] = __fmul_rn(kb[j], gate_value(to_f(static_cast<const T *>(a.z)[(int64_t)row * a.Cg + g.c0 + s.ty + j * a.TY]), a.act));
-                    }
-                }
-            }
-        }
         const uint32_t m0 = misfit<T>(a, g, s, w);
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
         int at[NCH];
@@ -520,6 +549,14 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
             ahead.next(a);
             stage_tile<T, NT>(a, g, ahead, src, stage0);
         }
+        if (at_row != w.row0) {
+            if (at_row >= 0) flush();
+            at_row = w.row0;
+            in_row = w.row0 + s.z < a.rows;
+            row_numbers<T, NCH, POST, NEXT>(a, g, s, at_row + s.z, in_row, has, wn, kb);
+            #pragma unroll
+            for (int j = 0; j < NCH; ++j) acc2[j] = acck[j] = f2(0.f);
+        }
         ptx::cp_async_wait_all();
         __syncthreads();
         if (a.stages == 2 && t + 1 < t1) {
@@ -527,23 +564,6 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
             stage_tile<T, NT>(a, g, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
         }
         const uint8_t *st = smem + buf * NT * a.tensor;
-        if (at_row != w.row0) {
-            if (at_row >= 0) flush();
-            at_row = w.row0;
-            in_row = w.row0 + s.z < a.rows;
-            const int row = w.row0 + s.z, ch0 = (row % a.G) * a.Cg + g.c0 + s.ty;
-            #pragma unroll
-            for (int j = 0; j < NCH; ++j) {
-                acc2[j] = acck[j] = f2(0.f);
-                wn[j] = kb[j] = 0.f;
-                if (in_row && has[j]) {
-                    if (NEXT) wn[j] = a.w2 ? a.w2[ch0 + j * a.TY] : 1.f;
-                    if (POST) kb[j] = branch_coeff(a, ch0 + j * a.TY);
-                    if (POST && a.gate == GCONV_GATE_CHANNEL)
-                        kb[j] *= gate_value(to_f(static_cast<const T *>(a.z)[(int64_t)row * a.Cg + g.c0 + s.ty + j * a.TY]), a.act);
-                }
-            }
-        }
         const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + s.apart < a.P;
         const uint32_t m0 = misfit<T>(a, g, s, w);
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
