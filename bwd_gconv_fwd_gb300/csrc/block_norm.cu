@@ -106,11 +106,13 @@ int pow2_up(int v)
     return p;
 }
 
-// Launch shape of the staged kernels: 16 elements a thread in at most 512 threads, as many lanes
-// a channel as that and shared memory leave.  Two tiles stand in shared memory; a channel's
-// positions in one are 32 bytes or more, or the whole plane, for which a group's channels go over
-// as few blocks of a cluster as needed.  Where a cluster of eight is not enough, one tile of 16
-// bytes a channel (its copies then wait for the tile before), or none (the walking kernels).
+// Launch shape of the staged kernels: at most 16 elements a thread and 512 threads, as many lanes
+// a channel as that and shared memory leave.  Two tiles stand in shared memory, a channel's
+// positions in one being 64 bytes, else 32, else (with the channels over a cluster, as small as
+// will do) 32 again, or the whole of a small plane.  Norm of [42,728,28,28] bf16: one block and 16
+// bytes 54 us, two blocks and 32 bytes 42, four and 64 bytes 68: a cluster's barrier costs more
+// than short runs, and both less than sectors read twice.  Last, one tile of 16 bytes a channel
+// in a cluster of eight (its copies wait for the tile before), or the walking kernels.
 bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
     const int tensors = bwd ? (kind == kBlockJoinNext ? 5 : 3) : (kind == kBlockNorm ? 1 : 3), sums = bwd ? 2 : 1;
@@ -123,15 +125,15 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
     const int held = vec > 1 ? vec : 2;   // positions a lane holds
     const int widest = P <= 64 ? pow2_up((P + held - 1) / held) : 32;
 
-    auto fits = [&](int cluster, int TX, int Z, int stages) {
-        const int Cc = (Cg + cluster - 1) / cluster, share = (Cc + stage_nch(vec) - 1) / stage_nch(vec);
+    auto fits = [&](int cluster, int TX, int Z, int stages, int least, int nch) {
+        const int Cc = (Cg + cluster - 1) / cluster, share = (Cc + nch - 1) / nch;
         if ((cluster - 1) * Cc >= Cg) return false;            // a block without channels
         // whole warps a row, or a power of two of rows a warp
         const int TY = TX * share >= 32 || cluster > 1 ? (share + 32 / TX - 1) / (32 / TX) * (32 / TX) : pow2_up(share);
         if (TX * TY * Z > 512) return false;
         s->flat = P <= 64 && held * TX >= P;
         s->PT = held * TX;
-        if (!s->flat && s->PT * es < (stages == 2 ? 32 : 16)) return false;
+        if (!s->flat && s->PT * es < least) return false;
         if (s->flat) {
             s->pieces = 1;
             s->pitch = P * es;
@@ -151,25 +153,37 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
         return true;
     };
     bool found = false;
-    for (int stages = 2; stages >= 1 && !found; --stages)
-        for (int cluster = 1; cluster <= 8 && !found; cluster *= 2)
-            for (int TX = widest; TX >= 1 && !found; TX >>= 1) {
-                int Z = 1;
-                while (cluster == 1 && TX * pow2_up((Cg + stage_nch(vec) - 1) / stage_nch(vec)) * Z < 32) Z *= 2;
-                found = fits(cluster, TX, Z, stages);
-            }
+    // stages, blocks of a cluster, least bytes of a channel
+    const int tries[][3] = {{2, 1, 64}, {2, 1, 32}, {2, 2, 32}, {2, 4, 32}, {2, 8, 32}, {1, 8, 16}};
+    int nch = stage_nch(vec);
+    for (const auto &k : tries)
+        for (int TX = widest; TX >= 1 && !found; TX >>= 1) {
+            int Z = 1;
+            while (k[1] == 1 && TX * pow2_up((Cg + nch - 1) / nch) * Z < 32) Z *= 2;
+            found = fits(k[1], TX, Z, k[0], k[2], nch);
+        }
     if (!found) return false;
     // several rows a block where one gives it few threads
     while (s->cluster == 1 && s->threads * 2 <= 256 && s->Z < rows) {
         const BlockShape kept = *s;
-        if (!fits(1, kept.TX, kept.Z * 2, kept.stages)) { *s = kept; break; }
+        if (!fits(1, kept.TX, kept.Z * 2, kept.stages, 16, nch)) { *s = kept; break; }
+    }
+    // fewer channels a thread where shared memory leaves the SM's threads unused: a tile's chain of
+    // instructions is then shorter
+    auto blocks_an_sm = [&] {
+        return (int)std::max<size_t>(1, std::min<size_t>(kBlockSmem / (s->smem + 1024), resident / s->threads));
+    };
+    while (nch > 1 && s->TX * s->TY >= 32 && 2 * s->threads * blocks_an_sm() <= resident) {
+        const BlockShape kept = *s;
+        if (!fits(kept.cluster, kept.TX, kept.Z, kept.stages, 16, nch / 2)) { *s = kept; break; }
+        nch /= 2;
     }
     s->vec = vec;
     s->lanes2 = pow2_up(s->pieces);
     s->staged = 1;
     s->tiles = s->flat ? 1 : (P + s->PT - 1) / s->PT;
     s->total = (rows + s->Z - 1) / s->Z * s->tiles;
-    const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(kBlockSmem / (s->smem + 1024), resident / s->threads));
+    const int per_sm = blocks_an_sm();
     const int walkers = std::max(1, num_sms() * per_sm / s->cluster);
     s->per = (s->total + walkers - 1) / walkers;
     s->grid = (unsigned)((s->total + s->per - 1) / s->per) * s->cluster;

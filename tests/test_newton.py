@@ -172,3 +172,55 @@ def test_refusals(dev):
                 lambda: gc.gconv_muon_step(g, g, out, lr=float("inf"))):
         with pytest.raises((gc.GconvError, ValueError, TypeError)):
             bad()
+
+
+@pytest.mark.parametrize("shape", [(150, 200, 1, 1), (64, 300, 1, 1), (64, 64, 1, 1)])
+def test_wait_timeout_is_reported_and_recovered(dev, shape):
+    """With a wait limit of zero a device-side wait that is not over at its first poll gives up (a poll
+    may itself last as long as a short product): the call then reports it, else its result is right,
+    and either way the next call, with the limit restored, is right."""
+    g = normal(shape, dev, 11)
+    out = torch.empty_like(g)
+    gc.gconv_orthogonalize(g, out, steps=1)
+    assert gc.gconv_check_device_error() == 0
+    B.gconv_debug_set_wait_limit(0)
+    try:
+        gc.gconv_orthogonalize(g, out, steps=1)
+        status = gc.gconv_check_device_error()
+    finally:
+        B.gconv_debug_set_wait_limit(-1)
+    assert status == B.GCONV_ERR_TIMEOUT or (status == B.GCONV_OK and off(out, orth(g, 1, 1)) <= WELL)
+    gc.gconv_orthogonalize(g, out)
+    assert gc.gconv_check_device_error() == 0
+    assert off(out, orth(g, 1)) <= WELL
+
+
+def test_residual_block_example(dev):
+    """The example's block: its output and every gradient against 64-bit autograd of the same block,
+    and its training.  Eight tensors are rounded to bf16 on the longest path (2^-9 each on
+    average, in root mean square adding to 0.6 %); 3 % is allowed."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "residual_block.py")
+    spec = importlib.util.spec_from_file_location("residual_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    C, G, N, hw = 64, 4, 4, 12
+    net = ex.Block(C, G, dev, 3)
+    x, gate, dy = (normal((N, C, hw, hw), dev, 20 + k, torch.bfloat16, 1.0) for k in range(3))
+    y = net.forward(x, gate)
+    dx, dgate = net.backward(dy)
+    v = {k: t.double().requires_grad_() for k, t in {**net.vec, "x": x, "gate": gate, **{"w_" + k: t for k, t in net.bf16.items()}}.items()}
+    unit = lambda t: t / torch.sqrt((t * t).mean(1, keepdim=True) + 1e-6)  # noqa: E731
+    col = lambda t: t[:, None, None]  # noqa: E731
+    conv = torch.nn.functional.conv2d
+    h = conv(unit(v["x"]) * col(v["norm"]), v["w_mid"], padding=1, groups=G)
+    s = v["x"] + col(v["scale"]) * v["gate"] * torch.sigmoid(v["gate"]) * unit(h) * col(v["weight"])
+    ref = conv(unit(s) * col(v["next"]), v["w_out"])
+    assert off(y, ref.detach()) <= 0.03
+    got = {"x": dx, "gate": dgate, **net.dvec, **{"w_" + k: t for k, t in net.grad.items()}}
+    grads = torch.autograd.grad(ref, list(v.values()), dy.double())
+    for k, g in zip(v, grads):
+        assert off(got[k], g) <= 0.03, k
+    losses = ex.train(steps=30)
+    assert losses[-1] < losses[0] and all(v == v for v in losses)
