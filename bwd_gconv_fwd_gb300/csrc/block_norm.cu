@@ -137,12 +137,12 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
         if (s->flat) {
             s->pieces = 1;
             s->pitch = P * es;
-            s->tensor = (Z * Cc * P * es + 15 + 16 + held * TX * es) & ~15;
+            s->tensor = ((Z * Cc * P * es + 15 + 16 + held * TX * es) & ~15) + kStageZeros;
         } else {
             const bool aligned = (int64_t)P * es % 16 == 0 && s->PT * es % 16 == 0;
             s->pieces = (s->PT * es + 15) / 16 + (aligned ? 0 : 1);
             s->pitch = s->pieces * 16;
-            s->tensor = Z * Cc * s->pitch + 16;
+            s->tensor = Z * Cc * s->pitch + 16 + kStageZeros;
         }
         const size_t width = (size_t)TX * stage_pairs(vec) * sums * 8;
         s->smem = (size_t)stages * tensors * s->tensor;

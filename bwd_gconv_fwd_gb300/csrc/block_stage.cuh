@@ -12,8 +12,9 @@
 // Two forms of a tile: PT positions of every channel of Z rows, or (flat) Z whole rows, which are
 // one run of memory, for planes of at most 64 positions.  A thread holds 16 elements: VEC
 // neighbouring positions (as many as divide P, at most 16 bytes) of 16 / VEC channels, so that an
-// address, a predicate and a channel's weight serve VEC elements; where P is odd, two positions TX
-// apart of 8 channels (VEC = 1).
+// address, a predicate and a channel's weight serve VEC elements; where P is odd, two neighbours
+// read one by one of 8 channels (VEC = 1).  A thread whose share has fewer channels reads zeros kept
+// at the end of each staged tensor instead of branching.
 #pragma once
 
 #include "block_norm.cuh"
@@ -22,6 +23,7 @@ namespace gconv {
 
 constexpr int stage_pairs(int vec) { return vec > 1 ? vec / 2 : 1; }      // pairs of positions a thread holds
 constexpr int stage_nch(int vec) { return 8 / stage_pairs(vec); }         // channels
+constexpr int kStageZeros = 32;                                          // bytes of zeros behind a staged tensor
 
 
 // ---- pairs of fp32 ------------------------------------------------------------------
@@ -61,17 +63,24 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b)
 }
 
 // 1 / (1 + e^-z) of both: the error is that of the base-2 exponential's and the reciprocal's
-// approximations, a few units in the last place.
+// approximations, a few units in the last place.  (Constants stand in single instructions, which
+// take them as immediates; a pair would need registers for them.)
+__device__ __forceinline__ float sigmoid1(float z)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(e + 1.f));
+    return e;
+}
 __device__ __forceinline__ F2 sigmoid2(F2 z)
 {
-    const float2 t = parts(mul2(z, f2(-1.4426950408889634f)));
-    float2 e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-    const float2 d = parts(add2(f2(e.x, e.y), f2(1.f)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(d.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(d.y));
-    return f2(e.x, e.y);
+    const float2 t = parts(z);
+    return f2(sigmoid1(t.x), sigmoid1(t.y));
+}
+__device__ __forceinline__ F2 one_minus(F2 s)
+{
+    const float2 t = parts(s);
+    return f2(1.f - t.x, 1.f - t.y);
 }
 
 // What a full gate does: a template argument, so that the arithmetic is straight-line code.
@@ -146,10 +155,11 @@ __device__ __forceinline__ void stage_tile(const BlockArgs &a, const Part &g, co
 
 // A thread's positions of a staged channel, and their store to a tensor.
 template <typename T, int VEC>
-__device__ __forceinline__ void read_vec(const uint8_t *at, int apart, F2 (&v)[stage_pairs(VEC)])
+__device__ __forceinline__ void read_vec(const uint8_t *at, F2 (&v)[stage_pairs(VEC)])
 {
     if constexpr (VEC == 1) {
-        v[0] = f2(to_f(*reinterpret_cast<const T *>(at)), to_f(*reinterpret_cast<const T *>(at + apart)));
+        const T *q = reinterpret_cast<const T *>(at);
+        v[0] = f2(to_f(q[0]), to_f(q[1]));
     } else {
         const Pack<T, VEC> p = *reinterpret_cast<const Pack<T, VEC> *>(at);
         #pragma unroll
@@ -158,13 +168,13 @@ __device__ __forceinline__ void read_vec(const uint8_t *at, int apart, F2 (&v)[s
 }
 
 template <typename T, int VEC>
-__device__ __forceinline__ void write_vec(void *p, uint32_t i, int apart, const F2 (&v)[stage_pairs(VEC)], bool ok0, bool ok1)
+__device__ __forceinline__ void write_vec(void *p, uint32_t i, const F2 (&v)[stage_pairs(VEC)], bool ok0, bool ok1)
 {
     if constexpr (VEC == 1) {
         const float2 f = parts(v[0]);
         T *q = static_cast<T *>(p) + i;
         if (ok0) from_f(f.x, q);
-        if (ok1) from_f(f.y, q + apart);
+        if (ok1) from_f(f.y, q + 1);
     } else {
         Pack<T, VEC> o;
         #pragma unroll
@@ -290,12 +300,25 @@ __device__ __forceinline__ void column_roots(F2 (&v)[TWO ? 2 * NP : NP], float *
     for (int i = 0; i < N; ++i) v[i].v = done[i * a.TX + tx];
 }
 
+// Zeros at the end of each staged tensor, and in the whole of the first where it has no source.
+template <int NT>
+__device__ __forceinline__ void stage_zeros(const BlockArgs &a, uint8_t *smem, bool first)
+{
+    constexpr int words = kStageZeros / 4;
+    for (int i = threadIdx.x; i < a.stages * NT * words; i += blockDim.x)
+        *reinterpret_cast<uint32_t *>(smem + (i / words + 1) * a.tensor - kStageZeros + (i % words) * 4) = 0;
+    if (first)
+        for (int s = 0; s < a.stages; ++s)
+            for (int i = threadIdx.x * 4; i < a.tensor; i += blockDim.x * 4)
+                *reinterpret_cast<uint32_t *>(smem + s * NT * a.tensor + i) = 0;
+}
+
 // A thread's place: vector tx, channels ty, ty + TY, ... of row z of the tile, and from it the
 // offsets of its first channel and the steps to the next.  (32 bits: the low four bits of a
 // byte address survive, and a tensor has fewer than 2^31 elements.)
 struct Seat {
     int tx, ty, z, pos, c0;
-    int apart, s_first, s_step, m_step;
+    int s_first, s_step, m_step;
     uint32_t e_step;
 };
 
@@ -308,9 +331,8 @@ __device__ __forceinline__ Seat seat(const BlockArgs &a, const Part &g)
     const int ry = threadIdx.x / a.TX;
     s.ty = ry % a.TY;
     s.z = ry / a.TY;
-    s.pos = VEC * s.tx;
+    s.pos = (VEC > 1 ? VEC : 2) * s.tx;
     s.c0 = s.z * g.n + s.ty;
-    s.apart = VEC > 1 ? VEC - 1 : a.TX;
     s.s_first = s.c0 * a.pitch + s.pos * es;
     s.s_step = a.TY * a.pitch;
     s.m_step = a.flat ? 0 : a.TY * a.P * es;
@@ -319,8 +341,9 @@ __device__ __forceinline__ Seat seat(const BlockArgs &a, const Part &g)
 }
 
 template <typename T>
-__device__ __forceinline__ int staged_at(const Seat &s, uint32_t m0, int j)
+__device__ __forceinline__ int staged_at(const BlockArgs &a, const Seat &s, uint32_t m0, int j, bool has)
 {
+    if (!has) return a.tensor - kStageZeros;
     return s.s_first + j * s.s_step + (int)((m0 + (uint32_t)(j * s.m_step)) & 15u);
 }
 
@@ -381,7 +404,6 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
     float *red = reinterpret_cast<float *>(smem + a.stages * NT * a.tensor);
     const Part g(a);
     const Seat s = seat<T, VEC>(a, g);
-    const int apart = s.apart * (int)sizeof(T);
     constexpr bool full = GATE != kGateOff;
     const bool plain = a.act == GCONV_ACT_NONE;
     const char *src[NT];
@@ -396,6 +418,7 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
+    stage_zeros<NT>(a, smem, !src[0]);
     stage_tile<T, NT>(a, g, ahead, src, stage0);
 
     int at_row = -1, turn = 0;
@@ -422,7 +445,7 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
             stage_tile<T, NT>(a, g, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
         }
         const uint8_t *st = smem + buf * NT * a.tensor;
-        const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + s.apart < a.P;
+        const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + 1 < a.P;
         const uint32_t m0 = misfit<T>(a, g, s, w);
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
         int at[NCH];
@@ -431,12 +454,10 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
         for (int k = 0; k < NP; ++k) r[k] = f2(0.f);
         #pragma unroll
         for (int j = 0; j < NCH; ++j) {
-            at[j] = staged_at<T>(s, m0, j);
-            if (has[j]) {
-                read_vec<T, VEC>(st + (POST ? a.tensor : 0) + at[j], apart, o[j]);
-                #pragma unroll
-                for (int k = 0; k < NP; ++k) r[k] = fma2(o[j][k], o[j][k], r[k]);
-            }
+            at[j] = staged_at<T>(a, s, m0, j, has[j]);
+            read_vec<T, VEC>(st + (POST ? a.tensor : 0) + at[j], o[j]);
+            #pragma unroll
+            for (int k = 0; k < NP; ++k) r[k] = fma2(o[j][k], o[j][k], r[k]);
         }
         column_roots<NP, false>(r, red, a, g, turn, s.tx, s.ty, s.z);
         if (POST) {
@@ -444,11 +465,10 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
             #pragma unroll
             for (int k = 0; k < NP; ++k) sum[k] = f2(0.f);
             #pragma unroll
-            for (int j = 0; j < NCH; ++j)
-                if (has[j]) {
+            for (int j = 0; j < NCH; ++j) {
                     F2 x[NP], z[NP];
-                    read_vec<T, VEC>(st + at[j], apart, x);
-                    if (full) read_vec<T, VEC>(st + 2 * a.tensor + at[j], apart, z);
+                    read_vec<T, VEC>(st + at[j], x);
+                    if (full) read_vec<T, VEC>(st + 2 * a.tensor + at[j], z);
                     #pragma unroll
                     for (int k = 0; k < NP; ++k) {
                         F2 kg = f2(kb[j]);
@@ -459,7 +479,7 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
                         o[j][k] = fma2(kg, mul2(o[j][k], r[k]), x[k]);
                         sum[k] = fma2(o[j][k], o[j][k], sum[k]);
                     }
-                    write_vec<T, VEC>(a.out, e0 + j * s.e_step, s.apart, o[j], ok0, ok1);
+                    write_vec<T, VEC>(a.out, e0 + j * s.e_step, o[j], has[j] && ok0, has[j] && ok1);
                 }
             if (!NEXT) continue;
             column_roots<NP, false>(sum, red, a, g, turn, s.tx, s.ty, s.z);
@@ -467,12 +487,11 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
             for (int k = 0; k < NP; ++k) r[k] = sum[k];
         }
         #pragma unroll
-        for (int j = 0; j < NCH; ++j)
-            if (has[j]) {
-                #pragma unroll
-                for (int k = 0; k < NP; ++k) o[j][k] = mul2(o[j][k], mul2(r[k], f2(wn[j])));
-                write_vec<T, VEC>(a.next, e0 + j * s.e_step, s.apart, o[j], ok0, ok1);
-            }
+        for (int j = 0; j < NCH; ++j) {
+            #pragma unroll
+            for (int k = 0; k < NP; ++k) o[j][k] = mul2(o[j][k], mul2(r[k], f2(wn[j])));
+            write_vec<T, VEC>(a.next, e0 + j * s.e_step, o[j], has[j] && ok0, has[j] && ok1);
+        }
     }
 }
 
@@ -497,7 +516,6 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
     float *red = reinterpret_cast<float *>(smem + a.stages * NT * a.tensor);
     const Part g(a);
     const Seat s = seat<T, VEC>(a, g);
-    const int apart = s.apart * (int)sizeof(T);
     constexpr bool full = GATE != kGateOff;
     const bool plain = a.act == GCONV_ACT_NONE;
     const char *src[NT];
@@ -515,6 +533,7 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
+    stage_zeros<NT>(a, smem, !src[0]);
     stage_tile<T, NT>(a, g, ahead, src, stage0);
 
     int at_row = -1, turn = 0;
@@ -564,23 +583,22 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
             stage_tile<T, NT>(a, g, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
         }
         const uint8_t *st = smem + buf * NT * a.tensor;
-        const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + s.apart < a.P;
+        const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + 1 < a.P;
         const uint32_t m0 = misfit<T>(a, g, s, w);
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
         int at[NCH];
         #pragma unroll
-        for (int j = 0; j < NCH; ++j) at[j] = staged_at<T>(s, m0, j);
+        for (int j = 0; j < NCH; ++j) at[j] = staged_at<T>(a, s, m0, j, has[j]);
         F2 d[NCH][NP], sum[2 * NP];
         F2 rm[2 * NP];   // r and m
         #pragma unroll
         for (int k = 0; k < 2 * NP; ++k) sum[k] = f2(0.f);
         if (NEXT) {
             #pragma unroll
-            for (int j = 0; j < NCH; ++j)
-                if (has[j]) {
+            for (int j = 0; j < NCH; ++j) {
                     F2 x[NP], g[NP];
-                    read_vec<T, VEC>(st + iX * a.tensor + at[j], apart, x);
-                    read_vec<T, VEC>(st + iG * a.tensor + at[j], apart, g);
+                    read_vec<T, VEC>(st + iX * a.tensor + at[j], x);
+                    read_vec<T, VEC>(st + iG * a.tensor + at[j], g);
                     #pragma unroll
                     for (int k = 0; k < NP; ++k) {
                         sum[k] = fma2(x[k], x[k], sum[k]);
@@ -593,15 +611,12 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
         }
         F2 sg[NCH][NP];   // the gate's sigmoid, or its value without one
         #pragma unroll
-        for (int j = 0; j < NCH; ++j)
-            if (has[j]) {
-                #pragma unroll
-                for (int k = 0; k < NP; ++k) d[j][k] = f2(0.f);
-                if (a.dout) read_vec<T, VEC>(st + at[j], apart, d[j]);
+        for (int j = 0; j < NCH; ++j) {
+                read_vec<T, VEC>(st + at[j], d[j]);
                 if (NEXT) {
                     F2 x[NP], g[NP], u = f2(0.f);
-                    read_vec<T, VEC>(st + iX * a.tensor + at[j], apart, x);
-                    read_vec<T, VEC>(st + iG * a.tensor + at[j], apart, g);
+                    read_vec<T, VEC>(st + iX * a.tensor + at[j], x);
+                    read_vec<T, VEC>(st + iG * a.tensor + at[j], g);
                     #pragma unroll
                     for (int k = 0; k < NP; ++k) {
                         g[k] = mul2(g[k], rm[k]);
@@ -609,12 +624,12 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
                         u = fma2(g[k], x[k], u);
                     }
                     acc2[j] = add2(acc2[j], live_only<VEC>(u, ok0, ok1));
-                    write_vec<T, VEC>(a.dx, e0 + j * s.e_step, s.apart, d[j], ok0, ok1);
+                    write_vec<T, VEC>(a.dx, e0 + j * s.e_step, d[j], has[j] && ok0, has[j] && ok1);
                 }
                 if (POST) {
                     F2 h[NP], z[NP];
-                    read_vec<T, VEC>(st + iH * a.tensor + at[j], apart, h);
-                    if (full) read_vec<T, VEC>(st + iZ * a.tensor + at[j], apart, z);
+                    read_vec<T, VEC>(st + iH * a.tensor + at[j], h);
+                    if (full) read_vec<T, VEC>(st + iZ * a.tensor + at[j], z);
                     #pragma unroll
                     for (int k = 0; k < NP; ++k) {
                         F2 v = mul2(d[j][k], f2(kb[j]));
@@ -630,19 +645,18 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
         if (!POST) continue;
         column_roots<NP, true>(sum, red, a, g, turn, s.tx, s.ty, s.z);
         #pragma unroll
-        for (int j = 0; j < NCH; ++j)
-            if (has[j]) {
+        for (int j = 0; j < NCH; ++j) {
                 const uint32_t e = e0 + j * s.e_step;
                 F2 h[NP], z[NP], u = f2(0.f);
-                read_vec<T, VEC>(st + iH * a.tensor + at[j], apart, h);
-                if (GATE == kGateSilu) read_vec<T, VEC>(st + iZ * a.tensor + at[j], apart, z);
+                read_vec<T, VEC>(st + iH * a.tensor + at[j], h);
+                if (GATE == kGateSilu) read_vec<T, VEC>(st + iZ * a.tensor + at[j], z);
                 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
                     const F2 dr = mul2(d[j][k], sum[k]), dk = mul2(dr, f2(kb[j]));
                     F2 dh = dk;   // the channel gate is in kb; its own gradient needs the sum without it
                     if (full) {
                         // act'(z): 1; s (1 - s); s (1 + z (1 - s)) = s + g (1 - s)
-                        const F2 rest = fma2(sg[j][k], f2(-1.f), f2(1.f));
+                        const F2 rest = one_minus(sg[j][k]);
                         const F2 g = GATE == kGateSilu ? mul2(z[k], sg[j][k]) : sg[j][k];
                         const F2 dg = GATE == kGateSilu ? fma2(g, rest, sg[j][k]) : plain ? f2(1.f) : mul2(g, rest);
                         sg[j][k] = mul2(mul2(dk, h[k]), dg);   // dz
@@ -654,8 +668,8 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
                     d[j][k] = fma2(h[k], sum[NP + k], dh);
                 }
                 acck[j] = add2(acck[j], live_only<VEC>(u, ok0, ok1));
-                write_vec<T, VEC>(a.dh, e, s.apart, d[j], ok0, ok1);
-                if (full && a.dz) write_vec<T, VEC>(a.dz, e, s.apart, sg[j], ok0, ok1);
+                write_vec<T, VEC>(a.dh, e, d[j], has[j] && ok0, has[j] && ok1);
+                if (full && a.dz) write_vec<T, VEC>(a.dz, e, sg[j], has[j] && ok0, has[j] && ok1);
             }
     }
     if (at_row >= 0) flush();
