@@ -3,6 +3,9 @@
 
 namespace gconv {
 
-void block_bwd_bf16(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st) { launch_t<__nv_bfloat16>(kind, s, a, st); }
+void block_bwd_bf16(int kind, const BlockShape &s, const BlockArgs &a, const StageMaps &maps, cudaStream_t st)
+{
+    launch_t<__nv_bfloat16>(kind, s, a, maps, st);
+}
 
 }  // namespace gconv

@@ -6,8 +6,8 @@ namespace gconv {
 
 namespace {
 
-template <void (*Kernel)(BlockArgs)>
-void launch_staged(const BlockShape &s, const BlockArgs &a, cudaStream_t st)
+template <void (*Kernel)(BlockArgs, StageMaps)>
+void launch_staged(const BlockShape &s, const BlockArgs &a, const StageMaps &maps, cudaStream_t st)
 {
     static bool attr[64] = {};
     int dev = 0;
@@ -16,30 +16,30 @@ void launch_staged(const BlockShape &s, const BlockArgs &a, cudaStream_t st)
         if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem) != cudaSuccess) return;
         attr[dev] = true;
     }
-    launch_dependent_clusters(Kernel, s.grid, s.threads, s.smem, s.cluster, st, a);
+    launch_dependent_clusters(Kernel, s.grid, s.threads, s.smem, s.cluster, st, a, maps);
 }
 
 template <typename T, int VEC>
-void staged(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
+void staged(int kind, const BlockShape &s, const BlockArgs &a, const StageMaps &maps, cudaStream_t st)
 {
     const int gate = a.gate != GCONV_GATE_FULL ? kGateOff : a.act == GCONV_ACT_SILU ? kGateSilu : kGateOther;
-    if (kind == kBlockNorm) launch_staged<block_fwd_stage_kernel<T, VEC, false, true, kGateOff>>(s, a, st);
-    else if (kind == kBlockJoin && gate == kGateOff) launch_staged<block_fwd_stage_kernel<T, VEC, true, false, kGateOff>>(s, a, st);
-    else if (kind == kBlockJoin && gate == kGateSilu) launch_staged<block_fwd_stage_kernel<T, VEC, true, false, kGateSilu>>(s, a, st);
-    else if (kind == kBlockJoin) launch_staged<block_fwd_stage_kernel<T, VEC, true, false, kGateOther>>(s, a, st);
-    else if (gate == kGateOff) launch_staged<block_fwd_stage_kernel<T, VEC, true, true, kGateOff>>(s, a, st);
-    else if (gate == kGateSilu) launch_staged<block_fwd_stage_kernel<T, VEC, true, true, kGateSilu>>(s, a, st);
-    else launch_staged<block_fwd_stage_kernel<T, VEC, true, true, kGateOther>>(s, a, st);
+    if (kind == kBlockNorm) launch_staged<block_fwd_stage_kernel<T, VEC, false, true, kGateOff>>(s, a, maps, st);
+    else if (kind == kBlockJoin && gate == kGateOff) launch_staged<block_fwd_stage_kernel<T, VEC, true, false, kGateOff>>(s, a, maps, st);
+    else if (kind == kBlockJoin && gate == kGateSilu) launch_staged<block_fwd_stage_kernel<T, VEC, true, false, kGateSilu>>(s, a, maps, st);
+    else if (kind == kBlockJoin) launch_staged<block_fwd_stage_kernel<T, VEC, true, false, kGateOther>>(s, a, maps, st);
+    else if (gate == kGateOff) launch_staged<block_fwd_stage_kernel<T, VEC, true, true, kGateOff>>(s, a, maps, st);
+    else if (gate == kGateSilu) launch_staged<block_fwd_stage_kernel<T, VEC, true, true, kGateSilu>>(s, a, maps, st);
+    else launch_staged<block_fwd_stage_kernel<T, VEC, true, true, kGateOther>>(s, a, maps, st);
 }
 
 template <typename T>
-void launch_t(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
+void launch_t(int kind, const BlockShape &s, const BlockArgs &a, const StageMaps &maps, cudaStream_t st)
 {
     if (s.staged) {
-        if (s.vec == 1) staged<T, 1>(kind, s, a, st);
-        else if (s.vec == 2) staged<T, 2>(kind, s, a, st);
-        else if (s.vec == 4) staged<T, 4>(kind, s, a, st);
-        else if constexpr (sizeof(T) == 2) staged<T, 8>(kind, s, a, st);
+        if (s.vec == 1) staged<T, 1>(kind, s, a, maps, st);
+        else if (s.vec == 2) staged<T, 2>(kind, s, a, maps, st);
+        else if (s.vec == 4) staged<T, 4>(kind, s, a, maps, st);
+        else if constexpr (sizeof(T) == 2) staged<T, 8>(kind, s, a, maps, st);
     } else if (kind == kBlockNorm)
         launch_dependent(block_fwd_walk_kernel<T, false, true>, s.grid, s.threads, s.smem, st, a);
     else if (kind == kBlockJoin)

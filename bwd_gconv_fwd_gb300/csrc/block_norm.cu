@@ -116,12 +116,12 @@ int pow2_up(int v)
 bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
     const int tensors = bwd ? (kind == kBlockJoinNext ? 5 : 3) : (kind == kBlockNorm ? 1 : 3), sums = bwd ? 2 : 1;
-    // threads an SM's registers hold: 128 a thread in the gradient of a join, 64 elsewhere
-    const int resident = bwd && kind != kBlockNorm ? 512 : 1024;
     const int P = b.H * b.W, Cg = b.C / b.groups, rows = b.N * b.groups;
     const int es = dt == GCONV_BF16 ? 2 : 4;
     int vec = 16 / es;
     while (P % vec) vec >>= 1;
+    // threads of a block, and those an SM's registers hold: one block in the gradient of a join, else two
+    const int most = stage_threads(vec), resident = bwd && kind != kBlockNorm ? most : 2 * most;
     const int held = vec > 1 ? vec : 2;   // positions a lane holds
     const int widest = P <= 64 ? pow2_up((P + held - 1) / held) : 32;
 
@@ -130,23 +130,29 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
         if ((cluster - 1) * Cc >= Cg) return false;            // a block without channels
         // whole warps a row, or a power of two of rows a warp
         const int TY = TX * share >= 32 || cluster > 1 ? (share + 32 / TX - 1) / (32 / TX) * (32 / TX) : pow2_up(share);
-        if (TX * TY * Z > 512) return false;
+        if (TX * TY * Z > most) return false;
         s->flat = P <= 64 && held * TX >= P;
         s->PT = held * TX;
         if (!s->flat && s->PT * es < least) return false;
+        s->boxes = s->box_rows = s->pieces = 0;
+        const bool aligned = (int64_t)P * es % 16 == 0 && s->PT * es % 16 == 0;
         if (s->flat) {
-            s->pieces = 1;
             s->pitch = P * es;
-            s->tensor = ((Z * Cc * P * es + 15 + 16 + held * TX * es) & ~15) + kStageZeros;
+            s->tensor = Z * Cc * P * es + 16 + 16 + held * TX * es;
+        } else if (aligned && s->PT * es >= 64) {
+            s->pitch = s->PT * es;
+            s->boxes = (Z * Cc + 255) / 256;
+            s->box_rows = ((Z * Cc + s->boxes - 1) / s->boxes + 1) & ~1;   // 128 bytes or a multiple: the next box follows
+            s->tensor = s->boxes * s->box_rows * s->pitch;
         } else {
-            const bool aligned = (int64_t)P * es % 16 == 0 && s->PT * es % 16 == 0;
             s->pieces = (s->PT * es + 15) / 16 + (aligned ? 0 : 1);
             s->pitch = s->pieces * 16;
-            s->tensor = Z * Cc * s->pitch + 16 + kStageZeros;
+            s->tensor = Z * Cc * s->pitch + 16;
         }
-        const size_t width = (size_t)TX * stage_pairs(vec) * sums * 8;
-        s->smem = (size_t)stages * tensors * s->tensor;
-        if (TX * TY > 32 || cluster > 1) s->smem += Z * (TX * TY / 32 + 1) * width + (cluster > 1 ? 2 * cluster * width : 0);
+        s->tensor = (s->tensor + kStageZeros + 127) & ~127;
+        const size_t width = (size_t)TX * stage_pairs(vec) * sums * 8;   // of column_roots
+        s->smem = 128 + (size_t)stages * tensors * s->tensor;
+        if (TX * TY > 32 || cluster > 1) s->smem += 2 * (Z * (TX * TY / 32) + (cluster > 1 ? cluster : 0)) * width;
         if (s->smem > kBlockSmem) return false;
         s->TX = TX; s->TY = TY; s->Z = Z; s->stages = stages; s->cluster = cluster; s->Cc = Cc;
         s->threads = TX * TY * Z;
@@ -164,7 +170,7 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
         }
     if (!found) return false;
     // several rows a block where one gives it few threads
-    while (s->cluster == 1 && s->threads * 2 <= 256 && s->Z < rows) {
+    while (s->cluster == 1 && s->threads * 2 <= most / 2 && s->Z < rows) {
         const BlockShape kept = *s;
         if (!fits(1, kept.TX, kept.Z * 2, kept.stages, 16, nch)) { *s = kept; break; }
     }
@@ -179,7 +185,6 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
         nch /= 2;
     }
     s->vec = vec;
-    s->lanes2 = pow2_up(s->pieces);
     s->staged = 1;
     s->tiles = s->flat ? 1 : (P + s->PT - 1) / s->PT;
     s->total = (rows + s->Z - 1) / s->Z * s->tiles;
@@ -216,11 +221,34 @@ void block_args(const gconv_block &b, gconv_dtype dt, const BlockShape &s, Block
     a->P = b.H * b.W;
     a->TX = s.TX; a->TY = s.TY; a->Z = s.Z; a->tiles = s.tiles; a->splits = s.splits;
     a->PT = s.PT; a->flat = s.flat; a->per = s.per; a->total = s.total; a->stages = s.stages; a->cluster = s.cluster; a->Cc = s.Cc;
-    a->pitch = s.pitch; a->tensor = s.tensor; a->pieces = s.pieces; a->lanes2 = s.lanes2;
+    a->pitch = s.pitch; a->tensor = s.tensor; a->boxes = s.boxes; a->box_rows = s.box_rows;
+    a->box_bytes = s.box_rows * s.pitch;
+    a->pieces = s.pieces; a->lanes2 = pow2_up(s.pieces);
+    a->err = device_error_word();
+    a->wait_ns = (uint64_t)wait_limit();
     a->bytes = (int64_t)b.N * b.C * a->P * (dt == GCONV_BF16 ? 2 : 4);
-    a->whole = a->bytes % 16 == 0;
     a->eps = b.eps; a->inv_cg = 1.f / (float)a->Cg;
     cudaGetLastError();   // clear a stale error: the check after the launches is about this call
+}
+
+// Launches the forward or backward kernel: the tensors' maps are in the order the kernels stage them.
+gconv_status run_block(bool bwd, int kind, const gconv_block &b, gconv_dtype dt, const BlockShape &s, const BlockArgs &a,
+                       cudaStream_t st)
+{
+    const bool next = kind != kBlockJoin, post = kind != kBlockNorm;
+    const void *src[5] = {bwd ? a.dout : a.x};
+    int n = 1;
+    if (bwd && next) { src[n++] = a.x; src[n++] = a.dnext; }
+    if (post) { src[n++] = a.h; src[n++] = a.gate == GCONV_GATE_FULL ? a.z : nullptr; }
+    if (!a.err) return GCONV_ERR_CUDA;
+    StageMaps maps;
+    for (int i = 0; s.boxes > 0 && i < n; ++i)
+        if (src[i] && !encode_matrix_tmap(&maps.m[i], dt, src[i], (uint64_t)a.P, (uint64_t)b.N * b.C, (uint32_t)s.PT,
+                                          (uint32_t)s.box_rows))
+            return GCONV_ERR_CUDA;
+    if (bwd) (dt == GCONV_BF16 ? block_bwd_bf16 : block_bwd_f32)(kind, s, a, maps, st);
+    else (dt == GCONV_BF16 ? block_fwd_bf16 : block_fwd_f32)(kind, s, a, maps, st);
+    return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA;
 }
 
 size_t block_ws(const gconv_block &b, gconv_dtype dt)
@@ -234,8 +262,6 @@ size_t block_ws(const gconv_block &b, gconv_dtype dt)
     }
     return most;
 }
-
-gconv_status done() { return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA; }
 
 // dw2, dw, ds, dz of an empty batch: sums over no terms
 gconv_status zero(float *p, int n, cudaStream_t st)
@@ -268,8 +294,7 @@ gconv_status gconv_norm_fwd(const gconv_block *block, gconv_dtype dtype, const v
     BlockArgs a{};
     block_args(*block, dtype, s, &a);
     a.x = x; a.w2 = weight; a.next = y;
-    (dtype == GCONV_BF16 ? block_fwd_bf16 : block_fwd_f32)(kBlockNorm, s, a, static_cast<cudaStream_t>(stream));
-    return done();
+    return run_block(false, kBlockNorm, *block, dtype, s, a, static_cast<cudaStream_t>(stream));
 }
 
 gconv_status gconv_join_fwd(const gconv_block *block, gconv_dtype dtype, const void *res, const void *h,
@@ -290,8 +315,7 @@ gconv_status gconv_join_fwd(const gconv_block *block, gconv_dtype dtype, const v
     block_args(*block, dtype, s, &a);
     a.gate = block->gate; a.act = block->act;
     a.x = res; a.h = h; a.z = gate; a.w = weight; a.s = scale; a.w2 = next_weight; a.out = out; a.next = next;
-    (dtype == GCONV_BF16 ? block_fwd_bf16 : block_fwd_f32)(kind, s, a, static_cast<cudaStream_t>(stream));
-    return done();
+    return run_block(false, kind, *block, dtype, s, a, static_cast<cudaStream_t>(stream));
 }
 
 static gconv_status finish(const gconv_block &b, gconv_dtype dt, const BlockShape &s, const BlockArgs &a, int next, int post,
@@ -306,7 +330,7 @@ static gconv_status finish(const gconv_block &b, gconv_dtype dt, const BlockShap
     const unsigned grid = (unsigned)((b.C + kFinChannels - 1) / kFinChannels);
     if (dt == GCONV_BF16) launch_dependent(block_finish_kernel<__nv_bfloat16>, grid, kFinChannels * kFinLanes, 0, st, f);
     else launch_dependent(block_finish_kernel<float>, grid, kFinChannels * kFinLanes, 0, st, f);
-    return done();
+    return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA;
 }
 
 gconv_status gconv_norm_bwd(const gconv_block *block, gconv_dtype dtype, const void *x, const float *weight,
@@ -327,8 +351,8 @@ gconv_status gconv_norm_bwd(const gconv_block *block, gconv_dtype dtype, const v
     block_args(*block, dtype, s, &a);
     a.x = x; a.w2 = weight; a.dnext = dy; a.dout = dres; a.dx = dx;
     a.part = static_cast<float *>(workspace);
-    (dtype == GCONV_BF16 ? block_bwd_bf16 : block_bwd_f32)(kBlockNorm, s, a, st);
-    if (!dweight) return done();
+    const gconv_status r = run_block(true, kBlockNorm, *block, dtype, s, a, st);
+    if (r != GCONV_OK || !dweight) return r;
     return finish(*block, dtype, s, a, 1, 0, dweight, nullptr, nullptr, nullptr, st);
 }
 
@@ -361,9 +385,10 @@ gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const v
     a.dout = dout; a.dnext = dnext; a.dx = dres; a.dh = dh;
     a.dz = block->gate == GCONV_GATE_FULL ? dgate : nullptr;
     a.part = static_cast<float *>(workspace);
-    (dtype == GCONV_BF16 ? block_bwd_bf16 : block_bwd_f32)(kind, s, a, st);
+    const gconv_status r = run_block(true, kind, *block, dtype, s, a, st);
+    if (r != GCONV_OK) return r;
     float *dzc = block->gate == GCONV_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr;
-    if (!dweight && !dscale && !dnext_weight && !dzc) return done();
+    if (!dweight && !dscale && !dnext_weight && !dzc) return GCONV_OK;
     return finish(*block, dtype, s, a, dnext != nullptr, 1, dnext_weight, dweight, dscale, dzc, st);
 }
 

@@ -30,9 +30,13 @@ struct BlockArgs {
     int stages;               // tiles in shared memory: 2, or 1
     int cluster, Cc;          // blocks that share a group's channels, and how many each has
     int pitch, tensor;        // bytes of a staged channel, of a staged tensor
-    int pieces, lanes2;       // 16-byte pieces of a channel, and the power of two threads for them
+    // a tile of a tensor as boxes of its map, as 16-byte pieces of each channel (a power of two threads
+    // for them), or (neither) as one run of memory
+    int boxes, box_rows, box_bytes;
+    int pieces, lanes2;
     int64_t bytes;            // of a whole tensor
-    int whole;                // bytes is a multiple of 16
+    unsigned int *err;
+    uint64_t wait_ns;
     int gate, act;
     float eps, inv_cg;
     const void *x, *h, *z;    // x: norm input / join residual (forward), join `out` (backward)
@@ -50,6 +54,9 @@ __host__ __device__ __forceinline__ int column_shares(int TY)
     while (s * s * 4 <= TY) s <<= 1;
     return s;
 }
+
+// The tensors of a staged launch as [N C][P] matrices, for tiles that are boxes of them.
+struct StageMaps { CUtensorMap m[5]; };
 
 template <typename T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const void *p, int64_t i)

@@ -1,11 +1,15 @@
 // block_stage.cuh -- the block norm / join kernels for groups whose tiles fit in shared memory
-// twice (or once): while a block computes one tile, the next lands by 16-byte asynchronous copies.
+// twice (or once): while a block computes one tile, the next lands by asynchronous copies.
 //
 // These operators do 4 to 40 operations an element against 4 to 16 bytes, so the memory is the
 // limit as long as enough of it is in flight: a whole tile of every input here (40 to 100 KB an
-// SM), where loads into registers end with each tile's reduction.  A copy moves aligned 16-byte
-// pieces whatever the plane's size: a channel whose positions start off a 16-byte boundary is
-// copied from the boundary before it, and read from where it starts in shared memory.
+// SM), where loads into registers end with each tile's reduction.  Where planes are multiples of 16
+// bytes and a channel's share of a tile 64 bytes or more, a tile of a tensor is a few boxes of a
+// tensor map, and whole rows are one bulk copy: one thread starts them.  Else the threads copy
+// aligned 16-byte pieces, each channel from the boundary before its positions, and read it from
+// where they start.  (Such pieces took 3000 of the 11000 cycles of a tile of 256 channels x 32
+// positions x 5 tensors, on the threads' own time.  Boxes of 32 bytes a row and bulk copies of one
+// channel each are slower still: norm of [42,728,28,28] 64 us against 42, gradients at 7 x 7 48 against 33.)
 // What is left is the number of instructions, so two positions go through each arithmetic
 // instruction (packed fp32 pairs) and every index is 32 bits and steps by constants.
 //
@@ -21,8 +25,14 @@
 
 namespace gconv {
 
+// Elements a thread holds of a tile, and threads of a block, at most.  What a thread does for a tile
+// beside its elements (two column sums, places, barriers) is most of the time when it has few: the
+// gradient of a join of [64,256,56,56] bf16 took WHAT with 8 in 1024 threads, 16 in 512 and 32 in 256.
+constexpr int stage_elements(int vec) { return vec >= 4 ? 32 : 16; }
+constexpr int stage_threads(int vec) { return vec >= 4 ? 256 : 512; }
 constexpr int stage_pairs(int vec) { return vec > 1 ? vec / 2 : 1; }      // pairs of positions a thread holds
-constexpr int stage_nch(int vec) { return 8 / stage_pairs(vec); }         // channels
+constexpr int stage_nch(int vec) { return stage_elements(vec) / 2 / stage_pairs(vec); }   // channels
+constexpr uint64_t kStageDrainNs = 1000000000ull;
 constexpr int kStageZeros = 32;                                          // bytes of zeros behind a staged tensor
 
 
@@ -119,38 +129,61 @@ struct Tile {
     }
 };
 
-// Starts the copies of one tile of NT tensors to `dst` (a.tensor bytes each; a null tensor is skipped).
+// Starts the copies of one tile of NT tensors to `dst` (a.tensor bytes each; a null tensor is
+// skipped).  Boxes and runs complete `full`, at which every thread arrives; pieces are the threads' own.
 template <typename T, int NT>
-__device__ __forceinline__ void stage_tile(const BlockArgs &a, const Part &g, const Tile &w, const char *const (&src)[NT],
-                                           uint32_t dst)
+__device__ __forceinline__ void stage_tile(const BlockArgs &a, const StageMaps &maps, const Part &g, const Tile &w,
+                                           const char *const (&src)[NT], uint8_t *dst, uint64_t *full)
 {
     constexpr int es = (int)sizeof(T);
+    const uint32_t bar = ptx::smem_u32(full), to0 = ptx::smem_u32(dst);
     const int rows = min(a.Z, a.rows - w.row0) * g.n;          // channels
     const int64_t first = ((int64_t)w.row0 * a.Cg + g.c0) * a.P * es;
-    auto copy = [&](uint32_t to, int64_t from) {
-        // a piece that a tensor's end cuts is read up to it
-        const uint32_t n = a.whole ? 16u : (uint32_t)min((int64_t)16, a.bytes - from);
-        #pragma unroll
-        for (int i = 0; i < NT; ++i)
-            if (src[i]) ptx::cp_async16(to + i * a.tensor, src[i] + from, n);
-    };
-    if (a.flat) {
-        const int64_t lo = first & ~(int64_t)15;
-        const int len = (int)(first - lo) + rows * a.P * es;
-        for (int i = threadIdx.x * 16; i < len; i += blockDim.x * 16) copy(dst + i, lo + i);
-    } else {
-        const int k = threadIdx.x & (a.lanes2 - 1);
-        int c = threadIdx.x / a.lanes2;
-        const int step = blockDim.x / a.lanes2, len = min(a.PT, a.P - w.p0) * es;
-        if (k >= a.pieces) return;
+    if (a.pieces > 0) {
+        // aligned 16-byte pieces, a power of two of threads a channel; a piece that the tensor's end
+        // cuts is read up to it
+        const int k = threadIdx.x & (a.lanes2 - 1), step = blockDim.x / a.lanes2, len = min(a.PT, a.P - w.p0) * es;
+        int c = k < a.pieces ? (int)threadIdx.x / a.lanes2 : rows;
         int64_t at = first + ((int64_t)c * a.P + w.p0) * es;
         const int64_t hop = (int64_t)step * a.P * es;
         #pragma unroll 2
         for (; c < rows; c += step, at += hop) {
             const int off = 16 * k - (int)(at & 15);           // of the piece, from the channel's first position
-            if (off < len) copy(dst + c * a.pitch + 16 * k, at + off);
+            if (off >= len) continue;
+            const uint32_t n = (uint32_t)min((int64_t)16, a.bytes - (at + off));
+            #pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (src[i]) ptx::cp_async16(to0 + i * a.tensor + c * a.pitch + 16 * k, src[i] + at + off, n);
         }
+        ptx::cp_async_commit();
+        return;
     }
+    uint32_t bytes = 0;
+    if (threadIdx.x == 0 && a.boxes > 0) {
+        #pragma unroll
+        for (int i = 0; i < NT; ++i)
+            if (src[i])
+                for (int k = 0; k < a.boxes; ++k) {
+                    ptx::tma_load_2d(to0 + i * a.tensor + k * a.box_bytes, &maps.m[i], w.p0, w.row0 * a.Cg + g.c0 + k * a.box_rows, bar);
+                    bytes += a.box_bytes;
+                }
+    } else if (threadIdx.x == 0) {
+        // one run of memory, widened to 16-byte boundaries; what of the last piece of a tensor is past its
+        // end is not read, what is before it goes element by element
+        const int64_t lo = first & ~(int64_t)15, end = (first + (int64_t)rows * a.P * es + 15) & ~(int64_t)15;
+        const int64_t stop = end <= a.bytes ? end : a.bytes & ~(int64_t)15;
+        #pragma unroll
+        for (int i = 0; i < NT; ++i)
+            if (src[i]) {
+                if (stop > lo) {
+                    ptx::bulk_g2s(to0 + i * a.tensor, src[i] + lo, (uint32_t)(stop - lo), bar);
+                    bytes += (uint32_t)(stop - lo);
+                }
+                for (int64_t at = max(lo, stop); end > a.bytes && at < a.bytes; at += es)
+                    *reinterpret_cast<T *>(dst + i * a.tensor + (int)(at - lo)) = *reinterpret_cast<const T *>(src[i] + at);
+            }
+    }
+    ptx::mbar_arrive_expect_tx(bar, bytes);
 }
 
 // A thread's positions of a staged channel, and their store to a tensor.
@@ -193,18 +226,15 @@ __device__ __forceinline__ F2 shfl_xor2(F2 v, int m)
     return f2(__shfl_xor_sync(0xffffffffu, f.x, m), __shfl_xor_sync(0xffffffffu, f.y, m));
 }
 
-// Adds N values over the lanes that differ in the bits M, M / 2, ..., TX: a lane keeps half of
-// its values at each level while it has two, and stores what it ends with as values base.. of its
-// vector tx.
-template <int N, int M>
-__device__ __forceinline__ void scatter_sum(const F2 (&v)[N], uint64_t *to, int TX, int tx, int base)
+// Adds N values over the lanes that differ in the bits 16, ..., TX: a lane keeps half of its values at
+// each level while it has two, and stores what it ends with as values base.. of its vector tx.
+template <int TX, int N, int M = 16>
+__device__ __forceinline__ void scatter_sum(const F2 (&v)[N], uint64_t *to, int tx, int base)
 {
-    if (M < TX || M == 0) {
+    if constexpr (M < TX || M == 0) {
         #pragma unroll
         for (int i = 0; i < N; ++i) to[(base + i) * TX + tx] = v[i].v;
-        return;
-    }
-    if constexpr (M > 0 && N > 1) {
+    } else if constexpr (N > 1) {
         const bool high = threadIdx.x & M;
         F2 keep[N / 2];
         #pragma unroll
@@ -212,11 +242,17 @@ __device__ __forceinline__ void scatter_sum(const F2 (&v)[N], uint64_t *to, int 
             const F2 mine = high ? v[N / 2 + i] : v[i], theirs = high ? v[i] : v[N / 2 + i];
             keep[i] = add2(mine, shfl_xor2(theirs, M));
         }
-        scatter_sum<N / 2, M / 2>(keep, to, TX, tx, base + (high ? N / 2 : 0));
-    } else if constexpr (M > 0) {
+        scatter_sum<TX, N / 2, M / 2>(keep, to, tx, base + (high ? N / 2 : 0));
+    } else {
         const F2 sum[1] = {add2(v[0], shfl_xor2(v[0], M))};
-        scatter_sum<1, M / 2>(sum, to, TX, tx, base);
+        scatter_sum<TX, 1, M / 2>(sum, to, tx, base);
     }
+}
+
+__device__ __forceinline__ F2 shfl2(F2 v, int lane)
+{
+    const float2 f = parts(v);
+    return f2(__shfl_sync(0xffffffffu, f.x, lane), __shfl_sync(0xffffffffu, f.y, lane));
 }
 
 // From the sum of squares of both positions r = 1 / sqrt(mean + eps), and from the sum of g w t
@@ -231,11 +267,70 @@ __device__ __forceinline__ F2 pull2(const BlockArgs &a, F2 sum, F2 r) { return m
 // Adds v over the TY threads that share a row and a vector and turns the sums into r (the first
 // NP) and m (the second NP, with TWO), the same bits in every thread: within a warp by shuffles
 // that split the values among its lanes, then over a row's warps through shared memory, where
-// one thread a pair of positions takes the roots; in a cluster that thread first sends its sums to
-// the other blocks and adds theirs to them in rank order.  `red`: for each row, N TX pairs a
-// warp and N TX more, then N TX a block of the cluster, twice (`turn` says which; a block writes into
-// another's half only after the barrier that follows the other's reading of it).  The next call may
-// follow at once: it writes what this one reads last only behind its own first barrier.
+// every warp adds all of its row's sums, a lane a few of them, and hands them round: one block
+// barrier in all.  In a cluster a row's first warp sends its block's sums to the other blocks, and every
+// warp adds those in rank order.  `red`: two halves (`turn`: a half is written again only two
+// barriers after it was read), each N TX pairs a warp, and behind them the same for the cluster's blocks.
+template <int NP, bool TWO, int TX>
+__device__ __forceinline__ void column_roots_tx(F2 (&v)[TWO ? 2 * NP : NP], float *red, const BlockArgs &a, const Part &g,
+                                                int &turn, int tx, int ty, int z)
+{
+    constexpr int N = TWO ? 2 * NP : NP, width = N * TX, half = NP * TX, slots = (half + 31) / 32;
+    const int lane = threadIdx.x & 31, warps = a.TY / (32 / TX), in_row = ty * TX + tx;
+    uint64_t *base = reinterpret_cast<uint64_t *>(red);
+    uint64_t *mine = base + (turn * a.Z + z) * warps * width;
+    scatter_sum<TX, N>(v, mine + (in_row >> 5) * width, tx, 0);
+    __syncthreads();
+    const int at = half >= 32 ? lane : lane % half;          // value (and sum of g w t `half` on) of this lane
+    F2 s[slots], u[slots];
+    #pragma unroll
+    for (int k = 0; k < slots; ++k) {
+        s[k] = F2{mine[at + 32 * k]};
+        u[k] = F2{TWO ? mine[half + at + 32 * k] : 0};
+    }
+    #pragma unroll 4
+    for (int w = 1; w < warps; ++w)
+        #pragma unroll
+        for (int k = 0; k < slots; ++k) {
+            s[k] = add2(s[k], F2{mine[w * width + at + 32 * k]});
+            if constexpr (TWO) u[k] = add2(u[k], F2{mine[w * width + half + at + 32 * k]});
+        }
+    if (a.cluster > 1) {
+        uint64_t *others = base + 2 * warps * width + turn * a.cluster * width;
+        if (in_row < 32 && lane < (half < 32 ? half : 32))
+            for (int k = 0; k < a.cluster; ++k)
+                #pragma unroll
+                for (int q = 0; q < slots; ++q) {
+                    const uint32_t to = ptx::map_to(ptx::smem_u32(others + g.rank * width + at + 32 * q), (uint32_t)k);
+                    ptx::st_cluster64(to, s[q].v);
+                    if constexpr (TWO) ptx::st_cluster64(to + half * 8, u[q].v);
+                }
+        __syncwarp();
+        ptx::cluster_sync();
+        #pragma unroll
+        for (int q = 0; q < slots; ++q) {
+            s[q] = F2{others[at + 32 * q]};
+            u[q] = F2{TWO ? others[half + at + 32 * q] : 0};
+            for (int k = 1; k < a.cluster; ++k) {
+                s[q] = add2(s[q], F2{others[k * width + at + 32 * q]});
+                if constexpr (TWO) u[q] = add2(u[q], F2{others[k * width + half + at + 32 * q]});
+            }
+        }
+    }
+    turn ^= 1;
+    #pragma unroll
+    for (int k = 0; k < slots; ++k) {
+        s[k] = root2(a, s[k]);
+        if constexpr (TWO) u[k] = pull2(a, u[k], s[k]);
+    }
+    #pragma unroll
+    for (int i = 0; i < NP; ++i) {   // value i of vector tx is number i TX + tx
+        const int from = (i * TX + tx) & 31, slot = i * TX / 32;
+        v[i] = TX == 32 ? s[slot] : shfl2(s[slot], from);
+        if constexpr (TWO) v[NP + i] = TX == 32 ? u[slot] : shfl2(u[slot], from);
+    }
+}
+
 template <int NP, bool TWO>
 __device__ __forceinline__ void column_roots(F2 (&v)[TWO ? 2 * NP : NP], float *red, const BlockArgs &a, const Part &g, int &turn,
                                              int tx, int ty, int z)
@@ -254,50 +349,14 @@ __device__ __forceinline__ void column_roots(F2 (&v)[TWO ? 2 * NP : NP], float *
         }
         return;
     }
-    const int warps = per_row >> 5, width = N * a.TX, half = NP * a.TX, in_row = ty * a.TX + tx;
-    uint64_t *mine = reinterpret_cast<uint64_t *>(red) + z * (warps + 1) * width;
-    uint64_t *done = mine + warps * width;
-    scatter_sum<N, 16>(v, mine + (in_row >> 5) * width, a.TX, tx, 0);
-    __syncthreads();
-    auto finish = [&](int i, F2 s, F2 u) {
-        const F2 r = root2(a, s);
-        done[i] = r.v;
-        if constexpr (TWO) done[half + i] = pull2(a, u, r).v;
-    };
-    uint64_t *others = mine + (warps + 1) * width + turn * a.cluster * width;
-    for (int i = in_row; i < half; i += per_row) {
-        F2 s{mine[i]}, u{TWO ? mine[half + i] : 0};
-        #pragma unroll 8
-        for (int w = 1; w < warps; ++w) {
-            s = add2(s, F2{mine[w * width + i]});
-            if constexpr (TWO) u = add2(u, F2{mine[w * width + half + i]});
-        }
-        if (a.cluster == 1) {
-            finish(i, s, u);
-        } else {
-            const uint32_t to = ptx::smem_u32(others + g.rank * width + i);
-            for (int k = 0; k < a.cluster; ++k) {
-                ptx::st_cluster64(ptx::map_to(to, (uint32_t)k), s.v);
-                if constexpr (TWO) ptx::st_cluster64(ptx::map_to(to + half * 8, (uint32_t)k), u.v);
-            }
-        }
+    switch (a.TX) {
+    case 32: column_roots_tx<NP, TWO, 32>(v, red, a, g, turn, tx, ty, z); break;
+    case 16: column_roots_tx<NP, TWO, 16>(v, red, a, g, turn, tx, ty, z); break;
+    case 8: column_roots_tx<NP, TWO, 8>(v, red, a, g, turn, tx, ty, z); break;
+    case 4: column_roots_tx<NP, TWO, 4>(v, red, a, g, turn, tx, ty, z); break;
+    case 2: column_roots_tx<NP, TWO, 2>(v, red, a, g, turn, tx, ty, z); break;
+    default: column_roots_tx<NP, TWO, 1>(v, red, a, g, turn, tx, ty, z); break;
     }
-    if (a.cluster > 1) {
-        __syncwarp();
-        ptx::cluster_sync();
-        for (int i = in_row; i < half; i += per_row) {
-            F2 s{others[i]}, u{TWO ? others[half + i] : 0};
-            for (int k = 1; k < a.cluster; ++k) {
-                s = add2(s, F2{others[k * width + i]});
-                if constexpr (TWO) u = add2(u, F2{others[k * width + half + i]});
-            }
-            finish(i, s, u);
-        }
-        turn ^= 1;
-    }
-    __syncthreads();
-    #pragma unroll
-    for (int i = 0; i < N; ++i) v[i].v = done[i * a.TX + tx];
 }
 
 // Zeros at the end of each staged tensor, and in the whole of the first where it has no source.
@@ -355,6 +414,16 @@ __device__ __forceinline__ uint32_t misfit(const BlockArgs &a, const Part &g, co
     return (first + (a.flat ? 0u : (uint32_t)s.c0 * (uint32_t)a.P + (uint32_t)w.p0)) * (uint32_t)sizeof(T);
 }
 
+// Every tile's copies were waited for, unless a wait gave up: then the last ones get the time to land
+// before the block's shared memory is another's.
+__device__ __forceinline__ void stage_drain(const BlockArgs &a, uint64_t *full, bool ok, int tiles)
+{
+    if (__syncthreads_or(!ok) && threadIdx.x == 0)   // pieces are always waited for
+        for (int k = max(0, tiles - a.stages); k < tiles; ++k)
+            ptx::mbar_wait(ptx::smem_u32(&full[k & (a.stages - 1)]), (uint32_t)(k / a.stages) & 1u, kStageDrainNs);
+    __syncthreads();
+}
+
 // The channel numbers of the thread's row: the next norm's weight and the branch's coefficient (times
 // the channel gate), 0 where there is no channel.  Every load is issued before the first use, none
 // behind a branch of its own.
@@ -397,10 +466,12 @@ __device__ __forceinline__ void row_numbers(const BlockArgs &a, const Part &g, c
 }
 
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
-__global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs a)
+__global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
 {
     constexpr int NT = POST ? 3 : 1, NP = stage_pairs(VEC), NCH = stage_nch(VEC);
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-ptx::smem_u32(smem_raw) & 127u);   // boxes land on 128-byte boundaries
+    __shared__ __align__(8) uint64_t bars[2];
     float *red = reinterpret_cast<float *>(smem + a.stages * NT * a.tensor);
     const Part g(a);
     const Seat s = seat<T, VEC>(a, g);
@@ -409,7 +480,29 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
     const char *src[NT];
     src[0] = static_cast<const char *>(a.x);
     if constexpr (POST) { src[1] = static_cast<const char *>(a.h); src[2] = full ? static_cast<const char *>(a.z) : nullptr; }
-    const uint32_t stage0 = ptx::smem_u32(smem);
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(ptx::smem_u32(&bars[0]), blockDim.x);
+        ptx::mbar_init(ptx::smem_u32(&bars[1]), blockDim.x);
+        ptx::fence_mbar_init();
+    }
+    stage_zeros<NT>(a, smem, !src[0]);
+    __syncthreads();
+    bool ok = true;
+    // Waits for a tile's copies; after a wait that gave up, none waits again.
+    auto landed = [&](int t, int t0, int t1) {
+        if (a.pieces > 0) {
+            // the next tile's pieces, started since, may stay in flight
+            if (a.stages == 2 && t + 1 < t1) ptx::cp_async_wait_group<1>();
+            else ptx::cp_async_wait_group<0>();
+            __syncthreads();
+            return;
+        }
+        const int k = t - t0, buf = k & (a.stages - 1);
+        if (ok && !ptx::mbar_wait(ptx::smem_u32(&bars[buf]), (uint32_t)(k / a.stages) & 1u, a.wait_ns)) {
+            ok = false;
+            raise_device_error(a.err, DEVERR_WAIT_TIMEOUT);
+        }
+    };
     const int walker = blockIdx.x / a.cluster;
     const int t0 = walker * a.per, t1 = min(a.total, t0 + a.per);
     Tile w, ahead;
@@ -418,8 +511,7 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
-    stage_zeros<NT>(a, smem, !src[0]);
-    stage_tile<T, NT>(a, g, ahead, src, stage0);
+    stage_tile<T, NT>(a, maps, g, ahead, src, smem, &bars[0]);
 
     int at_row = -1, turn = 0;
     float kb[NCH], wn[NCH];
@@ -431,19 +523,19 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
         if (a.stages == 1 && t > t0) {
             __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, g, ahead, src, stage0);
+            stage_tile<T, NT>(a, maps, g, ahead, src, smem, &bars[0]);
         }
         const bool in_row = w.row0 + s.z < a.rows;
         if (at_row != w.row0) {
             at_row = w.row0;
             row_numbers<T, NCH, POST, NEXT>(a, g, s, at_row + s.z, in_row, has, wn, kb);
         }
-        ptx::cp_async_wait_all();
-        __syncthreads();
         if (a.stages == 2 && t + 1 < t1) {
+            if (t > t0) __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, g, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
+            stage_tile<T, NT>(a, maps, g, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
         }
+        landed(t, t0, t1);
         const uint8_t *st = smem + buf * NT * a.tensor;
         const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + 1 < a.P;
         const uint32_t m0 = misfit<T>(a, g, s, w);
@@ -493,6 +585,7 @@ __global__ void __launch_bounds__(512, 2) block_fwd_stage_kernel(const BlockArgs
             write_vec<T, VEC>(a.next, e0 + j * s.e_step, o[j], has[j] && ok0, has[j] && ok1);
         }
     }
+    stage_drain(a, bars, ok, t1 - t0);
 }
 
 // A pair's sum, without what stands at a dead position.
@@ -509,10 +602,12 @@ __device__ __forceinline__ F2 live_only(F2 v, bool ok0, bool ok1)
 // share those rows.  Dead positions hold what an earlier tile left: they meet no live one but in
 // the channel sums, which leave them out.
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
-__global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(const BlockArgs a)
+__global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
 {
     constexpr int NT = POST && NEXT ? 5 : 3, NP = stage_pairs(VEC), NCH = stage_nch(VEC);
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-ptx::smem_u32(smem_raw) & 127u);   // boxes land on 128-byte boundaries
+    __shared__ __align__(8) uint64_t bars[2];
     float *red = reinterpret_cast<float *>(smem + a.stages * NT * a.tensor);
     const Part g(a);
     const Seat s = seat<T, VEC>(a, g);
@@ -523,7 +618,29 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
     constexpr int iX = 1, iG = 2, iH = NEXT ? 3 : 1, iZ = NEXT ? 4 : 2;
     if constexpr (NEXT) { src[iX] = static_cast<const char *>(a.x); src[iG] = static_cast<const char *>(a.dnext); }
     if constexpr (POST) { src[iH] = static_cast<const char *>(a.h); src[iZ] = full ? static_cast<const char *>(a.z) : nullptr; }
-    const uint32_t stage0 = ptx::smem_u32(smem);
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(ptx::smem_u32(&bars[0]), blockDim.x);
+        ptx::mbar_init(ptx::smem_u32(&bars[1]), blockDim.x);
+        ptx::fence_mbar_init();
+    }
+    stage_zeros<NT>(a, smem, !src[0]);
+    __syncthreads();
+    bool ok = true;
+    // Waits for a tile's copies; after a wait that gave up, none waits again.
+    auto landed = [&](int t, int t0, int t1) {
+        if (a.pieces > 0) {
+            // the next tile's pieces, started since, may stay in flight
+            if (a.stages == 2 && t + 1 < t1) ptx::cp_async_wait_group<1>();
+            else ptx::cp_async_wait_group<0>();
+            __syncthreads();
+            return;
+        }
+        const int k = t - t0, buf = k & (a.stages - 1);
+        if (ok && !ptx::mbar_wait(ptx::smem_u32(&bars[buf]), (uint32_t)(k / a.stages) & 1u, a.wait_ns)) {
+            ok = false;
+            raise_device_error(a.err, DEVERR_WAIT_TIMEOUT);
+        }
+    };
     const int walker = blockIdx.x / a.cluster;
     const int t0 = walker * a.per, t1 = min(a.total, t0 + a.per);
     const int64_t NC = (int64_t)a.rows * a.Cg;
@@ -533,8 +650,7 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
-    stage_zeros<NT>(a, smem, !src[0]);
-    stage_tile<T, NT>(a, g, ahead, src, stage0);
+    stage_tile<T, NT>(a, maps, g, ahead, src, smem, &bars[0]);
 
     int at_row = -1, turn = 0;
     bool in_row = false;
@@ -566,7 +682,7 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
         if (a.stages == 1 && t > t0) {
             __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, g, ahead, src, stage0);
+            stage_tile<T, NT>(a, maps, g, ahead, src, smem, &bars[0]);
         }
         if (at_row != w.row0) {
             if (at_row >= 0) flush();
@@ -576,12 +692,12 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
             #pragma unroll
             for (int j = 0; j < NCH; ++j) acc2[j] = acck[j] = f2(0.f);
         }
-        ptx::cp_async_wait_all();
-        __syncthreads();
         if (a.stages == 2 && t + 1 < t1) {
+            if (t > t0) __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, g, ahead, src, stage0 + (buf ^ 1) * NT * a.tensor);
+            stage_tile<T, NT>(a, maps, g, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
         }
+        landed(t, t0, t1);
         const uint8_t *st = smem + buf * NT * a.tensor;
         const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + 1 < a.P;
         const uint32_t m0 = misfit<T>(a, g, s, w);
@@ -673,6 +789,7 @@ __global__ void __launch_bounds__(512, POST ? 1 : 2) block_bwd_stage_kernel(cons
             }
     }
     if (at_row >= 0) flush();
+    stage_drain(a, bars, ok, t1 - t0);
 }
 
 }  // namespace gconv

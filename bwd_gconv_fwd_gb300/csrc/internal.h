@@ -111,6 +111,11 @@ gconv_status thin_launch(const Geom &g, gconv_dtype dt, gconv_pass pass, const v
 bool encode_rows_tmap(CUtensorMap *m, const void *base, uint64_t rows, uint64_t planes, uint32_t box_rows,
                       uint64_t plane_rows = 0);
 
+// Tensor map of a row-major [rows][cols] bf16 or fp32 matrix (rows a multiple of 16 bytes), boxes of
+// box_rows x box_cols without swizzle; what lies past its ends reads as zero.  False as above.
+bool encode_matrix_tmap(CUtensorMap *m, gconv_dtype dt, const void *base, uint64_t cols, uint64_t rows, uint32_t box_cols,
+                        uint32_t box_rows);
+
 // One training step on the tensor-core kernels with the blocked copies shared between the
 // passes (tc_conv.cu): forward, backward-data, weight gradient (+ bias).  The plan fails
 // for layers whose passes do not all run there on compatible copies.

@@ -331,6 +331,21 @@ bool encode_rows_tmap(CUtensorMap *m, const void *base, uint64_t rows, uint64_t 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_matrix_tmap(CUtensorMap *m, gconv_dtype dt, const void *base, uint64_t cols, uint64_t rows, uint32_t box_cols,
+                        uint32_t box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const uint64_t es = dt == GCONV_BF16 ? 2 : 4;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols * es};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1u, 1u};
+    return fn(m, dt == GCONV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 struct GemmShape {
