@@ -414,6 +414,31 @@ __device__ __forceinline__ uint32_t misfit(const BlockArgs &a, const Part &g, co
     return (first + (a.flat ? 0u : (uint32_t)s.c0 * (uint32_t)a.P + (uint32_t)w.p0)) * (uint32_t)sizeof(T);
 }
 
+// Adds N values over the TX lanes of a vector: at each level a lane keeps half of its values while it
+// has two, so that N and not N log TX values are exchanged; `put` gets each sum once.
+template <int N, int M, typename Put>
+__device__ __forceinline__ void lane_sums(const float (&v)[N], int TX, int tx, int base, const Put &put)
+{
+    if constexpr (M == 0) {
+        #pragma unroll
+        for (int i = 0; i < N; ++i) put(base + i, v[i]);
+    } else if (M >= TX) {
+        lane_sums<N, M / 2>(v, TX, tx, base, put);
+    } else if constexpr (N > 1) {
+        const bool high = tx & M;
+        float keep[N / 2];
+        #pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float mine = high ? v[N / 2 + i] : v[i], theirs = high ? v[i] : v[N / 2 + i];
+            keep[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, M);
+        }
+        lane_sums<N / 2, M / 2>(keep, TX, tx, base + (high ? N / 2 : 0), put);
+    } else {
+        const float sum[1] = {v[0] + __shfl_xor_sync(0xffffffffu, v[0], M)};
+        lane_sums<1, M / 2>(sum, TX, tx, base, put);
+    }
+}
+
 // Every tile's copies were waited for, unless a wait gave up: then the last ones get the time to land
 // before the block's shared memory is another's.
 __device__ __forceinline__ void stage_drain(const BlockArgs &a, uint64_t *full, bool ok, int tiles)
@@ -662,20 +687,20 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
     auto flush = [&] {
         const int share = walker - (int)((int64_t)(at_row / a.Z) * a.tiles / a.per);
         float *p0 = a.part + share * NC + (int64_t)(at_row + s.z) * a.Cg + g.c0 + s.ty;
+        float v[2 * NCH];
         #pragma unroll
-        for (int j = 0; j < NCH; ++j)
-            if (j * a.TY < g.n) {
-                const float2 f2v = parts(acc2[j]), fkv = parts(acck[j]);
-                float s2 = f2v.x + f2v.y, sk = fkv.x + fkv.y;
-                for (int m = 1; m < a.TX; m <<= 1) {
-                    if (NEXT) s2 += __shfl_xor_sync(0xffffffffu, s2, m);
-                    if (POST) sk += __shfl_xor_sync(0xffffffffu, sk, m);
-                }
-                if (s.tx == 0 && in_row && has[j]) {
-                    if (NEXT) p0[j * a.TY] = s2;
-                    if (POST) p0[a.splits * NC + j * a.TY] = sk;
-                }
-            }
+        for (int j = 0; j < NCH; ++j) {
+            const float2 x = parts(acc2[j]), y = parts(acck[j]);
+            v[j] = x.x + x.y;
+            v[NCH + j] = y.x + y.y;
+        }
+        lane_sums<2 * NCH, 16>(v, a.TX, s.tx, 0, [&](int n, float sum) {   // number n: of channel n % NCH
+            const int c = s.ty + (n % NCH) * a.TY;
+            if (!in_row || c >= g.n) return;
+            float *to = p0 + (n % NCH) * a.TY;
+            if (NEXT && n < NCH) to[0] = sum;
+            if (POST && n >= NCH) to[a.splits * NC] = sum;
+        });
     };
     for (int t = t0; t < t1; ++t, w.next(a)) {
         const int buf = (t - t0) & (a.stages - 1);
