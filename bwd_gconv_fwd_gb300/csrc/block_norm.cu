@@ -106,13 +106,13 @@ int pow2_up(int v)
     return p;
 }
 
-// Launch shape of the staged kernels: at most 16 elements a thread and 512 threads, as many lanes
-// a channel as that and shared memory leave.  Two tiles stand in shared memory, a channel's
-// positions in one being 64 bytes, else 32, else (with the channels over a cluster, as small as
-// will do) 32 again, or the whole of a small plane.  Norm of [42,728,28,28] bf16: one block and 16
-// bytes 54 us, two blocks and 32 bytes 42, four and 64 bytes 68: a cluster's barrier costs more
-// than short runs, and both less than sectors read twice.  Last, one tile of 16 bytes a channel
-// in a cluster of eight (its copies wait for the tile before), or the walking kernels.
+// Launch shape of the staged kernels: as many lanes a channel as the elements a thread holds and
+// shared memory leave.  Two tiles stand in shared memory, a channel's positions in one being 64
+// bytes, else 32, in one block, else with the channels over a cluster of two; then one tile in a
+// cluster of two; then larger clusters.  Measured: norm of [42,728,28,28] bf16, one block and 16
+// bytes 56 us, two blocks and 32 bytes 41, four and 64 bytes 61; join backward of [32,1024,7,7]
+// fp32, one tile in two blocks 29 us, two tiles in four 38, in eight 68: a cluster's barrier costs
+// more than copies that wait, and both less than sectors read twice.
 bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
     const int tensors = bwd ? (kind == kBlockJoinNext ? 5 : 3) : (kind == kBlockNorm ? 1 : 3), sums = bwd ? 2 : 1;
@@ -160,7 +160,7 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
     };
     bool found = false;
     // stages, blocks of a cluster, least bytes of a channel
-    const int tries[][3] = {{2, 1, 64}, {2, 1, 32}, {2, 2, 32}, {2, 4, 32}, {2, 8, 32}, {1, 8, 16}};
+    const int tries[][3] = {{2, 1, 64}, {2, 1, 32}, {2, 2, 64}, {2, 2, 32}, {1, 2, 32}, {2, 4, 32}, {1, 4, 32}, {2, 8, 32}, {1, 8, 16}};
     int nch = stage_nch(vec);
     for (const auto &k : tries)
         for (int TX = widest; TX >= 1 && !found; TX >>= 1) {
@@ -344,9 +344,9 @@ gconv_status gconv_norm_bwd(const gconv_block *block, gconv_dtype dtype, const v
     for (const void *p : {x, (const void *)weight, dy, dres, (const void *)dx, (const void *)dweight,
                           (const void *)workspace})
         if (!aligned16(p)) return GCONV_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < block_ws(*block, dtype)) return GCONV_ERR_WORKSPACE;
     BlockShape s;
     block_shape(*block, dtype, true, kBlockNorm, &s);
+    if (!workspace || workspace_bytes < block_ws(*block, dtype)) return GCONV_ERR_WORKSPACE;
     BlockArgs a{};
     block_args(*block, dtype, s, &a);
     a.x = x; a.w2 = weight; a.dnext = dy; a.dout = dres; a.dx = dx;
@@ -374,10 +374,10 @@ gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const v
                           (const void *)dres, (const void *)dh, (const void *)dgate, (const void *)dweight,
                           (const void *)dscale, (const void *)dnext_weight, (const void *)workspace})
         if (!aligned16(p)) return GCONV_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < block_ws(*block, dtype)) return GCONV_ERR_WORKSPACE;
     BlockShape s;
     const int kind = dnext ? kBlockJoinNext : kBlockJoin;
     block_shape(*block, dtype, true, kind, &s);
+    if (!workspace || workspace_bytes < block_ws(*block, dtype)) return GCONV_ERR_WORKSPACE;
     BlockArgs a{};
     block_args(*block, dtype, s, &a);
     a.gate = block->gate; a.act = block->act;
