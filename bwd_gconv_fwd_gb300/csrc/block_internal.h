@@ -7,10 +7,12 @@ namespace gconv {
 
 // The shape of one launch (block_norm.cu, block_shape).
 struct BlockShape {
+    int row;                  // the kernels of block_row.cuh
     int staged;               // the kernels of block_stage.cuh, with:
     int PT, flat, per, total, stages, cluster, Cc, pitch, tensor, boxes, box_rows, pieces;
     int vec;                  // positions a thread holds at once
     int TX, TY, Z, tiles, splits;
+    int images;               // of the channel sums a backward call keeps: N, or 1
     int threads;
     unsigned grid;
     size_t smem;

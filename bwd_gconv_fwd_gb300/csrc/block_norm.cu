@@ -1,6 +1,7 @@
 // block_norm.cu -- extern "C" entry points of the block norm and block join: checks,
 // launch shapes, the channel-gradient finish.  The kernels are in block_norm.cuh.
 #include "block_internal.h"
+#include "block_row.cuh"
 #include "block_stage.cuh"
 
 #include <algorithm>
@@ -196,15 +197,49 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
     return true;
 }
 
+// Launch shape of the row kernels: a lane a vector up to a warp, then row_nv vectors a lane, and fewer
+// again, and fewer rows a block, while there are more SMs than work.
+bool row_shape(const gconv_block &b, gconv_dtype dt, bool bwd, BlockShape *s)
+{
+    const int es = dt == GCONV_BF16 ? 2 : 4, Cg = b.C / b.groups, rows = b.N * b.groups;
+    if (b.H * b.W != 1) return false;
+    if (bwd && b.groups > 1 && Cg * es < 32) return false;   // a block's rows are a group's: shorter than a sector
+    const int vec = Cg % (16 / es) ? 1 : 16 / es, vectors = Cg / vec, nv = row_nv(vec);
+    if (vectors > kRowThreads * nv) return false;
+    const int walked = bwd ? b.N : rows, groups = bwd ? b.groups : 1;   // rows a walker may have, kinds of walkers
+    s->TY = std::min(pow2_up(vectors), std::max(32, pow2_up((vectors + nv - 1) / nv)));
+    while (s->TY < kRowThreads && s->TY < vectors && (int64_t)rows * s->TY < num_sms() * 256) s->TY *= 2;
+    s->threads = std::max(256, s->TY);
+    s->Z = s->threads / s->TY;
+    while (s->Z > 1 && s->threads > 32 && (int64_t)((walked + s->Z - 1) / s->Z) * groups < num_sms()) {
+        s->Z /= 2;
+        s->threads /= 2;
+    }
+    const int blocks = (walked + s->Z - 1) / s->Z, room = num_sms() * (bwd ? 512 : 2048) / s->threads;
+    s->splits = std::min(blocks, std::max(1, room / groups));
+    s->grid = (unsigned)(s->splits * groups);
+    s->images = 1;
+    s->row = 1;
+    s->vec = vec;
+    s->TX = s->tiles = s->per = s->cluster = 1;
+    s->smem = bwd && s->Z > 1 ? (size_t)s->threads * nv * vec * sizeof(float) : 0;
+    return true;
+}
+
 // Launch shape of a call; of the walking kernels where the staged ones do not fit: 32 positions of
 // a row a block.
 void block_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
     *s = BlockShape{};
+    if (row_shape(b, dt, bwd, s)) return;
+    s->images = b.N;
     if (stage_shape(b, dt, bwd, kind, s)) return;
     *s = BlockShape{};
+    s->images = b.N;
     const int P = b.H * b.W, rows = b.N * b.groups;
+    // half as many where the SMs would not all have a block, but 32 bytes
     s->TX = std::min(32, pow2_up(P));
+    while (s->TX * (dt == GCONV_BF16 ? 2 : 4) > 32 && rows * ((P + s->TX - 1) / s->TX) < num_sms()) s->TX /= 2;
     s->TY = 512 / s->TX;
     s->Z = 1;
     s->cluster = 1;
@@ -258,7 +293,7 @@ size_t block_ws(const gconv_block &b, gconv_dtype dt)
     for (int kind : {kBlockNorm, kBlockJoin, kBlockJoinNext}) {
         BlockShape s;
         block_shape(b, dt, true, kind, &s);
-        most = std::max(most, (size_t)2 * s.splits * b.N * b.C * sizeof(float));
+        most = std::max(most, (size_t)2 * s.splits * s.images * b.C * sizeof(float));
     }
     return most;
 }
@@ -322,10 +357,11 @@ static gconv_status finish(const gconv_block &b, gconv_dtype dt, const BlockShap
                            float *dw2, float *dw, float *ds, float *dzc, cudaStream_t st)
 {
     FinishArgs f{};
-    f.part = a.part; f.N = b.N; f.C = b.C; f.G = b.groups; f.Cg = a.Cg; f.Z = a.Z; f.splits = s.splits;
+    f.part = a.part; f.N = s.images; f.C = b.C; f.G = b.groups; f.Cg = a.Cg; f.Z = a.Z; f.splits = s.splits;
     f.tiles = s.staged ? s.tiles : s.splits;
     f.per = s.per;
-    f.next = next; f.post = post; f.gate = a.gate; f.act = a.act; f.z = a.z; f.w = a.w; f.s = a.s;
+    if (s.row) f.Z = b.groups;   // every walker has a share of the one row of sums
+    f.next = next; f.post = post; f.gate = s.row && a.gate == GCONV_GATE_CHANNEL ? GCONV_GATE_FULL : a.gate; f.act = a.act; f.z = a.z; f.w = a.w; f.s = a.s;
     f.dw2 = dw2; f.dw = dw; f.ds = ds; f.dzc = dzc;
     const unsigned grid = (unsigned)((b.C + kFinChannels - 1) / kFinChannels);
     if (dt == GCONV_BF16) launch_dependent(block_finish_kernel<__nv_bfloat16>, grid, kFinChannels * kFinLanes, 0, st, f);
@@ -383,11 +419,11 @@ gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const v
     a.gate = block->gate; a.act = block->act;
     a.x = out; a.h = h; a.z = gate; a.w = weight; a.s = scale; a.w2 = next_weight;
     a.dout = dout; a.dnext = dnext; a.dx = dres; a.dh = dh;
-    a.dz = block->gate == GCONV_GATE_FULL ? dgate : nullptr;
+    a.dz = block->gate == GCONV_GATE_FULL || s.row ? dgate : nullptr;
     a.part = static_cast<float *>(workspace);
     const gconv_status r = run_block(true, kind, *block, dtype, s, a, st);
     if (r != GCONV_OK) return r;
-    float *dzc = block->gate == GCONV_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr;
+    float *dzc = block->gate == GCONV_GATE_CHANNEL && !s.row ? static_cast<float *>(dgate) : nullptr;
     if (!dweight && !dscale && !dnext_weight && !dzc) return GCONV_OK;
     return finish(*block, dtype, s, a, dnext != nullptr, 1, dnext_weight, dweight, dscale, dzc, st);
 }

@@ -1,4 +1,5 @@
-// block_norm.cuh -- device code of the block norm and block join kernels (block_norm.cu).
+// block_norm.cuh -- what the block norm and block join kernels share, and those for very wide groups;
+// the others are in block_stage.cuh.
 //
 // With r(t) = 1 / sqrt(mean over a group's channels of t^2 + eps), per image and position:
 //   norm   y    = x r(x) w
@@ -57,12 +58,6 @@ __host__ __device__ __forceinline__ int column_shares(int TY)
 
 // The tensors of a staged launch as [N C][P] matrices, for tiles that are boxes of them.
 struct StageMaps { CUtensorMap m[5]; };
-
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load_pack(const void *p, int64_t i)
-{
-    return *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(p) + i);
-}
 
 __device__ __forceinline__ void from_f(float v, float *o) { *o = v; }
 __device__ __forceinline__ void from_f(float v, __nv_bfloat16 *o) { *o = __float2bfloat16_rn(v); }
@@ -138,16 +133,12 @@ __device__ __forceinline__ float branch_coeff(const BlockArgs &a, int ch)
     return (a.w ? a.w[ch] : 1.f) * (a.s ? a.s[ch] : 1.f);
 }
 
-// res + k g (h r), each rounding written out: out has the same bits with and without `next`.
-__device__ __forceinline__ float join_sum(float res, float k, float g, float h, float r)
-{
-    return fmaf(__fmul_rn(k, g), __fmul_rn(h, r), res);
-}
+// ---- groups too wide for the staged kernels (a channel's 16 bytes times C / G beyond a cluster of
+// eight blocks' shared memory): 32 positions a block, the channels walked in steps, inputs read again
+// in each sweep, which the L2 serves in part.  Rare, and kept simple. ----
 
-// ---- groups too wide for the staged kernels: the channels walked in steps, inputs read again in
-// each sweep ----
-
-// out of the join at one element, from its three inputs
+// out of the join at one element, from its three inputs; the roundings as in the staged kernel, so
+// that out has the same bits with and without `next`
 template <typename T>
 __device__ __forceinline__ float walk_out(const BlockArgs &a, int64_t at, int ch, int64_t nc, float r)
 {

@@ -2,7 +2,7 @@
 // twice (or once): while a block computes one tile, the next lands by asynchronous copies.
 //
 // These operators do 4 to 40 operations an element against 4 to 16 bytes, so the memory is the
-// limit as long as enough of it is in flight: a whole tile of every input here (40 to 100 KB an
+// limit as long as enough of it is in flight: a whole tile of every input here (40 to 200 KB an
 // SM), where loads into registers end with each tile's reduction.  Where planes are multiples of 16
 // bytes and a channel's share of a tile 64 bytes or more, a tile of a tensor is a few boxes of a
 // tensor map, and whole rows are one bulk copy: one thread starts them.  Else the threads copy
@@ -14,10 +14,10 @@
 // instruction (packed fp32 pairs) and every index is 32 bits and steps by constants.
 //
 // Two forms of a tile: PT positions of every channel of Z rows, or (flat) Z whole rows, which are
-// one run of memory, for planes of at most 64 positions.  A thread holds 16 elements: VEC
-// neighbouring positions (as many as divide P, at most 16 bytes) of 16 / VEC channels, so that an
-// address, a predicate and a channel's weight serve VEC elements; where P is odd, two neighbours
-// read one by one of 8 channels (VEC = 1).  A thread whose share has fewer channels reads zeros kept
+// one run of memory, for planes of at most 64 positions.  A thread holds 32 elements (16 where VEC
+// is below 4): VEC neighbouring positions (as many as divide P, at most 16 bytes) of 32 / VEC
+// channels, so that an address, a predicate and a channel's weight serve VEC elements; where P is
+// odd, two neighbours read one by one of 8 channels (VEC = 1).  A thread whose share has fewer channels reads zeros kept
 // at the end of each staged tensor instead of branching.
 #pragma once
 
@@ -27,7 +27,7 @@ namespace gconv {
 
 // Elements a thread holds of a tile, and threads of a block, at most.  What a thread does for a tile
 // beside its elements (two column sums, places, barriers) is most of the time when it has few: the
-// gradient of a join of [64,256,56,56] bf16 took WHAT with 8 in 1024 threads, 16 in 512 and 32 in 256.
+// gradient of a join of [64,256,56,56] bf16 took 365 us with 8 in 1024 threads, 214 with 16 in 512 and 196 with 32 in 256.
 constexpr int stage_elements(int vec) { return vec >= 4 ? 32 : 16; }
 constexpr int stage_threads(int vec) { return vec >= 4 ? 256 : 512; }
 constexpr int stage_pairs(int vec) { return vec > 1 ? vec / 2 : 1; }      // pairs of positions a thread holds
@@ -490,6 +490,12 @@ __device__ __forceinline__ void row_numbers(const BlockArgs &a, const Part &g, c
     }
 }
 
+// Forward.  One sweep over a tile gives sum h^2 a position, the second out (kept in registers) and
+// sum out^2, the third next; a norm alone is the first and the third.  Every tensor crosses the
+// memory once.  Two blocks an SM, so that one's reductions stand beside the other's sweeps (a join of
+// [64,256,56,56] bf16 167 us with one, 117 with two).  Now 103 us there, 514 MB, 5.0 TB/s against the
+// 6.8 of a plain copy: what is left is the sweeps' instructions and the wait of the first and the
+// last tile of a block.  Small calls are a launch: [8,1024] of one position, bf16, 2.6 us.
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
 {
@@ -624,8 +630,14 @@ __device__ __forceinline__ F2 live_only(F2 v, bool ok0, bool ok1)
 
 // Backward.  A block walks consecutive tiles; its channel sums of a block of rows stay in
 // registers and go to part[i][row][channel] when the rows change, i counting the blocks that
-// share those rows.  Dead positions hold what an earlier tile left: they meet no live one but in
+// share those rows: no atomics, so the same bits each time.  Dead positions hold what an earlier tile left: they meet no live one but in
 // the channel sums, which leave them out.
+//   Measured, each tensor crossing the memory once: join with next norm, [64,256,56,56] bf16, 822 MB,
+// 194 us (4.2 TB/s of the 6.8 of a plain copy): five tensors twice in shared memory leave one block
+// of 8 warps an SM, too few to hide the sweeps' latency.  Norm of [128,96,27,27] bf16 in 2 groups,
+// 72 MB, 39 us (1.8 TB/s): planes of odd size are read and stored element by element, 80
+// instructions each.  Join of [32,1024,7,7] fp32, 39 MB, 29 us: one tile a block, copies, sweeps and
+// a cluster's two exchanges in turn.
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
 {

@@ -13,7 +13,7 @@ namespace gconv {
 
 namespace {
 
-constexpr int kTinyRows = 16, kTinyCols = 1024;
+constexpr int kTinyRows = 16, kTinyCols = 1024, kTinyWork = 32768;
 
 struct TinyParams {
     NewtonIn in;
@@ -113,7 +113,12 @@ __global__ void __launch_bounds__(256) newton_tiny_kernel(const __grid_constant_
 
 }  // namespace
 
-bool newton_tiny_fits(const NewtonShape &s) { return s.m <= kTinyRows && s.n <= kTinyCols; }
+// A step's time grows with m^2 n and the cluster kernel's hardly does.  Measured, one matrix, here
+// against there: 8 x 72 8 us and 18, 16 x 256 30 and 19, 16 x 1024 105 and 21.
+bool newton_tiny_fits(const NewtonShape &s)
+{
+    return s.m <= kTinyRows && s.n <= kTinyCols && s.m * s.m * s.n <= kTinyWork;
+}
 
 gconv_status newton_tiny_launch(const NewtonShape &s, const NewtonIn &in, const NewtonOut &out, int steps,
                                 const float *coeffs, cudaStream_t st)

@@ -179,6 +179,36 @@ def test_join(dev, shape, gate, act, dtype):
     new.check()
 
 
+# planes of one position: few and many rows, rows of a part of a warp up to several warps, wider than
+# a block holds, groups, odd channels, groups shorter than a sector
+ROWS = [
+    (8, 1024, 1, 1, 1), (1000, 1024, 1, 1, 1), (700, 96, 1, 1, 2), (300, 33, 1, 1, 1), (2000, 64, 1, 1, 4), (3, 8192, 1, 1, 1),
+    (2, 9000, 1, 1, 1), (65, 4100, 1, 1, 1), (1200, 21, 1, 1, 7), (333, 40, 1, 1, 5), (1, 16, 1, 1, 1), (400, 2056, 1, 1, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", ROWS + [(1200, 7, 1, 1, 7)])
+def test_norm_of_one_position(dev, shape, dtype):
+    test_norm(dev, shape, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate,act", [("none", "none"), ("full", "silu"), ("channel", "sigmoid")])
+@pytest.mark.parametrize("shape", ROWS)
+def test_join_of_one_position(dev, shape, gate, act, dtype):
+    test_join(dev, shape, gate, act, dtype)
+
+
+def test_rows_beside_the_last_add_nothing(dev):
+    """eps = 0: r is infinite where a block has no row, which must not reach the channel sums."""
+    s, G = (5, 64, 1, 1), 1
+    d = make(s, torch.float32, dev, 9, G)
+    dx, dw = torch.empty(s, device=dev), torch.empty(s[1], device=dev)
+    gc.gconv_norm_bwd(d["x"], d["weight"], d["dnext"], dx, dw, groups=G, eps=0.0)
+    near("dweight", dw, (up(d["dnext"]) * unit(up(d["x"]), G, 0.0)).sum((0, 2, 3)), torch.float32)
+
+
 def test_join_without_vectors_or_dout(dev):
     """weight, scale and next_weight default to ones; dout may be missing beside dnext; the channel
     sums and dgate may be left out."""
