@@ -33,20 +33,22 @@ void staged(int kind, const BlockShape &s, const BlockArgs &a, const StageMaps &
     else launch_staged<block_fwd_stage_kernel<T, VEC, true, true, kGateOther>>(s, a, maps, st);
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, int NV>
 void rows(int kind, const BlockShape &s, const BlockArgs &a, cudaStream_t st)
 {
-    if (kind == kBlockNorm) launch_dependent(block_fwd_row_kernel<T, VEC, false, true>, s.grid, s.threads, s.smem, st, a);
-    else if (kind == kBlockJoin) launch_dependent(block_fwd_row_kernel<T, VEC, true, false>, s.grid, s.threads, s.smem, st, a);
-    else launch_dependent(block_fwd_row_kernel<T, VEC, true, true>, s.grid, s.threads, s.smem, st, a);
+    if (kind == kBlockNorm) launch_dependent(block_fwd_row_kernel<T, VEC, NV, false, true>, s.grid, s.threads, s.smem, st, a);
+    else if (kind == kBlockJoin) launch_dependent(block_fwd_row_kernel<T, VEC, NV, true, false>, s.grid, s.threads, s.smem, st, a);
+    else launch_dependent(block_fwd_row_kernel<T, VEC, NV, true, true>, s.grid, s.threads, s.smem, st, a);
 }
 
 template <typename T>
 void launch_t(int kind, const BlockShape &s, const BlockArgs &a, const StageMaps &maps, cudaStream_t st)
 {
     if (s.row) {
-        if (s.vec == 1) rows<T, 1>(kind, s, a, st);
-        else rows<T, 16 / (int)sizeof(T)>(kind, s, a, st);
+        constexpr int V = 16 / (int)sizeof(T);
+        if (s.vec == 1) rows<T, 1, kRowHeld>(kind, s, a, st);
+        else if (s.held == kRowHeld) rows<T, V, kRowHeld / V>(kind, s, a, st);
+        else rows<T, V, 2 * kRowHeld / V>(kind, s, a, st);
     } else if (s.staged) {
         if (s.vec == 1) staged<T, 1>(kind, s, a, maps, st);
         else if (s.vec == 2) staged<T, 2>(kind, s, a, maps, st);

@@ -7,7 +7,7 @@ namespace gconv {
 
 // The shape of one launch (block_norm.cu, block_shape).
 struct BlockShape {
-    int row;                  // the kernels of block_row.cuh
+    int row, held;            // the kernels of block_row.cuh; channels a thread holds
     int staged;               // the kernels of block_stage.cuh, with:
     int PT, flat, per, total, stages, cluster, Cc, pitch, tensor, boxes, box_rows, pieces;
     int vec;                  // positions a thread holds at once

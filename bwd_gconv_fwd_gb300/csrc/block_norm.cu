@@ -197,14 +197,19 @@ bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, Block
     return true;
 }
 
-// Launch shape of the row kernels: a lane a vector up to a warp, then row_nv vectors a lane, and fewer
-// again, and fewer rows a block, while there are more SMs than work.
-bool row_shape(const gconv_block &b, gconv_dtype dt, bool bwd, BlockShape *s)
+// Launch shape of the row kernels: a lane a vector up to a warp, then as many channels a lane as it
+// holds, and fewer again, and fewer rows a block, while there are more SMs than work.  The gradients'
+// blocks are as many as the SMs hold at once, so that channel sums are put down once.
+bool row_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
     const int es = dt == GCONV_BF16 ? 2 : 4, Cg = b.C / b.groups, rows = b.N * b.groups;
     if (b.H * b.W != 1) return false;
     if (bwd && b.groups > 1 && Cg * es < 32) return false;   // a block's rows are a group's: shorter than a sector
-    const int vec = Cg % (16 / es) ? 1 : 16 / es, vectors = Cg / vec, nv = row_nv(vec);
+    const int vec = Cg % (16 / es) ? 1 : 16 / es, vectors = Cg / vec;
+    // twice as many channels a thread where a row is too long, and where there is little to hold: norm of
+    // [65536,1024] bf16 69 us with 8 a thread, 59 with 16; gradient of a join 465 and 508
+    s->held = vec > 1 && (Cg > kRowThreads * kRowHeld || (vec == 8 && !bwd && kind == kBlockNorm)) ? 2 * kRowHeld : kRowHeld;
+    const int nv = s->held / vec;
     if (vectors > kRowThreads * nv) return false;
     const int walked = bwd ? b.N : rows, groups = bwd ? b.groups : 1;   // rows a walker may have, kinds of walkers
     s->TY = std::min(pow2_up(vectors), std::max(32, pow2_up((vectors + nv - 1) / nv)));
@@ -215,7 +220,8 @@ bool row_shape(const gconv_block &b, gconv_dtype dt, bool bwd, BlockShape *s)
         s->Z /= 2;
         s->threads /= 2;
     }
-    const int blocks = (walked + s->Z - 1) / s->Z, room = num_sms() * (bwd ? 512 : 2048) / s->threads;
+    const int threads = !bwd ? 2048 : kind == kBlockNorm && s->held == kRowHeld ? 1024 : 512;   // of an SM, by its registers
+    const int blocks = (walked + s->Z - 1) / s->Z, room = num_sms() * threads / s->threads;
     s->splits = std::min(blocks, std::max(1, room / groups));
     s->grid = (unsigned)(s->splits * groups);
     s->images = 1;
@@ -231,7 +237,7 @@ bool row_shape(const gconv_block &b, gconv_dtype dt, bool bwd, BlockShape *s)
 void block_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
     *s = BlockShape{};
-    if (row_shape(b, dt, bwd, s)) return;
+    if (row_shape(b, dt, bwd, kind, s)) return;
     s->images = b.N;
     if (stage_shape(b, dt, bwd, kind, s)) return;
     *s = BlockShape{};

@@ -1,11 +1,17 @@
 // block_row.cuh -- the block norm / join kernels for planes of one position (tokens, pooled
 // features): an image's group is then Cg elements in a run, so the sums go along memory.
 //
-// TY threads hold a row, VEC neighbouring channels (16 bytes, or one where Cg is odd) times row_nv
-// each, in registers from the loads to the stores; Z rows a block, and blocks walk the rows.  Every
+// TY threads hold a row, VEC neighbouring channels (16 bytes, or one where Cg is not a multiple) times
+// NV each, in registers from the loads to the stores; Z rows a block, and blocks walk the rows.  Every
 // tensor crosses the memory once, as 16-byte loads that are all in flight before the first
 // sum.  The gradients' channel sums stay in registers until a block's last row (a block keeps to one
 // group), so their partial sums are a block's and not an image's.
+//
+// Measured, [65536,1024] (the staged kernels' time, with their sums per image, in brackets): norm bf16
+// 59 us, 4.5 TB/s (172), its gradient 142, 2.8 TB/s (1409); fp32 85, 6.3 TB/s (161), and 149, 5.4 TB/s
+// (1388).  Join with next norm and a full silu gate, bf16 186, 3.6 TB/s (429), its gradient 465, 2.3 TB/s
+// (3792); fp32 202, 6.6 TB/s (542), and 430, 5.0 TB/s (3754).  The memory is fp32's limit; bf16's is
+// the arithmetic of its gradients, twice the elements a byte.  [8,1024] bf16, a launch: 1.8 us.
 #pragma once
 
 #include "block_norm.cuh"
@@ -13,7 +19,7 @@
 namespace gconv {
 
 constexpr int kRowThreads = 512;   // a row's, at most
-constexpr int row_nv(int vec) { return vec > 1 ? 2 : 8; }
+constexpr int kRowHeld = 8;        // channels a thread holds, or twice that
 
 // Adds v over the TY threads of a row, the same bits in each.  `red`: two halves of a float a warp and
 // sum (`turn`: a half is written again two barriers after it was read).
@@ -89,10 +95,9 @@ __device__ __forceinline__ void branch_weights(const BlockArgs &a, int c, bool o
 }
 
 // Forward: three steps a row (sum h^2; out and sum out^2; next), a norm alone two.
-template <typename T, int VEC, bool POST, bool NEXT>
+template <typename T, int VEC, int NV, bool POST, bool NEXT>
 __global__ void __launch_bounds__(kRowThreads) block_fwd_row_kernel(const BlockArgs a)
 {
-    constexpr int NV = row_nv(VEC);
     __shared__ float red[2 * (kRowThreads / 32)];
     const int ty = threadIdx.x % a.TY, z = threadIdx.x / a.TY;
     int turn = 0;
@@ -155,10 +160,9 @@ __global__ void __launch_bounds__(kRowThreads) block_fwd_row_kernel(const BlockA
 
 // Backward: block b walks images (b / G) Z + z, ... of group b % G; its channel sums go to
 // part[b / G][channel], and gridDim / G images' worth on, the branch's.
-template <typename T, int VEC, bool POST, bool NEXT>
-__global__ void __launch_bounds__(kRowThreads) block_bwd_row_kernel(const BlockArgs a)
+template <typename T, int VEC, int NV, bool POST, bool NEXT>
+__global__ void __launch_bounds__(kRowThreads, POST || NV * VEC > kRowHeld ? 1 : 2) block_bwd_row_kernel(const BlockArgs a)
 {
-    constexpr int NV = row_nv(VEC);
     extern __shared__ __align__(16) float seats[];   // Z rows of a block's sums
     __shared__ float red[2 * 2 * (kRowThreads / 32)];
     const int ty = threadIdx.x % a.TY, z = threadIdx.x / a.TY;

@@ -495,7 +495,7 @@ __device__ __forceinline__ void row_numbers(const BlockArgs &a, const Part &g, c
 // memory once.  Two blocks an SM, so that one's reductions stand beside the other's sweeps (a join of
 // [64,256,56,56] bf16 167 us with one, 117 with two).  Now 103 us there, 514 MB, 5.0 TB/s against the
 // 6.8 of a plain copy: what is left is the sweeps' instructions and the wait of the first and the
-// last tile of a block.  Small calls are a launch: [8,1024] of one position, bf16, 2.6 us.
+// last tile of a block.
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
 {
