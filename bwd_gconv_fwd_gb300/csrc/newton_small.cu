@@ -12,6 +12,9 @@
 // operations, which is why a matrix stays on one cluster.  The exchanges are bulk copies between
 // the blocks' shared memory that signal the receiver's barrier: reading the others' memory between
 // two cluster barriers cost half of a step (128 x 1200: 7500 of 14700 cycles).
+//   Measured, five steps: 64 x 576 24 us, two of 128 x 1200 45, 128 x 4096 53, 64 x 256 23; one launch a
+// product (newton.cu) takes 81, 103, 113 and 64.  A step is 4 to 9 us of latency: the two products' fill
+// and drain, two exchanges and three turns between the kinds of accesses to shared memory.
 //
 // The 128-byte swizzled tile of 64 columns x 128 rows that the first product reads with rows
 // as its outer side (K-major) is, with the roles of rows and columns exchanged, the tile
@@ -539,8 +542,9 @@ bool sixteen_fit()
     return cache[dev] > 0;
 }
 
-// Blocks a matrix: as few as their shared memory allows, more while they are idle and a slice is
-// longer than one chunk.  Clusters of sixteen, which not every
+// Blocks a matrix: as few as their shared memory allows, more while most SMs are idle and a slice is
+// longer than one chunk (64 x 576: two blocks 32 us, four 26, eight 24; 16 of them, which as clusters of
+// eight do not all run at once, 26 in fours and 47 in eights).  Clusters of sixteen, which not every
 // part of the device can hold, only where eight do not fit.
 int small_cluster(const NewtonShape &s, int *slice)
 {
@@ -549,7 +553,7 @@ int small_cluster(const NewtonShape &s, int *slice)
         SmallParams p;
         if (sl > kMaxChunks * 64 || small_layout(s, cs, sl, &p) > kSmallSmem) continue;
         if (cs == 16 && !sixteen_fit()) continue;
-        if (cs < 8 && sl > 64 && (int64_t)s.G * cs * 2 <= num_sms()) continue;
+        if (cs < 8 && sl > 64 && (int64_t)s.G * cs * 4 <= num_sms()) continue;
         *slice = sl;
         return cs;
     }
