@@ -242,7 +242,8 @@ gconv_status gconv_step_ex(const gconv_geometry *geometry, gconv_dtype dtype, gc
  * Activations and their gradients are `dtype` (GCONV_F32 or GCONV_BF16), weight, scale and
  * next_weight fp32 [C] (NULL: all ones), their gradients fp32.  All sums are fp32, each
  * result is rounded once, and every reduction has a fixed order (bitwise reproducible).
- * Inf and NaN spread through a position's group as the formulas say. */
+ * Inf and NaN spread through a position's group as the formulas say.  The kernels' waits are
+ * bounded: one that ran out shows in gconv_check_device_error. */
 typedef enum { GCONV_ACT_NONE = 0, GCONV_ACT_SIGMOID = 1, GCONV_ACT_SILU = 2 } gconv_act;
 typedef enum {
     GCONV_GATE_NONE = 0,      /* no gate: act(gate) is 1 */
@@ -305,8 +306,10 @@ gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const v
  * The iterates are kept in fp16 (11 bits) and products add in fp32: the result is about
  * 1e-3 (relative, 2-norm) from exact arithmetic for well-conditioned matrices and up to 1e-2 where
  * singular values span three decades.  Entries of an iterate must stay below 255 in magnitude,
- * which holds for coefficients that converge.  A zero matrix gives zeros; an Inf or NaN
- * makes its own matrix NaN.  Bitwise reproducible.
+ * which holds for coefficients that converge.  (Matrices of at most 16 rows and 1024 columns on their
+ * sides with rows^2 cols <= 32768, the shorter side being the rows, stay in fp32.)  A zero matrix gives zeros; an Inf or NaN
+ * makes its own matrix NaN.  Bitwise reproducible.  The kernels' waits are bounded: one that ran out
+ * shows in gconv_check_device_error.
  * Requirements: rows, cols >= 1, count >= 0, fewer than 2^31 elements in all, 1 <= steps <= 64,
  * eps >= 0, finite numbers, 16-byte aligned pointers.  The records and coeffs (host memory) are
  * read during the call only. */
