@@ -32,6 +32,10 @@ constexpr int stage_elements(int vec) { return vec >= 4 ? 32 : 16; }
 constexpr int stage_threads(int vec) { return vec >= 4 ? 256 : 512; }
 constexpr int stage_pairs(int vec) { return vec > 1 ? vec / 2 : 1; }      // pairs of positions a thread holds
 constexpr int stage_nch(int vec) { return stage_elements(vec) / 2 / stage_pairs(vec); }   // channels
+// Whether a thread's loops run over all the channels it can hold even where it has at most half: with four,
+// the branch costs more than it saves (gradient of a join of [64,128,56,56] bf16 in 32 groups 83 us
+// without, 90 with); with eight it is a third (the same at 55 x 55 194 and 143, [64,64,112,112] fp32 320 and 267).
+constexpr bool whole_share(int nch) { return nch <= 4; }
 constexpr uint64_t kStageDrainNs = 1000000000ull;
 constexpr int kStageZeros = 32;                                          // bytes of zeros behind a staged tensor
 
@@ -549,6 +553,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
     bool has[NCH];
     #pragma unroll
     for (int j = 0; j < NCH; ++j) has[j] = s.ty + j * a.TY < g.n;
+    const bool wide = whole_share(NCH) || a.TY * (NCH / 2) < g.n;   // more than half of them
     for (int t = t0; t < t1; ++t, w.next(a)) {
         const int buf = (t - t0) & (a.stages - 1);
         if (a.stages == 1 && t > t0) {
@@ -577,6 +582,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
         for (int k = 0; k < NP; ++k) r[k] = f2(0.f);
         #pragma unroll
         for (int j = 0; j < NCH; ++j) {
+            if (j == NCH / 2 && !wide) break;
             at[j] = staged_at<T>(a, s, m0, j, has[j]);
             read_vec<T, VEC>(st + (POST ? a.tensor : 0) + at[j], o[j]);
             #pragma unroll
@@ -589,6 +595,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
             for (int k = 0; k < NP; ++k) sum[k] = f2(0.f);
             #pragma unroll
             for (int j = 0; j < NCH; ++j) {
+                if (j == NCH / 2 && !wide) break;
                     F2 x[NP], z[NP];
                     read_vec<T, VEC>(st + at[j], x);
                     if (full) read_vec<T, VEC>(st + 2 * a.tensor + at[j], z);
@@ -611,6 +618,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
         }
         #pragma unroll
         for (int j = 0; j < NCH; ++j) {
+            if (j == NCH / 2 && !wide) break;
             #pragma unroll
             for (int k = 0; k < NP; ++k) o[j][k] = mul2(o[j][k], mul2(r[k], f2(wn[j])));
             write_vec<T, VEC>(a.next, e0 + j * s.e_step, o[j], has[j] && ok0, has[j] && ok1);
@@ -696,6 +704,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
     bool has[NCH];
     #pragma unroll
     for (int j = 0; j < NCH; ++j) has[j] = s.ty + j * a.TY < g.n;
+    const bool wide = whole_share(NCH) || a.TY * (NCH / 2) < g.n;   // more than half of them
     auto flush = [&] {
         const int share = walker - (int)((int64_t)(at_row / a.Z) * a.tiles / a.per);
         float *p0 = a.part + share * NC + (int64_t)(at_row + s.z) * a.Cg + g.c0 + s.ty;
@@ -741,7 +750,10 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
         int at[NCH];
         #pragma unroll
-        for (int j = 0; j < NCH; ++j) at[j] = staged_at<T>(a, s, m0, j, has[j]);
+        for (int j = 0; j < NCH; ++j) {
+            if (j == NCH / 2 && !wide) break;
+            at[j] = staged_at<T>(a, s, m0, j, has[j]);
+        }
         F2 d[NCH][NP], sum[2 * NP];
         F2 rm[2 * NP];   // r and m
         #pragma unroll
@@ -749,6 +761,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
         if (NEXT) {
             #pragma unroll
             for (int j = 0; j < NCH; ++j) {
+                if (j == NCH / 2 && !wide) break;
                     F2 x[NP], g[NP];
                     read_vec<T, VEC>(st + iX * a.tensor + at[j], x);
                     read_vec<T, VEC>(st + iG * a.tensor + at[j], g);
@@ -765,6 +778,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
         F2 sg[NCH][NP];   // the gate's sigmoid, or its value without one
         #pragma unroll
         for (int j = 0; j < NCH; ++j) {
+            if (j == NCH / 2 && !wide) break;
                 read_vec<T, VEC>(st + at[j], d[j]);
                 if (NEXT) {
                     F2 x[NP], g[NP], u = f2(0.f);
@@ -799,6 +813,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
         column_roots<NP, true>(sum, red, a, g, turn, s.tx, s.ty, s.z);
         #pragma unroll
         for (int j = 0; j < NCH; ++j) {
+            if (j == NCH / 2 && !wide) break;
                 const uint32_t e = e0 + j * s.e_step;
                 F2 h[NP], z[NP], u = f2(0.f);
                 read_vec<T, VEC>(st + iH * a.tensor + at[j], h);
