@@ -190,17 +190,38 @@ __device__ __forceinline__ void stage_tile(const BlockArgs &a, const StageMaps &
     ptx::mbar_arrive_expect_tx(bar, bytes);
 }
 
-// A thread's positions of a staged channel, and their store to a tensor.
-template <typename T, int VEC>
-__device__ __forceinline__ void read_vec(const uint8_t *at, F2 (&v)[stage_pairs(VEC)])
+// A thread's positions of a staged channel (a shared-memory address: 32 bits, an offset in the
+// instruction), and their store to a tensor.
+__device__ __forceinline__ F2 pair_of(uint32_t two_bf16)
 {
-    if constexpr (VEC == 1) {
-        const T *q = reinterpret_cast<const T *>(at);
-        v[0] = f2(to_f(q[0]), to_f(q[1]));
+    return f2(__uint_as_float(two_bf16 << 16), __uint_as_float(two_bf16 & 0xffff0000u));
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void read_vec(uint32_t at, F2 (&v)[stage_pairs(VEC)])
+{
+    constexpr int words = VEC * (int)sizeof(T) / 4;   // 32-bit words, where the positions are aligned
+    if constexpr (VEC == 1 && sizeof(T) == 2) {
+        uint16_t a, b;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(at));
+        asm volatile("ld.shared.u16 %0, [%1+2];" : "=h"(b) : "r"(at));
+        v[0] = f2(__uint_as_float((uint32_t)a << 16), __uint_as_float((uint32_t)b << 16));
+    } else if constexpr (VEC == 1) {
+        float a, b;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(a) : "r"(at));
+        asm volatile("ld.shared.f32 %0, [%1+4];" : "=f"(b) : "r"(at));
+        v[0] = f2(a, b);
     } else {
-        const Pack<T, VEC> p = *reinterpret_cast<const Pack<T, VEC> *>(at);
+        uint32_t w[words];
+        if constexpr (words == 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+        else if constexpr (words == 2)
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+        else
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
         #pragma unroll
-        for (int k = 0; k < VEC / 2; ++k) v[k] = f2(to_f(p.v[2 * k]), to_f(p.v[2 * k + 1]));
+        for (int k = 0; k < VEC / 2; ++k)
+            v[k] = sizeof(T) == 2 ? pair_of(w[k]) : f2(__uint_as_float(w[(2 * k) % words]), __uint_as_float(w[(2 * k + 1) % words]));
     }
 }
 
@@ -572,7 +593,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
             stage_tile<T, NT>(a, maps, g, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
         }
         landed(t, t0, t1);
-        const uint8_t *st = smem + buf * NT * a.tensor;
+        const uint32_t st = ptx::smem_u32(smem) + buf * NT * a.tensor;
         const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + 1 < a.P;
         const uint32_t m0 = misfit<T>(a, g, s, w);
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
@@ -744,7 +765,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
             stage_tile<T, NT>(a, maps, g, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
         }
         landed(t, t0, t1);
-        const uint8_t *st = smem + buf * NT * a.tensor;
+        const uint32_t st = ptx::smem_u32(smem) + buf * NT * a.tensor;
         const bool ok0 = in_row && w.p0 + s.pos < a.P, ok1 = in_row && w.p0 + s.pos + 1 < a.P;
         const uint32_t m0 = misfit<T>(a, g, s, w);
         const uint32_t e0 = ((uint32_t)w.row0 * (uint32_t)a.Cg + (uint32_t)(g.c0 + s.c0)) * (uint32_t)a.P + (uint32_t)(w.p0 + s.pos);
