@@ -265,7 +265,7 @@ void block_args(const gconv_block &b, gconv_dtype dt, const BlockShape &s, Block
     a->PT = s.PT; a->flat = s.flat; a->per = s.per; a->total = s.total; a->stages = s.stages; a->cluster = s.cluster; a->Cc = s.Cc;
     a->pitch = s.pitch; a->tensor = s.tensor; a->boxes = s.boxes; a->box_rows = s.box_rows;
     a->box_bytes = s.box_rows * s.pitch;
-    a->pieces = s.pieces; a->lanes2 = pow2_up(s.pieces);
+    a->pieces = s.pieces;
     a->err = device_error_word();
     a->wait_ns = (uint64_t)wait_limit();
     a->bytes = (int64_t)b.N * b.C * a->P * (dt == GCONV_BF16 ? 2 : 4);

@@ -31,10 +31,10 @@ struct BlockArgs {
     int stages;               // tiles in shared memory: 2, or 1
     int cluster, Cc;          // blocks that share a group's channels, and how many each has
     int pitch, tensor;        // bytes of a staged channel, of a staged tensor
-    // a tile of a tensor as boxes of its map, as 16-byte pieces of each channel (a power of two threads
-    // for them), or (neither) as one run of memory
+    // a tile of a tensor as boxes of its map, as 16-byte pieces of each channel, or (neither) as one run of
+    // memory
     int boxes, box_rows, box_bytes;
-    int pieces, lanes2;
+    int pieces;
     int64_t bytes;            // of a whole tensor
     unsigned int *err;
     uint64_t wait_ns;

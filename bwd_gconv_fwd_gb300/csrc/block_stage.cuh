@@ -133,10 +133,23 @@ struct Tile {
     }
 };
 
+// What a thread copies where a tile is in pieces: piece k of channels c, c + step, ...
+struct Place {
+    int k, c, step;
+    __device__ __forceinline__ explicit Place(const BlockArgs &a)
+    {
+        const int n = max(a.pieces, 1);
+        step = blockDim.x / n;
+        c = threadIdx.x / n;
+        k = threadIdx.x - c * n;
+        if (c >= step) c = 1 << 30;   // threads left over: no channel is theirs
+    }
+};
+
 // Starts the copies of one tile of NT tensors to `dst` (a.tensor bytes each; a null tensor is
 // skipped).  Boxes and runs complete `full`, at which every thread arrives; pieces are the threads' own.
 template <typename T, int NT>
-__device__ __forceinline__ void stage_tile(const BlockArgs &a, const StageMaps &maps, const Part &g, const Tile &w,
+__device__ __forceinline__ void stage_tile(const BlockArgs &a, const StageMaps &maps, const Part &g, const Place &pl, const Tile &w,
                                            const char *const (&src)[NT], uint8_t *dst, uint64_t *full)
 {
     constexpr int es = (int)sizeof(T);
@@ -144,20 +157,21 @@ __device__ __forceinline__ void stage_tile(const BlockArgs &a, const StageMaps &
     const int rows = min(a.Z, a.rows - w.row0) * g.n;          // channels
     const int64_t first = ((int64_t)w.row0 * a.Cg + g.c0) * a.P * es;
     if (a.pieces > 0) {
-        // aligned 16-byte pieces, a power of two of threads a channel; a piece that the tensor's end
-        // cuts is read up to it
-        const int k = threadIdx.x & (a.lanes2 - 1), step = blockDim.x / a.lanes2, len = min(a.PT, a.P - w.p0) * es;
-        int c = k < a.pieces ? (int)threadIdx.x / a.lanes2 : rows;
-        int64_t at = first + ((int64_t)c * a.P + w.p0) * es;
-        const int64_t hop = (int64_t)step * a.P * es;
+        // aligned 16-byte pieces, a.pieces threads a channel; a piece that the tensor's end cuts is read up to it
+        const int len = min(a.PT, a.P - w.p0) * es;
+        const int64_t hop = (int64_t)pl.step * a.P * es;
+        const bool cut = first + ((int64_t)rows * a.P + w.p0) * es + 16 > a.bytes;   // the tensor may end in this tile
+        int64_t at = first + ((int64_t)pl.c * a.P + w.p0) * es;
+        uint32_t to = to0 + (uint32_t)pl.c * (uint32_t)a.pitch + 16u * pl.k;
         #pragma unroll 2
-        for (; c < rows; c += step, at += hop) {
-            const int off = 16 * k - (int)(at & 15);           // of the piece, from the channel's first position
+        for (int c = pl.c; c < rows; c += pl.step, at += hop, to += pl.step * a.pitch) {
+            const int off = 16 * pl.k - (int)((uint32_t)at & 15u);   // of the piece, from the channel's first position
             if (off >= len) continue;
-            const uint32_t n = (uint32_t)min((int64_t)16, a.bytes - (at + off));
+            const int64_t from = at + off;
+            const uint32_t n = cut ? (uint32_t)min((int64_t)16, a.bytes - from) : 16u;
             #pragma unroll
             for (int i = 0; i < NT; ++i)
-                if (src[i]) ptx::cp_async16(to0 + i * a.tensor + c * a.pitch + 16 * k, src[i] + at + off, n);
+                if (src[i]) ptx::cp_async16(to + i * a.tensor, src[i] + from, n);
         }
         ptx::cp_async_commit();
         return;
@@ -530,6 +544,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
     __shared__ __align__(8) uint64_t bars[2];
     float *red = reinterpret_cast<float *>(smem + a.stages * NT * a.tensor);
     const Part g(a);
+    const Place pl(a);
     const Seat s = seat<T, VEC>(a, g);
     constexpr bool full = GATE != kGateOff;
     const bool plain = a.act == GCONV_ACT_NONE;
@@ -567,7 +582,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
-    stage_tile<T, NT>(a, maps, g, ahead, src, smem, &bars[0]);
+    stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0]);
 
     int at_row = -1, turn = 0;
     float kb[NCH], wn[NCH];
@@ -580,7 +595,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
         if (a.stages == 1 && t > t0) {
             __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, maps, g, ahead, src, smem, &bars[0]);
+            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0]);
         }
         const bool in_row = w.row0 + s.z < a.rows;
         if (at_row != w.row0) {
@@ -590,7 +605,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
         if (a.stages == 2 && t + 1 < t1) {
             if (t > t0) __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, maps, g, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
+            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
         }
         landed(t, t0, t1);
         const uint32_t st = ptx::smem_u32(smem) + buf * NT * a.tensor;
@@ -676,6 +691,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
     __shared__ __align__(8) uint64_t bars[2];
     float *red = reinterpret_cast<float *>(smem + a.stages * NT * a.tensor);
     const Part g(a);
+    const Place pl(a);
     const Seat s = seat<T, VEC>(a, g);
     constexpr bool full = GATE != kGateOff;
     const bool plain = a.act == GCONV_ACT_NONE;
@@ -716,7 +732,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
-    stage_tile<T, NT>(a, maps, g, ahead, src, smem, &bars[0]);
+    stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0]);
 
     int at_row = -1, turn = 0;
     bool in_row = false;
@@ -749,7 +765,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
         if (a.stages == 1 && t > t0) {
             __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, maps, g, ahead, src, smem, &bars[0]);
+            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0]);
         }
         if (at_row != w.row0) {
             if (at_row >= 0) flush();
@@ -762,7 +778,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
         if (a.stages == 2 && t + 1 < t1) {
             if (t > t0) __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, maps, g, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
+            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
         }
         landed(t, t0, t1);
         const uint32_t st = ptx::smem_u32(smem) + buf * NT * a.tensor;
