@@ -7,8 +7,9 @@
 // bytes and a channel's share of a tile 64 bytes or more, a tile of a tensor is a few boxes of a
 // tensor map, and whole rows are one bulk copy: one thread starts them.  Else the threads copy
 // aligned 16-byte pieces, each channel from the boundary before its positions, and read it from
-// where they start.  (Such pieces took 3000 of the 11000 cycles of a tile of 256 channels x 32
-// positions x 5 tensors, on the threads' own time.  Boxes of 32 bytes a row and bulk copies of one
+// where they start.  (Such pieces take the threads' own time: a tenth of the
+// instructions at 27 x 27, a third while a power of two of threads took a channel and ends were checked
+// piece by piece, 39 us there and 35.  Boxes of 32 bytes a row and bulk copies of one
 // channel each are slower still: norm of [42,728,28,28] 64 us against 42, gradients at 7 x 7 48 against 33.)
 // What is left is the number of instructions, so two positions go through each arithmetic
 // instruction (packed fp32 pairs) and every index is 32 bits and steps by constants.
@@ -532,8 +533,8 @@ __device__ __forceinline__ void row_numbers(const BlockArgs &a, const Part &g, c
 // Forward.  One sweep over a tile gives sum h^2 a position, the second out (kept in registers) and
 // sum out^2, the third next; a norm alone is the first and the third.  Every tensor crosses the
 // memory once.  Two blocks an SM, so that one's reductions stand beside the other's sweeps (a join of
-// [64,256,56,56] bf16 167 us with one, 117 with two).  Now 103 us there, 514 MB, 5.0 TB/s against the
-// 6.8 of a plain copy: what is left is the sweeps' instructions and the wait of the first and the
+// [64,256,56,56] bf16 167 us with one, 117 with two).  Now 103 to 111 us there, 514 MB, 4.6 to 5.0 TB/s
+// against the 6.8 of a plain copy: what is left is the sweeps' instructions and the wait of the first and the
 // last tile of a block.
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
@@ -677,10 +678,10 @@ __device__ __forceinline__ F2 live_only(F2 v, bool ok0, bool ok1)
 // share those rows: no atomics, so the same bits each time.  Dead positions hold what an earlier tile left: they meet no live one but in
 // the channel sums, which leave them out.
 //   Measured, each tensor crossing the memory once: join with next norm, [64,256,56,56] bf16, 822 MB,
-// 194 us (4.2 TB/s of the 6.8 of a plain copy): five tensors twice in shared memory leave one block
+// 189 us (4.3 TB/s of the 6.8 of a plain copy): five tensors twice in shared memory leave one block
 // of 8 warps an SM, too few to hide the sweeps' latency.  Norm of [128,96,27,27] bf16 in 2 groups,
-// 72 MB, 39 us (1.8 TB/s): planes of odd size are read and stored element by element, 80
-// instructions each.  Join of [32,1024,7,7] fp32, 39 MB, 29 us: one tile a block, copies, sweeps and
+// 72 MB, 35 us (2.1 TB/s): planes of odd size are copied in pieces, read and stored element by
+// element, 64 instructions each.  Join of [32,1024,7,7] fp32, 39 MB, 28 us: one tile a block, copies, sweeps and
 // a cluster's two exchanges in turn.
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
