@@ -135,7 +135,8 @@ __device__ __forceinline__ float branch_coeff(const BlockArgs &a, int ch)
 
 // ---- groups too wide for the staged kernels (a channel's 16 bytes times C / G beyond a cluster of
 // eight blocks' shared memory): 32 positions a block, the channels walked in steps, inputs read again
-// in each sweep, which the L2 serves in part.  Rare, and kept simple. ----
+// in each sweep, which the L2 serves in part.  Rare, and kept simple: norm of [8,32768,14,14] bf16
+// 610 us (1220 with 32 positions a block on 56 of the SMs), 0.34 TB/s, bound by latency. ----
 
 // out of the join at one element, from its three inputs; the roundings as in the staged kernel, so
 // that out has the same bits with and without `next`
