@@ -203,7 +203,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     // The first sweep adds the squares, the second scales; between them the values wait in what
-    // A, S and the shares will use, where that is large enough, else they are read again.
+    // A, S and the shares will use, where that is large enough, else they are read again.  So no block
+    // may send a share before every block of the cluster has ended its second sweep: a block with few
+    // columns, or none, would be there long before the others.
     constexpr int kBatch = 8;                               // reads in flight
     float *kept = reinterpret_cast<float *>(sgen + p.oA) + tid * V;
     auto sweep = [&](auto first, auto use) {
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     });
     ptx::fence_proxy_async_smem();
     __syncthreads();
+    ptx::cluster_arrive();   // this block's values have been read; waited for before the first share is sent
 
     uint32_t phase = 0;
     bool ok = true;
@@ -337,10 +340,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncthreads();
+        if (step == 0) ptx::cluster_wait();
         if (CS > 1) {
-            // What a block overwrites here has been read: S was received everywhere before A's rows came
-            // back last step; R was added up before its rows of A left; A's old rows were read before
-            // the sums that replace them were sent.
+            // What a block overwrites here has been read: in the first step by the barrier above (the values
+            // between the sweeps stand in A, S and R); later, S was received everywhere before A's rows
+            // came back last step, R was added up before its rows of A left, and A's old rows were read
+            // before the sums that replace them were sent.
             const uint32_t bar_s = ptx::smem_u32(&bar_shares), bar_r = ptx::smem_u32(&bar_rows);
             const int a_chunks = (m16 + 63) >> 6;
             if (tid == 0) {

@@ -77,6 +77,38 @@ def test_orthogonalize(dev, shape, dtype, out_dtype):
     assert torch.equal(out, again)
 
 
+# (rows, cols) on a cluster of blocks whose last one has few columns of the longer side or none, where what
+# the others send may land on values that a block still has to read: tall and wide, odd sides, one
+# and several chunks of 64 columns a block, clusters of eight and sixteen
+CLUSTERS = [(1728, 96), (1792, 96), (3712, 96), (1040, 33), (64, 1089), (64, 1025), (64, 1152), (64, 1600), (96, 1152),
+            (128, 1200), (120, 4000)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", CLUSTERS)
+def test_clusters_with_narrow_blocks(dev, rows, cols, dtype):
+    g = normal((rows, cols, 1, 1), dev, 12, dtype)
+    out, again = torch.empty_like(g, dtype=torch.float32), torch.empty_like(g, dtype=torch.float32)
+    gc.gconv_orthogonalize(g, out)
+    assert gc.gconv_check_device_error() == 0
+    assert off(out, orth(g, 1)) <= WELL
+    for _ in range(50):
+        gc.gconv_orthogonalize(g, again)
+        assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("rows,cols", [(1728, 96), (64, 1089)])
+def test_muon_on_clusters_with_narrow_blocks(dev, rows, cols):
+    w, grad, mom = (normal((rows, cols, 1, 1), dev, 13 + k, sd=sd) for k, sd in enumerate((0.1, 1e-3, 3e-3)))
+    w2, m2 = torch.empty_like(w), torch.empty_like(w)
+    gc.gconv_muon_step(w, grad, mom, w_out=w2, m_out=m2, lr=0.02, beta=0.9)
+    m = 0.9 * mom.double() + grad.double()
+    o = orth(grad.double() + 0.9 * m, 1)
+    rate = 0.02 * max(1.0, rows / cols) ** 0.5
+    assert off(m2, m) <= 1e-6
+    assert float((w2.double() - w.double() + rate * o).norm()) <= WELL * rate * float(o.norm()) + 1e-6 * float(w.norm())
+
+
 @pytest.mark.parametrize("m,n", [(16, 144), (64, 576), (128, 1200), (200, 200), (300, 900)])
 def test_wide_spectrum(dev, m, n):
     gen = torch.Generator().manual_seed(3)
