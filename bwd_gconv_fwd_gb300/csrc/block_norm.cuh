@@ -249,10 +249,12 @@ __global__ void __launch_bounds__(512) block_bwd_walk_kernel(const BlockArgs a)
         m2 = sum[1][0] * a.inv_cg * r2 * r2 * r2;
     }
     sum[0][0] = sum[1][0] = 0.f;
-    // every lane of a warp goes round as often: the sums over positions are shuffles
-    for (int c = ty; c < a.Cg; c += a.TY) {
+    // every thread goes round as often, with a channel or without: the sums over positions are shuffles
+    // of whole warps, which hold several channels where TX is below 32
+    for (int c0 = 0; c0 < a.Cg; c0 += a.TY) {
+        const int c = c0 + ty;
         float unit_grad = 0.f;
-        if (live) {
+        if (live && c < a.Cg) {
             const int64_t at = base + (int64_t)c * a.P;
             const float d = walk_grad<T, NEXT>(a, at, ch0 + c, r2, m2, &unit_grad);
             if (NEXT) walk_store<T>(a.dx, at, d);
@@ -267,16 +269,17 @@ __global__ void __launch_bounds__(512) block_bwd_walk_kernel(const BlockArgs a)
         }
         if (NEXT) {
             for (int k = 1; k < a.TX; k <<= 1) unit_grad += __shfl_xor_sync(0xffffffffu, unit_grad, k);
-            if (tx == 0 && row_ok) a.part[split * NC + nc0 + c] = unit_grad;
+            if (tx == 0 && row_ok && c < a.Cg) a.part[split * NC + nc0 + c] = unit_grad;
         }
     }
     if (!POST) return;
     column_sum<2, 1>(sum, red, a, tx, ty, z);
     const float r1 = rsqrtf(sum[0][0] * a.inv_cg + a.eps);
     const float m1 = sum[1][0] * a.inv_cg * r1 * r1 * r1;
-    for (int c = ty; c < a.Cg; c += a.TY) {
+    for (int c0 = 0; c0 < a.Cg; c0 += a.TY) {
+        const int c = c0 + ty;
         float acc = 0.f;
-        if (live) {
+        if (live && c < a.Cg) {
             const int64_t at = base + (int64_t)c * a.P;
             float unused;
             const float d = walk_grad<T, NEXT>(a, at, ch0 + c, r2, m2, &unused);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(512) block_bwd_walk_kernel(const BlockArgs a)
             if (a.gate == GCONV_GATE_FULL && a.dz) walk_store<T>(a.dz, at, dr * kc * h * dg);
         }
         for (int k = 1; k < a.TX; k <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, k);
-        if (tx == 0 && row_ok) a.part[(a.splits + split) * NC + nc0 + c] = acc;
+        if (tx == 0 && row_ok && c < a.Cg) a.part[(a.splits + split) * NC + nc0 + c] = acc;
     }
 }
 

@@ -200,6 +200,25 @@ def test_join_of_one_position(dev, shape, gate, act, dtype):
     test_join(dev, shape, gate, act, dtype)
 
 
+# groups beyond a cluster's shared memory, in one type or both, of channel counts that do not divide into
+# whole warps: planes of one tile, of a tile and a part, of many tiles, two groups
+WALKED = [(1, 9001, 4, 4, 1), (2, 9001, 14, 14, 1), (1, 8193, 5, 5, 1), (3, 12345, 3, 3, 1), (1, 16401, 4, 4, 1),
+          (2, 18014, 1, 7, 2), (1, 33001, 1, 2, 1)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", WALKED)
+def test_norm_of_wide_odd_groups(dev, shape, dtype):
+    test_norm(dev, shape, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate,act", [("none", "none"), ("full", "silu"), ("channel", "sigmoid")])
+@pytest.mark.parametrize("shape", WALKED)
+def test_join_of_wide_odd_groups(dev, shape, gate, act, dtype):
+    test_join(dev, shape, gate, act, dtype)
+
+
 def test_rows_beside_the_last_add_nothing(dev):
     """eps = 0: r is infinite where a block has no row, which must not reach the channel sums."""
     s, G = (5, 64, 1, 1), 1
