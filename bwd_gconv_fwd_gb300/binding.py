@@ -356,13 +356,28 @@ def _dev(t: torch.Tensor, name: str):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _workspace(geom, dt, pass_, workspace, device):
+def _scratch(nbytes, device, stream):
+    """A workspace tensor from the pool of the stream that the call's kernels run on: what the
+    allocator hands out next with the same memory, and what had it before, are then ordered with them.
+    The caller holds it until the kernels are launched."""
+    if stream is not None:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if handle != torch.cuda.current_stream(device).cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+            with torch.cuda.stream(stream):
+                return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _workspace(geom, dt, pass_, workspace, device, stream):
+    """(tensor, pointer, bytes) of a pass's workspace."""
     need = gconv_workspace_size(geom, dt, pass_)
     if need == 0:
-        return None, 0
+        return None, None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+        workspace = _scratch(need, device, stream)
+    return workspace, ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
 
 
 # ---- the four passes (tensor level) -------------------------------------------
@@ -379,7 +394,7 @@ def gconv_fwd(x, w, bias, y, *, stride=1, padding=0, dilation=1, groups=1, works
     """y <- conv(x, w) + bias (bias may be None).  y: fp32 or bf16 [N, C_out, Ho, Wo]."""
     geom = geometry(x.shape, w.shape, stride, padding, dilation, groups)
     dt, odt = dtype_code(x.dtype), _out_code(y)
-    ws, wsb = _workspace(geom, dt, PASS_FWD, workspace, x.device)
+    held, ws, wsb = _workspace(geom, dt, PASS_FWD, workspace, x.device, stream)
     args = (_dev(x, "x"), _dev(w, "w"), _dev(bias, "bias"), _dev(y, "y"), ws, wsb, _stream_ptr(stream))
     if len(geom) == 14 and odt == GCONV_F32:
         _check(lib().gconv_fwd(*geom, dt, *args), "gconv_fwd")
@@ -393,7 +408,7 @@ def gconv_bwd_data(dy, w, dx, *, stride=1, padding=0, dilation=1, groups=1, work
     """dx <- gradient of <y, dy> w.r.t. x.  dx: fp32 or bf16 [N, C_in, H, W]."""
     geom = geometry(dx.shape, w.shape, stride, padding, dilation, groups)
     dt, odt = dtype_code(dy.dtype), _out_code(dx)
-    ws, wsb = _workspace(geom, dt, PASS_BWD_DATA, workspace, dy.device)
+    held, ws, wsb = _workspace(geom, dt, PASS_BWD_DATA, workspace, dy.device, stream)
     args = (_dev(dy, "dy"), _dev(w, "w"), _dev(dx, "dx"), ws, wsb, _stream_ptr(stream))
     if len(geom) == 14 and odt == GCONV_F32:
         _check(lib().gconv_bwd_data(*geom, dt, *args), "gconv_bwd_data")
@@ -409,7 +424,7 @@ def gconv_bwd_weight(x, dy, dw, *, db=None, stride=1, padding=0, dilation=1, gro
     [C_out]) also the bias gradient of the same dy, in the same call."""
     geom = geometry(x.shape, dw.shape, stride, padding, dilation, groups)
     dt = dtype_code(x.dtype)
-    ws, wsb = _workspace(geom, dt, PASS_BWD_WEIGHT, workspace, x.device)
+    held, ws, wsb = _workspace(geom, dt, PASS_BWD_WEIGHT, workspace, x.device, stream)
     if len(geom) == 14 and db is None:
         _check(lib().gconv_bwd_weight(*geom, dt, _dev(x, "x"), _dev(dy, "dy"), _dev(dw, "dw"), ws, wsb,
                                       _stream_ptr(stream)), "gconv_bwd_weight")
@@ -460,7 +475,7 @@ def gconv_step(x, w, bias, dy, y, dx, dw, db=None, *, stride=1, padding=0, dilat
         raise TypeError("y and dx must have the same dtype")
     need = gconv_step_workspace_size(geom, dt)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, x.device, stream)
     ws = ctypes.c_void_p(workspace.data_ptr()) if need else None
     wsb = workspace.numel() * workspace.element_size() if need else 0
     rec = geometry_record(geom)
@@ -497,7 +512,7 @@ def gconv_bwd_bias(dy, db, *, geom=None, workspace=None, stream=None):
         N, C, Ho, Wo = (int(v) for v in dy.shape)
         geom = (N, C, Ho, Wo, C, 1, 1, 1, 0, 0, 0, 0, 1, 1)
     dt = dtype_code(dy.dtype)
-    ws, wsb = _workspace(geom, dt, PASS_BWD_BIAS, workspace, dy.device)
+    held, ws, wsb = _workspace(geom, dt, PASS_BWD_BIAS, workspace, dy.device, stream)
     if len(geom) == 14:
         _check(lib().gconv_bwd_bias(*geom, dt, _dev(dy, "dy"), _dev(db, "db"), ws, wsb, _stream_ptr(stream)),
                "gconv_bwd_bias")
@@ -557,9 +572,9 @@ def _block(x, name, groups, eps, gate=None, act="none"):
     return shape, dtype, dt, kind, *record
 
 
-def _block_workspace(need, workspace, device):
+def _block_workspace(need, workspace, device, stream):
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _scratch(need, device, stream)
     elif not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -586,7 +601,7 @@ def gconv_norm_bwd(x, weight, dy, dx, dweight=None, *, dres=None, groups=1, eps=
     """dx <- dres + gradient of the norm w.r.t. x; dweight (fp32 [C]) <- gradient w.r.t. weight."""
     s, d, dt, _, _, ref, need, c = _block(x, "x", groups, eps)
     f = torch.float32
-    ws, wp, wb = _block_workspace(need, workspace, x.device)
+    ws, wp, wb = _block_workspace(need, workspace, x.device, stream)
     st = lib().gconv_norm_bwd(ref, dt, _like(x, s, d, "x"), _like(weight, c, f, "weight"), _like(dy, s, d, "dy"),
                               _like(dres, s, d, "dres"), _like(dx, s, d, "dx"), _like(dweight, c, f, "dweight"), wp, wb,
                               _raw_stream(stream))
@@ -620,7 +635,7 @@ def gconv_join_bwd(h, dout, dh, *, gate=None, act="none", weight=None, scale=Non
     f = torch.float32
     by_channel = kind == GATE_CHANNEL
     nc = s[:2] if by_channel else s
-    ws, wp, wb = _block_workspace(need, workspace, h.device)
+    ws, wp, wb = _block_workspace(need, workspace, h.device, stream)
     st = lib().gconv_join_bwd(ref, dt, _like(out, s, d, "out"), _like(h, s, d, "h"), _like(gate, nc, d, "gate"),
                               _like(weight, c, f, "weight"), _like(scale, c, f, "scale"),
                               _like(next_weight, c, f, "next_weight"), _like(dout, s, d, "dout"),
@@ -667,11 +682,11 @@ def _coeffs(coeffs, steps):
     return _coeff_array(tuple(tuple(c) if hasattr(c, "__len__") else c for c in coeffs), int(steps))
 
 
-def _orth_workspace(need, workspace, device):
+def _orth_workspace(need, workspace, device, stream):
     if workspace is None:
         if need == 0:
             return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _scratch(need, device, stream)
     elif not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -689,7 +704,7 @@ def gconv_orthogonalize(g, out, *, groups=1, steps=5, coeffs=None, eps=1e-7, wor
     dt, odt = dtype_code(g.dtype), _out_code(out)
     _, ref, need = _matrices(shape, int(groups))
     c = _coeffs(coeffs, steps)
-    ws, wp, wb = _orth_workspace(need, workspace, g.device)
+    ws, wp, wb = _orth_workspace(need, workspace, g.device, stream)
     st = lib().gconv_orthogonalize(ref, dt, odt, _like(g, shape, g.dtype, "g"), _like(out, shape, out.dtype, "out"),
                                    int(steps), c, float(eps), wp, wb, _raw_stream(stream))
     if st:
@@ -706,7 +721,7 @@ def gconv_muon_step(w, grad, momentum, *, w_out=None, m_out=None, w_bf16=None, g
     shape, f = w.shape, torch.float32
     _, ref, need = _matrices(shape, int(groups))
     opt = Muon(lr, beta, weight_decay, scale, eps, 1 if nesterov else 0, steps, _coeffs(coeffs, steps))
-    ws, wp, wb = _orth_workspace(need, workspace, w.device)
+    ws, wp, wb = _orth_workspace(need, workspace, w.device, stream)
     st = lib().gconv_muon_step(ref, ctypes.byref(opt), _like(w, shape, f, "w"), _like(grad, shape, f, "grad"),
                                _like(momentum, shape, f, "momentum"), _like(w_out, shape, f, "w_out"),
                                _like(m_out, shape, f, "m_out"), _like(w_bf16, shape, torch.bfloat16, "w_bf16"), wp, wb,
