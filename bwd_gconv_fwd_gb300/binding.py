@@ -527,7 +527,13 @@ def gconv_bwd_bias(dy, db, *, geom=None, workspace=None, stream=None):
 #
 # These calls take microseconds on the GPU for small layers, so their marshalling is lean: a
 # tensor's checks are five attribute reads, pointers pass as integers, and the records and
-# workspace sizes, which depend on sizes alone, are made once for each set of sizes.
+# workspace sizes, which depend on the sizes and the device's number of SMs, are made once for each set
+# of sizes and device.
+
+def _device_index():
+    """The current device: part of what is kept for a set of sizes."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
 
 def _like(t, shape, dtype, name):
     """Address of a contiguous CUDA tensor of this shape and dtype (0 for None)."""
@@ -547,7 +553,7 @@ def _raw_stream(stream):
 
 
 @functools.lru_cache(maxsize=1024)
-def _block_record(N, C, H, W, groups, eps, gate, act, dt):
+def _block_record(N, C, H, W, groups, eps, gate, act, dt, device):
     """(record, its reference, workspace bytes of the backward calls, [C])."""
     if act not in ACTS:
         raise ValueError(f"act is one of {sorted(ACTS)}")
@@ -568,7 +574,7 @@ def _block(x, name, groups, eps, gate=None, act="none"):
         if kind == GATE_CHANNEL and gate.shape != shape[:2]:
             raise ValueError("gate is [N, C, H, W] or [N, C]")
     dt = GCONV_BF16 if dtype is torch.bfloat16 else dtype_code(dtype)
-    record = _block_record(*shape, int(groups), float(eps), kind, act, dt)
+    record = _block_record(*shape, int(groups), float(eps), kind, act, dt, _device_index())
     return shape, dtype, dt, kind, *record
 
 
@@ -583,7 +589,7 @@ def _block_workspace(need, workspace, device, stream):
 def gconv_block_workspace_size(x_shape, dtype: int, groups: int = 1) -> int:
     """Workspace bytes gconv_norm_bwd and gconv_join_bwd need for activations of this shape."""
     N, C, H, W = (int(v) for v in x_shape)
-    return _block_record(N, C, H, W, int(groups), 0.0, GATE_NONE, "none", int(dtype))[2]
+    return _block_record(N, C, H, W, int(groups), 0.0, GATE_NONE, "none", int(dtype), _device_index())[2]
 
 
 def gconv_norm_fwd(x, weight, y, *, groups=1, eps=1e-6, stream=None):
@@ -651,7 +657,7 @@ def gconv_join_bwd(h, dout, dh, *, gate=None, act="none", weight=None, scale=Non
 # ---- orthogonalised updates ------------------------------------------------------
 
 @functools.lru_cache(maxsize=1024)
-def _matrices(shape, groups):
+def _matrices(shape, groups, device):
     """(record, its reference, workspace bytes) of a weight shape."""
     if len(shape) < 2 or groups < 1 or shape[0] % groups:
         raise GconvError(GCONV_ERR_INVALID_ARG, f"{tuple(shape)} is not {groups} groups of matrices")
@@ -694,7 +700,7 @@ def _orth_workspace(need, workspace, device, stream):
 
 def gconv_orthogonalize_workspace_size(w_shape, groups: int = 1) -> int:
     """Workspace bytes of gconv_orthogonalize and gconv_muon_step for weights of this shape."""
-    return _matrices(torch.Size(w_shape), int(groups))[2]
+    return _matrices(torch.Size(w_shape), int(groups), _device_index())[2]
 
 
 def gconv_orthogonalize(g, out, *, groups=1, steps=5, coeffs=None, eps=1e-7, workspace=None, stream=None):
@@ -702,7 +708,7 @@ def gconv_orthogonalize(g, out, *, groups=1, steps=5, coeffs=None, eps=1e-7, wor
     Newton-Schulz steps.  g, out: fp32 or bf16; coeffs: (a, b, c), or one triple a step."""
     shape = g.shape
     dt, odt = dtype_code(g.dtype), _out_code(out)
-    _, ref, need = _matrices(shape, int(groups))
+    _, ref, need = _matrices(shape, int(groups), _device_index())
     c = _coeffs(coeffs, steps)
     ws, wp, wb = _orth_workspace(need, workspace, g.device, stream)
     st = lib().gconv_orthogonalize(ref, dt, odt, _like(g, shape, g.dtype, "g"), _like(out, shape, out.dtype, "out"),
@@ -719,7 +725,7 @@ def gconv_muon_step(w, grad, momentum, *, w_out=None, m_out=None, w_bf16=None, g
     the fp32 weight gradient; w_bf16, when given, gets the new weights rounded to bf16."""
     w_out, m_out = w if w_out is None else w_out, momentum if m_out is None else m_out
     shape, f = w.shape, torch.float32
-    _, ref, need = _matrices(shape, int(groups))
+    _, ref, need = _matrices(shape, int(groups), _device_index())
     opt = Muon(lr, beta, weight_decay, scale, eps, 1 if nesterov else 0, steps, _coeffs(coeffs, steps))
     ws, wp, wb = _orth_workspace(need, workspace, w.device, stream)
     st = lib().gconv_muon_step(ref, ctypes.byref(opt), _like(w, shape, f, "w"), _like(grad, shape, f, "grad"),

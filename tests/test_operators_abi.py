@@ -114,3 +114,30 @@ def test_muon_arguments(L):
             p[k] = wrong
             assert L.gconv_muon_step(m, opt, *p, None, OK, 1 << 30, None) == B.GCONV_ERR_INVALID_ARG
     assert L.gconv_muon_step(m, None, OK, OK, OK, OK, OK, None, OK, 1 << 30, None) == B.GCONV_ERR_INVALID_ARG
+
+
+def test_sizes_are_kept_by_device(monkeypatch):
+    """Workspace sizes depend on the device's number of SMs: what was asked on one is not taken for another."""
+    torch = pytest.importorskip("torch")
+    now = [0]
+
+    class Fake:
+        def gconv_block_workspace_size(self, block, dt):
+            return 1000 + now[0]
+
+        def gconv_orthogonalize_workspace_size(self, matrices):
+            return 2000 + now[0]
+
+    monkeypatch.setattr(B, "_lib", Fake())
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    for k in (B._block_record, B._matrices):
+        k.cache_clear()
+    try:
+        for device in (0, 1, 0):
+            now[0] = device
+            assert B.gconv_block_workspace_size((2, 8, 3, 3), B.GCONV_F32) == 1000 + device
+            assert B.gconv_orthogonalize_workspace_size((300, 400)) == 2000 + device
+    finally:
+        for k in (B._block_record, B._matrices):
+            k.cache_clear()
