@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kRowThreads, POST || NV * VEC > kRowHeld ? 1 :
             }
             row_sum<2>(sum, red, a.TY, turn);
             r = live ? rsqrtf(fmaf(sum[0], a.inv_cg, a.eps)) : 0.f;
-            m = -sum[1] * a.inv_cg * (r * r * r);
+            m = -sum[1] * a.inv_cg * r * r * r;   // from the left: r^3 alone may leave fp32
         }
         sum[0] = sum[1] = 0.f;
         #pragma unroll
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kRowThreads, POST || NV * VEC > kRowHeld ? 1 :
         if (!POST) continue;
         row_sum<2>(sum, red, a.TY, turn);
         r = live ? rsqrtf(fmaf(sum[0], a.inv_cg, a.eps)) : 0.f;
-        m = -sum[1] * a.inv_cg * (r * r * r);
+        m = -sum[1] * a.inv_cg * r * r * r;
         #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (ty + j * a.TY) * VEC;

@@ -296,13 +296,13 @@ __device__ __forceinline__ F2 shfl2(F2 v, int lane)
 }
 
 // From the sum of squares of both positions r = 1 / sqrt(mean + eps), and from the sum of g w t
-// m = -mean(g w t) r^3.
+// m = -mean(g w t) r^3, a factor at a time: r^3 alone leaves fp32 where r is beyond 1e-13 .. 1e13.
 __device__ __forceinline__ F2 root2(const BlockArgs &a, F2 sum)
 {
     const float2 s = parts(sum);
     return f2(rsqrtf(fmaf(s.x, a.inv_cg, a.eps)), rsqrtf(fmaf(s.y, a.inv_cg, a.eps)));
 }
-__device__ __forceinline__ F2 pull2(const BlockArgs &a, F2 sum, F2 r) { return mul2(mul2(sum, f2(-a.inv_cg)), mul2(r, mul2(r, r))); }
+__device__ __forceinline__ F2 pull2(const BlockArgs &a, F2 sum, F2 r) { return mul2(mul2(mul2(mul2(sum, f2(-a.inv_cg)), r), r), r); }
 
 // Adds v over the TY threads that share a row and a vector and turns the sums into r (the first
 // NP) and m (the second NP, with TWO), the same bits in every thread: within a warp by shuffles

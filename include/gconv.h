@@ -242,7 +242,9 @@ gconv_status gconv_step_ex(const gconv_geometry *geometry, gconv_dtype dtype, gc
  * Activations and their gradients are `dtype` (GCONV_F32 or GCONV_BF16), weight, scale and
  * next_weight fp32 [C] (NULL: all ones), their gradients fp32.  All sums are fp32, each
  * result is rounded once, and every reduction has a fixed order (bitwise reproducible).
- * Inf and NaN spread through a position's group as the formulas say.  The kernels' waits are
+ * Inf and NaN spread through a position's group as the formulas say; so does r = Inf where eps is 0 and
+ * a position's group is all zeros (0 times Inf is NaN).  The sums of squares have to stay in fp32:
+ * mean(t^2) + eps from about 1e-38 to 1e38 divided by the group's channels.  The kernels' waits are
  * bounded: one that ran out shows in gconv_check_device_error. */
 typedef enum { GCONV_ACT_NONE = 0, GCONV_ACT_SIGMOID = 1, GCONV_ACT_SILU = 2 } gconv_act;
 typedef enum {

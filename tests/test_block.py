@@ -228,6 +228,60 @@ def test_rows_beside_the_last_add_nothing(dev):
     near("dweight", dw, (up(d["dnext"]) * unit(up(d["x"]), G, 0.0)).sum((0, 2, 3)), torch.float32)
 
 
+# one of each kernel family: rows, whole rows in shared memory, boxes, pieces, a cluster, walked groups
+FAMILIES = [(9, 64, 1, 1, 1), (40, 66, 1, 1, 2), (3, 64, 7, 7, 1), (2, 64, 8, 16, 2), (2, 96, 27, 27, 2), (1, 1024, 14, 14, 1),
+            (1, 16401, 4, 4, 1)]
+# r(t)^3 alone leaves fp32 at each; the largest only where a group's squares stay in fp32 themselves
+RANGES = [(1e-13, 0.0), (1e14, EPS), (1e16, EPS), (1e18, EPS)]
+
+
+def far_apart(t, g, groups, eps):
+    """Root mean square of r(t) g, as first_term, for any eps."""
+    n, c, h, w = t.shape
+    m = t.double().reshape(n, groups, c // groups, h, w)
+    r = 1 / torch.sqrt((m * m).mean(2, keepdim=True) + eps)
+    return (r * g.double().reshape(m.shape)).square().mean().sqrt().cpu()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size,eps", RANGES)
+@pytest.mark.parametrize("shape", FAMILIES)
+def test_gradients_of_small_and_large_activations(dev, shape, size, eps, dtype):
+    *s, G = shape
+    if size == 1e18 and s[1] // G > 64:
+        pytest.skip("the sum of squares is beyond fp32")
+    d = make(s, dtype, dev, 10, G)
+    t = (d["x"].double() * size).to(dtype)
+    dx, dw = torch.empty_like(t), torch.empty(s[1], device=dev)
+    gc.gconv_norm_bwd(t, d["weight"], d["dnext"], dx, dw, groups=G, eps=eps)
+    x, w = up(t).requires_grad_(), up(d["weight"]).requires_grad_()
+    gx, gw = torch.autograd.grad(unit(x, G, eps) * vec(w), (x, w), up(d["dnext"]))
+    near("dx", dx, gx, dtype, far_apart(t, up(d["dnext"]) * vec(up(d["weight"])), G, eps))
+    near("dweight", dw, gw, torch.float32)
+    dh, dw, ds = torch.empty_like(t), torch.empty(s[1], device=dev), torch.empty(s[1], device=dev)
+    gc.gconv_join_bwd(t, d["dout"], dh, weight=d["weight"], scale=d["scale"], dweight=dw, dscale=ds, groups=G, eps=eps)
+    k = up(d["weight"]) * up(d["scale"])
+    gh, gw = torch.autograd.grad(unit(x, G, eps) * vec(w) * vec(up(d["scale"])), (x, w), up(d["dout"]))
+    near("dh", dh, gh, dtype, far_apart(t, up(d["dout"]) * vec(k), G, eps))
+    near("dweight", dw, gw, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", FAMILIES)
+def test_gradient_at_zeros_with_a_tiny_eps(dev, shape, dtype):
+    """A position of zeros: the gradient is r g with r = 1 / sqrt(eps) = 1e15, whose cube is beyond fp32."""
+    *s, G = shape
+    d = make(s, dtype, dev, 11, G)
+    x = d["x"].clone()
+    x[0, :, 0, 0] = 0
+    dx, dh = torch.empty_like(x), torch.empty_like(x)
+    gc.gconv_norm_bwd(x, d["weight"], d["dnext"], dx, groups=G, eps=1e-30)
+    near("dx at zeros", dx[0, :, 0, 0], up(d["dnext"])[0, :, 0, 0] * up(d["weight"]) * 1e15, dtype)
+    gc.gconv_join_bwd(x, d["dout"], dh, weight=d["weight"], groups=G, eps=1e-30)
+    near("dh at zeros", dh[0, :, 0, 0], up(d["dout"])[0, :, 0, 0] * up(d["weight"]) * 1e15, dtype)
+    assert bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dh).all())
+
+
 def test_join_without_vectors_or_dout(dev):
     """weight, scale and next_weight default to ones; dout may be missing beside dnext; the channel
     sums and dgate may be left out."""
