@@ -154,7 +154,7 @@ __device__ __forceinline__ float inverse_norm(const float *part, int parts, floa
     __syncthreads();
     float t = 0.f;
     for (int k = 0; k < 8; ++k) t += sh[k];
-    return kScale / (sqrtf(t) + eps);
+    return unit_factor(kScale, t, eps);
 }
 
 // X = 2^8 u / (|u| + eps) in fp16 for matrices as wide as X and a multiple of eight columns:

@@ -52,6 +52,14 @@ __device__ __forceinline__ float lookahead(const NewtonIn &p, float g, float m)
     return p.nesterov ? fmaf(p.beta, m, g) : m;
 }
 
+// scale / (|u| + eps) from the sum of squares; 0, so that zeros stay zeros, where that is infinite (a
+// matrix of zeros, or whose squares are below fp32, without an eps).
+__device__ __forceinline__ float unit_factor(float scale, float squares, float eps)
+{
+    const float f = scale / (sqrtf(squares) + eps);
+    return isinf(f) ? 0.f : f;
+}
+
 // One element (at, in the caller's layout) of what a call writes: o, or the updated weight.
 __device__ __forceinline__ void put_result(const NewtonOut &o, int64_t at, float v)
 {

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     ptx::cluster_sync();
     float total = 0.f;
     for (uint32_t k = 0; k < CS; ++k) total += rank_sum[k];
-    const float inv = kNewtonScale / (sqrtf(total) + p.in.eps);
+    const float inv = unit_factor(kNewtonScale, total, p.in.eps);
     sweep(std::false_type{}, [&](int r, int c, int, const float (&u)[V]) {
         if (p.in.tall) {
             #pragma unroll

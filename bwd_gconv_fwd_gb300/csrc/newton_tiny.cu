@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) newton_tiny_kernel(const __grid_constant_
     __syncthreads();
     float total = 0.f;
     for (int k = 0; k < threads / 32; ++k) total += sums[k];
-    float inv = 1.f / (sqrtf(total) + p.in.eps);   // of the first X: applied where it is read
+    float inv = unit_factor(1.f, total, p.in.eps);   // of the first X: applied where it is read
     const int lane = tid & (p.lanes - 1), first = tid / p.lanes, hop = threads / p.lanes;
     const int rounds = (p.pairs + hop - 1) / hop, m4 = (m + 3) / 4;
 

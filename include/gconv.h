@@ -309,8 +309,9 @@ gconv_status gconv_join_bwd(const gconv_block *block, gconv_dtype dtype, const v
  * 1e-3 (relative, 2-norm) from exact arithmetic for well-conditioned matrices and up to 1e-2 where
  * singular values span three decades.  Entries of an iterate must stay below 255 in magnitude,
  * which holds for coefficients that converge.  (Matrices of at most 16 rows and 1024 columns on their
- * sides with rows^2 cols <= 32768, the shorter side being the rows, stay in fp32.)  A zero matrix gives zeros; an Inf or NaN
- * makes its own matrix NaN.  Bitwise reproducible.  The kernels' waits are bounded: one that ran out
+ * sides with rows^2 cols <= 32768, the shorter side being the rows, stay in fp32.)  A zero matrix gives zeros, also with
+ * eps 0; an Inf or NaN makes its own matrix NaN.  The squares are added in fp32: elements of about 1e-19
+ * to 1e19 (a matrix whose sum is beyond fp32, or below it with eps 0, gives zeros).  Bitwise reproducible.  The kernels' waits are bounded: one that ran out
  * shows in gconv_check_device_error.
  * Requirements: rows, cols >= 1, count >= 0, fewer than 2^31 elements in all, 1 <= steps <= 64,
  * eps >= 0, finite numbers, 16-byte aligned pointers.  The records and coeffs (host memory) are

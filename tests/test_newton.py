@@ -152,6 +152,25 @@ def test_zero_nan_and_scale(dev, s):
         assert off(out, orth(g, 2)) <= WELL
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-7])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("s", [(12, 6, 3, 3), (64, 64, 3, 3), (96, 33, 1, 1), (260, 140, 1, 1), (140, 260, 1, 1)])
+def test_zero_groups_for_any_eps(dev, s, dtype, eps):
+    """A group of zeros gives zeros, and its weights decay only, on one block, a cluster and by products."""
+    g = normal((2 * s[0],) + s[1:], dev, 15, dtype)
+    want, out = torch.empty_like(g, dtype=torch.float32), torch.empty_like(g, dtype=torch.float32)
+    gc.gconv_orthogonalize(g, want, groups=2, eps=eps)
+    bad = g.clone()
+    bad[s[0]:] = 0
+    gc.gconv_orthogonalize(bad, out, groups=2, eps=eps)
+    assert bool((out[s[0]:] == 0).all()) and torch.equal(out[:s[0]], want[:s[0]])
+    w, mom, grad = normal(g.shape, dev, 16, sd=0.1), torch.zeros_like(want), bad.float()
+    w2, m2 = torch.empty_like(w), torch.empty_like(w)
+    gc.gconv_muon_step(w, grad, mom, w_out=w2, m_out=m2, groups=2, lr=0.02, weight_decay=0.1, eps=eps)
+    assert float((w2[s[0]:] - (1 - 0.02 * 0.1) * w[s[0]:]).abs().max()) <= 1e-6 * float(w.abs().max())
+    assert bool(torch.isfinite(w2).all())
+
+
 @pytest.mark.parametrize("nesterov", [True, False])
 @pytest.mark.parametrize("shape", [(64, 64, 3, 3, 1), (256, 64, 1, 1, 1), (128, 4, 3, 3, 32), (256, 48, 5, 5, 2), (300, 150, 1, 3, 1)])
 def test_muon_step(dev, shape, nesterov):
