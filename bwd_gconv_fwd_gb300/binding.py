@@ -574,7 +574,7 @@ def _block(x, name, groups, eps, gate=None, act="none"):
         if kind == GATE_CHANNEL and gate.shape != shape[:2]:
             raise ValueError("gate is [N, C, H, W] or [N, C]")
     dt = GCONV_BF16 if dtype is torch.bfloat16 else dtype_code(dtype)
-    record = _block_record(*shape, int(groups), float(eps), kind, act, dt, _device_index())
+    record = _block_record(*shape, int(groups), float(eps), kind, act, dt, x.get_device())
     return shape, dtype, dt, kind, *record
 
 
@@ -708,7 +708,7 @@ def gconv_orthogonalize(g, out, *, groups=1, steps=5, coeffs=None, eps=1e-7, wor
     Newton-Schulz steps.  g, out: fp32 or bf16; coeffs: (a, b, c), or one triple a step."""
     shape = g.shape
     dt, odt = dtype_code(g.dtype), _out_code(out)
-    _, ref, need = _matrices(shape, int(groups), _device_index())
+    _, ref, need = _matrices(shape, int(groups), g.get_device())
     c = _coeffs(coeffs, steps)
     ws, wp, wb = _orth_workspace(need, workspace, g.device, stream)
     st = lib().gconv_orthogonalize(ref, dt, odt, _like(g, shape, g.dtype, "g"), _like(out, shape, out.dtype, "out"),
@@ -725,7 +725,7 @@ def gconv_muon_step(w, grad, momentum, *, w_out=None, m_out=None, w_bf16=None, g
     the fp32 weight gradient; w_bf16, when given, gets the new weights rounded to bf16."""
     w_out, m_out = w if w_out is None else w_out, momentum if m_out is None else m_out
     shape, f = w.shape, torch.float32
-    _, ref, need = _matrices(shape, int(groups), _device_index())
+    _, ref, need = _matrices(shape, int(groups), w.get_device())
     opt = Muon(lr, beta, weight_decay, scale, eps, 1 if nesterov else 0, steps, _coeffs(coeffs, steps))
     ws, wp, wb = _orth_workspace(need, workspace, w.device, stream)
     st = lib().gconv_muon_step(ref, ctypes.byref(opt), _like(w, shape, f, "w"), _like(grad, shape, f, "grad"),
