@@ -149,9 +149,11 @@ struct Place {
 
 // Starts the copies of one tile of NT tensors to `dst` (a.tensor bytes each; a null tensor is
 // skipped).  Boxes and runs complete `full`, at which every thread arrives; pieces are the threads' own.
+// A thread whose wait gave up (`ok`) arrives at no barrier again, for the phase it did not see end may still
+// be open.
 template <typename T, int NT>
 __device__ __forceinline__ void stage_tile(const BlockArgs &a, const StageMaps &maps, const Part &g, const Place &pl, const Tile &w,
-                                           const char *const (&src)[NT], uint8_t *dst, uint64_t *full)
+                                           const char *const (&src)[NT], uint8_t *dst, uint64_t *full, bool ok)
 {
     constexpr int es = (int)sizeof(T);
     const uint32_t bar = ptx::smem_u32(full), to0 = ptx::smem_u32(dst);
@@ -177,6 +179,7 @@ __device__ __forceinline__ void stage_tile(const BlockArgs &a, const StageMaps &
         ptx::cp_async_commit();
         return;
     }
+    if (!ok) return;
     uint32_t bytes = 0;
     if (threadIdx.x == 0 && a.boxes > 0) {
         #pragma unroll
@@ -480,12 +483,10 @@ __device__ __forceinline__ void lane_sums(const float (&v)[N], int TX, int tx, i
 }
 
 // Every tile's copies were waited for, unless a wait gave up: then the last ones get the time to land
-// before the block's shared memory is another's.
-__device__ __forceinline__ void stage_drain(const BlockArgs &a, uint64_t *full, bool ok, int tiles)
+// before the block's shared memory is another's.  (Pieces are always waited for.)
+__device__ __forceinline__ void stage_drain(bool ok)
 {
-    if (__syncthreads_or(!ok) && threadIdx.x == 0)   // pieces are always waited for
-        for (int k = max(0, tiles - a.stages); k < tiles; ++k)
-            ptx::mbar_wait(ptx::smem_u32(&full[k & (a.stages - 1)]), (uint32_t)(k / a.stages) & 1u, kStageDrainNs);
+    if (__syncthreads_or(!ok) && threadIdx.x == 0) ptx::let_pass(kStageDrainNs);
     __syncthreads();
 }
 
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
-    stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0]);
+    stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0], ok);
 
     int at_row = -1, turn = 0;
     float kb[NCH], wn[NCH];
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
         if (a.stages == 1 && t > t0) {
             __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0]);
+            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0], ok);
         }
         const bool in_row = w.row0 + s.z < a.rows;
         if (at_row != w.row0) {
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
         if (a.stages == 2 && t + 1 < t1) {
             if (t > t0) __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
+            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1], ok);
         }
         landed(t, t0, t1);
         const uint32_t st = ptx::smem_u32(smem) + buf * NT * a.tensor;
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(
             write_vec<T, VEC>(a.next, e0 + j * s.e_step, o[j], has[j] && ok0, has[j] && ok1);
         }
     }
-    stage_drain(a, bars, ok, t1 - t0);
+    stage_drain(ok);
 }
 
 // A pair's sum, without what stands at a dead position.
@@ -733,7 +734,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (a.cluster > 1) ptx::cluster_sync();   // the others' shared memory may be written from here on
-    stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0]);
+    stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0], ok);
 
     int at_row = -1, turn = 0;
     bool in_row = false;
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
         if (a.stages == 1 && t > t0) {
             __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0]);
+            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem, &bars[0], ok);
         }
         if (at_row != w.row0) {
             if (at_row >= 0) flush();
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
         if (a.stages == 2 && t + 1 < t1) {
             if (t > t0) __syncthreads();   // the tile before has been read
             ahead.next(a);
-            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1]);
+            stage_tile<T, NT>(a, maps, g, pl, ahead, src, smem + (buf ^ 1) * NT * a.tensor, &bars[buf ^ 1], ok);
         }
         landed(t, t0, t1);
         const uint32_t st = ptx::smem_u32(smem) + buf * NT * a.tensor;
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_st
             }
     }
     if (at_row >= 0) flush();
-    stage_drain(a, bars, ok, t1 - t0);
+    stage_drain(ok);
 }
 
 }  // namespace gconv

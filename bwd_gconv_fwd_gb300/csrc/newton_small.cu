@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
             // before the sums that replace them were sent.
             const uint32_t bar_s = ptx::smem_u32(&bar_shares), bar_r = ptx::smem_u32(&bar_rows);
             const int a_chunks = (m16 + 63) >> 6;
-            if (tid == 0) {
+            if (tid == 0 && ok) {   // not at a barrier whose last phase may still be open
                 ptx::mbar_arrive_expect_tx(bar_s, CS * share_bytes);
                 ptx::mbar_arrive_expect_tx(bar_r, (CS - 1) * (uint32_t)(a_chunks * share * 128));
             }
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     }
     // Copies to and from this block have ended: each was waited for where it arrived, or, after a wait
     // that gave up, has the time to land.
-    if (CS > 1 && !ok && lane == 0) ptx::mbar_wait(ptx::smem_u32(&bar_rows), (p.steps - 1) & 1, kSmallDrainNs);
+    if (__syncthreads_or(!ok) && tid == 0) ptx::let_pass(kSmallDrainNs);
     __syncwarp();
     ptx::tc_fence_before();
     ptx::cluster_sync();

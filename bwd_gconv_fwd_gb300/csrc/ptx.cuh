@@ -82,6 +82,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// Lets `ns` nanoseconds pass: the time copies in flight get to land after a wait that gave up.
+__device__ __forceinline__ void let_pass(uint64_t ns)
+{
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < ns) { }
+}
+
 // The bounded wait as an out-of-line call, for the MMA-issuing threads: with the polling
 // loop inlined into an issue loop, the code between consecutive MMAs grew and the tensor
 // core idled (the issuing thread runs only about one MMA ahead of it).  Their fast path is

@@ -394,3 +394,27 @@ def test_empty_batch_and_refusals(dev):
                 lambda: gc.gconv_join_bwd(x, x, y, gate=x[:, :, 0, 0].contiguous(), dgate=torch.empty_like(x))):
         with pytest.raises((gc.GconvError, ValueError, TypeError)):
             bad()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", FAMILIES + [(64, 128, 56, 56, 1), (32, 1024, 7, 7, 1)])
+def test_wait_timeout_is_reported_and_recovered(dev, shape, dtype):
+    """With a wait limit of zero a wait that is not over at its first poll gives up (a poll may itself last
+    until the copies have landed, and some kernels have no such wait): the call then reports it, else its
+    result is right, and either way the next call, with the limit restored, is right."""
+    *s, G = shape
+    d = make(s, dtype, dev, 12, G)
+    call = lambda dx, dw: gc.gconv_norm_bwd(d["x"], d["weight"], d["dnext"], dx, dw, dres=d["dout"], groups=G)  # noqa: E731
+    want, tried, got = ((torch.empty_like(d["x"]), torch.empty(s[1], device=dev)) for _ in range(3))
+    call(*want)
+    assert gc.gconv_check_device_error() == B.GCONV_OK
+    B.gconv_debug_set_wait_limit(0)
+    try:
+        call(*tried)
+        status = gc.gconv_check_device_error()
+    finally:
+        B.gconv_debug_set_wait_limit(-1)
+    same = lambda a: all(torch.equal(u, v) for u, v in zip(a, want))  # noqa: E731
+    assert status == B.GCONV_ERR_TIMEOUT or (status == B.GCONV_OK and same(tried))
+    call(*got)
+    assert gc.gconv_check_device_error() == B.GCONV_OK and same(got)
