@@ -41,7 +41,7 @@ struct SmallParams {
     NewtonOut out;
     int m, n, steps, slice;                   // slice: columns a block holds, a multiple of 64
     int cluster;
-    int m16, pitch, keep;                     // m up to 16; bytes of a row of S_r, a power of two; see sweep
+    int m16, pitch, keep, ordered;            // m up to 16; bytes of a row of S_r, a power of two; see sweep
     uint32_t oA, oS, oR, oOut;                // A; S_r, and P in its place; the shares received; the result's stage
     unsigned int *err;
     uint64_t wait_ns;
@@ -203,9 +203,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     // The first sweep adds the squares, the second scales; between them the values wait in what
-    // A, S and the shares will use, where that is large enough, else they are read again.  So no block
-    // may send a share before every block of the cluster has ended its second sweep: a block with few
-    // columns, or none, would be there long before the others.
+    // A, S and the shares will use, where that is large enough, else they are read again.  Where they reach
+    // the shares (`ordered`), no block may send one before every block of the cluster has ended its
+    // second sweep: a block with few columns, or none, would be there long before the others.  (A Muon step of
+    // 256 x 64, whose values do not reach, 30.8 us without the barrier and 31.4 with it.)
     constexpr int kBatch = 8;                               // reads in flight
     float *kept = reinterpret_cast<float *>(sgen + p.oA) + tid * V;
     auto sweep = [&](auto first, auto use) {
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
     });
     ptx::fence_proxy_async_smem();
     __syncthreads();
-    ptx::cluster_arrive();   // this block's values have been read; waited for before the first share is sent
+    if (p.ordered) ptx::cluster_arrive();   // this block's values have been read; waited for before the first share is sent
 
     uint32_t phase = 0;
     bool ok = true;
@@ -340,12 +341,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) newton_small_kernel(const __
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncthreads();
-        if (step == 0) ptx::cluster_wait();
+        if (step == 0 && p.ordered) ptx::cluster_wait();
         if (CS > 1) {
-            // What a block overwrites here has been read: in the first step by the barrier above (the values
-            // between the sweeps stand in A, S and R); later, S was received everywhere before A's rows
-            // came back last step, R was added up before its rows of A left, and A's old rows were read
-            // before the sums that replace them were sent.
+            // What a block overwrites here has been read: in the first step by the barrier above (rows of A come
+            // only after this block's share, which it sends behind its second sweep); later, S was received
+            // everywhere before A's rows came back last step, R was added up before its rows of A left,
+            // and A's old rows were read before the sums that replace them were sent.
             const uint32_t bar_s = ptx::smem_u32(&bar_shares), bar_r = ptx::smem_u32(&bar_rows);
             const int a_chunks = (m16 + 63) >> 6;
             if (tid == 0 && ok) {   // not at a barrier whose last phase may still be open
@@ -565,6 +566,24 @@ int small_cluster(const NewtonShape &s, int *slice)
     return 0;
 }
 
+// The rest of a launch's plan from its cluster and slice, and a block's shared memory.
+size_t small_plan(const NewtonShape &s, SmallParams *p)
+{
+    p->m = s.m; p->n = s.n;
+    // More than half an SM's shared memory: two blocks on one SM would wait for each other's
+    // tensor memory, and two clusters that each hold what the other waits for would never end.
+    const size_t smem = std::max<size_t>(small_layout(s, p->cluster, p->slice, p), 120 * 1024);
+    // items of the sweep a thread has, at most, against the room for them
+    const int V = s.cols % 4 == 0 ? 4 : 1, rows = s.tall ? p->slice : s.m, wide = s.tall ? s.m : std::min(p->slice, s.n);
+    int lpr = 1;
+    while (lpr < 32 && lpr * V < wide) lpr <<= 1;
+    const int64_t items = (int64_t)((rows + kSmallThreads / lpr - 1) / (kSmallThreads / lpr)) * ((wide + lpr * V - 1) / (lpr * V));
+    const int64_t kept = items * kSmallThreads * V * 4;
+    p->keep = kept <= (int64_t)smem - 1024 - p->oA;
+    p->ordered = p->cluster > 1 && p->keep && p->oA + kept > p->oR;
+    return smem;
+}
+
 }  // namespace
 
 bool newton_small_fits(const NewtonShape &s)
@@ -577,20 +596,12 @@ gconv_status newton_small_launch(const NewtonShape &s, const NewtonIn &in, const
                                  const float *coeffs, unsigned int *err, cudaStream_t st)
 {
     SmallParams p{};
-    p.in = in; p.out = out; p.m = s.m; p.n = s.n; p.steps = steps;
+    p.in = in; p.out = out; p.steps = steps;
     p.cluster = small_cluster(s, &p.slice);
     p.err = err; p.wait_ns = (uint64_t)wait_limit();
     for (int k = 0; k < 3 * steps; ++k) p.coeffs[k] = coeffs ? coeffs[k] : kNewtonCoeffs[k % 3];
-    // More than half an SM's shared memory: two blocks on one SM would wait for each other's
-    // tensor memory, and two clusters that each hold what the other waits for would never end.
-    const size_t smem = std::max<size_t>(small_layout(s, p.cluster, p.slice, &p), 120 * 1024);
     const bool vec = s.cols % 4 == 0;
-    // items of the sweep a thread has, at most, against the room for them
-    const int V = vec ? 4 : 1, rows = s.tall ? p.slice : s.m, wide = s.tall ? s.m : std::min(p.slice, s.n);
-    int lpr = 1;
-    while (lpr < 32 && lpr * V < wide) lpr <<= 1;
-    const int64_t items = (int64_t)((rows + kSmallThreads / lpr - 1) / (kSmallThreads / lpr)) * ((wide + lpr * V - 1) / (lpr * V));
-    p.keep = items * kSmallThreads * V * 4 <= (int64_t)smem - 1024 - p.oA;
+    const size_t smem = small_plan(s, &p);
     static bool attr[64][2] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GCONV_ERR_CUDA;
