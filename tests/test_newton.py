@@ -97,6 +97,18 @@ def test_clusters_with_narrow_blocks(dev, rows, cols, dtype):
         assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(32, 4, 3, 3, 8), (64, 64, 3, 3, 1), (1728, 96, 1, 1, 1), (64, 1089, 1, 1, 1), (300, 150, 1, 3, 1),
+                                   (260, 130, 1, 1, 2)])
+def test_in_place(dev, shape, dtype):
+    *s, G = shape
+    g = normal(s, dev, 17, dtype)
+    want = torch.empty_like(g)
+    gc.gconv_orthogonalize(g, want, groups=G)
+    gc.gconv_orthogonalize(g, g, groups=G)
+    assert torch.equal(g, want)
+
+
 @pytest.mark.parametrize("rows,cols", [(1728, 96), (64, 1089)])
 def test_muon_on_clusters_with_narrow_blocks(dev, rows, cols):
     w, grad, mom = (normal((rows, cols, 1, 1), dev, 13 + k, sd=sd) for k, sd in enumerate((0.1, 1e-3, 3e-3)))

@@ -1,5 +1,6 @@
 """Calls on another stream than the current one, without a workspace of the caller's: the memory the
-binding takes must stay the call's until its kernels have run."""
+binding takes must stay the call's until its kernels have run.  And the block and orthogonalisation calls
+captured into a CUDA graph."""
 import pytest
 import torch
 
@@ -27,6 +28,7 @@ def calls(dev):
     x, h, dy, dn = (t(*S) for _ in range(4))
     w = t(64, 32, 3, 3)
     weight, g, mom = t(64, dt=torch.float32), t(150, 200, 1, 1, dt=torch.float32), t(150, 200, 1, 1, dt=torch.float32)
+    small, tiny = t(64, 64, 3, 3, dt=torch.float32), t(32, 4, 3, 3, dt=torch.float32)
     f = lambda *s: torch.empty(s, device=dev)  # noqa: E731
     b = lambda: torch.empty(S, device=dev, dtype=torch.bfloat16)  # noqa: E731
     geom = gc.geometry(S, w.shape, padding=1, groups=G)
@@ -39,6 +41,12 @@ def calls(dev):
         "join_bwd": (block, lambda o, s: gc.gconv_join_bwd(h, dy, o[0], weight=weight, dweight=o[1], out=x, dnext=dn, dres=o[2],
                                                            dnext_weight=o[3], groups=G, stream=s),
                      lambda: [b(), f(64), b(), f(64)]),
+        "norm_fwd": (0, lambda o, s: gc.gconv_norm_fwd(x, weight, o[0], groups=G, stream=s), lambda: [b()]),
+        "join_fwd": (0, lambda o, s: gc.gconv_join_fwd(x, h, o[0], gate=dy, act="silu", weight=weight, next=o[1], groups=G, stream=s),
+                     lambda: [b(), b()]),
+        "orthogonalize_cluster": (0, lambda o, s: gc.gconv_orthogonalize(small, o[0], stream=s), lambda: [f(*small.shape)]),
+        "muon_step_block": (0, lambda o, s: gc.gconv_muon_step(tiny, tiny, tiny, w_out=o[0], m_out=o[1], groups=8, stream=s),
+                            lambda: [f(*tiny.shape), f(*tiny.shape)]),
         "orthogonalize": (orth, lambda o, s: gc.gconv_orthogonalize(g, o[0], stream=s), lambda: [f(*g.shape)]),
         "muon_step": (orth, lambda o, s: gc.gconv_muon_step(g, g, mom, w_out=o[0], m_out=o[1], stream=s),
                       lambda: [f(*g.shape), f(*g.shape)]),
@@ -76,3 +84,22 @@ def test_workspace_lives_as_long_as_its_stream_needs(dev, name, raw):
     for a, b in zip(want, got):
         assert torch.equal(a, b)
     assert all(bool((t == 255).all()) for t in taken)
+
+
+@pytest.mark.parametrize("name", ["norm_fwd", "norm_bwd", "join_fwd", "join_bwd", "orthogonalize", "orthogonalize_cluster", "muon_step",
+                                  "muon_step_block"])
+def test_captured_calls_replay(dev, name):
+    _, call, outputs = calls(dev)[name]
+    want, got = outputs(), outputs()
+    call(want, None)   # what is set up at a kernel's first launch is set up before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(got, None)
+    for _ in range(3):
+        for t in got:
+            t.fill_(7.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert gc.gconv_check_device_error() == B.GCONV_OK
