@@ -114,7 +114,8 @@ int pow2_up(int v)
 // cluster of two; then larger clusters.  Measured: norm of [42,728,28,28] bf16, one block and 16
 // bytes 56 us, two blocks and 32 bytes 41, four and 64 bytes 61; join backward of [32,1024,7,7]
 // fp32, one tile in two blocks 29 us, two tiles in four 38, in eight 68: a cluster's barrier costs
-// more than copies that wait, and both less than sectors read twice.
+// more than copies that wait, and both less than sectors read twice.  The tensors are counted as if the
+// call had a full gate and every gradient: without them their shared memory stands empty.
 bool stage_shape(const gconv_block &b, gconv_dtype dt, bool bwd, int kind, BlockShape *s)
 {
     const int tensors = bwd ? (kind == kBlockJoinNext ? 5 : 3) : (kind == kBlockNorm ? 1 : 3), sums = bwd ? 2 : 1;

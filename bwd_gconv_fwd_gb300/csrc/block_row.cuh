@@ -10,8 +10,10 @@
 // Measured, [65536,1024] (the staged kernels' time, with their sums per image, in brackets): norm bf16
 // 59 us, 4.5 TB/s (172), its gradient 142, 2.8 TB/s (1409); fp32 85, 6.3 TB/s (161), and 149, 5.4 TB/s
 // (1388).  Join with next norm and a full silu gate, bf16 186, 3.6 TB/s (429), its gradient 465, 2.3 TB/s
-// (3792); fp32 202, 6.6 TB/s (542), and 430, 5.0 TB/s (3754).  The memory is fp32's limit; bf16's is
-// the arithmetic of its gradients, twice the elements a byte.  [8,1024] bf16, a launch: 1.8 us.
+// (3792); fp32 202, 6.6 TB/s (542), and 430, 5.0 TB/s (3754).  The memory is fp32's limit.  bf16, with twice the
+// elements a byte, has none of its own: 19, 50, 72 and 133 instructions an element keep the issue slots 54, 61,
+// 65 and 48 % busy at 38, 28, 29 and 16 warps an SM, which wait for their loads, as a block starts a row's
+// only after the row before, and for their own results.  [8,1024] bf16, a launch: 1.9 us.
 #pragma once
 
 #include "block_norm.cuh"

@@ -536,7 +536,8 @@ __device__ __forceinline__ void row_numbers(const BlockArgs &a, const Part &g, c
 // memory once.  Two blocks an SM, so that one's reductions stand beside the other's sweeps (a join of
 // [64,256,56,56] bf16 167 us with one, 117 with two).  Now 103 to 111 us there, 514 MB, 4.6 to 5.0 TB/s
 // against the 6.8 of a plain copy: what is left is the sweeps' instructions and the wait of the first and the
-// last tile of a block.
+// last tile of a block.  (With VEC 1 and 2 a block has 512 threads, so 64 registers each: the joins
+// spill 40 to 72 bytes there without `next` and 140 to 168 with it.)
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(stage_threads(VEC), 2) block_fwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
 {
@@ -682,8 +683,9 @@ __device__ __forceinline__ F2 live_only(F2 v, bool ok0, bool ok1)
 // 189 us (4.3 TB/s of the 6.8 of a plain copy): five tensors twice in shared memory leave one block
 // of 8 warps an SM, too few to hide the sweeps' latency.  Norm of [128,96,27,27] bf16 in 2 groups,
 // 72 MB, 35 us (2.1 TB/s): planes of odd size are copied in pieces, read and stored element by
-// element, 64 instructions each.  Join of [32,1024,7,7] fp32, 39 MB, 28 us: one tile a block, copies, sweeps and
-// a cluster's two exchanges in turn.
+// element, 64 instructions each.  Join of [32,1024,7,7] fp32, 39 MB, 27 us: 128 tiles on 64 clusters of two
+// blocks that hold one tile at a time, so that each walks two with copies, sweeps and the cluster's two exchanges in
+// turn, and 24 of the SMs have no block.
 template <typename T, int VEC, bool POST, bool NEXT, int GATE>
 __global__ void __launch_bounds__(stage_threads(VEC), POST ? 1 : 2) block_bwd_stage_kernel(const BlockArgs a, const __grid_constant__ StageMaps maps)
 {
