@@ -42,7 +42,10 @@ EXPORTED = ("gconv_out_shape", "gconv_workspace_size", "gconv_plan", "gconv_fwd"
             "gconv_bwd_weight_ex", "gconv_bwd_bias_ex", "gconv_step_workspace_size_ex", "gconv_step_plan_ex", "gconv_step_ex",
             "gconv_debug_set_step_events", "gconv_debug_set_wgrad_tma",
             "gconv_block_workspace_size", "gconv_norm_fwd", "gconv_norm_bwd", "gconv_join_fwd", "gconv_join_bwd",
-            "gconv_orthogonalize_workspace_size", "gconv_orthogonalize", "gconv_muon_step")
+            "gconv_orthogonalize_workspace_size", "gconv_orthogonalize", "gconv_muon_step",
+            "gconv_causal_workspace_size", "gconv_causal_fwd", "gconv_causal_bwd",
+            "gconv_scan_saved_size", "gconv_scan_workspace_size", "gconv_scan_fwd", "gconv_scan_bwd",
+            "gconv_dropout_fwd", "gconv_dropout_bwd")
 
 GATE_NONE, GATE_FULL, GATE_CHANNEL = range(3)
 ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
@@ -70,6 +73,18 @@ class Muon(ctypes.Structure):
     """The gconv_muon record of include/gconv.h."""
     _fields_ = [(n, ctypes.c_float) for n in ("lr", "beta", "weight_decay", "scale", "eps")] + \
         [("nesterov", ctypes.c_int), ("steps", ctypes.c_int), ("coeffs", ctypes.POINTER(ctypes.c_float))]
+
+
+class Causal(ctypes.Structure):
+    """The gconv_causal record of include/gconv.h."""
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "C", "L", "taps", "act")] + \
+        [(n, ctypes.c_longlong) for n in ("x_batch", "y_batch", "dy_batch", "dx_batch")]
+
+
+class Scan(ctypes.Structure):
+    """The gconv_scan record of include/gconv.h."""
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "C", "L", "groups", "states", "softplus")] + \
+        [(n + "_batch", ctypes.c_longlong) for n in ("u", "delta", "z", "B", "C", "y", "dy", "du", "ddelta", "dz", "dB", "dC")]
 
 
 def per_axis(geom):
@@ -190,6 +205,26 @@ def lib():
     L.gconv_orthogonalize.restype = i
     L.gconv_muon_step.argtypes = [mp, ctypes.POINTER(Muon)] + [vp] * 7 + [sz, vp]
     L.gconv_muon_step.restype = i
+    cp, sp = ctypes.POINTER(Causal), ctypes.POINTER(Scan)
+    L.gconv_causal_workspace_size.argtypes = [cp, i]
+    L.gconv_causal_workspace_size.restype = sz
+    L.gconv_causal_fwd.argtypes = [cp, i] + [vp] * 8
+    L.gconv_causal_fwd.restype = i
+    L.gconv_causal_bwd.argtypes = [cp, i] + [vp] * 12 + [sz, vp]
+    L.gconv_causal_bwd.restype = i
+    L.gconv_scan_saved_size.argtypes = [sp, i, i]
+    L.gconv_scan_saved_size.restype = sz
+    L.gconv_scan_workspace_size.argtypes = [sp, i, i]
+    L.gconv_scan_workspace_size.restype = sz
+    L.gconv_scan_fwd.argtypes = [sp, i] + [vp] * 14 + [sz, vp]
+    L.gconv_scan_fwd.restype = i
+    L.gconv_scan_bwd.argtypes = [sp, i] + [vp] * 22 + [sz, vp]
+    L.gconv_scan_bwd.restype = i
+    ll, db = ctypes.c_longlong, ctypes.c_double
+    L.gconv_dropout_fwd.argtypes = [ll, i, vp, vp, vp, db, vp, vp]
+    L.gconv_dropout_fwd.restype = i
+    L.gconv_dropout_bwd.argtypes = [ll, i, vp, vp, db, vp, vp]
+    L.gconv_dropout_bwd.restype = i
     _lib = L
     return L
 
@@ -735,6 +770,227 @@ def gconv_muon_step(w, grad, momentum, *, w_out=None, m_out=None, w_bf16=None, g
     if st:
         _check(st, "gconv_muon_step")
     return w_out, m_out
+
+
+# ---- sequences: causal convolution and selective scan ------------------------------
+#
+# Activations are [N, C, L], or [N, C, H, W] and [N, C] with L = H W and 1: what follows the channels is one run of
+# positions.  A tensor may be a slice of the channels of a larger one (whole sequences, further apart).
+
+def _positions(shape):
+    if len(shape) < 2:
+        raise ValueError("activations are [N, C, ...]")
+    count = 1
+    for v in shape[2:]:
+        count *= v
+    return count
+
+
+def _sequences(t, shape, dtype, name):
+    """(address, elements between sequences or 0 for dense) of an activation tensor; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must have shape {tuple(shape)} and dtype {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    if t.stride(0) <= 0 or not t[0].is_contiguous():
+        raise ValueError(f"{name} must have contiguous sequences")
+    return t.data_ptr(), t.stride(0)
+
+
+def _lengths(lengths, n):
+    return _like(lengths, torch.Size((n,)), torch.int32, "lengths")
+
+
+@functools.lru_cache(maxsize=1024)
+def _causal_record(N, C, L, taps, act, strides, dt, device):
+    """(record, its reference, workspace bytes of the gradient)."""
+    if act not in ACTS:
+        raise ValueError(f"act is one of {sorted(ACTS)}")
+    rec = Causal(N, C, L, taps, ACTS[act], *strides)
+    need = lib().gconv_causal_workspace_size(ctypes.byref(rec), dt)
+    if need == ctypes.c_size_t(-1).value:
+        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_causal_workspace_size")
+    return rec, ctypes.byref(rec), int(need)
+
+
+def _taps(w, C):
+    """(address, taps) of causal weights [C, K] or, as the convolutions have them, [C, 1, 1, K]."""
+    if w.dim() not in (2, 4) or w.shape[0] != C or w.numel() != C * w.shape[-1]:
+        raise ValueError("w is [C, K] or [C, 1, 1, K]")
+    return _like(w, w.shape, torch.float32, "w"), w.shape[-1]
+
+
+def gconv_causal_workspace_size(x_shape, taps: int, dtype: int) -> int:
+    """Workspace bytes gconv_causal_bwd needs for activations of this shape."""
+    return _causal_record(int(x_shape[0]), int(x_shape[1]), _positions(x_shape), int(taps), "none", (0, 0, 0, 0), int(dtype),
+                          _device_index())[2]
+
+
+def gconv_causal_fwd(x, w, bias, y, *, act="none", state=None, state_out=None, lengths=None, stream=None):
+    """y[t] <- act(bias + sum_k w[k] x[t - K + 1 + k]) for every channel; w: fp32 [C, K], bias: fp32 [C] or
+    None, act: "none" or "silu".  state [N, C, K-1] holds the positions before the first (None: zeros), state_out, which
+    may be state, gets the last ones.  lengths: int32 [N] or None; results behind a sequence's length are zero."""
+    s, d = x.shape, x.dtype
+    dt = dtype_code(d)
+    L = _positions(s)
+    wp, taps = _taps(w, s[1])
+    (xp, xs), (yp, ys) = _sequences(x, s, d, "x"), _sequences(y, s, d, "y")
+    held = torch.Size((s[0], s[1], taps - 1))
+    ref = _causal_record(s[0], s[1], L, taps, act, (xs, ys, 0, 0), dt, x.get_device())[1]
+    st = lib().gconv_causal_fwd(ref, dt, xp, wp, _like(bias, s[1:2], torch.float32, "bias"), _like(state, held, d, "state"),
+                                _lengths(lengths, s[0]), yp, _like(state_out, held, d, "state_out"), _raw_stream(stream))
+    if st:
+        _check(st, "gconv_causal_fwd")
+    return y
+
+
+def gconv_causal_bwd(x, w, bias, dy, dx, dw, dbias=None, *, act="none", state=None, lengths=None, dstate_out=None, dstate=None,
+                     workspace=None, stream=None):
+    """Gradients of gconv_causal_fwd: dx like x, dw and dbias fp32; dstate gets the gradient of state, dstate_out is that of
+    state_out (None: none)."""
+    s, d, f = x.shape, x.dtype, torch.float32
+    dt = dtype_code(d)
+    L = _positions(s)
+    wp, taps = _taps(w, s[1])
+    (xp, xs), (yp, ys), (dp, ds) = _sequences(x, s, d, "x"), _sequences(dy, s, d, "dy"), _sequences(dx, s, d, "dx")
+    held = torch.Size((s[0], s[1], taps - 1))
+    _, ref, need = _causal_record(s[0], s[1], L, taps, act, (xs, 0, ys, ds), dt, x.get_device())
+    ws, sp, sb = _orth_workspace(need, workspace, x.device, stream)
+    st = lib().gconv_causal_bwd(ref, dt, xp, wp, _like(bias, s[1:2], f, "bias"), _like(state, held, d, "state"),
+                                _lengths(lengths, s[0]), yp, _like(dstate_out, held, d, "dstate_out"), dp,
+                                _like(dw, w.shape, f, "dw"), _like(dbias, s[1:2], f, "dbias"), _like(dstate, held, d, "dstate"),
+                                sp, sb, _raw_stream(stream))
+    if st:
+        _check(st, "gconv_causal_bwd")
+    return dx, dw, dbias
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_record(N, C, L, groups, states, softplus, strides, dt, device):
+    """(record, its reference, workspace bytes forward and backward, [N, C, states], [C, states], [C])."""
+    rec = Scan(N, C, L, groups, states, softplus, *strides)
+    need = [lib().gconv_scan_workspace_size(ctypes.byref(rec), dt, back) for back in (0, 1)]
+    if ctypes.c_size_t(-1).value in need:
+        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_scan_workspace_size")
+    return rec, ctypes.byref(rec), int(need[0]), int(need[1]), torch.Size((N, C, states)), torch.Size((C, states)), torch.Size((C,))
+
+
+def _scan_states(B, A, s, groups):
+    """States of B [N, groups * states, positions ...] or [N, groups, states, positions ...]."""
+    states = A.shape[-1]
+    if B.dim() < 2 or B.shape[0] != s[0] or B.numel() != s[0] * groups * states * _positions(s):
+        raise ValueError("B and C are [N, groups * states, ...] with A [C, states]")
+    return states
+
+
+def gconv_scan_saved_size(x_shape, states: int, dtype: int, gated: bool = False) -> int:
+    """Bytes of what gconv_scan_fwd keeps for gconv_scan_bwd."""
+    rec = Scan(int(x_shape[0]), int(x_shape[1]), _positions(x_shape), 1, int(states), 0)
+    n = lib().gconv_scan_saved_size(ctypes.byref(rec), int(dtype), 1 if gated else 0)
+    if n == ctypes.c_size_t(-1).value:
+        raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_scan_saved_size")
+    return int(n)
+
+
+def gconv_scan_workspace_size(x_shape, states: int, dtype: int, groups: int = 1, backward: bool = False) -> int:
+    """Workspace bytes of gconv_scan_fwd or gconv_scan_bwd for activations of this shape."""
+    return _scan_record(int(x_shape[0]), int(x_shape[1]), _positions(x_shape), int(groups), int(states), 0, (0,) * 12, int(dtype),
+                        _device_index())[3 if backward else 2]
+
+
+def _scan_saved(saved, need):
+    if saved is None:
+        return 0
+    if not (saved.is_cuda and saved.is_contiguous()) or saved.numel() * saved.element_size() < need:
+        raise ValueError(f"saved is a contiguous CUDA tensor of at least {need} bytes (gconv_scan_saved_size)")
+    return saved.data_ptr()
+
+
+def gconv_scan_fwd(u, delta, A, B, C, y, *, D=None, z=None, delta_bias=None, softplus=True, groups=1, state=None,
+                   state_out=None, lengths=None, saved=None, workspace=None, stream=None):
+    """The selective scan: with d = softplus(delta + delta_bias), h[t] = exp(d A) h[t-1] + d B[t] u[t] and
+    y <- (sum over the states of C[t] h[t] + D u) silu(z).  A: fp32 [C, states]; B, C: [N, groups * states, positions];
+    D, delta_bias: fp32 [C]; state, state_out (which may be state): fp32 [N, C, states]; lengths: int32 [N].
+    saved (gconv_scan_saved_size bytes) keeps what gconv_scan_bwd needs."""
+    s, d, f, groups = u.shape, u.dtype, torch.float32, int(groups)
+    dt = dtype_code(d)
+    L = _positions(s)
+    states = _scan_states(B, A, s, groups)
+    up, us = _sequences(u, s, d, "u")
+    dp, ds = _sequences(delta, s, d, "delta")
+    zp, zs = _sequences(z, s, d, "z")
+    yp, ys = _sequences(y, s, d, "y")
+    Bp, Bs = _sequences(B, B.shape, d, "B")
+    Cp, Cs = _sequences(C, B.shape, d, "C")
+    _, ref, need, _, full, cs, c = _scan_record(s[0], s[1], L, groups, states, 1 if softplus else 0,
+                                                (us, ds, zs, Bs, Cs, ys, 0, 0, 0, 0, 0, 0), dt, u.get_device())
+    ws, wp, wb = _orth_workspace(need, workspace, u.device, stream)
+    keep = 0 if saved is None else _scan_saved(saved, gconv_scan_saved_size(s, states, dt, z is not None))
+    st = lib().gconv_scan_fwd(ref, dt, up, dp, _like(A, cs, f, "A"), Bp, Cp, _like(D, c, f, "D"), zp,
+                              _like(delta_bias, c, f, "delta_bias"), _like(state, full, f, "state"), _lengths(lengths, s[0]), yp,
+                              _like(state_out, full, f, "state_out"), keep, wp, wb, _raw_stream(stream))
+    if st:
+        _check(st, "gconv_scan_fwd")
+    return y
+
+
+def gconv_scan_bwd(u, delta, A, B, C, dy, saved, du, ddelta, dA, dB, dC, *, D=None, z=None, delta_bias=None, softplus=True,
+                   groups=1, lengths=None, dD=None, dz=None, ddelta_bias=None, dstate_out=None, dstate=None, workspace=None,
+                   stream=None):
+    """Gradients of gconv_scan_fwd from its inputs and what it saved.  du, ddelta, dz like u, dB and dC like B; dA, dD,
+    ddelta_bias fp32; dstate (fp32) gets the gradient of state, dstate_out is that of state_out (None: none)."""
+    s, d, f, groups = u.shape, u.dtype, torch.float32, int(groups)
+    dt = dtype_code(d)
+    L = _positions(s)
+    states = _scan_states(B, A, s, groups)
+    t = {}
+    for name, v, shape in (("u", u, s), ("delta", delta, s), ("z", z, s), ("B", B, B.shape), ("C", C, B.shape), ("dy", dy, s),
+                           ("du", du, s), ("ddelta", ddelta, s), ("dz", dz, s), ("dB", dB, B.shape), ("dC", dC, B.shape)):
+        t[name] = _sequences(v, shape, d, name)
+    strides = tuple(t[k][1] if k else 0 for k in ("u", "delta", "z", "B", "C", None, "dy", "du", "ddelta", "dz", "dB", "dC"))
+    _, ref, _, need, full, cs, c = _scan_record(s[0], s[1], L, groups, states, 1 if softplus else 0, strides, dt, u.get_device())
+    ws, wp, wb = _orth_workspace(need, workspace, u.device, stream)
+    keep = _scan_saved(saved, gconv_scan_saved_size(s, states, dt, z is not None))
+    p = {k: v[0] for k, v in t.items()}
+    st = lib().gconv_scan_bwd(ref, dt, p["u"], p["delta"], _like(A, cs, f, "A"), p["B"], p["C"], _like(D, c, f, "D"), p["z"],
+                              _like(delta_bias, c, f, "delta_bias"), _lengths(lengths, s[0]), keep, p["dy"],
+                              _like(dstate_out, full, f, "dstate_out"), p["du"], p["ddelta"], _like(dA, cs, f, "dA"), p["dB"],
+                              p["dC"], _like(dD, c, f, "dD"), p["dz"], _like(ddelta_bias, c, f, "ddelta_bias"),
+                              _like(dstate, full, f, "dstate"), wp, wb, _raw_stream(stream))
+    if st:
+        _check(st, "gconv_scan_bwd")
+    return du, ddelta
+
+
+# ---- dropout -----------------------------------------------------------------------
+
+def _rng(rng):
+    return _like(rng, torch.Size((2,)), torch.int64, "rng")
+
+
+def gconv_dropout_fwd(x, y, rng, p, *, res=None, stream=None):
+    """y <- x / (1 - p) where kept, else 0, plus res.  rng: int64 CUDA tensor (seed, step), which the mask follows from;
+    use another pair for every tensor and step, and the same for the gradient.  y may be x or res."""
+    s, d = x.shape, x.dtype
+    st = lib().gconv_dropout_fwd(x.numel(), dtype_code(d), _like(x, s, d, "x"), _like(res, s, d, "res"), _rng(rng), p,
+                                 _like(y, s, d, "y"), _raw_stream(stream))
+    if st:
+        _check(st, "gconv_dropout_fwd")
+    return y
+
+
+def gconv_dropout_bwd(dy, dx, rng, p, *, stream=None):
+    """dx <- dy / (1 - p) where the forward call with this rng kept the element, else 0 (the gradient of res is dy)."""
+    s, d = dy.shape, dy.dtype
+    st = lib().gconv_dropout_bwd(dy.numel(), dtype_code(d), _like(dy, s, d, "dy"), _rng(rng), p, _like(dx, s, d, "dx"),
+                                 _raw_stream(stream))
+    if st:
+        _check(st, "gconv_dropout_bwd")
+    return dx
 
 
 # ---- raw pointer level (same C signatures), for callers holding pointers ------

@@ -1,0 +1,407 @@
+// scan.cu -- extern "C" entry points of the selective scan: checks, launch shapes, and the kernels around the scans
+// (short sequences, the join of a sequence's pieces, the gradients' sums over blocks).
+#include "scan_internal.h"
+
+#include <algorithm>
+#include <climits>
+
+namespace gconv {
+
+namespace {
+
+constexpr int kTokenMost = 8;     // positions of the short form
+
+// ---- short sequences ----------------------------------------------------------------
+//
+// What a single new position has to move is its state, 8 bytes a state and channel.  Four lanes share a channel, four
+// neighbouring states each, so that a warp's reads are whole lines; sums over states are two shuffles.
+template <typename T, int LT>
+__global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs a)
+{
+    int64_t id = blockIdx.x;
+    const int cb = (int)(id % a.ncb); id /= a.ncb;
+    const int g = (int)(id % a.G), n = (int)(id / a.G);
+    const int q = threadIdx.x & 3, ch = cb * 32 + (threadIdx.x >> 2);
+    const bool there = ch < a.Cg;
+    const int c = g * a.Cg + (there ? ch : 0);
+    ptx::griddep_wait();
+    const int end = sequence_end(a, n);
+    const T *u = static_cast<const T *>(a.u) + n * a.su + (int64_t)c * a.L;
+    const T *dl = static_cast<const T *>(a.delta) + n * a.sdelta + (int64_t)c * a.L;
+    const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * a.S * a.L;
+    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * a.S * a.L;
+    const float bias = a.bias ? a.bias[c] : 0.f, skip = a.D ? a.D[c] : 0.f;
+    float d[LT], du[LT], out[LT];
+    #pragma unroll
+    for (int t = 0; t < LT; ++t) {
+        const bool on = t < end;
+        float v = on ? to_f(dl[t]) + bias : 0.f;
+        if (a.softplus) v = scan_softplus(v);
+        const float x = on ? to_f(u[t]) : 0.f;
+        d[t] = on ? v : 0.f;
+        du[t] = d[t] * x;
+        out[t] = q == 0 ? skip * x : 0.f;
+    }
+    const int64_t at = ((int64_t)n * a.C + c) * a.S;
+    for (int s0 = 0; s0 < a.S; s0 += 16) {
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s = s0 + q * 4 + j;
+            if (s >= a.S || !there) continue;
+            const float rate = decay_rate(a.A[(int64_t)c * a.S + s]);
+            float h = a.state ? a.state[at + s] : 0.f;
+            if (a.mark) a.mark[((int64_t)n * a.S + s) * a.C + c] = h;
+            #pragma unroll
+            for (int t = 0; t < LT; ++t) {
+                if (t >= end) continue;
+                h = fmaf(ex2(d[t] * rate), h, du[t] * to_f(B[(int64_t)s * a.L + t]));
+                out[t] = fmaf(to_f(Cm[(int64_t)s * a.L + t]), h, out[t]);
+            }
+            if (a.state_out) a.state_out[at + s] = h;
+        }
+    }
+    #pragma unroll
+    for (int t = 0; t < LT; ++t) {
+        out[t] += __shfl_xor_sync(~0u, out[t], 1);
+        out[t] += __shfl_xor_sync(~0u, out[t], 2);
+        if ((t & 3) != q || t >= a.L || !there) continue;
+        const int64_t row = (int64_t)c * a.L + t;
+        float v = out[t];
+        if (a.z && t < end) {
+            if (a.pre) static_cast<T *>(a.pre)[(int64_t)n * a.C * a.L + row] = from_f<T>(v);
+            const float z = to_f(static_cast<const T *>(a.z)[n * a.sz + row]);
+            v *= z * scan_sigmoid(z);
+        }
+        static_cast<T *>(a.y)[n * a.sy + row] = from_f<T>(t < end ? v : 0.f);
+    }
+}
+
+// What enters each piece of a sequence, in place of what leaves it when nothing enters: a thread takes a state of a
+// channel through the pieces, backwards for the gradient.
+__global__ void __launch_bounds__(128) scan_join_kernel(const ScanArgs a, int back)
+{
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (int64_t)a.N * a.S * a.C) return;
+    const int c = (int)(i % a.C), s = (int)(i / a.C % a.S), n = (int)(i / a.C / a.S);
+    ptx::griddep_wait();
+    const float rate = decay_rate(a.A[(int64_t)c * a.S + s]);
+    const float *first = back ? a.dstate_out : a.state;
+    float h = first ? first[((int64_t)n * a.C + c) * a.S + s] : 0.f;
+    for (int k = 0; k < a.chunks; ++k) {
+        const int64_t piece = (int64_t)n * a.chunks + (back ? a.chunks - 1 - k : k);
+        float *at = a.init + (piece * a.S + s) * a.C + c;
+        const float left = *at;
+        *at = h;
+        h = fmaf(ex2(a.dsum[piece * a.C + c] * rate), h, left);
+    }
+}
+
+// ---- sums over the gradient's blocks ------------------------------------------------
+
+struct SumArgs {
+    const float *part, *pA, *pD, *pb;
+    int N, G, ncb, S, C, L, rows;       // rows: of pA, pD and pb
+    unsigned blocks;                    // that add dB and dC; the rest add the parameters' gradients
+    void *dB, *dC;
+    int64_t sdB, sdC;
+    float *dA, *dD, *db;
+    const int *lengths;
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(256) scan_sum_kernel(const SumArgs a)
+{
+    ptx::griddep_wait();
+    if (blockIdx.x < a.blocks) {
+        const int64_t SL = (int64_t)a.S * a.L, per = SL / V;
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        if (i >= (int64_t)a.N * a.G * 2 * per) return;
+        const int64_t e = i % per * V;
+        const int which = (int)(i / per % 2);
+        const int64_t ng = i / per / 2;
+        const int n = (int)(ng / a.G), g = (int)(ng % a.G);
+        int end = a.L;
+        if (a.lengths) end = min(max(a.lengths[n], 0), a.L);
+        const int t = (int)(e % a.L);
+        Pack<float, V> v{};
+        bool any = false;
+        #pragma unroll
+        for (int j = 0; j < V; ++j) any |= (V == 1 ? t : (int)((e + j) % a.L)) < end;
+        if (any) {
+            const float *p = a.part + (ng * a.ncb * 2 + which) * SL + e;
+            #pragma unroll 8
+            for (int b = 0; b < a.ncb; ++b) {
+                const Pack<float, V> x = *reinterpret_cast<const Pack<float, V> *>(p + (int64_t)b * 2 * SL);
+                #pragma unroll
+                for (int j = 0; j < V; ++j) v.v[j] += x.v[j];
+            }
+        }
+        Pack<T, V> o;
+        #pragma unroll
+        for (int j = 0; j < V; ++j) o.v[j] = static_cast<T>((V == 1 ? t : (int)((e + j) % a.L)) < end ? v.v[j] : 0.f);
+        T *to = static_cast<T *>(which ? a.dC : a.dB) + n * (which ? a.sdC : a.sdB) + g * SL + e;
+        *reinterpret_cast<Pack<T, V> *>(to) = o;
+        return;
+    }
+    // 32 columns a block, eight threads a column
+    __shared__ float sh[8][32];
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t CS = (int64_t)a.C * a.S, col = (int64_t)(blockIdx.x - a.blocks) * 32 + lane;
+    const float *p = nullptr;
+    float *to = nullptr;
+    int64_t step = a.C;
+    if (col < CS) { p = a.pA + col; to = a.dA + col; step = CS; }
+    else if (col < CS + a.C) { p = a.pD + (col - CS); to = a.dD ? a.dD + (col - CS) : nullptr; }
+    else if (col < CS + 2 * a.C) { p = a.pb + (col - CS - a.C); to = a.db ? a.db + (col - CS - a.C) : nullptr; }
+    float v = 0.f;
+    if (to)
+        for (int r = k; r < a.rows; r += 8) v += p[r * step];
+    sh[k][lane] = v;
+    __syncthreads();
+    if (k == 0 && to) {
+        #pragma unroll
+        for (int j = 1; j < 8; ++j) v += sh[j][lane];
+        *to = v;
+    }
+}
+
+// ---- checks and shapes ----------------------------------------------------------------
+
+int esize(gconv_dtype dt) { return dt == GCONV_BF16 ? 2 : 4; }
+
+bool check_scan(const gconv_scan *s, gconv_dtype dt)
+{
+    if (!s || (dt != GCONV_F32 && dt != GCONV_BF16)) return false;
+    if (s->N < 0 || s->C < 1 || s->L < 1 || s->groups < 1 || s->C % s->groups) return false;
+    if (s->states < 1 || s->states > kScanMaxStates || s->softplus < 0 || s->softplus > 1) return false;
+    const int64_t CL = (int64_t)s->C * s->L, GSL = (int64_t)s->groups * s->states * s->L;
+    // 2^40 elements a tensor, which also keeps every product below 64 bits
+    if (std::max(CL, GSL) > ((int64_t)1 << 40) / std::max(1, s->N) || (int64_t)s->C * s->states > INT_MAX) return false;
+    for (long long b : {s->u_batch, s->delta_batch, s->z_batch, s->y_batch, s->dy_batch, s->du_batch, s->ddelta_batch, s->dz_batch})
+        if (b != 0 && (b < CL || b > ((int64_t)1 << 40))) return false;
+    for (long long b : {s->B_batch, s->C_batch, s->dB_batch, s->dC_batch})
+        if (b != 0 && (b < GSL || b > ((int64_t)1 << 40))) return false;
+    return true;
+}
+
+int64_t marks_of(const gconv_scan &s) { return (s.L + kScanMark - 1) / kScanMark; }
+
+size_t up16(size_t v) { return (v + 15) / 16 * 16; }
+
+size_t saved_marks(const gconv_scan &s) { return up16((size_t)s.N * marks_of(s) * s.states * s.C * sizeof(float)); }
+
+struct ScanPlan {
+    ScanShape shape, ends;
+    int token;
+    int ncb, sets, chunks, chunk_tiles;
+    size_t o_init, o_dsum, o_part, o_pA, o_pD, o_pb, bytes;
+};
+
+bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
+{
+    *p = ScanPlan{};
+    const int Cg = s.C / s.groups, S = s.states;
+    p->sets = p->chunks = 1;
+    if (!back && s.L <= kTokenMost) {
+        p->token = 1;
+        p->ncb = (Cg + 31) / 32;
+        const int64_t grid = (int64_t)s.N * s.groups * p->ncb;
+        p->shape.grid = (unsigned)grid;
+        return grid <= INT_MAX;
+    }
+    const int form = 0;
+    const ScanForm f = back ? kBwdForms[form] : kFwdForms[form];
+    const int CL = 32 / f.TL, own = CL * f.P, TT = f.TL * f.K;
+    int warps = 4;
+    while (warps > 1 && (warps / 2) * own >= Cg) warps /= 2;
+    const int per = warps * own * p->sets;
+    p->ncb = (Cg + per - 1) / per;
+    const int tiles = (s.L + TT - 1) / TT;
+    p->chunks = 1;
+    p->chunk_tiles = (tiles + p->chunks - 1) / p->chunks;
+    p->chunks = (tiles + p->chunk_tiles - 1) / p->chunk_tiles;
+    const int64_t grid = (int64_t)s.N * s.groups * p->ncb * p->chunks;
+    const int64_t ends_grid = back ? (int64_t)s.N * s.groups * ((Cg + warps * own - 1) / (warps * own)) * p->chunks : grid;
+    if (grid > INT_MAX || ends_grid > INT_MAX) return false;
+    const int row = spots(TT);
+    auto floats = [&](bool ends) -> size_t {
+        if (!back) return (size_t)(ends ? 1 : 2) * kScanStates * row + 3 * (size_t)warps * own * S;
+        if (ends) return (size_t)kScanStates * row + 3 * (size_t)warps * own * S;
+        return (size_t)(2 + 2 * CL) * kScanStates * row + (size_t)warps * own * kScanStates + 4 * (size_t)per * S + 2 * per;
+    };
+    p->shape = {form, warps, 0, (unsigned)grid, floats(false) * 4};
+    p->ends = {form, warps, 0, (unsigned)ends_grid, floats(true) * 4};
+    size_t at = 0;
+    auto take = [&](size_t n) { const size_t was = at; at += up16(n * sizeof(float)); return was; };
+    const size_t pieces = (size_t)s.N * p->chunks;
+    if (p->chunks > 1) {
+        p->o_init = take(pieces * S * s.C);
+        p->o_dsum = take(pieces * s.C);
+    }
+    if (back) {
+        if (p->ncb > 1) p->o_part = take((size_t)s.N * s.groups * p->ncb * 2 * S * s.L);
+        p->o_pA = take(pieces * s.C * S);
+        p->o_pD = take(pieces * s.C);
+        p->o_pb = take(pieces * s.C);
+    }
+    p->bytes = at;
+    return true;
+}
+
+void scan_args(const gconv_scan &s, const ScanPlan &p, void *ws, ScanArgs *a)
+{
+    a->N = s.N; a->C = s.C; a->L = s.L; a->G = s.groups; a->S = s.states; a->Cg = s.C / s.groups;
+    a->softplus = s.softplus;
+    a->ncb = p.ncb; a->sets = p.sets; a->chunks = p.chunks; a->chunk_tiles = p.chunk_tiles;
+    a->marks = (int)marks_of(s);
+    const int64_t CL = (int64_t)s.C * s.L, GSL = (int64_t)s.groups * s.states * s.L;
+    auto step = [](long long b, int64_t dense) { return b ? (int64_t)b : dense; };
+    a->su = step(s.u_batch, CL); a->sdelta = step(s.delta_batch, CL); a->sz = step(s.z_batch, CL); a->sy = step(s.y_batch, CL);
+    a->sB = step(s.B_batch, GSL); a->sC = step(s.C_batch, GSL);
+    a->sdy = step(s.dy_batch, CL); a->sdu = step(s.du_batch, CL); a->sddelta = step(s.ddelta_batch, CL);
+    a->sdz = step(s.dz_batch, CL); a->sdB = step(s.dB_batch, GSL); a->sdC = step(s.dC_batch, GSL);
+    char *w = static_cast<char *>(ws);
+    a->init = reinterpret_cast<float *>(w + p.o_init);
+    a->dsum = reinterpret_cast<float *>(w + p.o_dsum);
+    a->part = reinterpret_cast<float *>(w + p.o_part);
+    a->pA = reinterpret_cast<float *>(w + p.o_pA);
+    a->pD = reinterpret_cast<float *>(w + p.o_pD);
+    a->pb = reinterpret_cast<float *>(w + p.o_pb);
+}
+
+bool on(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// Rows that 16-byte vectors cover: L, the steps between sequences and the addresses are multiples of 16 bytes.
+struct Rows { const void *p; int64_t step; };
+bool vectors(const gconv_scan &s, gconv_dtype dt, std::initializer_list<Rows> rows)
+{
+    const int E = 16 / esize(dt);
+    if (s.L % E) return false;
+    for (const Rows &r : rows)
+        if (!on(r.p, 16) || (s.N > 1 && r.step % E)) return false;
+    return true;
+}
+
+gconv_status done() { return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA; }
+
+}  // namespace
+
+}  // namespace gconv
+
+using namespace gconv;
+
+extern "C" {
+
+size_t gconv_scan_saved_size(const gconv_scan *scan, gconv_dtype dtype, int gated)
+{
+    if (!check_scan(scan, dtype)) return (size_t)-1;
+    return saved_marks(*scan) + (gated ? (size_t)scan->N * scan->C * scan->L * esize(dtype) : 0);
+}
+
+size_t gconv_scan_workspace_size(const gconv_scan *scan, gconv_dtype dtype, int backward)
+{
+    ScanPlan p;
+    if (!check_scan(scan, dtype) || !plan_scan(*scan, backward != 0, &p)) return (size_t)-1;
+    return scan->N ? p.bytes : 0;
+}
+
+gconv_status gconv_scan_fwd(const gconv_scan *scan, gconv_dtype dtype, const void *u, const void *delta, const float *A,
+                            const void *B, const void *C, const float *D, const void *z, const float *delta_bias,
+                            const float *state, const int *lengths, void *y, float *state_out, void *saved, void *workspace,
+                            size_t workspace_bytes, void *stream)
+{
+    ScanPlan p;
+    if (!check_scan(scan, dtype) || !plan_scan(*scan, false, &p)) return GCONV_ERR_INVALID_ARG;
+    if (scan->N == 0) return GCONV_OK;
+    if (!u || !delta || !A || !B || !C || !y) return GCONV_ERR_INVALID_ARG;
+    for (const void *q : {u, delta, B, C, z, (const void *)y})
+        if (!on(q, esize(dtype))) return GCONV_ERR_INVALID_ARG;
+    for (const void *q : {(const void *)A, (const void *)D, (const void *)delta_bias, (const void *)state, (const void *)lengths,
+                          (const void *)state_out})
+        if (!on(q, 4)) return GCONV_ERR_INVALID_ARG;
+    if (!on(saved, 16)) return GCONV_ERR_INVALID_ARG;
+    if (p.bytes && (!workspace || workspace_bytes < p.bytes || !on(workspace, 16))) return GCONV_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    ScanArgs a{};
+    scan_args(*scan, p, workspace, &a);
+    a.u = u; a.delta = delta; a.A = A; a.B = B; a.Cm = C; a.D = D; a.z = z; a.bias = delta_bias; a.state = state;
+    a.lengths = lengths; a.y = y; a.state_out = state_out;
+    a.mark = static_cast<float *>(saved);
+    a.pre = saved && z ? static_cast<char *>(saved) + saved_marks(*scan) : nullptr;
+    if (p.token) {
+        auto *kernel = dtype == GCONV_BF16 ? (scan->L == 1 ? scan_token_kernel<__nv_bfloat16, 1> : scan_token_kernel<__nv_bfloat16, kTokenMost>)
+                                           : (scan->L == 1 ? scan_token_kernel<float, 1> : scan_token_kernel<float, kTokenMost>);
+        launch_dependent(kernel, p.shape.grid, 128u, 0, st, a);
+        return done();
+    }
+    p.shape.vec = p.ends.vec = vectors(*scan, dtype, {{u, a.su}, {delta, a.sdelta}, {z, a.sz}, {B, a.sB}, {C, a.sC}, {y, a.sy},
+                                                      {a.pre, (int64_t)scan->C * scan->L}});
+    auto *start = dtype == GCONV_BF16 ? scan_fwd_bf16 : scan_fwd_f32;
+    if (p.chunks > 1) {
+        start(p.ends, true, a, st);
+        launch_dependent(scan_join_kernel, (unsigned)(((int64_t)a.N * a.S * a.C + 127) / 128), 128u, 0, st, a, 0);
+    }
+    start(p.shape, false, a, st);
+    return done();
+}
+
+gconv_status gconv_scan_bwd(const gconv_scan *scan, gconv_dtype dtype, const void *u, const void *delta, const float *A,
+                            const void *B, const void *C, const float *D, const void *z, const float *delta_bias,
+                            const int *lengths, const void *saved, const void *dy, const float *dstate_out, void *du,
+                            void *ddelta, float *dA, void *dB, void *dC, float *dD, void *dz, float *ddelta_bias, float *dstate,
+                            void *workspace, size_t workspace_bytes, void *stream)
+{
+    ScanPlan p;
+    if (!check_scan(scan, dtype) || !plan_scan(*scan, true, &p)) return GCONV_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((z == nullptr) != (dz == nullptr) || !A || !dA || !on(dA, 4) || !on(dD, 4) || !on(ddelta_bias, 4)) return GCONV_ERR_INVALID_ARG;
+    if (scan->N == 0) {
+        const size_t c = (size_t)scan->C * sizeof(float);
+        if (cudaMemsetAsync(dA, 0, c * scan->states, st) != cudaSuccess || (dD && cudaMemsetAsync(dD, 0, c, st) != cudaSuccess) ||
+            (ddelta_bias && cudaMemsetAsync(ddelta_bias, 0, c, st) != cudaSuccess))
+            return GCONV_ERR_CUDA;
+        return GCONV_OK;
+    }
+    if (!u || !delta || !B || !C || !saved || !dy || !du || !ddelta || !dB || !dC) return GCONV_ERR_INVALID_ARG;
+    for (const void *q : {u, delta, B, C, z, dy, (const void *)du, (const void *)ddelta, (const void *)dB, (const void *)dC,
+                          (const void *)dz})
+        if (!on(q, esize(dtype))) return GCONV_ERR_INVALID_ARG;
+    for (const void *q : {(const void *)A, (const void *)D, (const void *)delta_bias, (const void *)lengths, (const void *)dstate_out,
+                          (const void *)dstate})
+        if (!on(q, 4)) return GCONV_ERR_INVALID_ARG;
+    if (!on(saved, 16)) return GCONV_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < p.bytes || !on(workspace, 16)) return GCONV_ERR_WORKSPACE;
+    ScanArgs a{};
+    scan_args(*scan, p, workspace, &a);
+    a.u = u; a.delta = delta; a.A = A; a.B = B; a.Cm = C; a.D = D; a.z = z; a.bias = delta_bias; a.lengths = lengths;
+    a.mark = const_cast<float *>(static_cast<const float *>(saved));
+    a.pre = z ? const_cast<char *>(static_cast<const char *>(saved)) + saved_marks(*scan) : nullptr;
+    a.dy = dy; a.dstate_out = dstate_out; a.du = du; a.ddelta = ddelta; a.dB = dB; a.dC = dC; a.dz = dz; a.dstate = dstate;
+    p.shape.vec = p.ends.vec = vectors(*scan, dtype, {{u, a.su}, {delta, a.sdelta}, {z, a.sz}, {B, a.sB}, {C, a.sC}, {dy, a.sdy},
+                                                      {du, a.sdu}, {ddelta, a.sddelta}, {dz, a.sdz},
+                                                      {a.pre, (int64_t)scan->C * scan->L}});
+    auto *start = dtype == GCONV_BF16 ? scan_bwd_bf16 : scan_bwd_f32;
+    if (p.chunks > 1) {
+        start(p.ends, true, a, st);
+        launch_dependent(scan_join_kernel, (unsigned)(((int64_t)a.N * a.S * a.C + 127) / 128), 128u, 0, st, a, 1);
+    }
+    start(p.shape, false, a, st);
+    SumArgs f{};
+    f.part = a.part; f.pA = a.pA; f.pD = a.pD; f.pb = a.pb;
+    f.N = a.N; f.G = a.G; f.ncb = p.ncb; f.S = a.S; f.C = a.C; f.L = a.L; f.rows = a.N * p.chunks;
+    f.dB = dB; f.dC = dC; f.sdB = a.sdB; f.sdC = a.sdC; f.dA = dA; f.dD = dD; f.db = ddelta_bias; f.lengths = lengths;
+    const size_t v4 = 4 * esize(dtype);
+    const bool four = (int64_t)a.S * a.L % 4 == 0 && on(dB, v4) && on(dC, v4) && (a.N == 1 || (a.sdB % 4 == 0 && a.sdC % 4 == 0));
+    if (p.ncb > 1) {
+        const int64_t items = (int64_t)a.N * a.G * 2 * a.S * a.L / (four ? 4 : 1);
+        if ((items + 255) / 256 > INT_MAX) return GCONV_ERR_INVALID_ARG;
+        f.blocks = (unsigned)((items + 255) / 256);
+    }
+    const unsigned grid = f.blocks + (unsigned)(((int64_t)a.C * (a.S + 2) + 31) / 32);
+    auto *sum = dtype == GCONV_BF16 ? (four ? scan_sum_kernel<__nv_bfloat16, 4> : scan_sum_kernel<__nv_bfloat16, 1>)
+                                    : (four ? scan_sum_kernel<float, 4> : scan_sum_kernel<float, 1>);
+    launch_dependent(sum, grid, 256u, 0, st, f);
+    return done();
+}
+
+}  // extern "C"

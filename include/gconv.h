@@ -339,6 +339,105 @@ gconv_status gconv_muon_step(const gconv_matrices *matrices, const gconv_muon *o
                              const float *momentum, float *w_out, float *momentum_out, void *w_bf16, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* ---- Causal convolution -----------------------------------------------------------
+ *
+ * The depthwise convolution along the positions of a sequence that looks back only: with K = taps, for every
+ * sequence n and channel c,
+ *
+ *   y[t] = act(bias + sum over k < K of w[k] x[t - K + 1 + k])      x[-j] = state[K - 1 - j], or zero
+ *
+ * and state_out the last K - 1 of (state, x), with which the next call goes on where this one stopped.
+ * x, y: dtype [N][C][L] (planes of L = H W positions in the order they have in memory); w: fp32 [C][K]; bias:
+ * fp32 [C] (NULL: 0); state, state_out: dtype [N][C][K-1] (ignored where K is 1).  The *_batch members and
+ * `lengths` are those of the scan below: elements between sequences (0: dense), and positions of each
+ * (device, or NULL); what lies behind them is not used, and y and dx are zero there.  Sums are fp32, results are rounded once,
+ * and every reduction has a fixed order.
+ * Requirements: C, L >= 1, N >= 0, 1 <= taps <= 8, act GCONV_ACT_NONE or GCONV_ACT_SILU, tensors of at most 2^40
+ * elements, pointers aligned to their elements (the workspace to 16 bytes; tensors whose rows begin at the same place
+ * within 16 bytes are faster).  The record is read during the call only. */
+typedef struct {
+    int N, C, L, taps, act;
+    long long x_batch, y_batch, dy_batch, dx_batch;      /* the last two are read by gconv_causal_bwd only */
+} gconv_causal;
+
+size_t gconv_causal_workspace_size(const gconv_causal *causal, gconv_dtype dtype);   /* of gconv_causal_bwd; (size_t)-1: invalid */
+
+/* y, and state_out unless it is NULL; state_out may be state.  N == 0 is a no-op.  Other outputs of these calls must not
+ * overlap inputs or each other. */
+gconv_status gconv_causal_fwd(const gconv_causal *causal, gconv_dtype dtype, const void *x, const float *w, const float *bias,
+                              const void *state, const int *lengths, void *y, void *state_out, void *stream);
+
+/* With dv = dy act'(v):  dx[t] = sum over k of w[k] dv[t + K - 1 - k],  dw[k] = sum of dv[t] x[t - K + 1 + k],
+ * dbias = sum of dv (may be NULL); dstate (may be NULL) is the gradient of state, and dstate_out (NULL: none) that of state_out,
+ * both dtype [N][C][K-1].  dw, dbias: fp32.  N == 0 sets dw and dbias to zero. */
+gconv_status gconv_causal_bwd(const gconv_causal *causal, gconv_dtype dtype, const void *x, const float *w, const float *bias,
+                              const void *state, const int *lengths, const void *dy, const void *dstate_out, void *dx,
+                              float *dw, float *dbias, void *dstate, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Selective scan --------------------------------------------------------------
+ *
+ * The recurrence of a selective state space layer along the L positions of each sequence, in the
+ * layout of the convolutions (a sequence is a plane: L = H W positions in the order they have in memory; group g of `groups` owns
+ * C/groups consecutive channels, which share `states` channels of B and of C).  For every sequence n,
+ * channel c and state s, with d[t] = softplus(delta[t] + delta_bias) (softplus 0: delta[t] + delta_bias):
+ *
+ *   h[t] = exp(d[t] A) h[t-1] + d[t] u[t] B[t]        h[-1] = state, or zero
+ *   y[t] = (sum over s of C[t] h[t] + D u[t]) silu(z[t])     without z: no gate
+ *
+ * u, delta, z, y: dtype [N][C][L]; B, C: dtype [N][groups][states][L]; A: fp32 [C][states]; D, delta_bias:
+ * fp32 [C] (NULL: 0); state, state_out: fp32 [N][C][states].  Sequences may lie further apart than C L (or
+ * groups states L) elements: the *_batch members give the elements from one to the next, 0 standing for
+ * dense, so that halves of one tensor are read and written in place.
+ * lengths (device, [N], or NULL: L): sequence n has min(max(lengths[n], 0), L) positions.  What lies behind
+ * them is not used; y and the gradients are zero there, and state_out is the state after the last of them
+ * (of none: the state that came in).
+ * States, sums and exponentials are fp32 whatever dtype is; a result is rounded once.  Bitwise reproducible.
+ * Requirements: C, L, groups, states >= 1, N >= 0, C divisible by groups, states <= 256, C states below 2^31,
+ * tensors of at most 2^40 elements, pointers aligned to their elements (those of saved and workspace
+ * to 16 bytes; rows of a multiple of 16 bytes on 16-byte boundaries are faster).  The record is read during the
+ * call only.  N == 0 is a no-op (the gradients of A, D and delta_bias are set to zero). */
+typedef struct {
+    int N, C, L, groups, states, softplus;
+    long long u_batch, delta_batch, z_batch, B_batch, C_batch, y_batch;
+    long long dy_batch, du_batch, ddelta_batch, dz_batch, dB_batch, dC_batch;   /* read by gconv_scan_bwd only */
+} gconv_scan;
+
+/* Bytes that gconv_scan_fwd keeps for gconv_scan_bwd (states at intervals and, with a gate, the sums before it, in
+ * dtype: the one value of the gradient dz that is rounded twice), and workspace bytes of either call ((size_t)-1: invalid). */
+size_t gconv_scan_saved_size(const gconv_scan *scan, gconv_dtype dtype, int gated);
+size_t gconv_scan_workspace_size(const gconv_scan *scan, gconv_dtype dtype, int backward);
+
+/* y, and unless NULL state_out and saved (what the gradient needs).  state_out may be state; other outputs must not
+ * overlap inputs or each other.  With L = 1 and a state it is the step for a single new position. */
+gconv_status gconv_scan_fwd(const gconv_scan *scan, gconv_dtype dtype, const void *u, const void *delta, const float *A,
+                            const void *B, const void *C, const float *D, const void *z, const float *delta_bias,
+                            const float *state, const int *lengths, void *y, float *state_out, void *saved, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Gradients, from the same inputs, the forward call's `saved`, dy, and dstate_out (gradient of state_out, or NULL).  dz is
+ * NULL exactly when z is; dD, ddelta_bias and dstate (gradient of state) may be NULL.  du, ddelta, dz, dB, dC: dtype, like
+ * their tensors; the others fp32. */
+gconv_status gconv_scan_bwd(const gconv_scan *scan, gconv_dtype dtype, const void *u, const void *delta, const float *A,
+                            const void *B, const void *C, const float *D, const void *z, const float *delta_bias,
+                            const int *lengths, const void *saved, const void *dy, const float *dstate_out, void *du,
+                            void *ddelta, float *dA, void *dB, void *dC, float *dD, void *dz, float *ddelta_bias, float *dstate,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Dropout ------------------------------------------------------------------------
+ *
+ * y = keep x / (1 - p) + res (res may be NULL) over `count` elements in memory order, and its gradient dx = keep dy / (1 - p) (that
+ * of res is dy).  The mask is made again from `rng` = (seed, step), two 64-bit integers on the device: element
+ * e is kept when word e % 4 of the Philox-4x32-10 generator (Salmon et al., 2011) at counter (e / 4, step) with key seed is at
+ * least floor(p 2^32); 1 / (1 - p) is taken of that share.  A program uses another (seed, step) for every tensor and training step, and
+ * the forward call's for the gradient; as both are read when the kernel runs, a captured call can be replayed
+ * with other values.  A dropped element gives exactly 0 (+ res), whatever x is.  fp32 arithmetic, one rounding.
+ * Requirements: 0 <= count <= 2^40, 0 <= p <= 1, pointers aligned to their elements (to 16 bytes: faster).  y may be x or
+ * res, and dx dy. */
+gconv_status gconv_dropout_fwd(long long count, gconv_dtype dtype, const void *x, const void *res, const long long *rng, double p,
+                               void *y, void *stream);
+gconv_status gconv_dropout_bwd(long long count, gconv_dtype dtype, const void *dy, const long long *rng, double p, void *dx,
+                               void *stream);
+
 /* Weight gradient that allocates nothing, for callers that cannot allocate device
  * memory themselves: code embedded in a host application that owns every
  * device allocation through its own pool or budget (plug-ins, engines with a
