@@ -778,6 +778,8 @@ def gconv_muon_step(w, grad, momentum, *, w_out=None, m_out=None, w_bf16=None, g
 # positions.  A tensor may be a slice of the channels of a larger one (whole sequences, further apart).
 
 def _positions(shape):
+    if len(shape) == 3:
+        return shape[2]
     if len(shape) < 2:
         raise ValueError("activations are [N, C, ...]")
     count = 1
@@ -790,7 +792,7 @@ def _sequences(t, shape, dtype, name):
     """(address, elements between sequences or 0 for dense) of an activation tensor; (0, 0) for None."""
     if t is None:
         return 0, 0
-    if t.shape != shape or t.dtype != dtype:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} and dtype {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -802,46 +804,38 @@ def _sequences(t, shape, dtype, name):
 
 
 def _lengths(lengths, n):
-    return _like(lengths, torch.Size((n,)), torch.int32, "lengths")
+    return 0 if lengths is None else _like(lengths, torch.Size((n,)), torch.int32, "lengths")
 
 
 @functools.lru_cache(maxsize=1024)
-def _causal_record(N, C, L, taps, act, strides, dt, device):
-    """(record, its reference, workspace bytes of the gradient)."""
+def _causal_record(shape, w_shape, act, strides, dt, device):
+    """(record, its reference, workspace bytes of the gradient, [C], [N, C, K-1])."""
+    if len(w_shape) not in (2, 4) or w_shape[0] != shape[1] or w_shape.numel() != shape[1] * w_shape[-1]:
+        raise ValueError("w is [C, K] or [C, 1, 1, K]")
     if act not in ACTS:
         raise ValueError(f"act is one of {sorted(ACTS)}")
+    N, C, L, taps = shape[0], shape[1], _positions(shape), w_shape[-1]
     rec = Causal(N, C, L, taps, ACTS[act], *strides)
     need = lib().gconv_causal_workspace_size(ctypes.byref(rec), dt)
     if need == ctypes.c_size_t(-1).value:
         raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_causal_workspace_size")
-    return rec, ctypes.byref(rec), int(need)
-
-
-def _taps(w, C):
-    """(address, taps) of causal weights [C, K] or, as the convolutions have them, [C, 1, 1, K]."""
-    if w.dim() not in (2, 4) or w.shape[0] != C or w.numel() != C * w.shape[-1]:
-        raise ValueError("w is [C, K] or [C, 1, 1, K]")
-    return _like(w, w.shape, torch.float32, "w"), w.shape[-1]
+    return rec, ctypes.byref(rec), int(need), torch.Size((C,)), torch.Size((N, C, taps - 1))
 
 
 def gconv_causal_workspace_size(x_shape, taps: int, dtype: int) -> int:
     """Workspace bytes gconv_causal_bwd needs for activations of this shape."""
-    return _causal_record(int(x_shape[0]), int(x_shape[1]), _positions(x_shape), int(taps), "none", (0, 0, 0, 0), int(dtype),
-                          _device_index())[2]
+    return _causal_record(torch.Size(x_shape), torch.Size((x_shape[1], taps)), "none", (0, 0, 0, 0), int(dtype), _device_index())[2]
 
 
 def gconv_causal_fwd(x, w, bias, y, *, act="none", state=None, state_out=None, lengths=None, stream=None):
     """y[t] <- act(bias + sum_k w[k] x[t - K + 1 + k]) for every channel; w: fp32 [C, K], bias: fp32 [C] or
     None, act: "none" or "silu".  state [N, C, K-1] holds the positions before the first (None: zeros), state_out, which
     may be state, gets the last ones.  lengths: int32 [N] or None; results behind a sequence's length are zero."""
-    s, d = x.shape, x.dtype
-    dt = dtype_code(d)
-    L = _positions(s)
-    wp, taps = _taps(w, s[1])
+    s, d, ws, f = x.shape, x.dtype, w.shape, torch.float32
+    dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
     (xp, xs), (yp, ys) = _sequences(x, s, d, "x"), _sequences(y, s, d, "y")
-    held = torch.Size((s[0], s[1], taps - 1))
-    ref = _causal_record(s[0], s[1], L, taps, act, (xs, ys, 0, 0), dt, x.get_device())[1]
-    st = lib().gconv_causal_fwd(ref, dt, xp, wp, _like(bias, s[1:2], torch.float32, "bias"), _like(state, held, d, "state"),
+    _, ref, _, c, held = _causal_record(s, ws, act, (xs, ys, 0, 0), dt, x.get_device())
+    st = lib().gconv_causal_fwd(ref, dt, xp, _like(w, ws, f, "w"), _like(bias, c, f, "bias"), _like(state, held, d, "state"),
                                 _lengths(lengths, s[0]), yp, _like(state_out, held, d, "state_out"), _raw_stream(stream))
     if st:
         _check(st, "gconv_causal_fwd")
@@ -852,39 +846,33 @@ def gconv_causal_bwd(x, w, bias, dy, dx, dw, dbias=None, *, act="none", state=No
                      workspace=None, stream=None):
     """Gradients of gconv_causal_fwd: dx like x, dw and dbias fp32; dstate gets the gradient of state, dstate_out is that of
     state_out (None: none)."""
-    s, d, f = x.shape, x.dtype, torch.float32
-    dt = dtype_code(d)
-    L = _positions(s)
-    wp, taps = _taps(w, s[1])
+    s, d, ws, f = x.shape, x.dtype, w.shape, torch.float32
+    dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
     (xp, xs), (yp, ys), (dp, ds) = _sequences(x, s, d, "x"), _sequences(dy, s, d, "dy"), _sequences(dx, s, d, "dx")
-    held = torch.Size((s[0], s[1], taps - 1))
-    _, ref, need = _causal_record(s[0], s[1], L, taps, act, (xs, 0, ys, ds), dt, x.get_device())
-    ws, sp, sb = _orth_workspace(need, workspace, x.device, stream)
-    st = lib().gconv_causal_bwd(ref, dt, xp, wp, _like(bias, s[1:2], f, "bias"), _like(state, held, d, "state"),
-                                _lengths(lengths, s[0]), yp, _like(dstate_out, held, d, "dstate_out"), dp,
-                                _like(dw, w.shape, f, "dw"), _like(dbias, s[1:2], f, "dbias"), _like(dstate, held, d, "dstate"),
-                                sp, sb, _raw_stream(stream))
+    _, ref, need, c, held = _causal_record(s, ws, act, (xs, 0, ys, ds), dt, x.get_device())
+    hold, sp, sb = _orth_workspace(need, workspace, x.device, stream)
+    st = lib().gconv_causal_bwd(ref, dt, xp, _like(w, ws, f, "w"), _like(bias, c, f, "bias"), _like(state, held, d, "state"),
+                                _lengths(lengths, s[0]), yp, _like(dstate_out, held, d, "dstate_out"), dp, _like(dw, ws, f, "dw"),
+                                _like(dbias, c, f, "dbias"), _like(dstate, held, d, "dstate"), sp, sb, _raw_stream(stream))
     if st:
         _check(st, "gconv_causal_bwd")
     return dx, dw, dbias
 
 
 @functools.lru_cache(maxsize=1024)
-def _scan_record(N, C, L, groups, states, softplus, strides, dt, device):
-    """(record, its reference, workspace bytes forward and backward, [N, C, states], [C, states], [C])."""
+def _scan_record(shape, B_shape, states, groups, softplus, strides, dt, device):
+    """(record, its reference, workspace bytes forward and backward, bytes saved without and with a gate, [C], [C, states],
+    [N, C, states])."""
+    N, C, L = shape[0], shape[1], _positions(shape)
+    if len(B_shape) < 2 or B_shape[0] != N or B_shape.numel() != N * groups * states * L:
+        raise ValueError("B and C are [N, groups * states, ...] with A [C, states]")
     rec = Scan(N, C, L, groups, states, softplus, *strides)
-    need = [lib().gconv_scan_workspace_size(ctypes.byref(rec), dt, back) for back in (0, 1)]
+    ref = ctypes.byref(rec)
+    need = [lib().gconv_scan_workspace_size(ref, dt, back) for back in (0, 1)] + \
+        [lib().gconv_scan_saved_size(ref, dt, gated) for gated in (0, 1)]
     if ctypes.c_size_t(-1).value in need:
         raise GconvError(GCONV_ERR_INVALID_ARG, "gconv_scan_workspace_size")
-    return rec, ctypes.byref(rec), int(need[0]), int(need[1]), torch.Size((N, C, states)), torch.Size((C, states)), torch.Size((C,))
-
-
-def _scan_states(B, A, s, groups):
-    """States of B [N, groups * states, positions ...] or [N, groups, states, positions ...]."""
-    states = A.shape[-1]
-    if B.dim() < 2 or B.shape[0] != s[0] or B.numel() != s[0] * groups * states * _positions(s):
-        raise ValueError("B and C are [N, groups * states, ...] with A [C, states]")
-    return states
+    return rec, ref, *map(int, need), torch.Size((C,)), torch.Size((C, states)), torch.Size((N, C, states))
 
 
 def gconv_scan_saved_size(x_shape, states: int, dtype: int, gated: bool = False) -> int:
@@ -898,13 +886,12 @@ def gconv_scan_saved_size(x_shape, states: int, dtype: int, gated: bool = False)
 
 def gconv_scan_workspace_size(x_shape, states: int, dtype: int, groups: int = 1, backward: bool = False) -> int:
     """Workspace bytes of gconv_scan_fwd or gconv_scan_bwd for activations of this shape."""
-    return _scan_record(int(x_shape[0]), int(x_shape[1]), _positions(x_shape), int(groups), int(states), 0, (0,) * 12, int(dtype),
-                        _device_index())[3 if backward else 2]
+    s = torch.Size(x_shape)
+    B = torch.Size((s[0], groups * states, _positions(s)))
+    return _scan_record(s, B, int(states), int(groups), 0, (0,) * 12, int(dtype), _device_index())[3 if backward else 2]
 
 
 def _scan_saved(saved, need):
-    if saved is None:
-        return 0
     if not (saved.is_cuda and saved.is_contiguous()) or saved.numel() * saved.element_size() < need:
         raise ValueError(f"saved is a contiguous CUDA tensor of at least {need} bytes (gconv_scan_saved_size)")
     return saved.data_ptr()
@@ -916,23 +903,21 @@ def gconv_scan_fwd(u, delta, A, B, C, y, *, D=None, z=None, delta_bias=None, sof
     y <- (sum over the states of C[t] h[t] + D u) silu(z).  A: fp32 [C, states]; B, C: [N, groups * states, positions];
     D, delta_bias: fp32 [C]; state, state_out (which may be state): fp32 [N, C, states]; lengths: int32 [N].
     saved (gconv_scan_saved_size bytes) keeps what gconv_scan_bwd needs."""
-    s, d, f, groups = u.shape, u.dtype, torch.float32, int(groups)
-    dt = dtype_code(d)
-    L = _positions(s)
-    states = _scan_states(B, A, s, groups)
+    s, d, bs, f = u.shape, u.dtype, B.shape, torch.float32
+    dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
     up, us = _sequences(u, s, d, "u")
     dp, ds = _sequences(delta, s, d, "delta")
     zp, zs = _sequences(z, s, d, "z")
     yp, ys = _sequences(y, s, d, "y")
-    Bp, Bs = _sequences(B, B.shape, d, "B")
-    Cp, Cs = _sequences(C, B.shape, d, "C")
-    _, ref, need, _, full, cs, c = _scan_record(s[0], s[1], L, groups, states, 1 if softplus else 0,
-                                                (us, ds, zs, Bs, Cs, ys, 0, 0, 0, 0, 0, 0), dt, u.get_device())
-    ws, wp, wb = _orth_workspace(need, workspace, u.device, stream)
-    keep = 0 if saved is None else _scan_saved(saved, gconv_scan_saved_size(s, states, dt, z is not None))
+    Bp, Bs = _sequences(B, bs, d, "B")
+    Cp, Cs = _sequences(C, bs, d, "C")
+    _, ref, need, _, plain, gated, c, cs, full = _scan_record(s, bs, A.shape[-1], int(groups), 1 if softplus else 0,
+                                                              (us, ds, zs, Bs, Cs, ys, 0, 0, 0, 0, 0, 0), dt, u.get_device())
+    hold, wp, wb = _orth_workspace(need, workspace, u.device, stream)
     st = lib().gconv_scan_fwd(ref, dt, up, dp, _like(A, cs, f, "A"), Bp, Cp, _like(D, c, f, "D"), zp,
                               _like(delta_bias, c, f, "delta_bias"), _like(state, full, f, "state"), _lengths(lengths, s[0]), yp,
-                              _like(state_out, full, f, "state_out"), keep, wp, wb, _raw_stream(stream))
+                              _like(state_out, full, f, "state_out"),
+                              0 if saved is None else _scan_saved(saved, plain if z is None else gated), wp, wb, _raw_stream(stream))
     if st:
         _check(st, "gconv_scan_fwd")
     return y
@@ -943,24 +928,21 @@ def gconv_scan_bwd(u, delta, A, B, C, dy, saved, du, ddelta, dA, dB, dC, *, D=No
                    stream=None):
     """Gradients of gconv_scan_fwd from its inputs and what it saved.  du, ddelta, dz like u, dB and dC like B; dA, dD,
     ddelta_bias fp32; dstate (fp32) gets the gradient of state, dstate_out is that of state_out (None: none)."""
-    s, d, f, groups = u.shape, u.dtype, torch.float32, int(groups)
-    dt = dtype_code(d)
-    L = _positions(s)
-    states = _scan_states(B, A, s, groups)
-    t = {}
-    for name, v, shape in (("u", u, s), ("delta", delta, s), ("z", z, s), ("B", B, B.shape), ("C", C, B.shape), ("dy", dy, s),
-                           ("du", du, s), ("ddelta", ddelta, s), ("dz", dz, s), ("dB", dB, B.shape), ("dC", dC, B.shape)):
-        t[name] = _sequences(v, shape, d, name)
-    strides = tuple(t[k][1] if k else 0 for k in ("u", "delta", "z", "B", "C", None, "dy", "du", "ddelta", "dz", "dB", "dC"))
-    _, ref, _, need, full, cs, c = _scan_record(s[0], s[1], L, groups, states, 1 if softplus else 0, strides, dt, u.get_device())
-    ws, wp, wb = _orth_workspace(need, workspace, u.device, stream)
-    keep = _scan_saved(saved, gconv_scan_saved_size(s, states, dt, z is not None))
-    p = {k: v[0] for k, v in t.items()}
-    st = lib().gconv_scan_bwd(ref, dt, p["u"], p["delta"], _like(A, cs, f, "A"), p["B"], p["C"], _like(D, c, f, "D"), p["z"],
-                              _like(delta_bias, c, f, "delta_bias"), _lengths(lengths, s[0]), keep, p["dy"],
-                              _like(dstate_out, full, f, "dstate_out"), p["du"], p["ddelta"], _like(dA, cs, f, "dA"), p["dB"],
-                              p["dC"], _like(dD, c, f, "dD"), p["dz"], _like(ddelta_bias, c, f, "ddelta_bias"),
-                              _like(dstate, full, f, "dstate"), wp, wb, _raw_stream(stream))
+    s, d, bs, f = u.shape, u.dtype, B.shape, torch.float32
+    dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
+    t = [_sequences(v, shape, d, name) for name, v, shape in
+         (("u", u, s), ("delta", delta, s), ("z", z, s), ("B", B, bs), ("C", C, bs), ("dy", dy, s), ("du", du, s),
+          ("ddelta", ddelta, s), ("dz", dz, s), ("dB", dB, bs), ("dC", dC, bs))]
+    (up, us), (dp, ds), (zp, zs), (Bp, Bs), (Cp, Cs), (gp, gs), (dup, dus), (ddp, dds), (dzp, dzs), (dBp, dBs), (dCp, dCs) = t
+    _, ref, _, need, plain, gated, c, cs, full = _scan_record(s, bs, A.shape[-1], int(groups), 1 if softplus else 0,
+                                                              (us, ds, zs, Bs, Cs, 0, gs, dus, dds, dzs, dBs, dCs), dt,
+                                                              u.get_device())
+    hold, wp, wb = _orth_workspace(need, workspace, u.device, stream)
+    st = lib().gconv_scan_bwd(ref, dt, up, dp, _like(A, cs, f, "A"), Bp, Cp, _like(D, c, f, "D"), zp,
+                              _like(delta_bias, c, f, "delta_bias"), _lengths(lengths, s[0]),
+                              _scan_saved(saved, plain if z is None else gated), gp, _like(dstate_out, full, f, "dstate_out"), dup,
+                              ddp, _like(dA, cs, f, "dA"), dBp, dCp, _like(dD, c, f, "dD"), dzp,
+                              _like(ddelta_bias, c, f, "ddelta_bias"), _like(dstate, full, f, "dstate"), wp, wb, _raw_stream(stream))
     if st:
         _check(st, "gconv_scan_bwd")
     return du, ddelta

@@ -3,10 +3,12 @@
 //   v[t] = bias + sum_k w[k] x[t - K + 1 + k],   y = act(v),   x before position 0 from the state
 //   dv = dy act'(v),   dx[t] = sum_k w[k] dv[t + K - 1 - k],   dw[k] = sum dv[t] x[t - K + 1 + k],   db = sum dv
 //
-// Two or three tensors go through once, at 2 K + 8 operations an element, so memory bounds it: every access is 16 bytes.
-// A thread takes the elements of one row (channel of a sequence) that lie in one aligned 16-byte piece of memory, so rows of
-// odd length, which begin anywhere, are read in whole pieces too; only a row's two ends go element by element.  What
-// the window needs from the pieces beside it is read again (from L1).
+// Two or three tensors go through once, at 2 K + 8 operations an element (6 K + 12 for the gradients), so memory bounds it:
+// every access is 16 bytes.  A lane takes the elements of one row (channel of a sequence) that lie in one or two
+// neighbouring 16-byte pieces of memory, so rows of odd length, which begin anywhere, are read in whole pieces too; only a row's
+// two ends go element by element.  What the window needs from the piece before is read again (from L1).
+// TX lanes (a power of two, a warp where rows are long) are a worker: it keeps a channel's weights, and its sums for their
+// gradients, over its share of the sequences and their pieces.
 #include "scan.cuh"
 
 #include <algorithm>
@@ -18,12 +20,12 @@ namespace {
 
 constexpr int kCausalMost = 8;          // taps
 constexpr int kCausalShort = 4;         // positions of the form with one thread a row
-constexpr int kCausalThreads = 256;
+constexpr int kCausalThreads = 128;
+constexpr int kCausalBack = 8;          // elements a lane of the gradient
 
 struct CausalArgs {
     int N, C, L, act;
-    int TX, segs;                       // threads of a row in a block (a power of two), pieces of a row
-    int splits;                         // gradient: blocks that share a channel
+    int TX, segs, splits;               // lanes of a worker, pieces of a row, workers that share a channel
     const void *x, *y, *dy;
     int64_t sx, sy, sdy, sdx;
     const float *w, *bias;
@@ -43,58 +45,86 @@ __device__ __forceinline__ int causal_end(const CausalArgs &a, int n)
     return v < 0 ? 0 : v < a.L ? v : a.L;
 }
 
-// Elements t .. t + V - 1 of a row, zeros outside [0, end); an address on 16 bytes where VEC.
-template <typename T, int V, bool VEC>
-__device__ __forceinline__ void load_piece(const T *row, int t, int end, float (&v)[V])
+// Elements t .. t + M - 1 of a row, zeros outside [0, end): the slow way, for a row's ends.
+template <typename T, int M>
+__device__ __forceinline__ void load_some(const T *row, int t, int end, float *v)
 {
-    if (VEC && t >= 0 && t + V <= end) {
-        const Pack<T, V> x = *reinterpret_cast<const Pack<T, V> *>(row + t);
-        #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = to_f(x.v[j]);
-    } else {
-        #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = t + j >= 0 && t + j < end ? to_f(row[t + j]) : 0.f;
-    }
+    #pragma unroll
+    for (int j = 0; j < M; ++j) v[j] = t + j >= 0 && t + j < end ? to_f(row[t + j]) : 0.f;
 }
 
-template <typename T, int V, bool VEC>
-__device__ __forceinline__ void store_piece(T *row, int t, int L, const float (&v)[V])
+// Elements t .. t + M - 1 to a row of L; an address on 16 bytes where VEC.
+template <typename T, int M, bool VEC>
+__device__ __forceinline__ void store_pieces(T *row, int t, int L, const float (&v)[M])
 {
-    if (VEC && t >= 0 && t + V <= L) {
-        Pack<T, V> x;
+    constexpr int V = 16 / (int)sizeof(T);
+    if (VEC && t >= 0 && t + M <= L) {
         #pragma unroll
-        for (int j = 0; j < V; ++j) x.v[j] = from_f<T>(v[j]);
-        *reinterpret_cast<Pack<T, V> *>(row + t) = x;
+        for (int i = 0; i < M; i += V) {
+            Pack<T, V> x;
+            #pragma unroll
+            for (int j = 0; j < V; j += 2) put2(x.v + j, v[i + j], v[i + j + 1]);
+            *reinterpret_cast<Pack<T, V> *>(row + t + i) = x;
+        }
     } else {
         #pragma unroll
-        for (int j = 0; j < V; ++j)
+        for (int j = 0; j < M; ++j)
             if (t + j >= 0 && t + j < L) row[t + j] = from_f<T>(v[j]);
     }
 }
 
-// win[i]: x at t - H + i for i < H + V (zeros outside the sequence, the state before it).
-template <typename T, int V, int H, bool VEC>
-__device__ __forceinline__ void load_window(const T *row, const T *state, int t, int end, float (&win)[H + V])
+// win[i]: x at t - H + i for i < H + M (zeros outside the sequence, the state before it); d, unless `other` is null: another
+// tensor's M elements from t.  All the loads are on their way before the first is used.
+template <typename T, int M, int H, bool VEC>
+__device__ __forceinline__ void load_window(const T *row, const T *state, int t, int end, float (&win)[H + M], const T *other, float *d)
 {
-    float cur[V];
-    load_piece<T, V, VEC>(row, t, end, cur);
-    #pragma unroll
-    for (int j = 0; j < V; ++j) win[H + j] = cur[j];
-    #pragma unroll
-    for (int b = 1; b <= (H + V - 1) / V; ++b) {
-        float old[V];
-        load_piece<T, V, VEC>(row, t - b * V, end, old);
+    constexpr int V = 16 / (int)sizeof(T), BACK = (H + V - 1) / V;      // pieces before t
+    const bool inside = VEC && t >= 0 && t + M <= end, behind = VEC && t >= BACK * V;
+    Pack<T, V> p[BACK ? BACK : 1], x[M / V], o[M / V];
+    if (inside) {
         #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (H - b * V + j >= 0) win[H - b * V + j] = old[j];
+        for (int i = 0; i < M / V; ++i) x[i] = *reinterpret_cast<const Pack<T, V> *>(row + t + i * V);
+        if (other) {
+            #pragma unroll
+            for (int i = 0; i < M / V; ++i) o[i] = *reinterpret_cast<const Pack<T, V> *>(other + t + i * V);
+        }
     }
-    if (state) {
+    if (behind) {
         #pragma unroll
-        for (int i = 0; i < H + V; ++i) {
+        for (int i = 0; i < BACK; ++i) p[i] = *reinterpret_cast<const Pack<T, V> *>(row + t + (i - BACK) * V);
+    }
+    if (behind) {
+        #pragma unroll
+        for (int i = 0; i < H; ++i) win[i] = to_f(p[(BACK * V - H + i) / V].v[(BACK * V - H + i) % V]);
+    } else {
+        load_some<T, H>(row, t - H, end, win);
+    }
+    if (inside) {
+        #pragma unroll
+        for (int i = 0; i < M; ++i) win[H + i] = to_f(x[i / V].v[i % V]);
+        if (other) {
+            #pragma unroll
+            for (int i = 0; i < M; ++i) d[i] = to_f(o[i / V].v[i % V]);
+        }
+    } else {
+        load_some<T, M>(row, t, end, win + H);
+        if (other) load_some<T, M>(other, t, end, d);
+    }
+    if (state && t < H) {
+        #pragma unroll
+        for (int i = 0; i < H + M; ++i) {
             const int at = t - H + i;
             if (at < 0 && at >= -H) win[i] = to_f(state[H + at]);
         }
     }
+}
+
+// dy act'(v)
+__device__ __forceinline__ float causal_back(int act, float v, float d)
+{
+    if (act != GCONV_ACT_SILU) return d;
+    const float s = scan_sigmoid(v);
+    return d * (s * fmaf(v, 1.f - s, 1.f));
 }
 
 template <typename T>
@@ -104,61 +134,80 @@ __device__ __forceinline__ int phase_of(const T *row)
 }
 
 template <typename T, int K, bool VEC>
-__global__ void __launch_bounds__(kCausalThreads) causal_fwd_kernel(const CausalArgs a)
+__global__ void __launch_bounds__(kCausalThreads) causal_fwd_kernel(const __grid_constant__ CausalArgs a)
 {
-    constexpr int V = 16 / (int)sizeof(T), H = K - 1;
-    const int seg = (int)(blockIdx.x % a.segs);
-    const int64_t r = (int64_t)(blockIdx.x / a.segs) * (kCausalThreads / a.TX) + threadIdx.x / a.TX;
-    const bool there = r < (int64_t)a.N * a.C;
-    const int n = there ? (int)(r / a.C) : 0, c = there ? (int)(r % a.C) : 0;
-    const int i = seg * a.TX + threadIdx.x % a.TX;
+    constexpr int V = 16 / (int)sizeof(T), M = 2 * V, H = K - 1;
+    const unsigned worker = (blockIdx.x * (unsigned)kCausalThreads + threadIdx.x) / (unsigned)a.TX, tx = threadIdx.x % a.TX;
+    const int c = (int)(worker / (unsigned)a.splits);
+    const unsigned split = worker % (unsigned)a.splits;
+    const bool there = c < a.C;
     ptx::griddep_wait();
-    const int end = there ? causal_end(a, n) : 0;
-    const T *row = static_cast<const T *>(a.x) + n * a.sx + (int64_t)c * a.L;
-    T *out = static_cast<T *>(a.out) + n * a.sy + (int64_t)c * a.L;
-    const T *state = a.state && H ? static_cast<const T *>(a.state) + ((int64_t)n * a.C + c) * H : nullptr;
-    const int t = i * V - (VEC ? phase_of(row) : 0);
-    float win[H + V];
-    if (there && t < a.L) {
-        load_window<T, V, H, VEC>(row, state, t, end, win);
-        float w[K], y[V];
-        #pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = a.w[(int64_t)c * K + k];
-        const float bias = a.bias ? a.bias[c] : 0.f;
-        #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float v = bias;
+    float w[K];
+    #pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = there ? a.w[(int64_t)c * K + k] : 0.f;
+    const float bias = a.bias && there ? a.bias[c] : 0.f;
+    // every lane of a warp makes the same rounds: state_out needs the warp together
+    const unsigned items = (unsigned)a.N * (unsigned)a.segs, rounds = (items + a.splits - 1) / a.splits;
+    for (unsigned round = 0; round < rounds; ++round) {
+        const unsigned item = split + round * a.splits;
+        const bool on = there && item < items;
+        const int n = !on ? 0 : a.segs == 1 ? (int)item : (int)(item / (unsigned)a.segs), seg = (int)(item - (unsigned)n * a.segs);
+        const int end = on ? causal_end(a, n) : 0;
+        const T *row = static_cast<const T *>(a.x) + n * a.sx + (int64_t)c * a.L;
+        T *out = static_cast<T *>(a.out) + n * a.sy + (int64_t)c * a.L;
+        const T *state = a.state && H && on ? static_cast<const T *>(a.state) + ((int64_t)n * a.C + c) * H : nullptr;
+        const int64_t t_ = ((int64_t)seg * a.TX + tx) * M - (VEC ? phase_of(row) : 0);
+        if (VEC && round + 1 < rounds && item + a.splits < items) {       // the next round's lines, on their way to L2
+            const unsigned next = item + a.splits;
+            const int n2 = a.segs == 1 ? (int)next : (int)(next / (unsigned)a.segs), s2 = (int)(next - (unsigned)n2 * a.segs);
+            const int64_t t2 = ((int64_t)s2 * a.TX + tx) * M;
+            if (there && t2 < a.L) fetch(static_cast<const T *>(a.x) + n2 * a.sx + (int64_t)c * a.L + t2);
+        }
+        if (on && t_ < a.L) {
+            const int t = (int)t_;
+            float win[H + M], y[M];
+            load_window<T, M, H, VEC>(row, state, t, end, win, nullptr, nullptr);
             #pragma unroll
-            for (int k = 0; k < K; ++k) v = fmaf(w[k], win[j + k], v);
-            if (a.act == GCONV_ACT_SILU) v *= scan_sigmoid(v);
-            y[j] = t + j < end ? v : 0.f;
+            for (int j = 0; j < M; ++j) {
+                float v = bias;
+                #pragma unroll
+                for (int k = 0; k < K; ++k) v = fmaf(w[k], win[j + k], v);
+                if (a.act == GCONV_ACT_SILU) v *= scan_sigmoid(v);
+                y[j] = v;
+            }
+            if (t + M > end) {
+                #pragma unroll
+                for (int j = 0; j < M; ++j) y[j] = t + j < end ? y[j] : 0.f;
+            }
+            store_pieces<T, M, VEC>(out, t, a.L, y);
         }
-        store_piece<T, V, VEC>(out, t, a.L, y);
-    }
-    if (H && a.state_out && seg == 0) {
-        // the window's reads of the state are over before any thread of the row writes it: it may be the same memory
-        float last[H ? H : 1];
-        const bool writes = there && i == 0;
-        #pragma unroll
-        for (int j = 0; j < H; ++j) {
-            const int at = end - H + j;
-            last[j] = !writes ? 0.f : at >= 0 ? to_f(row[at]) : state ? to_f(state[H + at]) : 0.f;
+        if (H && a.state_out) {
+            // only a row's first piece reads the state, and its lanes are through with that before the first of them
+            // writes: it may be the same memory
+            const bool writes = on && seg == 0 && tx == 0;
+            float last[H ? H : 1];
+            #pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const int at = end - H + j;
+                last[j] = !writes ? 0.f : at >= 0 ? to_f(row[at]) : state ? to_f(state[H + at]) : 0.f;
+            }
+            __syncwarp();
+            #pragma unroll
+            for (int j = 0; j < H; ++j)
+                if (writes) static_cast<T *>(a.state_out)[((int64_t)n * a.C + c) * H + j] = from_f<T>(last[j]);
         }
-        __syncthreads();
-        #pragma unroll
-        for (int j = 0; j < H; ++j)
-            if (writes) static_cast<T *>(a.state_out)[r * H + j] = from_f<T>(last[j]);
     }
 }
 
 // A few positions (a new one of every sequence): a thread a row, its window in registers.
 template <typename T, int K>
-__global__ void __launch_bounds__(128) causal_short_kernel(const CausalArgs a)
+__global__ void __launch_bounds__(128) causal_short_kernel(const __grid_constant__ CausalArgs a)
 {
     constexpr int H = K - 1;
-    const int64_t r = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    if (r >= (int64_t)a.N * a.C) return;
-    const int n = (int)(r / a.C), c = (int)(r % a.C);
+    const unsigned r_ = blockIdx.x * 128u + threadIdx.x;
+    if (r_ >= (unsigned)a.N * (unsigned)a.C) return;
+    const int64_t r = r_;
+    const int n = (int)(r_ / (unsigned)a.C), c = (int)(r_ % (unsigned)a.C);
     ptx::griddep_wait();
     const int end = causal_end(a, n);
     const T *row = static_cast<const T *>(a.x) + n * a.sx + (int64_t)c * a.L;
@@ -190,101 +239,103 @@ __global__ void __launch_bounds__(128) causal_short_kernel(const CausalArgs a)
     }
 }
 
-// Gradients.  A block takes TY channels and walks over its share of the sequences and row pieces; dw and db stay in
-// registers until the end.  dv of the next thread's first positions comes through shared memory; the last thread of a
-// row's piece makes it itself.
+// Gradients.  dv of the next lane's first positions comes by shuffles.  Where a row has more pieces than one, a worker's last
+// lane makes its dv for the lane before alone, and its run is the first of the next piece: 31 of 32 lanes' work counts.
+// (Exchanging through shared memory by the whole block instead took a barrier a piece: 132 us against the time below.)
 template <typename T, int K, bool VEC>
-__global__ void __launch_bounds__(kCausalThreads) causal_bwd_kernel(const CausalArgs a)
+__global__ void __launch_bounds__(kCausalThreads, 5) causal_bwd_kernel(const __grid_constant__ CausalArgs a)
 {
-    constexpr int V = 16 / (int)sizeof(T), H = K - 1;
-    __shared__ float ahead[2][H ? H : 1][kCausalThreads];
-    __shared__ float sums[kCausalThreads / 32][K + 1];
-    const int TY = kCausalThreads / a.TX, tx = threadIdx.x % a.TX;
-    const int c = (int)(blockIdx.x / a.splits) * TY + threadIdx.x / a.TX, split = (int)(blockIdx.x % a.splits);
+    constexpr int M = kCausalBack, H = K - 1;
+    static_assert(H <= M, "what a lane needs from the next one is in that one's run");
+    const unsigned worker = (blockIdx.x * (unsigned)kCausalThreads + threadIdx.x) / (unsigned)a.TX, tx = threadIdx.x % a.TX;
+    const int c = (int)(worker / (unsigned)a.splits), runs = a.segs > 1 ? a.TX - 1 : a.TX;
+    const unsigned split = worker % (unsigned)a.splits;
     const bool there = c < a.C;
     ptx::griddep_wait();
     float w[K], dw[K], db = 0.f;
     #pragma unroll
     for (int k = 0; k < K; ++k) { w[k] = there ? a.w[(int64_t)c * K + k] : 0.f; dw[k] = 0.f; }
     const float bias = a.bias && there ? a.bias[c] : 0.f;
-    int turn = 0;
-    const int64_t items = (int64_t)a.N * a.segs;
-    for (int64_t item = split; item < items; item += a.splits, turn ^= 1) {
-        const int n = (int)(item / a.segs), seg = (int)(item % a.segs);
-        const int i = seg * a.TX + tx, end = there ? causal_end(a, n) : 0;
+    // every lane of a warp makes the same rounds, for the shuffles
+    const unsigned items = (unsigned)a.N * (unsigned)a.segs, rounds = (items + a.splits - 1) / a.splits;
+    for (unsigned round = 0; round < rounds; ++round) {
+        const unsigned item = split + round * a.splits;
+        const bool on = there && item < items;
+        const int n = !on ? 0 : a.segs == 1 ? (int)item : (int)(item / (unsigned)a.segs), seg = (int)(item - (unsigned)n * a.segs);
+        const int end = on ? causal_end(a, n) : 0;
         const T *row = static_cast<const T *>(a.x) + n * a.sx + (int64_t)c * a.L;
         const T *grad = static_cast<const T *>(a.dy) + n * a.sdy + (int64_t)c * a.L;
-        const T *state = a.state && H && there ? static_cast<const T *>(a.state) + ((int64_t)n * a.C + c) * H : nullptr;
-        const int t = i * V - (VEC && there ? phase_of(row) : 0);
-        const bool any = t < end;
-        float dv[V + H], win[H + V];
-        #pragma unroll
-        for (int j = 0; j < V + H; ++j) dv[j] = 0.f;
-        auto back = [&](float v, float d) {          // dy act'(v)
-            if (a.act != GCONV_ACT_SILU) return d;
-            const float s = scan_sigmoid(v);
-            return d * (s * fmaf(v, 1.f - s, 1.f));
-        };
-        if (any) {
-            float d[V];
-            load_window<T, V, H, VEC>(row, state, t, end, win);
-            load_piece<T, V, VEC>(grad, t, end, d);
+        const T *state = a.state && H && on ? static_cast<const T *>(a.state) + ((int64_t)n * a.C + c) * H : nullptr;
+        const int64_t t_ = ((int64_t)seg * runs + tx) * M - (VEC ? phase_of(row) : 0);
+        const int t = t_ < a.L ? (int)t_ : a.L;
+        const bool mine = (int)tx < runs;
+        if (VEC && round + 1 < rounds && item + a.splits < items) {       // the next round's lines, on their way to L2
+            const unsigned next = item + a.splits;
+            const int n2 = a.segs == 1 ? (int)next : (int)(next / (unsigned)a.segs), s2 = (int)(next - (unsigned)n2 * a.segs);
+            const int64_t t2 = ((int64_t)s2 * runs + tx) * M;
+            if (there && t2 < a.L && (tx & 1) == 0) {
+                fetch(static_cast<const T *>(a.x) + n2 * a.sx + (int64_t)c * a.L + t2);
+                fetch(static_cast<const T *>(a.dy) + n2 * a.sdy + (int64_t)c * a.L + t2);
+            }
+        }
+        float dv[M + H], win[H + M];
+        if (t < end) {
+            load_window<T, M, H, VEC>(row, state, t, end, win, grad, dv);
             #pragma unroll
-            for (int j = 0; j < V; ++j) {
+            for (int j = 0; j < M; ++j) {
                 float v = bias;
                 #pragma unroll
                 for (int k = 0; k < K; ++k) v = fmaf(w[k], win[j + k], v);
-                const float x = back(v, d[j]);
-                dv[j] = t + j >= 0 && t + j < end ? x : 0.f;
-                db += dv[j];
-                #pragma unroll
-                for (int k = 0; k < K; ++k) dw[k] = fmaf(dv[j], win[j + k], dw[k]);
+                dv[j] = causal_back(a.act, v, dv[j]);
             }
-        }
-        if constexpr (H > 0) {
-            #pragma unroll
-            for (int j = 0; j < H; ++j) ahead[turn][j][threadIdx.x] = j < V ? dv[j < V ? j : 0] : 0.f;
-            if (V >= H) __syncthreads();
-            if (any && (tx == a.TX - 1 || V < H)) {
+            if (t < 0 || t + M > end) {
                 #pragma unroll
-                for (int j = 0; j < H; ++j) {
-                    const int at = t + V + j;
-                    if (at >= end) continue;
-                    float v = bias;
+                for (int j = 0; j < M; ++j) dv[j] = t + j >= 0 && t + j < end ? dv[j] : 0.f;
+            }
+            if (mine) {
+                #pragma unroll
+                for (int j = 0; j < M; ++j) {
+                    db += dv[j];
                     #pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        const int from = at - H + k;
-                        const float x = from >= 0 ? to_f(row[from]) : state && from >= -H ? to_f(state[H + from]) : 0.f;
-                        v = fmaf(w[k], x, v);
-                    }
-                    if (at >= 0) dv[V + j] = back(v, to_f(grad[at]));
+                    for (int k = 0; k < K; ++k) dw[k] = fmaf(dv[j], win[j + k], dw[k]);
                 }
-            } else if (any) {
-                #pragma unroll
-                for (int j = 0; j < H; ++j) dv[V + j] = ahead[turn][j][threadIdx.x + 1];
             }
+        } else {
+            #pragma unroll
+            for (int j = 0; j < M; ++j) dv[j] = 0.f;
         }
-        if (there && t < a.L) {
-            float dx[V];
+        #pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const float next = __shfl_down_sync(~0u, dv[j], 1);
+            dv[M + j] = (int)tx + 1 < a.TX ? next : 0.f;
+        }
+        if (on && mine && t < a.L) {
+            float dx[M];
             const T *more = a.dstate_out ? static_cast<const T *>(a.dstate_out) + ((int64_t)n * a.C + c) * H : nullptr;
             #pragma unroll
-            for (int j = 0; j < V; ++j) {
+            for (int j = 0; j < M; ++j) {
                 float v = 0.f;
                 #pragma unroll
                 for (int k = 0; k < K; ++k) v = fmaf(w[k], dv[j + H - k], v);
-                const int from = t + j - (end - H);
-                if (H && more && from >= 0 && from < H) v += to_f(more[from]);
-                dx[j] = t + j < end ? v : 0.f;
+                dx[j] = v;
             }
-            store_piece<T, V, VEC>(static_cast<T *>(a.out) + n * a.sdx + (int64_t)c * a.L, t, a.L, dx);
-            if (H && a.dstate && i == 0) {
+            if (t + M > end - H) {                   // near the end, or behind it
+                #pragma unroll
+                for (int j = 0; j < M; ++j) {
+                    const int from = t + j - (end - H);
+                    if (H && more && from >= 0 && from < H) dx[j] += to_f(more[from]);
+                    dx[j] = t + j < end ? dx[j] : 0.f;
+                }
+            }
+            store_pieces<T, M, VEC>(static_cast<T *>(a.out) + n * a.sdx + (int64_t)c * a.L, t, a.L, dx);
+            if (H && a.dstate && seg == 0 && tx == 0) {
                 #pragma unroll
                 for (int j = 0; j < H; ++j) {
                     float v = 0.f;
                     #pragma unroll
                     for (int k = 0; k <= j; ++k) {
                         #pragma unroll
-                        for (int m = 0; m < V + H; ++m)
+                        for (int m = 0; m < M + H; ++m)
                             if (t + m == j - k) v = fmaf(w[k], dv[m], v);
                     }
                     if (more && j - end >= 0 && j - end < H) v += to_f(more[j - end]);
@@ -293,29 +344,15 @@ __global__ void __launch_bounds__(kCausalThreads) causal_bwd_kernel(const Causal
             }
         }
     }
-    // over the TX threads of a channel: a warp's by shuffles, the warps' in order
-    const int width = a.TX < 32 ? a.TX : 32;
     #pragma unroll
     for (int k = 0; k <= K; ++k) {
         float v = k < K ? dw[k < K ? k : 0] : db;
-        for (int o = width / 2; o > 0; o >>= 1) v += __shfl_down_sync(~0u, v, o, width);
-        if (a.TX <= 32) {
-            if (tx == 0 && there) a.part[((int64_t)split * a.C + c) * (K + 1) + k] = v;
-        } else if ((threadIdx.x & 31) == 0) {
-            sums[threadIdx.x >> 5][k] = v;
-        }
-    }
-    if (a.TX > 32) {
-        __syncthreads();
-        if (there && tx <= K) {
-            float v = 0.f;
-            for (int j = 0; j < a.TX / 32; ++j) v += sums[threadIdx.x / a.TX * (a.TX / 32) + j][tx];
-            a.part[((int64_t)split * a.C + c) * (K + 1) + tx] = v;
-        }
+        for (int o = a.TX / 2; o > 0; o >>= 1) v += __shfl_down_sync(~0u, v, o, a.TX);
+        if (tx == 0 && there) a.part[((int64_t)split * a.C + c) * (K + 1) + k] = v;
     }
 }
 
-// dw and db from the blocks' sums, in order: 32 columns a block, eight threads a column.
+// dw and db from the workers' sums, in order: 32 columns a block, eight threads a column.
 __global__ void __launch_bounds__(256) causal_sum_kernel(const float *part, int splits, int C, int K, float *dw, float *db)
 {
     __shared__ float sh[8][32];
@@ -343,10 +380,10 @@ bool on(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to
 bool check_causal(const gconv_causal *s, gconv_dtype dt)
 {
     if (!s || (dt != GCONV_F32 && dt != GCONV_BF16)) return false;
-    if (s->N < 0 || s->C < 1 || s->L < 1 || s->taps < 1 || s->taps > kCausalMost) return false;
+    if (s->N < 0 || s->C < 1 || s->L < 1 || s->L > (1 << 30) || s->taps < 1 || s->taps > kCausalMost) return false;
     if (s->act != GCONV_ACT_NONE && s->act != GCONV_ACT_SILU) return false;
     const int64_t CL = (int64_t)s->C * s->L;
-    if (CL > ((int64_t)1 << 40) / std::max(1, s->N)) return false;
+    if (CL > ((int64_t)1 << 40) / std::max(1, s->N) || (int64_t)s->N * s->C > INT_MAX) return false;
     for (long long b : {s->x_batch, s->y_batch, s->dy_batch, s->dx_batch})
         if (b != 0 && (b < CL || b > ((int64_t)1 << 40))) return false;
     return true;
@@ -354,30 +391,30 @@ bool check_causal(const gconv_causal *s, gconv_dtype dt)
 
 struct CausalShape { int TX, segs, splits; int64_t grid; };
 
-CausalShape causal_shape(const gconv_causal &s, gconv_dtype dt, bool back)
+// `whole`: every row begins on 16 bytes.
+CausalShape causal_shape(const gconv_causal &s, gconv_dtype dt, bool back, bool whole)
 {
-    const int V = 16 / esize(dt);
+    const int V = 16 / esize(dt), M = back ? kCausalBack : 2 * V;
+    const int64_t runs = ((int64_t)s.L + V - 1 + M - 1) / M, real = whole ? ((int64_t)s.L + M - 1) / M : runs;
     CausalShape p{};
-    const int64_t pieces = ((int64_t)s.L + 2 * V - 2) / V;       // of a row that begins anywhere
     p.TX = 1;
-    while (p.TX < kCausalThreads && p.TX < pieces) p.TX *= 2;
-    p.segs = (int)((pieces + p.TX - 1) / p.TX);
-    const int TY = kCausalThreads / p.TX;
-    if (!back) {
-        p.grid = ((int64_t)s.N * s.C + TY - 1) / TY * p.segs;
-        return p;
-    }
-    const int64_t blocks = (s.C + TY - 1) / TY, items = (int64_t)s.N * p.segs;
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(items, ((int64_t)num_sms() * 16 + blocks - 1) / blocks));
-    p.grid = blocks * p.splits;
+    while (p.TX < 32 && p.TX < real) p.TX *= 2;
+    const int64_t each = back && real > 32 ? 31 : p.TX;
+    p.segs = (int)((real + each - 1) / each);
+    // workers that share a channel: warps for the whole GPU about twice over; the workspace's size, which does not
+    // know the alignment, goes by the longer rows
+    int TX = 1;
+    while (TX < 32 && TX < runs) TX *= 2;
+    const int64_t most = (int64_t)s.N * ((runs + 30) / (TX < 32 ? runs + 30 : 31)), want = (int64_t)num_sms() * 64 * (32 / TX);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, (want + s.C - 1) / s.C));
+    p.grid = ((int64_t)s.C * p.splits + kCausalThreads / p.TX - 1) / (kCausalThreads / p.TX);
     return p;
 }
 
-void causal_args(const gconv_causal &s, const CausalShape &p, CausalArgs *a)
+void causal_args(const gconv_causal &s, CausalArgs *a)
 {
     const int64_t CL = (int64_t)s.C * s.L;
     a->N = s.N; a->C = s.C; a->L = s.L; a->act = s.act;
-    a->TX = p.TX; a->segs = p.segs; a->splits = p.splits;
     a->sx = s.x_batch ? s.x_batch : CL; a->sy = s.y_batch ? s.y_batch : CL;
     a->sdy = s.dy_batch ? s.dy_batch : CL; a->sdx = s.dx_batch ? s.dx_batch : CL;
 }
@@ -387,6 +424,12 @@ bool together(const gconv_causal &s, gconv_dtype dt, const void *p, int64_t sp, 
 {
     const int E = 16 / esize(dt);
     return ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0 && (s.N == 1 || (sp - sq) % E == 0);
+}
+
+bool whole_rows(const gconv_causal &s, gconv_dtype dt, const void *p, int64_t sp)
+{
+    const int E = 16 / esize(dt);
+    return on(p, 16) && s.L % E == 0 && (s.N == 1 || sp % E == 0);
 }
 
 template <typename T, int K = 1>
@@ -405,7 +448,7 @@ void causal_start(int K_, int kind, bool vec, const CausalArgs &a, int64_t grid,
 
 size_t causal_ws(const gconv_causal &s, gconv_dtype dt)
 {
-    return s.N ? (size_t)causal_shape(s, dt, true).splits * s.C * (s.taps + 1) * sizeof(float) : 0;
+    return s.N ? (size_t)causal_shape(s, dt, true, true).splits * s.C * (s.taps + 1) * sizeof(float) : 0;
 }
 
 gconv_status done() { return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA; }
@@ -431,15 +474,16 @@ gconv_status gconv_causal_fwd(const gconv_causal *causal, gconv_dtype dtype, con
     const int es = esize(dtype);
     if (!x || !w || !y || !on(x, es) || !on(y, es) || !on(state, es) || !on(state_out, es)) return GCONV_ERR_INVALID_ARG;
     if (!on(w, 4) || !on(bias, 4) || !on(lengths, 4)) return GCONV_ERR_INVALID_ARG;
-    const CausalShape p = causal_shape(*causal, dtype, false);
     CausalArgs a{};
-    causal_args(*causal, p, &a);
+    causal_args(*causal, &a);
+    const bool vec = together(*causal, dtype, x, a.sx, y, a.sy);
+    const CausalShape p = causal_shape(*causal, dtype, false, !vec || whole_rows(*causal, dtype, x, a.sx));
+    a.TX = p.TX; a.segs = p.segs; a.splits = p.splits;
     a.x = x; a.w = w; a.bias = bias; a.state = state; a.state_out = causal->taps > 1 ? state_out : nullptr; a.lengths = lengths;
     a.out = y;
     const bool brief = causal->L <= kCausalShort;
     const int64_t grid = brief ? ((int64_t)a.N * a.C + 127) / 128 : p.grid;
-    if (grid > INT_MAX) return GCONV_ERR_INVALID_ARG;
-    const bool vec = together(*causal, dtype, x, a.sx, y, a.sy);
+    if (grid > INT_MAX || (int64_t)causal->N * p.segs > INT_MAX) return GCONV_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == GCONV_BF16) causal_start<__nv_bfloat16>(causal->taps, brief ? 0 : 1, vec, a, grid, st);
     else causal_start<float>(causal->taps, brief ? 0 : 1, vec, a, grid, st);
@@ -464,15 +508,16 @@ gconv_status gconv_causal_bwd(const gconv_causal *causal, gconv_dtype dtype, con
     for (const void *q : {x, dy, state, dstate_out, (const void *)dx, (const void *)dstate})
         if (!on(q, es)) return GCONV_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < causal_ws(*causal, dtype) || !on(workspace, 16)) return GCONV_ERR_WORKSPACE;
-    const CausalShape p = causal_shape(*causal, dtype, true);
-    if (p.grid > INT_MAX) return GCONV_ERR_INVALID_ARG;
     CausalArgs a{};
-    causal_args(*causal, p, &a);
+    causal_args(*causal, &a);
+    const bool vec = together(*causal, dtype, x, a.sx, dy, a.sdy) && together(*causal, dtype, x, a.sx, dx, a.sdx);
+    const CausalShape p = causal_shape(*causal, dtype, true, !vec || whole_rows(*causal, dtype, x, a.sx));
+    if (p.grid > INT_MAX || (int64_t)causal->N * p.segs > INT_MAX) return GCONV_ERR_INVALID_ARG;
+    a.TX = p.TX; a.segs = p.segs; a.splits = p.splits;
     const bool held = causal->taps > 1;
     a.x = x; a.w = w; a.bias = bias; a.state = state; a.lengths = lengths; a.dy = dy; a.out = dx;
     a.dstate_out = held ? dstate_out : nullptr; a.dstate = held ? dstate : nullptr;
     a.part = static_cast<float *>(workspace);
-    const bool vec = together(*causal, dtype, x, a.sx, dy, a.sdy) && together(*causal, dtype, x, a.sx, dx, a.sdx);
     if (dtype == GCONV_BF16) causal_start<__nv_bfloat16>(causal->taps, 2, vec, a, p.grid, st);
     else causal_start<float>(causal->taps, 2, vec, a, p.grid, st);
     const int64_t cols = (int64_t)a.C * (causal->taps + 1);

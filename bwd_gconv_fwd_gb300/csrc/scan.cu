@@ -172,7 +172,7 @@ int esize(gconv_dtype dt) { return dt == GCONV_BF16 ? 2 : 4; }
 bool check_scan(const gconv_scan *s, gconv_dtype dt)
 {
     if (!s || (dt != GCONV_F32 && dt != GCONV_BF16)) return false;
-    if (s->N < 0 || s->C < 1 || s->L < 1 || s->groups < 1 || s->C % s->groups) return false;
+    if (s->N < 0 || s->C < 1 || s->L < 1 || s->L > (1 << 30) || s->groups < 1 || s->C % s->groups) return false;
     if (s->states < 1 || s->states > kScanMaxStates || s->softplus < 0 || s->softplus > 1) return false;
     const int64_t CL = (int64_t)s->C * s->L, GSL = (int64_t)s->groups * s->states * s->L;
     // 2^40 elements a tensor, which also keeps every product below 64 bits
@@ -197,6 +197,18 @@ struct ScanPlan {
     size_t o_init, o_dsum, o_part, o_pA, o_pD, o_pb, bytes;
 };
 
+// Time of a launch, in units of a tile of one block alone on an SM.  A tile's time with k blocks on each SM is about 1, 1.2,
+// 1.4, 1.6 (forward; 7.5 us with 16 states alone, 12 us four at a time) or 1, 1.35 (gradient; 13 and 17 us, two fit).
+// A block's start is another half tile.
+double scan_cost(bool back, int64_t blocks, double tiles)
+{
+    tiles += 0.5;
+    const int most = back ? 2 : 4;
+    const double more = back ? 0.35 : 0.2;
+    const int64_t slots = (int64_t)num_sms() * most, last = blocks % slots;
+    return tiles * (blocks / slots * (1 + more * (most - 1)) + (last ? 1 + more * ((last + num_sms() - 1) / num_sms() - 1) : 0));
+}
+
 bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
 {
     *p = ScanPlan{};
@@ -209,28 +221,44 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
         p->shape.grid = (unsigned)grid;
         return grid <= INT_MAX;
     }
-    const int form = 0;
-    const ScanForm f = back ? kBwdForms[form] : kFwdForms[form];
-    const int CL = 32 / f.TL, own = CL * f.P, TT = f.TL * f.K;
-    int warps = 4;
-    while (warps > 1 && (warps / 2) * own >= Cg) warps /= 2;
+    const int own = kScanOwn, CL = 32 / kScanLanes, TT = kScanTile;
+    const int units = (Cg + own - 1) / own, tiles = (s.L + TT - 1) / TT;      // a warp's channels, tiles of a sequence
+    // Warps a block, channel sets that a block of the gradient takes in turn (fewer partial sums of dB and dC; where B and C
+    // of all the states fit), and pieces that a sequence is cut into: the cheapest.  A cut takes a pass over the
+    // pieces before (0.45 of the forward pass, 0.3 of the gradient) and two launches.  Measured in us, uncut and cut:
+    // forward [1,2048,4096] 482 and 147 (16 pieces), [1,256,65536] 6987 and 292 (64), [8,2048,2048] 373 and 400 (2);
+    // gradient [1,2048,4096] 822 and 342 (8), [8,2048,2048] 1023, 985 in two sets, 1115 in 4 pieces.
+    double best = 0;
+    int warps = 1;
+    for (int sets = 1; sets <= (back && S <= kScanStates ? 2 : 1); ++sets) {
+        const int ncb = (units + 4 * sets - 1) / (4 * sets), w = (units + ncb * sets - 1) / (ncb * sets);
+        const int64_t blocks = (int64_t)s.N * s.groups * ncb;
+        for (int chunks = 1; chunks <= tiles; chunks += chunks < 8 ? 1 : chunks / 8) {
+            const int each = (tiles + chunks - 1) / chunks, real = (tiles + each - 1) / each;
+            double cost = scan_cost(back, blocks * real, (double)each * sets);
+            if (real > 1) cost = cost * (back ? 1.3 : 1.45) + 1.0;
+            if (sets == 1) cost *= 1.02;             // twice the partial sums
+            if (best == 0 || cost < best) {
+                best = cost;
+                warps = w; p->sets = sets; p->ncb = ncb; p->chunks = real; p->chunk_tiles = each;
+            }
+            if (blocks * real > (int64_t)num_sms() * 64) break;
+        }
+    }
     const int per = warps * own * p->sets;
-    p->ncb = (Cg + per - 1) / per;
-    const int tiles = (s.L + TT - 1) / TT;
-    p->chunks = 1;
-    p->chunk_tiles = (tiles + p->chunks - 1) / p->chunks;
-    p->chunks = (tiles + p->chunk_tiles - 1) / p->chunk_tiles;
     const int64_t grid = (int64_t)s.N * s.groups * p->ncb * p->chunks;
     const int64_t ends_grid = back ? (int64_t)s.N * s.groups * ((Cg + warps * own - 1) / (warps * own)) * p->chunks : grid;
     if (grid > INT_MAX || ends_grid > INT_MAX) return false;
     const int row = spots(TT);
+    const int SP = S | 1;
     auto floats = [&](bool ends) -> size_t {
-        if (!back) return (size_t)(ends ? 1 : 2) * kScanStates * row + 3 * (size_t)warps * own * S;
-        if (ends) return (size_t)kScanStates * row + 3 * (size_t)warps * own * S;
-        return (size_t)(2 + 2 * CL) * kScanStates * row + (size_t)warps * own * kScanStates + 4 * (size_t)per * S + 2 * per;
+        if (!back) return (size_t)(ends ? 1 : 2) * kScanStates * row + 3 * (size_t)warps * own * SP;
+        if (ends) return (size_t)kScanStates * row + 3 * (size_t)warps * own * SP;
+        return (size_t)(2 + 2 * CL) * kScanStates * row + (size_t)warps * (own * (kScanStates + 1) + 64 * kScanStates) +
+               4 * (size_t)per * SP + 4 * per;
     };
-    p->shape = {form, warps, 0, (unsigned)grid, floats(false) * 4};
-    p->ends = {form, warps, 0, (unsigned)ends_grid, floats(true) * 4};
+    p->shape = {warps, 0, (unsigned)grid, floats(false) * 4};
+    p->ends = {warps, 0, (unsigned)ends_grid, floats(true) * 4};
     size_t at = 0;
     auto take = [&](size_t n) { const size_t was = at; at += up16(n * sizeof(float)); return was; };
     const size_t pieces = (size_t)s.N * p->chunks;

@@ -2,12 +2,13 @@
 //
 //   h[t] = exp(d[t] A) h[t-1] + d[t] u[t] B[t],   y[t] = sum_s C[t] h[t] + D u[t]
 //
-// for every sequence, channel and state s.  A thread holds K consecutive positions of P channels in
+// for every sequence, channel and state s.  A thread holds K consecutive positions of a pair of channels in
 // registers and walks over the states: the recurrence over its run starts from zero, a scan over the TL lanes
 // that hold neighbouring runs of the same channels gives what enters each run, and a second walk makes the
 // states.  The exponentials, one a state and position, are taken once.  What crosses from one tile of TL K
 // positions to the next, and what enters a tile, stays in shared memory, as do B and C (in fp32, shared by all the
-// channels of a block).
+// channels of a block).  Both channels of a pair go through one instruction (packed fp32), the recurrences too; B and C
+// are the same for both, which such an instruction takes from a single register.
 #pragma once
 
 #include "internal.h"
@@ -18,6 +19,11 @@ namespace gconv {
 constexpr int kScanMark = 64;       // positions between the states that the forward pass keeps for the gradient
 constexpr int kScanStates = 16;     // states whose B and C are in shared memory at once
 constexpr int kScanMaxStates = 256;
+// Lanes along the positions and positions a lane: a tile is 64 positions of 8 channels a warp.  Longer runs take fewer
+// scans but twice the registers (16 positions: [8,2048,2048] forward 384 us against 359), more lanes more steps a
+// scan (32: 533 us), and fewer blocks each; where blocks are few, sequences are cut in pieces instead.
+constexpr int kScanLanes = 8, kScanRun = 8, kScanTile = kScanLanes * kScanRun;
+constexpr int kScanOwn = 32 / kScanLanes * 2;      // channels a warp
 
 struct ScanArgs {
     int N, C, L, G, S, Cg;
@@ -64,45 +70,89 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float scan_sigmoid(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
 
+// ---- pairs of channels ---------------------------------------------------------------
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float2 rcp(float2 x) { return make_float2(rcp(x.x), rcp(x.y)); }
+__device__ __forceinline__ float2 operator*(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 operator+(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+__device__ __forceinline__ float2 scan_sigmoid(float2 x) { return rcp(both(1.f) + ex2(x * both(-kLog2e))); }
+
 // log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x|.  The product with log2 e is carried in two parts, as its rounding
 // alone would be |x| 2^-24 of a small result; log1p(e) = 2 atanh(e / (2 + e)) by its series, whose terms fall by
 // nine at least (seven of them: 2^-25).
-__device__ __forceinline__ float scan_softplus(float x)
+__device__ __forceinline__ float2 scan_softplus(float2 x)
 {
-    const float m = fmaxf(-fabsf(x), -104.f);
-    const float hi = m * kLog2e;
-    const float lo = fmaf(m, kLog2e, -hi);
-    const float e0 = ex2(hi);
-    const float e = fmaf(e0, lo * kLn2, e0);
-    const float s = e * rcp(2.f + e), q = s * s;
-    float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    r = fmaf(q, r, 1.f / 9.f);
-    r = fmaf(q, r, 1.f / 7.f);
-    r = fmaf(q, r, 1.f / 5.f);
-    r = fmaf(q, r, 1.f / 3.f);
-    r = fmaf(q, r, 1.f);
-    r = fmaf(s + s, r, x > 0.f ? x : 0.f);
-    return x == x ? r : x;
+    const float2 m = make_float2(fmaxf(-fabsf(x.x), -104.f), fmaxf(-fabsf(x.y), -104.f));
+    const float2 hi = m * both(kLog2e);
+    const float2 lo = fma2(m, both(kLog2e), make_float2(-hi.x, -hi.y));
+    const float2 e0 = ex2(hi);
+    const float2 e = fma2(e0, lo * both(kLn2), e0);
+    const float2 s = e * rcp(both(2.f) + e), q = s * s;
+    float2 r = fma2(q, both(1.f / 13.f), both(1.f / 11.f));
+    r = fma2(q, r, both(1.f / 9.f));
+    r = fma2(q, r, both(1.f / 7.f));
+    r = fma2(q, r, both(1.f / 5.f));
+    r = fma2(q, r, both(1.f / 3.f));
+    r = fma2(q, r, both(1.f));
+    r = fma2(s + s, r, make_float2(x.x > 0.f ? x.x : 0.f, x.y > 0.f ? x.y : 0.f));
+    return make_float2(x.x == x.x ? r.x : x.x, x.y == x.y ? r.y : x.y);
 }
+__device__ __forceinline__ float scan_softplus(float x) { return scan_softplus(both(x)).x; }
 
-// Its values of a run of K positions from t, zeros from `end` on (which may lie before t).  VEC: rows and t are
-// multiples of 16 bytes, so that a vector is inside the row of L positions or behind it.
+// Where a thread's run lies within a sequence: positions t .. t + K - 1 of a pair of channels whose rows lie L apart,
+// in 16-byte pieces where VEC (rows and t are multiples of that).  Pieces behind the row, and a second channel that is
+// none, stand for others that are there, so that no load needs a condition; clear_run takes out what is not to be used.
 template <typename T, int K, bool VEC>
-__device__ __forceinline__ void load_run(const T *row, int t, int L, int end, float (&v)[K])
-{
-    if constexpr (VEC) {
-        constexpr int E = 16 / (int)sizeof(T);
-        static_assert(K % E == 0, "");
-        #pragma unroll
-        for (int i = 0; i < K; i += E) {
-            Pack<T, E> x;
-            if (t + i < end) x = *reinterpret_cast<const Pack<T, E> *>(row + t + i);
+struct Place {
+    static constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;
+    int64_t x[VEC ? K / E : 1];     // of the first channel; the second's are `step` further
+    int64_t step;
+    int t, L;
+
+    __device__ __forceinline__ Place(int64_t row, int t_, int L_, bool there0, bool there1) : step(there1 ? L_ : 0), t(t_), L(L_)
+    {
+        if (!there0) row = 0;
+        if constexpr (VEC) {
             #pragma unroll
-            for (int j = 0; j < E; ++j) v[i + j] = t + i + j < end ? to_f(x.v[j]) : 0.f;
+            for (int i = 0; i < K / E; ++i) x[i] = row + (t + i * E < L ? t + i * E : 0);
+        } else {
+            x[0] = row;
         }
-    } else {
+    }
+};
+
+// A run's values as they lie in memory.  Loading and converting are apart so that all of a tile's loads are on their
+// way before the first is waited for.
+template <typename T, int K, bool VEC>
+struct Run {
+    static constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;
+    Pack<T, E> x[K / E], y[K / E];
+
+    __device__ __forceinline__ void load(const T *base, const Place<T, K, VEC> &at)
+    {
         #pragma unroll
-        for (int i = 0; i < K; ++i) v[i] = t + i < end ? to_f(row[t + i]) : 0.f;
+        for (int i = 0; i < K / E; ++i) {
+            const int64_t o = VEC ? at.x[VEC ? i : 0] : at.x[0] + min(at.t + i, at.L - 1);
+            x[i] = *reinterpret_cast<const Pack<T, E> *>(base + o);
+            y[i] = *reinterpret_cast<const Pack<T, E> *>(base + o + at.step);
+        }
+    }
+    __device__ __forceinline__ float2 at(int k) const { return make_float2(to_f(x[k / E].v[k % E]), to_f(y[k / E].v[k % E])); }
+};
+
+// Zeros from the ends on, whatever came before.
+template <int K>
+__device__ __forceinline__ void clear_run(int t, int end0, int end1, float2 (&v)[K])
+{
+    if (t + K <= min(end0, end1)) return;
+    #pragma unroll
+    for (int i = 0; i < K; ++i) {
+        v[i].x = t + i < end0 ? v[i].x : 0.f;
+        v[i].y = t + i < end1 ? v[i].y : 0.f;
     }
 }
 
@@ -110,67 +160,119 @@ template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+__device__ __forceinline__ void put2(float *to, float x, float y) { to[0] = x; to[1] = y; }
+__device__ __forceinline__ void put2(__nv_bfloat16 *to, float x, float y)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(to) = __floats2bfloat162_rn(x, y);
+}
+
+// The same, stored up to L positions of the channels that are there.
 template <typename T, int K, bool VEC>
-__device__ __forceinline__ void store_run(T *row, int t, int L, const float (&v)[K])
+__device__ __forceinline__ void store_run(T *row, int64_t L, int t, bool there0, bool there1, const float2 (&v)[K])
 {
     if constexpr (VEC) {
         constexpr int E = 16 / (int)sizeof(T);
         #pragma unroll
         for (int i = 0; i < K; i += E) {
             if (t + i >= L) continue;
-            Pack<T, E> x;
+            Pack<T, E> x, y;
             #pragma unroll
-            for (int j = 0; j < E; ++j) x.v[j] = from_f<T>(v[i + j]);
-            *reinterpret_cast<Pack<T, E> *>(row + t + i) = x;
+            for (int j = 0; j < E; j += 2) {
+                put2(x.v + j, v[i + j].x, v[i + j + 1].x);
+                put2(y.v + j, v[i + j].y, v[i + j + 1].y);
+            }
+            if (there0) *reinterpret_cast<Pack<T, E> *>(row + t + i) = x;
+            if (there1) *reinterpret_cast<Pack<T, E> *>(row + L + t + i) = y;
         }
     } else {
         #pragma unroll
-        for (int i = 0; i < K; ++i)
-            if (t + i < L) row[t + i] = from_f<T>(v[i]);
+        for (int i = 0; i < K; ++i) {
+            if (t + i >= L) continue;
+            if (there0) row[t + i] = from_f<T>(v[i].x);
+            if (there1) row[L + t + i] = from_f<T>(v[i].y);
+        }
     }
 }
 
 // Place of position t of a tile in a row of shared memory: four floats of gap after every 32, so that eight lanes
-// eight positions apart read 16 bytes each without meeting in a bank.
+// eight positions apart read 16 bytes each without meeting in a bank.  A run of 8 has no gap inside.
 __device__ __forceinline__ int spot(int t) { return t + ((t >> 5) << 2); }
 constexpr int spots(int TT) { return TT + (TT / 32) * 4; }
 
-// B or C of `count` states from s0 and TT positions from t0, in fp32, zeros from `end` on.
+// B or C of up to kScanStates states from s0 and TT positions from t0, in fp32, zeros from `end` on: loaded first,
+// stored to shared memory later.
 template <typename T, int TT, bool VEC>
-__device__ __forceinline__ void stage_states(const T *base, int64_t L, int s0, int count, int t0, int end, float *sh)
-{
-    constexpr int E = VEC ? 16 / (int)sizeof(T) : 1;
-    constexpr int PER = TT / E;
-    for (int i = threadIdx.x; i < count * PER; i += blockDim.x) {
-        const int s = i / PER, t = (i % PER) * E;
-        float *to = sh + s * spots(TT) + spot(t);
+struct States {
+    static constexpr int E = VEC ? 16 / (int)sizeof(T) : 1, PER = TT / E;
+    static constexpr int ALL = kScanStates * PER / 128, HELD = ALL < 1 ? 1 : ALL < 8 ? ALL : 8;   // pieces a thread holds; more are stored as they come
+    Pack<T, E> x[HELD];
+
+    __device__ __forceinline__ static void put(float *sh, int i, int t0, int end, const Pack<T, E> &v)
+    {
+        const int t = (i % PER) * E, left = end - t0 - t;
+        float *to = sh + (i / PER) * spots(TT) + spot(t);
         if constexpr (VEC) {
-            Pack<T, E> x;
-            if (t0 + t < end) x = *reinterpret_cast<const Pack<T, E> *>(base + (s0 + s) * L + t0 + t);
+            float f[E];
             #pragma unroll
-            for (int j = 0; j < E; j += 4) {
-                float4 f;
-                f.x = t0 + t + j < end ? to_f(x.v[j]) : 0.f;
-                f.y = t0 + t + j + 1 < end ? to_f(x.v[j + 1]) : 0.f;
-                f.z = t0 + t + j + 2 < end ? to_f(x.v[j + 2]) : 0.f;
-                f.w = t0 + t + j + 3 < end ? to_f(x.v[j + 3]) : 0.f;
-                *reinterpret_cast<float4 *>(to + j) = f;
+            for (int j = 0; j < E; ++j) f[j] = to_f(v.v[j]);
+            if (left < E) {
+                #pragma unroll
+                for (int j = 0; j < E; ++j) f[j] = j < left ? f[j] : 0.f;
             }
+            #pragma unroll
+            for (int j = 0; j < E; j += 4) *reinterpret_cast<float4 *>(to + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
         } else {
-            *to = t0 + t < end ? to_f(base[(s0 + s) * L + t0 + t]) : 0.f;
+            *to = to_f(v.v[0]);
         }
     }
-}
+    __device__ __forceinline__ static Pack<T, E> get(const T *base, int64_t L, int i, int t0, int end)
+    {
+        Pack<T, E> v{};
+        const int t = t0 + (i % PER) * E;
+        if (t < end) v = *reinterpret_cast<const Pack<T, E> *>(base + (i / PER) * L + t);
+        return v;
+    }
+    __device__ __forceinline__ void load(const T *base, int64_t L, int count, int t0, int end)
+    {
+        #pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            const int i = threadIdx.x + j * blockDim.x;
+            x[j] = i < count * PER ? get(base, L, i, t0, end) : Pack<T, E>{};
+        }
+    }
+    __device__ __forceinline__ void store(const T *base, int64_t L, int count, int t0, int end, float *sh) const
+    {
+        #pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            const int i = threadIdx.x + j * blockDim.x;
+            if (i < count * PER) put(sh, i, t0, end, x[j]);
+        }
+        for (int i = threadIdx.x + HELD * blockDim.x; i < count * PER; i += blockDim.x) put(sh, i, t0, end, get(base, L, i, t0, end));
+    }
+};
+
+// Asks for the line at a pointer, ahead of its load.
+__device__ __forceinline__ void fetch(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <int K>
-__device__ __forceinline__ void read_run(const float *row, int t, float (&v)[K])
+__device__ __forceinline__ void read_run(const float *row, float (&v)[K])
 {
     #pragma unroll
     for (int i = 0; i < K; i += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(row + spot(t + i));
+        const float4 f = *reinterpret_cast<const float4 *>(row + i);
         v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
     }
 }
+
+__device__ __forceinline__ float2 shift_up(float2 v, int o, int width)
+{
+    return make_float2(__shfl_up_sync(~0u, v.x, o, width), __shfl_up_sync(~0u, v.y, o, width));
+}
+__device__ __forceinline__ float2 shift_down(float2 v, int o, int width)
+{
+    return make_float2(__shfl_down_sync(~0u, v.x, o, width), __shfl_down_sync(~0u, v.y, o, width));
+}
+__device__ __forceinline__ float2 pick(bool c, float2 a, float2 b) { return make_float2(c ? a.x : b.x, c ? a.y : b.y); }
 
 // A log2 e, finite, so that a step of zero leaves a state as it was whatever A is.
 __device__ __forceinline__ float decay_rate(float a)

@@ -1,12 +1,12 @@
 // scan_bwd.cuh -- gradients of the selective scan (see scan.cuh for the forward pass).
 //
-// With dy the gradient before the gate, w[t] what reaches h[t] from later positions and q[t] = exp(d[t] A) h[t-1]:
+// With dy the gradient before the gate and w[t] what reaches h[t] from later positions:
 //   g[t] = C[t] dy[t] + w[t],   w[t-1] = exp(d[t] A) g[t]
 //   dC[t] = sum_c dy h,   dB[t] = sum_c g d u,   du = d sum_s B g + D dy,   dd = u sum_s B g + sum_s A g q,
-//   dA = sum_t d g q
+//   dA = sum_t d g q   (q[t] = exp(d[t] A) h[t-1])
 // A tile's states are made again from the state that the forward pass kept before it, then the tile is walked
 // backwards.  Sums over states stay in registers.  Sums over channels, which B and C share, are the costly ones: a
-// thread adds its P channels in registers and then into a place of its own channel lane in shared memory; the warps of a
+// thread adds its pair of channels and then into a place of its own channel lane in shared memory; the warps of a
 // block take different quarters of the states at a time, so that nothing is added by two of them at once and the order
 // is fixed.
 #pragma once
@@ -15,18 +15,20 @@
 
 namespace gconv {
 
-template <typename T, int TL, int K, int P, bool VEC>
-__global__ void __launch_bounds__(128) scan_bwd_kernel(const ScanArgs a)
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant__ ScanArgs a)
 {
-    constexpr int CL = 32 / TL, TT = TL * K, ROW = spots(TT), OWN = CL * P;
-    static_assert(TT % kScanMark == 0, "");
+    constexpr int TL = kScanLanes, K = kScanRun, CL = 32 / TL, TT = kScanTile, ROW = spots(TT), OWN = kScanOwn;
+    static_assert(TT % kScanMark == 0, "a tile begins at a kept state");
     extern __shared__ __align__(16) float smem[];
-    const int warps = blockDim.x >> 5, CB = warps * OWN, all = CB * a.sets;
+    const int warps = blockDim.x >> 5, CB = warps * OWN, all = CB * a.sets, S = a.S, SP = S | 1;
     float *sB = smem, *sC = sB + kScanStates * ROW, *accB = sC + kScanStates * ROW, *accC = accB + kScanStates * CL * ROW;
-    float *sM = accC + kScanStates * CL * ROW;      // [CB][kScanStates]: states before the tile
-    float *sA = sM + CB * kScanStates;              // [all][S]
-    float *sdA = sA + all * a.S, *carry = sdA + all * a.S;        // [all][S], [2][all][S]
-    float *sdD = carry + 2 * all * a.S, *sdb = sdD + all;         // [all]
+    constexpr int MP = kScanStates + 1;             // SP and MP are odd, for the banks
+    float *sM = accC + kScanStates * CL * ROW;      // [CB / 2][MP][2]: states before the tile
+    float *sdA = sM + CB * MP;             // [warps][kScanStates][32][2]: the lanes' sums for dA
+    float *sA = sdA + warps * kScanStates * 64;     // [all / 2][SP][2]
+    float *accA = sA + all * SP, *carry = accA + all * SP;          // the same, [2] of the same
+    float *sdD = carry + 2 * all * SP, *sdb = sdD + all, *sbias = sdb + all, *sskip = sbias + all;           // [all]
     int64_t id = blockIdx.x;
     const int cb = (int)(id % a.ncb); id /= a.ncb;
     const int g = (int)(id % a.G); id /= a.G;
@@ -35,251 +37,297 @@ __global__ void __launch_bounds__(128) scan_bwd_kernel(const ScanArgs a)
     const int c0 = g * a.Cg + cb * all, left = min(all, a.Cg - cb * all);
     ptx::griddep_wait();
     const int end = sequence_end(a, n);
-    for (int i = threadIdx.x; i < all * a.S; i += blockDim.x) {
-        const int ch = i / a.S, s = i % a.S;
-        sA[i] = ch < left ? decay_rate(a.A[(int64_t)c0 * a.S + i]) : 0.f;
-        sdA[i] = 0.f;
+    for (int i = threadIdx.x; i < all * S; i += blockDim.x) {
+        const int ch = i / S, s = i % S, to = (ch >> 1) * 2 * SP + 2 * s + (ch & 1);
+        sA[to] = ch < left ? decay_rate(a.A[(int64_t)c0 * S + i]) : 0.f;
+        accA[to] = 0.f;
         float w = 0.f;
         if (ch < left) {
-            if (a.chunks > 1) w = a.init[(((int64_t)n * a.chunks + chunk) * a.S + s) * a.C + c0 + ch];
-            else if (a.dstate_out) w = a.dstate_out[((int64_t)n * a.C + c0) * a.S + i];
+            if (a.chunks > 1) w = a.init[(((int64_t)n * a.chunks + chunk) * S + s) * a.C + c0 + ch];
+            else if (a.dstate_out) w = a.dstate_out[((int64_t)n * a.C + c0) * S + i];
         }
-        carry[i] = w;
+        carry[to] = w;
     }
-    for (int i = threadIdx.x; i < all; i += blockDim.x) sdD[i] = sdb[i] = 0.f;
-    const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * a.S * a.L;
-    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * a.S * a.L;
-    const T *ub = static_cast<const T *>(a.u) + n * a.su, *db = static_cast<const T *>(a.delta) + n * a.sdelta;
-    const T *yb = static_cast<const T *>(a.dy) + n * a.sdy;
-    const T *zb = a.z ? static_cast<const T *>(a.z) + n * a.sz : nullptr;
-    const T *pb = a.z ? static_cast<const T *>(a.pre) + (int64_t)n * a.C * a.L : nullptr;
-    T *dub = static_cast<T *>(a.du) + n * a.sdu, *ddb = static_cast<T *>(a.ddelta) + n * a.sddelta;
-    T *dzb = a.z ? static_cast<T *>(a.dz) + n * a.sdz : nullptr;
-    float *part = a.ncb > 1 ? a.part + (((int64_t)n * a.G + g) * a.ncb + cb) * 2 * a.S * a.L : nullptr;
+    for (int i = threadIdx.x; i < all; i += blockDim.x) {
+        sdD[i] = sdb[i] = 0.f;
+        sbias[i] = a.bias && i < left ? a.bias[c0 + i] : 0.f;
+        sskip[i] = a.D && i < left ? a.D[c0 + i] : 0.f;
+    }
+    const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * S * a.L;
+    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * S * a.L;
+    float *part = a.ncb > 1 ? a.part + (((int64_t)n * a.G + g) * a.ncb + cb) * 2 * S * a.L : nullptr;
+    const int run = spot(tl * K);
     int turn = 0;
     const int first = chunk * a.chunk_tiles, last = min(first + a.chunk_tiles, (a.L + TT - 1) / TT);
     for (int tile = last - 1; tile >= first; --tile) {
         const int t0 = tile * TT, t = t0 + tl * K;
-        if (t0 >= end) {                            // behind the sequence: zeros (finish writes those of dB and dC from part)
-            float zero[K];
+        if (t0 >= end) {                            // behind the sequence: zeros (scan_sum_kernel writes those of dB and dC from part)
+            float2 zero[K];
             #pragma unroll
-            for (int k = 0; k < K; ++k) zero[k] = 0.f;
-            for (int ch = warp * CL + cl; ch < left; ch += warps * CL) {
+            for (int k = 0; k < K; ++k) zero[k] = both(0.f);
+            for (int ch = 2 * (warp * CL + cl); ch < left; ch += CB) {
                 const int64_t row = (int64_t)(c0 + ch) * a.L;
-                store_run<T, K, VEC>(dub + row, t, a.L, zero);
-                store_run<T, K, VEC>(ddb + row, t, a.L, zero);
-                if (dzb) store_run<T, K, VEC>(dzb + row, t, a.L, zero);
+                const bool more = ch + 1 < left;
+                store_run<T, K, VEC>(static_cast<T *>(a.du) + n * a.sdu + row, a.L, t, true, more, zero);
+                store_run<T, K, VEC>(static_cast<T *>(a.ddelta) + n * a.sddelta + row, a.L, t, true, more, zero);
+                if (a.z) store_run<T, K, VEC>(static_cast<T *>(a.dz) + n * a.sdz + row, a.L, t, true, more, zero);
             }
             if (a.ncb == 1)
-                for (int i = threadIdx.x; i < 2 * a.S * TT; i += blockDim.x) {
-                    const int which = i / (a.S * TT), s = i / TT % a.S, at = t0 + i % TT;
+                for (int i = threadIdx.x; i < 2 * S * TT; i += blockDim.x) {
+                    const int r = i / TT, which = r >= S, s = r - which * S, at = t0 + i % TT;
                     T *to = static_cast<T *>(which ? a.dC : a.dB) + n * (which ? a.sdC : a.sdB);
-                    if (at < a.L) to[((int64_t)g * a.S + s) * a.L + at] = from_f<T>(0.f);
+                    if (at < a.L) to[((int64_t)g * S + s) * a.L + at] = from_f<T>(0.f);
                 }
             continue;
         }
-        const float *in = carry + turn * all * a.S;
-        float *next = carry + (turn ^ 1) * all * a.S;
         for (int set = 0; set < a.sets; ++set) {
-            const int mine = set * CB + warp * OWN + cl * P;
-            float d[P][K], du[P][K], dy[P][K], sb[P][K], aq[P][K], sum[P];
-            #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const int stop = mine + p < left ? end : 0;
-                const int64_t row = (int64_t)(c0 + mine + p) * a.L;
-                load_run<T, K, VEC>(ub + row, t, a.L, stop, du[p]);
-                load_run<T, K, VEC>(db + row, t, a.L, stop, d[p]);
-                load_run<T, K, VEC>(yb + row, t, a.L, stop, dy[p]);
-                const float bias = a.bias && mine + p < left ? a.bias[c0 + mine + p] : 0.f;
-                sum[p] = 0.f;
-                #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    float v = d[p][k] + bias;
-                    if (a.softplus) v = scan_softplus(v);
-                    v = t + k < stop ? v : 0.f;
-                    d[p][k] = v;
-                    sum[p] += v;
-                    du[p][k] *= v;
-                    sb[p][k] = aq[p][k] = 0.f;
-                }
-                if (zb) {
-                    float z[K];
-                    load_run<T, K, VEC>(zb + row, t, a.L, stop, z);
-                    #pragma unroll
-                    for (int k = 0; k < K; ++k) dy[p][k] *= z[k] * scan_sigmoid(z[k]);
-                    #pragma unroll
-                    for (int k = 0; k < K; ++k) dy[p][k] = t + k < stop ? dy[p][k] : 0.f;
+            const int mine = set * CB + 2 * (warp * CL + cl), pair = mine >> 1;
+            const bool there0 = mine < left, there1 = mine + 1 < left;
+            const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;
+            const int64_t row = (int64_t)(c0 + mine) * a.L;
+            const Place<T, K, VEC> at(row, t, a.L, there0, there1);
+            const T *ub = static_cast<const T *>(a.u) + n * a.su, *db = static_cast<const T *>(a.delta) + n * a.sdelta;
+            const T *yb = static_cast<const T *>(a.dy) + n * a.sdy, *zb = static_cast<const T *>(a.z) + n * a.sz;
+            const T *pb = static_cast<const T *>(a.pre) + (int64_t)n * a.C * a.L;
+            Run<T, K, VEC> ru, rd, ry, rz;
+            ru.load(ub, at);
+            rd.load(db, at);
+            ry.load(yb, at);
+            if (a.z) rz.load(zb, at);
+            if (VEC && tile > first && t < a.L && there0) {        // the next tile's lines
+                const int64_t o = at.x[0] - TT;
+                fetch(ub + o);
+                fetch(ub + o + at.step);
+                fetch(db + o);
+                fetch(db + o + at.step);
+                fetch(yb + o);
+                fetch(yb + o + at.step);
+                if (a.z) {
+                    fetch(zb + o);
+                    fetch(zb + o + at.step);
+                    fetch(pb + o);
+                    fetch(pb + o + at.step);
                 }
             }
-            for (int s0 = 0; s0 < a.S; s0 += kScanStates) {        // one round where there are several sets
-                const int count = min(kScanStates, a.S - s0);
+            States<T, TT, VEC> fB, fC;
+            constexpr int M = OWN * kScanStates / 32;
+            float marks[M];
+            auto ask = [&](int s0) {                // for what the next round of states needs from memory
+                const int count = min(kScanStates, S - s0);
                 if (set == 0) {
-                    __syncthreads();                // the tile or states before are done with what is staged
-                    stage_states<T, TT, VEC>(B, a.L, s0, count, t0, end, sB);
-                    stage_states<T, TT, VEC>(Cm, a.L, s0, count, t0, end, sC);
+                    fB.load(B + (int64_t)s0 * a.L, a.L, count, t0, end);
+                    fC.load(Cm + (int64_t)s0 * a.L, a.L, count, t0, end);
                 }
-                __syncwarp();                       // the set before is done with sM
-                for (int i = lane; i < OWN * count; i += 32) {
-                    const int ch = warp * OWN + i % OWN, s = i / OWN;
-                    sM[ch * kScanStates + s] = set * CB + ch < left
-                        ? a.mark[(((int64_t)n * a.marks + t0 / kScanMark) * a.S + s0 + s) * a.C + c0 + set * CB + ch] : 0.f;
+                #pragma unroll
+                for (int j = 0; j < M; ++j) {
+                    const int i = lane + j * 32, s = i / OWN, at = set * CB + warp * OWN + i % OWN;
+                    marks[j] = s < count && at < left
+                        ? a.mark[(((int64_t)n * a.marks + t0 / kScanMark) * S + s0 + s) * a.C + c0 + at] : 0.f;
                 }
-                __syncwarp();
-                if (set == 0) __syncthreads();
+            };
+            ask(0);
+            __syncthreads();                        // sbias, the first time; the tile or set before is done with what is staged
+            float2 d[K], du[K], dy[K], sb[K], aq[K], sum = both(0.f);
+            const float2 bias = *reinterpret_cast<const float2 *>(sbias + mine);
+            #pragma unroll
+            for (int k = 0; k < K; ++k) {
+                d[k] = rd.at(k) + bias;
+                if (a.softplus) d[k] = scan_softplus(d[k]);
+                du[k] = ru.at(k);
+                dy[k] = ry.at(k);
+                if (a.z) dy[k] = dy[k] * (rz.at(k) * scan_sigmoid(rz.at(k)));
+            }
+            clear_run<K>(t, end0, end1, d);
+            clear_run<K>(t, end0, end1, du);
+            clear_run<K>(t, end0, end1, dy);
+            #pragma unroll
+            for (int k = 0; k < K; ++k) {
+                sum = sum + d[k];
+                du[k] = du[k] * d[k];
+                sb[k] = aq[k] = both(0.f);
+            }
+            for (int s0 = 0; s0 < S; s0 += kScanStates) {          // one round where there are several sets
+                const int count = min(kScanStates, S - s0);
+                if (s0) {
+                    ask(s0);
+                    __syncthreads();
+                }
+                if (set == 0) {
+                    fB.store(B + (int64_t)s0 * a.L, a.L, count, t0, end, sB);
+                    fC.store(Cm + (int64_t)s0 * a.L, a.L, count, t0, end, sC);
+                }
+                #pragma unroll
+                for (int j = 0; j < M; ++j) {
+                    const int i = lane + j * 32, ch = i % OWN;
+                    sM[((warp * CL + (ch >> 1)) * MP + i / OWN) * 2 + (ch & 1)] = marks[j];
+                }
+                __syncthreads();
                 const int per = (count + warps - 1) / warps;
+                const float2 *rates = reinterpret_cast<const float2 *>(sA) + pair * SP + s0;
+                const float2 *in = reinterpret_cast<const float2 *>(carry + turn * all * SP) + pair * SP + s0;
+                float2 *next = reinterpret_cast<float2 *>(carry + (turn ^ 1) * all * SP) + pair * SP + s0;
+                const float2 *before = reinterpret_cast<const float2 *>(sM) + (warp * CL + cl) * MP;
+                float2 *dAs = reinterpret_cast<float2 *>(sdA) + warp * kScanStates * 32;
                 for (int round = 0; round < warps; ++round) {
-                    const int from = (warp + round) % warps * per, to = min(count, from + per);
+                    const int begin = (warp + round) % warps * per, stop = min(count, begin + per);
+                    const bool fresh = !(set | round);
+                    const float *rowB = sB + begin * ROW + run, *rowC = sC + begin * ROW + run;
+                    float *toB = accB + (begin * CL + cl) * ROW + run, *toC = accC + (begin * CL + cl) * ROW + run;
                     #pragma unroll 1
-                    for (int s = from; s < to; ++s) {
+                    for (int s = begin; s < stop; ++s, rowB += ROW, rowC += ROW, toB += CL * ROW, toC += CL * ROW) {
                         float Bv[K], Cv[K], aB[K], aC[K];
-                        read_run<K>(sB + s * ROW, tl * K, Bv);
-                        read_run<K>(sC + s * ROW, tl * K, Cv);
+                        float2 e[K], q[K], h = both(0.f), w = both(0.f);
+                        read_run<K>(rowB, Bv);
+                        read_run<K>(rowC, Cv);
+                        const float2 rate = rates[s], cin = in[s], hin = before[s];
                         #pragma unroll
-                        for (int k = 0; k < K; ++k) aB[k] = aC[k] = 0.f;
-                        #pragma unroll
-                        for (int p = 0; p < P; ++p) {
-                            const int at = (mine + p) * a.S + s0 + s;
-                            const float rate = sA[at], cin = in[at];
-                            const float before = sM[(warp * OWN + cl * P + p) * kScanStates + s];
-                            float e[K], q[K], h = 0.f;
-                            #pragma unroll
-                            for (int k = 0; k < K; ++k) {
-                                e[k] = ex2(d[p][k] * rate);
-                                h = fmaf(e[k], h, du[p][k] * Bv[k]);
-                            }
-                            const float whole = ex2(sum[p] * rate);
-                            float w = 0.f;
-                            #pragma unroll
-                            for (int k = K - 1; k >= 0; --k) w = e[k] * fmaf(Cv[k], dy[p][k], w);
-                            float qh = whole, qw = whole;
-                            if (tl == 0) h = fmaf(whole, before, h);
-                            if (tl == TL - 1) w = fmaf(whole, cin, w);
-                            #pragma unroll
-                            for (int o = 1; o < TL; o <<= 1) {
-                                const float hp = __shfl_up_sync(~0u, h, o, TL), qp = __shfl_up_sync(~0u, qh, o, TL);
-                                const float wp = __shfl_down_sync(~0u, w, o, TL), rp = __shfl_down_sync(~0u, qw, o, TL);
-                                if (tl >= o) { h = fmaf(qh, hp, h); qh *= qp; }
-                                if (tl + o < TL) { w = fmaf(qw, wp, w); qw *= rp; }
-                            }
-                            if (tl == 0) next[at] = w;
-                            h = __shfl_up_sync(~0u, h, 1, TL);
-                            w = __shfl_down_sync(~0u, w, 1, TL);
-                            if (tl == 0) h = before;
-                            if (tl == TL - 1) w = cin;
-                            #pragma unroll
-                            for (int k = 0; k < K; ++k) {
-                                q[k] = e[k] * h;
-                                h = fmaf(du[p][k], Bv[k], q[k]);
-                                aC[k] = fmaf(dy[p][k], h, aC[k]);
-                            }
-                            float dA = 0.f;
-                            #pragma unroll
-                            for (int k = K - 1; k >= 0; --k) {
-                                const float gr = fmaf(Cv[k], dy[p][k], w);
-                                aB[k] = fmaf(gr, du[p][k], aB[k]);
-                                sb[p][k] = fmaf(gr, Bv[k], sb[p][k]);
-                                const float x = gr * q[k];
-                                aq[p][k] = fmaf(rate, x, aq[p][k]);
-                                dA = fmaf(x, d[p][k], dA);
-                                w = e[k] * gr;
-                            }
-                            #pragma unroll
-                            for (int o = TL / 2; o > 0; o >>= 1) dA += __shfl_down_sync(~0u, dA, o, TL);
-                            if (tl == 0) sdA[at] += dA;
+                        for (int k = 0; k < K; ++k) {
+                            e[k] = ex2(d[k] * rate);
+                            h = fma2(e[k], h, du[k] * both(Bv[k]));
                         }
-                        float *toB = accB + (s * CL + cl) * ROW, *toC = accC + (s * CL + cl) * ROW;
+                        #pragma unroll
+                        for (int k = K - 1; k >= 0; --k) w = e[k] * fma2(both(Cv[k]), dy[k], w);
+                        float2 qh = ex2(sum * rate), qw = qh;
+                        h = pick(tl == 0, fma2(qh, hin, h), h);
+                        w = pick(tl == TL - 1, fma2(qw, cin, w), w);
+                        #pragma unroll
+                        for (int o = 1; o < TL; o <<= 1) {
+                            // qh of a lane below 2 o (qw of one above TL - 2 o) is not read again
+                            h = pick(tl >= o, fma2(qh, shift_up(h, o, TL), h), h);
+                            w = pick(tl + o < TL, fma2(qw, shift_down(w, o, TL), w), w);
+                            if (2 * o < TL) {
+                                qh = qh * shift_up(qh, o, TL);
+                                qw = qw * shift_down(qw, o, TL);
+                            }
+                        }
+                        if (tl == 0) next[s] = w;
+                        h = pick(tl == 0, hin, shift_up(h, 1, TL));
+                        w = pick(tl == TL - 1, cin, shift_down(w, 1, TL));
+                        #pragma unroll
+                        for (int k = 0; k < K; ++k) {
+                            q[k] = e[k] * h;
+                            h = fma2(du[k], both(Bv[k]), q[k]);
+                            const float2 x = dy[k] * h;
+                            aC[k] = x.x + x.y;
+                        }
+                        float2 dA = both(0.f);
+                        #pragma unroll
+                        for (int k = K - 1; k >= 0; --k) {
+                            const float2 gr = fma2(both(Cv[k]), dy[k], w), y = gr * du[k];
+                            const float2 x = gr * q[k];
+                            w = e[k] * gr;
+                            aB[k] = y.x + y.y;
+                            sb[k] = fma2(gr, both(Bv[k]), sb[k]);
+                            aq[k] = fma2(rate, x, aq[k]);
+                            dA = fma2(x, d[k], dA);
+                        }
+                        dAs[s * 32 + lane] = dA;
                         #pragma unroll
                         for (int k = 0; k < K; k += 4) {
-                            float4 *pB = reinterpret_cast<float4 *>(toB + spot(tl * K + k));
-                            float4 *pC = reinterpret_cast<float4 *>(toC + spot(tl * K + k));
                             float4 vB = make_float4(aB[k], aB[k + 1], aB[k + 2], aB[k + 3]);
                             float4 vC = make_float4(aC[k], aC[k + 1], aC[k + 2], aC[k + 3]);
-                            if (set | round) {
-                                const float4 oB = *pB, oC = *pC;
+                            if (!fresh) {
+                                const float4 oB = *reinterpret_cast<const float4 *>(toB + k), oC = *reinterpret_cast<const float4 *>(toC + k);
                                 vB.x += oB.x; vB.y += oB.y; vB.z += oB.z; vB.w += oB.w;
                                 vC.x += oC.x; vC.y += oC.y; vC.z += oC.z; vC.w += oC.w;
                             }
-                            *pB = vB;
-                            *pC = vC;
+                            *reinterpret_cast<float4 *>(toB + k) = vB;
+                            *reinterpret_cast<float4 *>(toC + k) = vC;
                         }
                     }
                     __syncthreads();
                 }
+                ru.load(ub, at);                    // on their way during what follows (read after the last round of states)
+                rd.load(db, at);
+                // dA of the warp's channels: a lane adds the time lanes of its state and pair
+                for (int i = lane; i < count * CL; i += 32) {
+                    const int s = i / CL, j = i % CL;
+                    float2 v = both(0.f);
+                    #pragma unroll
+                    for (int k = 0; k < TL; ++k) v = v + dAs[s * 32 + j * TL + (k + s) % TL];     // turned, for the banks
+                    float2 *to = reinterpret_cast<float2 *>(accA) + ((set * CB + warp * OWN) / 2 + j) * SP + s0 + s;
+                    *to = *to + v;
+                }
                 if (set == a.sets - 1) {
-                    for (int i = threadIdx.x; i < 2 * count * TT; i += blockDim.x) {
-                        const int which = i / (count * TT), s = i / TT % count, at = i % TT;
-                        const float *from = (which ? accC : accB) + s * CL * ROW + spot(at);
-                        float v = 0.f;
+                    for (int i = threadIdx.x; i < 2 * count * (TT / 4); i += blockDim.x) {
+                        const int r = i / (TT / 4), which = r >= count, s = r - which * count, at = i % (TT / 4) * 4;
+                        const float *src = (which ? accC : accB) + s * CL * ROW + spot(at);
+                        float4 v = *reinterpret_cast<const float4 *>(src);
                         #pragma unroll
-                        for (int j = 0; j < CL; ++j) v += from[j * ROW];
-                        if (t0 + at >= a.L) continue;
-                        if (t0 + at >= end) v = 0.f;
-                        if (part) {
-                            part[((int64_t)which * a.S + s0 + s) * a.L + t0 + at] = v;
+                        for (int j = 1; j < CL; ++j) {
+                            const float4 x = *reinterpret_cast<const float4 *>(src + j * ROW);
+                            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+                        }
+                        const float o[4] = {v.x, v.y, v.z, v.w};
+                        const int64_t line = ((int64_t)(part ? which : 0) * S + s0 + s) * a.L + t0 + at;
+                        if (part && VEC) {
+                            if (t0 + at < a.L) *reinterpret_cast<float4 *>(part + line) = v;
                         } else {
-                            T *to = static_cast<T *>(which ? a.dC : a.dB) + n * (which ? a.sdC : a.sdB);
-                            to[((int64_t)g * a.S + s0 + s) * a.L + t0 + at] = from_f<T>(v);
+                            T *to = part ? nullptr : static_cast<T *>(which ? a.dC : a.dB) + n * (which ? a.sdC : a.sdB) + (int64_t)g * S * a.L;
+                            #pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if (t0 + at + j >= a.L) continue;
+                                if (part) part[line + j] = o[j];
+                                else to[line + j] = from_f<T>(t0 + at + j < end ? o[j] : 0.f);
+                            }
                         }
                     }
                 }
             }
+            const float2 skip = *reinterpret_cast<const float2 *>(sskip + mine);
+            float2 dD = both(0.f), dbias = both(0.f);
             #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const bool there = mine + p < left;
-                const int64_t row = (int64_t)(c0 + mine + p) * a.L;
-                const int stop = there ? end : 0;
-                const float bias = a.bias && there ? a.bias[c0 + mine + p] : 0.f;
-                const float skip = a.D && there ? a.D[c0 + mine + p] : 0.f;
-                float v[K], dD = 0.f, dbias = 0.f;
-                load_run<T, K, VEC>(ub + row, t, a.L, stop, v);
+            for (int k = 0; k < K; ++k) {
+                const float2 x = ru.at(k);
+                aq[k] = fma2(x, sb[k], aq[k] * both(kLn2));
+                if (a.softplus) aq[k] = aq[k] * scan_sigmoid(rd.at(k) + bias);
+                sb[k] = fma2(d[k], sb[k], skip * dy[k]);
+                dy[k] = dy[k] * x;
+            }
+            if (a.z) {
+                rz.load(zb, at);
+                ry.load(yb, at);
+                ru.load(pb, at);
+            }
+            clear_run<K>(t, end0, end1, aq);
+            clear_run<K>(t, end0, end1, sb);
+            clear_run<K>(t, end0, end1, dy);
+            #pragma unroll
+            for (int k = 0; k < K; ++k) {
+                dbias = dbias + aq[k];
+                dD = dD + dy[k];
+            }
+            store_run<T, K, VEC>(static_cast<T *>(a.du) + n * a.sdu + row, a.L, t, there0, there1, sb);
+            store_run<T, K, VEC>(static_cast<T *>(a.ddelta) + n * a.sddelta + row, a.L, t, there0, there1, aq);
+            if (a.z) {
                 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    dD = fmaf(dy[p][k], v[k], dD);
-                    aq[p][k] = fmaf(v[k], sb[p][k], aq[p][k] * kLn2);
-                    du[p][k] = t + k < stop ? fmaf(d[p][k], sb[p][k], skip * dy[p][k]) : 0.f;
+                    const float2 z = rz.at(k), sg = scan_sigmoid(z);
+                    const float2 rest = fma2(sg, both(-1.f), both(1.f));
+                    sb[k] = ry.at(k) * ru.at(k) * (sg * fma2(z, rest, both(1.f)));
                 }
-                if (there) store_run<T, K, VEC>(dub + row, t, a.L, du[p]);
-                if (a.softplus) {
-                    load_run<T, K, VEC>(db + row, t, a.L, stop, v);
-                    #pragma unroll
-                    for (int k = 0; k < K; ++k) aq[p][k] *= scan_sigmoid(v[k] + bias);
-                }
-                #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    aq[p][k] = t + k < stop ? aq[p][k] : 0.f;
-                    dbias += aq[p][k];
-                }
-                if (there) store_run<T, K, VEC>(ddb + row, t, a.L, aq[p]);
-                if (zb) {
-                    float z[K];
-                    load_run<T, K, VEC>(zb + row, t, a.L, stop, z);
-                    load_run<T, K, VEC>(pb + row, t, a.L, stop, v);
-                    load_run<T, K, VEC>(yb + row, t, a.L, stop, du[p]);
-                    #pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        const float sg = scan_sigmoid(z[k]);
-                        v[k] = du[p][k] * v[k] * (sg * fmaf(z[k], 1.f - sg, 1.f));
-                    }
-                    #pragma unroll
-                    for (int k = 0; k < K; ++k) v[k] = t + k < stop ? v[k] : 0.f;
-                    if (there) store_run<T, K, VEC>(dzb + row, t, a.L, v);
-                }
-                #pragma unroll
-                for (int o = TL / 2; o > 0; o >>= 1) {
-                    dD += __shfl_down_sync(~0u, dD, o, TL);
-                    dbias += __shfl_down_sync(~0u, dbias, o, TL);
-                }
-                if (tl == 0) { sdD[mine + p] += dD; sdb[mine + p] += dbias; }
+                clear_run<K>(t, end0, end1, sb);
+                store_run<T, K, VEC>(static_cast<T *>(a.dz) + n * a.sdz + row, a.L, t, there0, there1, sb);
+            }
+            #pragma unroll
+            for (int o = TL / 2; o > 0; o >>= 1) {
+                dD = dD + shift_down(dD, o, TL);
+                dbias = dbias + shift_down(dbias, o, TL);
+            }
+            if (tl == 0) {
+                sdD[mine] += dD.x; sdD[mine + 1] += dD.y;
+                sdb[mine] += dbias.x; sdb[mine + 1] += dbias.y;
             }
         }
         turn ^= 1;
     }
     __syncthreads();
-    const float *fin = carry + turn * all * a.S;
+    const float *fin = carry + turn * all * SP;
     const int64_t base = ((int64_t)n * a.chunks + chunk) * a.C + c0;
-    for (int i = threadIdx.x; i < left * a.S; i += blockDim.x) {
-        a.pA[base * a.S + i] = sdA[i];
-        if (a.dstate && chunk == 0) a.dstate[((int64_t)n * a.C + c0) * a.S + i] = fin[i];
+    for (int i = threadIdx.x; i < left * S; i += blockDim.x) {
+        const int ch = i / S, s = i % S, from = (ch >> 1) * 2 * SP + 2 * s + (ch & 1);
+        a.pA[base * S + i] = accA[from];
+        if (a.dstate && chunk == 0) a.dstate[((int64_t)n * a.C + c0) * S + i] = fin[from];
     }
     for (int i = threadIdx.x; i < left; i += blockDim.x) {
         a.pD[base + i] = sdD[i];
@@ -288,105 +336,97 @@ __global__ void __launch_bounds__(128) scan_bwd_kernel(const ScanArgs a)
 }
 
 // What leaves a piece of a sequence backwards when nothing enters it, and its sum of d.
-template <typename T, int TL, int K, int P, bool VEC>
-__global__ void __launch_bounds__(128) scan_bwd_ends_kernel(const ScanArgs a)
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(128) scan_bwd_ends_kernel(const __grid_constant__ ScanArgs a)
 {
-    constexpr int CL = 32 / TL, TT = TL * K, ROW = spots(TT);
+    constexpr int TL = kScanLanes, K = kScanRun, CL = 32 / TL, TT = kScanTile, ROW = spots(TT);
     extern __shared__ __align__(16) float smem[];
-    const int warps = blockDim.x >> 5, CB = warps * CL * P;
-    float *sC = smem, *sA = sC + kScanStates * ROW, *carry = sA + CB * a.S;
+    const int CB = (blockDim.x >> 5) * CL * 2, S = a.S, SP = S | 1;
+    float *sC = smem, *sA = sC + kScanStates * ROW, *carry = sA + CB * SP;
     int64_t id = blockIdx.x;
     const int blocks = (a.Cg + CB - 1) / CB;
     const int cb = (int)(id % blocks); id /= blocks;
     const int g = (int)(id % a.G); id /= a.G;
     const int chunk = (int)(id % a.chunks), n = (int)(id / a.chunks);
     const int lane = threadIdx.x & 31, tl = lane % TL;
-    const int mine = ((threadIdx.x >> 5) * CL + lane / TL) * P;
+    const int pair = (threadIdx.x >> 5) * CL + lane / TL, mine = 2 * pair;
     const int c0 = g * a.Cg + cb * CB, left = min(CB, a.Cg - cb * CB);
     ptx::griddep_wait();
     const int end = sequence_end(a, n);
-    for (int i = threadIdx.x; i < CB * a.S; i += blockDim.x) {
-        sA[i] = i / a.S < left ? decay_rate(a.A[(int64_t)c0 * a.S + i]) : 0.f;
-        carry[i] = 0.f;
+    for (int i = threadIdx.x; i < CB * S; i += blockDim.x) {
+        const int ch = i / S, s = i % S;
+        sA[(ch >> 1) * 2 * SP + 2 * s + (ch & 1)] = ch < left ? decay_rate(a.A[(int64_t)c0 * S + i]) : 0.f;
     }
-    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * a.S * a.L;
-    float total[P];
-    #pragma unroll
-    for (int p = 0; p < P; ++p) total[p] = 0.f;
+    for (int i = threadIdx.x; i < CB * SP; i += blockDim.x) carry[i] = 0.f;
+    const bool there0 = mine < left, there1 = mine + 1 < left;
+    const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;
+    const int64_t row = (int64_t)(c0 + mine) * a.L;
+    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * S * a.L;
+    const float2 bias = make_float2(a.bias && there0 ? a.bias[c0 + mine] : 0.f, a.bias && there1 ? a.bias[c0 + mine + 1] : 0.f);
+    float2 total = both(0.f);
     int turn = 0;
     const int first = chunk * a.chunk_tiles, last = min(first + a.chunk_tiles, (a.L + TT - 1) / TT);
     for (int tile = last - 1; tile >= first; --tile) {
         const int t0 = tile * TT, t = t0 + tl * K;
         if (t0 >= end) continue;
-        float d[P][K], dy[P][K], sum[P];
+        Run<T, K, VEC> rd, ry, rz;
+        const Place<T, K, VEC> at(row, t, a.L, there0, there1);
+        rd.load(static_cast<const T *>(a.delta) + n * a.sdelta, at);
+        ry.load(static_cast<const T *>(a.dy) + n * a.sdy, at);
+        if (a.z) rz.load(static_cast<const T *>(a.z) + n * a.sz, at);
+        float2 d[K], dy[K], sum = both(0.f);
         #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int stop = mine + p < left ? end : 0;
-            const int64_t row = (int64_t)(c0 + mine + p) * a.L;
-            load_run<T, K, VEC>(static_cast<const T *>(a.delta) + n * a.sdelta + row, t, a.L, stop, d[p]);
-            load_run<T, K, VEC>(static_cast<const T *>(a.dy) + n * a.sdy + row, t, a.L, stop, dy[p]);
-            const float bias = a.bias && mine + p < left ? a.bias[c0 + mine + p] : 0.f;
-            sum[p] = 0.f;
-            #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float v = d[p][k] + bias;
-                if (a.softplus) v = scan_softplus(v);
-                d[p][k] = t + k < stop ? v : 0.f;
-                sum[p] += d[p][k];
-            }
-            total[p] += sum[p];
-            if (a.z) {
-                float z[K];
-                load_run<T, K, VEC>(static_cast<const T *>(a.z) + n * a.sz + row, t, a.L, stop, z);
-                #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    dy[p][k] *= z[k] * scan_sigmoid(z[k]);
-                    dy[p][k] = t + k < stop ? dy[p][k] : 0.f;
-                }
-            }
+        for (int k = 0; k < K; ++k) {
+            d[k] = rd.at(k) + bias;
+            if (a.softplus) d[k] = scan_softplus(d[k]);
+            dy[k] = ry.at(k);
+            if (a.z) dy[k] = dy[k] * (rz.at(k) * scan_sigmoid(rz.at(k)));
         }
-        const float *in = carry + turn * CB * a.S;
-        float *next = carry + (turn ^ 1) * CB * a.S;
-        for (int s0 = 0; s0 < a.S; s0 += kScanStates) {
-            const int count = min(kScanStates, a.S - s0);
+        clear_run<K>(t, end0, end1, d);
+        clear_run<K>(t, end0, end1, dy);
+        #pragma unroll
+        for (int k = 0; k < K; ++k) sum = sum + d[k];
+        total = total + sum;
+        for (int s0 = 0; s0 < S; s0 += kScanStates) {
+            const int count = min(kScanStates, S - s0);
+            States<T, TT, VEC> fC;
+            fC.load(Cm + (int64_t)s0 * a.L, a.L, count, t0, end);
             __syncthreads();
-            stage_states<T, TT, VEC>(Cm, a.L, s0, count, t0, end, sC);
+            fC.store(Cm + (int64_t)s0 * a.L, a.L, count, t0, end, sC);
             __syncthreads();
+            const float2 *rates = reinterpret_cast<const float2 *>(sA) + pair * SP + s0;
+            const float2 *in = reinterpret_cast<const float2 *>(carry + turn * CB * SP) + pair * SP + s0;
+            float2 *next = reinterpret_cast<float2 *>(carry + (turn ^ 1) * CB * SP) + pair * SP + s0;
             #pragma unroll 1
             for (int s = 0; s < count; ++s) {
                 float Cv[K];
-                read_run<K>(sC + s * ROW, tl * K, Cv);
+                read_run<K>(sC + s * ROW + spot(tl * K), Cv);
+                const float2 rate = rates[s];
+                float2 w = both(0.f), q = ex2(sum * rate);
                 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const int at = (mine + p) * a.S + s0 + s;
-                    const float rate = sA[at];
-                    float w = 0.f, qw = ex2(sum[p] * rate);
-                    #pragma unroll
-                    for (int k = K - 1; k >= 0; --k) w = ex2(d[p][k] * rate) * fmaf(Cv[k], dy[p][k], w);
-                    if (tl == TL - 1) w = fmaf(qw, in[at], w);
-                    #pragma unroll
-                    for (int o = 1; o < TL; o <<= 1) {
-                        const float wp = __shfl_down_sync(~0u, w, o, TL), rp = __shfl_down_sync(~0u, qw, o, TL);
-                        if (tl + o < TL) { w = fmaf(qw, wp, w); qw *= rp; }
-                    }
-                    if (tl == 0) next[at] = w;
+                for (int k = K - 1; k >= 0; --k) w = ex2(d[k] * rate) * fma2(both(Cv[k]), dy[k], w);
+                w = pick(tl == TL - 1, fma2(q, in[s], w), w);
+                #pragma unroll
+                for (int o = 1; o < TL; o <<= 1) {
+                    w = pick(tl + o < TL, fma2(q, shift_down(w, o, TL), w), w);
+                    if (2 * o < TL) q = q * shift_down(q, o, TL);
                 }
+                if (tl == 0) next[s] = w;
             }
         }
         turn ^= 1;
     }
     __syncthreads();
-    const float *fin = carry + turn * CB * a.S;
-    for (int i = threadIdx.x; i < left * a.S; i += blockDim.x) {
+    const float *fin = carry + turn * CB * SP;
+    for (int i = threadIdx.x; i < left * S; i += blockDim.x) {
         const int s = i / left, ch = i % left;
-        a.init[(((int64_t)n * a.chunks + chunk) * a.S + s) * a.C + c0 + ch] = fin[ch * a.S + s];
+        a.init[(((int64_t)n * a.chunks + chunk) * S + s) * a.C + c0 + ch] = fin[(ch >> 1) * 2 * SP + 2 * s + (ch & 1)];
     }
     #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        #pragma unroll
-        for (int o = TL / 2; o > 0; o >>= 1) total[p] += __shfl_down_sync(~0u, total[p], o, TL);
-        if (tl == 0 && mine + p < left) a.dsum[((int64_t)n * a.chunks + chunk) * a.C + c0 + mine + p] = total[p];
-    }
+    for (int o = TL / 2; o > 0; o >>= 1) total = total + shift_down(total, o, TL);
+    float *to = a.dsum + ((int64_t)n * a.chunks + chunk) * a.C + c0 + mine;
+    if (tl == 0 && there0) to[0] = total.x;
+    if (tl == 0 && there1) to[1] = total.y;
 }
 
 }  // namespace gconv

@@ -16,38 +16,18 @@ void scan_start(F *kernel, const ScanShape &s, const ScanArgs &a, cudaStream_t s
     launch_dependent(kernel, s.grid, (unsigned)s.warps * 32, s.smem, st, a);
 }
 
-template <typename T, int F = 0>
+template <typename T>
 void scan_fwd_start(const ScanShape &s, bool ends, const ScanArgs &a, cudaStream_t st)
 {
-    constexpr ScanForm f = kFwdForms[F];
-    if (s.form == F) {
-        if (s.vec) {
-            if (ends) scan_start(scan_fwd_kernel<T, f.TL, f.K, f.P, true, true>, s, a, st);
-            else scan_start(scan_fwd_kernel<T, f.TL, f.K, f.P, true, false>, s, a, st);
-        } else {
-            if (ends) scan_start(scan_fwd_kernel<T, f.TL, f.K, f.P, false, true>, s, a, st);
-            else scan_start(scan_fwd_kernel<T, f.TL, f.K, f.P, false, false>, s, a, st);
-        }
-        return;
-    }
-    if constexpr (F + 1 < kFwdFormCount) scan_fwd_start<T, F + 1>(s, ends, a, st);
+    if (s.vec) scan_start(ends ? scan_fwd_kernel<T, true, true> : scan_fwd_kernel<T, true, false>, s, a, st);
+    else scan_start(ends ? scan_fwd_kernel<T, false, true> : scan_fwd_kernel<T, false, false>, s, a, st);
 }
 
-template <typename T, int F = 0>
+template <typename T>
 void scan_bwd_start(const ScanShape &s, bool ends, const ScanArgs &a, cudaStream_t st)
 {
-    constexpr ScanForm f = kBwdForms[F];
-    if (s.form == F) {
-        if (s.vec) {
-            if (ends) scan_start(scan_bwd_ends_kernel<T, f.TL, f.K, f.P, true>, s, a, st);
-            else scan_start(scan_bwd_kernel<T, f.TL, f.K, f.P, true>, s, a, st);
-        } else {
-            if (ends) scan_start(scan_bwd_ends_kernel<T, f.TL, f.K, f.P, false>, s, a, st);
-            else scan_start(scan_bwd_kernel<T, f.TL, f.K, f.P, false>, s, a, st);
-        }
-        return;
-    }
-    if constexpr (F + 1 < kBwdFormCount) scan_bwd_start<T, F + 1>(s, ends, a, st);
+    if (s.vec) scan_start(ends ? scan_bwd_ends_kernel<T, true> : scan_bwd_kernel<T, true>, s, a, st);
+    else scan_start(ends ? scan_bwd_ends_kernel<T, false> : scan_bwd_kernel<T, false>, s, a, st);
 }
 
 }  // namespace gconv

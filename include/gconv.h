@@ -352,8 +352,8 @@ gconv_status gconv_muon_step(const gconv_matrices *matrices, const gconv_muon *o
  * `lengths` are those of the scan below: elements between sequences (0: dense), and positions of each
  * (device, or NULL); what lies behind them is not used, and y and dx are zero there.  Sums are fp32, results are rounded once,
  * and every reduction has a fixed order.
- * Requirements: C, L >= 1, N >= 0, 1 <= taps <= 8, act GCONV_ACT_NONE or GCONV_ACT_SILU, tensors of at most 2^40
- * elements, pointers aligned to their elements (the workspace to 16 bytes; tensors whose rows begin at the same place
+ * Requirements: C, L >= 1, N >= 0, 1 <= taps <= 8, act GCONV_ACT_NONE or GCONV_ACT_SILU, L at most 2^30, N C below
+ * 2^31, tensors of at most 2^40 elements, pointers aligned to their elements (the workspace to 16 bytes; tensors whose rows begin at the same place
  * within 16 bytes are faster).  The record is read during the call only. */
 typedef struct {
     int N, C, L, taps, act;
@@ -392,8 +392,8 @@ gconv_status gconv_causal_bwd(const gconv_causal *causal, gconv_dtype dtype, con
  * them is not used; y and the gradients are zero there, and state_out is the state after the last of them
  * (of none: the state that came in).
  * States, sums and exponentials are fp32 whatever dtype is; a result is rounded once.  Bitwise reproducible.
- * Requirements: C, L, groups, states >= 1, N >= 0, C divisible by groups, states <= 256, C states below 2^31,
- * tensors of at most 2^40 elements, pointers aligned to their elements (those of saved and workspace
+ * Requirements: C, L, groups, states >= 1, N >= 0, C divisible by groups, L at most 2^30, states <= 256,
+ * C states below 2^31, tensors of at most 2^40 elements, pointers aligned to their elements (those of saved and workspace
  * to 16 bytes; rows of a multiple of 16 bytes on 16-byte boundaries are faster).  The record is read during the
  * call only.  N == 0 is a no-op (the gradients of A, D and delta_bias are set to zero). */
 typedef struct {
