@@ -53,12 +53,12 @@ __device__ __forceinline__ void load_some(const T *row, int t, int end, float *v
     for (int j = 0; j < M; ++j) v[j] = t + j >= 0 && t + j < end ? to_f(row[t + j]) : 0.f;
 }
 
-// Elements t .. t + M - 1 to a row of L; an address on 16 bytes where VEC.
+// Elements t .. t + M - 1 to a row of L; `whole`: all of them are in it, and the address is on 16 bytes.
 template <typename T, int M, bool VEC>
-__device__ __forceinline__ void store_pieces(T *row, int t, int L, const float (&v)[M])
+__device__ __forceinline__ void store_pieces(T *row, int t, int L, bool whole, const float (&v)[M])
 {
     constexpr int V = 16 / (int)sizeof(T);
-    if (VEC && t >= 0 && t + M <= L) {
+    if (VEC && whole) {
         #pragma unroll
         for (int i = 0; i < M; i += V) {
             Pack<T, V> x;
@@ -74,42 +74,37 @@ __device__ __forceinline__ void store_pieces(T *row, int t, int L, const float (
 }
 
 // win[i]: x at t - H + i for i < H + M (zeros outside the sequence, the state before it); d, unless `other` is null: another
-// tensor's M elements from t.  All the loads are on their way before the first is used.
+// tensor's M elements from t.  `whole`: the run is inside the sequence or behind it, and begins the row or has whole pieces
+// before it.  What it has not is then read from `safe`, the row's first place on 16 bytes, so that no load needs a
+// condition and all are on their way before the first is used; a lane behind the sequence gets values that are not its own.
 template <typename T, int M, int H, bool VEC>
-__device__ __forceinline__ void load_window(const T *row, const T *state, int t, int end, float (&win)[H + M], const T *other, float *d)
+__device__ __forceinline__ void load_window(const T *row, const T *state, int t, int end, bool whole, int safe, float (&win)[H + M],
+                                            const T *other, float (&d)[M])
 {
     constexpr int V = 16 / (int)sizeof(T), BACK = (H + V - 1) / V;      // pieces before t
-    const bool inside = VEC && t >= 0 && t + M <= end, behind = VEC && t >= BACK * V;
-    Pack<T, V> p[BACK ? BACK : 1], x[M / V], o[M / V];
-    if (inside) {
+    if (VEC && whole) {
+        const int from = t < end ? t : safe, before = from >= BACK * V ? from - BACK * V : safe;
+        Pack<T, V> p[BACK ? BACK : 1], x[M / V], o[M / V];
         #pragma unroll
-        for (int i = 0; i < M / V; ++i) x[i] = *reinterpret_cast<const Pack<T, V> *>(row + t + i * V);
+        for (int i = 0; i < M / V; ++i) x[i] = *reinterpret_cast<const Pack<T, V> *>(row + from + i * V);
+        #pragma unroll
+        for (int i = 0; i < BACK; ++i) p[i] = *reinterpret_cast<const Pack<T, V> *>(row + before + i * V);
         if (other) {
             #pragma unroll
-            for (int i = 0; i < M / V; ++i) o[i] = *reinterpret_cast<const Pack<T, V> *>(other + t + i * V);
+            for (int i = 0; i < M / V; ++i) o[i] = *reinterpret_cast<const Pack<T, V> *>(other + from + i * V);
         }
-    }
-    if (behind) {
         #pragma unroll
-        for (int i = 0; i < BACK; ++i) p[i] = *reinterpret_cast<const Pack<T, V> *>(row + t + (i - BACK) * V);
-    }
-    if (behind) {
-        #pragma unroll
-        for (int i = 0; i < H; ++i) win[i] = to_f(p[(BACK * V - H + i) / V].v[(BACK * V - H + i) % V]);
-    } else {
-        load_some<T, H>(row, t - H, end, win);
-    }
-    if (inside) {
+        for (int i = 0; i < H; ++i) win[i] = t ? to_f(p[(BACK * V - H + i) / V].v[(BACK * V - H + i) % V]) : 0.f;
         #pragma unroll
         for (int i = 0; i < M; ++i) win[H + i] = to_f(x[i / V].v[i % V]);
         if (other) {
             #pragma unroll
             for (int i = 0; i < M; ++i) d[i] = to_f(o[i / V].v[i % V]);
         }
-    } else {
-        load_some<T, M>(row, t, end, win + H);
-        if (other) load_some<T, M>(other, t, end, d);
+        return;
     }
+    load_some<T, H + M>(row, t - H, end, win);
+    if (other) load_some<T, M>(other, t, end, d);
     if (state && t < H) {
         #pragma unroll
         for (int i = 0; i < H + M; ++i) {
@@ -119,12 +114,14 @@ __device__ __forceinline__ void load_window(const T *row, const T *state, int t,
     }
 }
 
-// dy act'(v)
-__device__ __forceinline__ float causal_back(int act, float v, float d)
+// Whether a run of M elements from t takes the short way through load_window and the stores.
+template <typename T, int M, int H>
+__device__ __forceinline__ bool whole_run(int t, int end, int L, bool state)
 {
-    if (act != GCONV_ACT_SILU) return d;
-    const float s = scan_sigmoid(v);
-    return d * (s * fmaf(v, 1.f - s, 1.f));
+    constexpr int V = 16 / (int)sizeof(T), BACK = (H + V - 1) / V;
+    if (end < M + V) return t >= L;              // `safe` and a run from there are in the sequence
+    if (t >= end) return t >= L || t + M <= L;
+    return t + M <= end && (t >= BACK * V || (t == 0 && !state));
 }
 
 template <typename T>
@@ -132,6 +129,46 @@ __device__ __forceinline__ int phase_of(const T *row)
 {
     return (int)((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % (16 / sizeof(T)));
 }
+
+template <typename T>
+__device__ __forceinline__ int first_place(int phase) { return phase ? 16 / (int)sizeof(T) - phase : 0; }
+
+// A worker's way through its share of a channel's rows: pieces in order, row after row.
+struct Walk {
+    unsigned made, all, left;            // left: pieces that are still its own
+    int n, seg, end;
+    int64_t t;                          // of the piece's first run, were the row on 16 bytes
+    bool on;
+
+    __device__ __forceinline__ Walk(const CausalArgs &a, unsigned split, int c, bool there) : made(0), t(0)
+    {
+        const unsigned items = (unsigned)a.N * (unsigned)a.segs;
+        all = (items + a.splits - 1) / a.splits;
+        const unsigned first = min(items, split * all);
+        left = there ? min(items - first, all) : 0;
+        on = left > 0;
+        n = on ? (int)(first / (unsigned)a.segs) : 0;
+        seg = on ? (int)(first - (unsigned)n * a.segs) : 0;
+        end = on ? causal_end(a, n) : 0;
+    }
+    template <typename F>
+    __device__ __forceinline__ void step(const CausalArgs &a, int width, F next_row)
+    {
+        ++made;
+        ++seg;
+        t += width;
+        on = made < left;
+        if (seg == a.segs) {
+            seg = 0;
+            t = 0;
+            ++n;
+            next_row();
+            end = on ? causal_end(a, n) : 0;
+        } else if (!on) {
+            end = 0;
+        }
+    }
+};
 
 template <typename T, int K, bool VEC>
 __global__ void __launch_bounds__(kCausalThreads) causal_fwd_kernel(const __grid_constant__ CausalArgs a)
@@ -146,45 +183,46 @@ __global__ void __launch_bounds__(kCausalThreads) causal_fwd_kernel(const __grid
     #pragma unroll
     for (int k = 0; k < K; ++k) w[k] = there ? a.w[(int64_t)c * K + k] : 0.f;
     const float bias = a.bias && there ? a.bias[c] : 0.f;
+    Walk at(a, split, c, there);
+    at.t = (int64_t)at.seg * a.TX * M;
+    const T *row = static_cast<const T *>(a.x) + at.n * a.sx + (int64_t)c * a.L;
+    T *out = static_cast<T *>(a.out) + at.n * a.sy + (int64_t)c * a.L;
     // every lane of a warp makes the same rounds: state_out needs the warp together
-    const unsigned items = (unsigned)a.N * (unsigned)a.segs, rounds = (items + a.splits - 1) / a.splits;
-    for (unsigned round = 0; round < rounds; ++round) {
-        const unsigned item = split + round * a.splits;
-        const bool on = there && item < items;
-        const int n = !on ? 0 : a.segs == 1 ? (int)item : (int)(item / (unsigned)a.segs), seg = (int)(item - (unsigned)n * a.segs);
-        const int end = on ? causal_end(a, n) : 0;
-        const T *row = static_cast<const T *>(a.x) + n * a.sx + (int64_t)c * a.L;
-        T *out = static_cast<T *>(a.out) + n * a.sy + (int64_t)c * a.L;
+    for (; at.made < at.all; at.step(a, a.TX * M, [&] { row += a.sx; out += a.sy; })) {
+        const bool on = at.on;
+        const int n = at.n, end = at.end, phase = VEC ? phase_of(row) : 0;
         const T *state = a.state && H && on ? static_cast<const T *>(a.state) + ((int64_t)n * a.C + c) * H : nullptr;
-        const int64_t t_ = ((int64_t)seg * a.TX + tx) * M - (VEC ? phase_of(row) : 0);
-        if (VEC && round + 1 < rounds && item + a.splits < items) {       // the next round's lines, on their way to L2
-            const unsigned next = item + a.splits;
-            const int n2 = a.segs == 1 ? (int)next : (int)(next / (unsigned)a.segs), s2 = (int)(next - (unsigned)n2 * a.segs);
-            const int64_t t2 = ((int64_t)s2 * a.TX + tx) * M;
-            if (there && t2 < a.L) fetch(static_cast<const T *>(a.x) + n2 * a.sx + (int64_t)c * a.L + t2);
+        const int64_t t_ = at.t + (int64_t)tx * M - phase;
+        const int t = on && t_ < a.L ? (int)t_ : a.L;
+        const bool whole = VEC && whole_run<T, M, H>(t, end, a.L, state != nullptr);
+        if (VEC && on) {                            // the next round's lines, on their way to L2
+            if (t_ + a.TX * M < a.L) fetch(row + t_ + a.TX * M);
+            else if (at.seg + 1 == a.segs && n + 1 < a.N && (int64_t)tx * M < a.L) fetch(row + a.sx + tx * M);
         }
-        if (on && t_ < a.L) {
-            const int t = (int)t_;
+        if (t < a.L) {
             float win[H + M], y[M];
-            load_window<T, M, H, VEC>(row, state, t, end, win, nullptr, nullptr);
+            load_window<T, M, H, VEC>(row, state, t, end, whole, first_place<T>(phase), win, nullptr, y);
             #pragma unroll
             for (int j = 0; j < M; ++j) {
                 float v = bias;
                 #pragma unroll
                 for (int k = 0; k < K; ++k) v = fmaf(w[k], win[j + k], v);
-                if (a.act == GCONV_ACT_SILU) v *= scan_sigmoid(v);
                 y[j] = v;
+            }
+            if (a.act == GCONV_ACT_SILU) {
+                #pragma unroll
+                for (int j = 0; j < M; ++j) y[j] *= scan_sigmoid(y[j]);
             }
             if (t + M > end) {
                 #pragma unroll
                 for (int j = 0; j < M; ++j) y[j] = t + j < end ? y[j] : 0.f;
             }
-            store_pieces<T, M, VEC>(out, t, a.L, y);
+            store_pieces<T, M, VEC>(out, t, a.L, whole, y);
         }
         if (H && a.state_out) {
             // only a row's first piece reads the state, and its lanes are through with that before the first of them
             // writes: it may be the same memory
-            const bool writes = on && seg == 0 && tx == 0;
+            const bool writes = on && at.seg == 0 && tx == 0;
             float last[H ? H : 1];
             #pragma unroll
             for (int j = 0; j < H; ++j) {
@@ -243,7 +281,7 @@ __global__ void __launch_bounds__(128) causal_short_kernel(const __grid_constant
 // lane makes its dv for the lane before alone, and its run is the first of the next piece: 31 of 32 lanes' work counts.
 // (Exchanging through shared memory by the whole block instead took a barrier a piece: 132 us against the time below.)
 template <typename T, int K, bool VEC>
-__global__ void __launch_bounds__(kCausalThreads, 5) causal_bwd_kernel(const __grid_constant__ CausalArgs a)
+__global__ void __launch_bounds__(kCausalThreads, 6) causal_bwd_kernel(const __grid_constant__ CausalArgs a)
 {
     constexpr int M = kCausalBack, H = K - 1;
     static_assert(H <= M, "what a lane needs from the next one is in that one's run");
@@ -256,45 +294,61 @@ __global__ void __launch_bounds__(kCausalThreads, 5) causal_bwd_kernel(const __g
     #pragma unroll
     for (int k = 0; k < K; ++k) { w[k] = there ? a.w[(int64_t)c * K + k] : 0.f; dw[k] = 0.f; }
     const float bias = a.bias && there ? a.bias[c] : 0.f;
+    Walk at(a, split, c, there);
+    at.t = (int64_t)at.seg * runs * M;
+    const T *row = static_cast<const T *>(a.x) + at.n * a.sx + (int64_t)c * a.L;
+    const T *grad = static_cast<const T *>(a.dy) + at.n * a.sdy + (int64_t)c * a.L;
+    T *out = static_cast<T *>(a.out) + at.n * a.sdx + (int64_t)c * a.L;
+    const bool mine = (int)tx < runs;
     // every lane of a warp makes the same rounds, for the shuffles
-    const unsigned items = (unsigned)a.N * (unsigned)a.segs, rounds = (items + a.splits - 1) / a.splits;
-    for (unsigned round = 0; round < rounds; ++round) {
-        const unsigned item = split + round * a.splits;
-        const bool on = there && item < items;
-        const int n = !on ? 0 : a.segs == 1 ? (int)item : (int)(item / (unsigned)a.segs), seg = (int)(item - (unsigned)n * a.segs);
-        const int end = on ? causal_end(a, n) : 0;
-        const T *row = static_cast<const T *>(a.x) + n * a.sx + (int64_t)c * a.L;
-        const T *grad = static_cast<const T *>(a.dy) + n * a.sdy + (int64_t)c * a.L;
+    for (; at.made < at.all; at.step(a, runs * M, [&] { row += a.sx; grad += a.sdy; out += a.sdx; })) {
+        const bool on = at.on;
+        const int n = at.n, end = at.end, phase = VEC ? phase_of(row) : 0;
         const T *state = a.state && H && on ? static_cast<const T *>(a.state) + ((int64_t)n * a.C + c) * H : nullptr;
-        const int64_t t_ = ((int64_t)seg * runs + tx) * M - (VEC ? phase_of(row) : 0);
-        const int t = t_ < a.L ? (int)t_ : a.L;
-        const bool mine = (int)tx < runs;
-        if (VEC && round + 1 < rounds && item + a.splits < items) {       // the next round's lines, on their way to L2
-            const unsigned next = item + a.splits;
-            const int n2 = a.segs == 1 ? (int)next : (int)(next / (unsigned)a.segs), s2 = (int)(next - (unsigned)n2 * a.segs);
-            const int64_t t2 = ((int64_t)s2 * runs + tx) * M;
-            if (there && t2 < a.L && (tx & 1) == 0) {
-                fetch(static_cast<const T *>(a.x) + n2 * a.sx + (int64_t)c * a.L + t2);
-                fetch(static_cast<const T *>(a.dy) + n2 * a.sdy + (int64_t)c * a.L + t2);
+        const int64_t t_ = at.t + (int64_t)tx * M - phase;
+        const int t = on && t_ < a.L ? (int)t_ : a.L;
+        const T *more = a.dstate_out && on ? static_cast<const T *>(a.dstate_out) + ((int64_t)n * a.C + c) * H : nullptr;
+        const bool whole = VEC && !a.dstate_out && whole_run<T, M, H>(t, end, a.L, state != nullptr);
+        if (VEC && on) {                            // the next round's lines, on their way to L2
+            if (t_ + runs * M < a.L) {
+                fetch(row + t_ + runs * M);
+                fetch(grad + t_ + runs * M);
+            } else if (at.seg + 1 == a.segs && n + 1 < a.N && (int64_t)tx * M < a.L) {
+                fetch(row + a.sx + tx * M);
+                fetch(grad + a.sdy + tx * M);
             }
         }
-        float dv[M + H], win[H + M];
+        float dv[M + H], win[H + M], d[M];
         if (t < end) {
-            load_window<T, M, H, VEC>(row, state, t, end, win, grad, dv);
-            #pragma unroll
-            for (int j = 0; j < M; ++j) {
-                float v = bias;
-                #pragma unroll
-                for (int k = 0; k < K; ++k) v = fmaf(w[k], win[j + k], v);
-                dv[j] = causal_back(a.act, v, dv[j]);
-            }
-            if (t < 0 || t + M > end) {
-                #pragma unroll
-                for (int j = 0; j < M; ++j) dv[j] = t + j >= 0 && t + j < end ? dv[j] : 0.f;
-            }
-            if (mine) {
+            load_window<T, M, H, VEC>(row, state, t, end, whole, first_place<T>(phase), win, grad, d);
+            if (a.act == GCONV_ACT_SILU) {
                 #pragma unroll
                 for (int j = 0; j < M; ++j) {
+                    float v = bias;
+                    #pragma unroll
+                    for (int k = 0; k < K; ++k) v = fmaf(w[k], win[j + k], v);
+                    const float s = scan_sigmoid(v);
+                    dv[j] = d[j] * (s * fmaf(v, 1.f - s, 1.f));
+                }
+            } else {
+                #pragma unroll
+                for (int j = 0; j < M; ++j) dv[j] = d[j];
+            }
+            if (whole) {
+                if (mine) {
+                    #pragma unroll
+                    for (int j = 0; j < M; ++j) {
+                        db += dv[j];
+                        #pragma unroll
+                        for (int k = 0; k < K; ++k) dw[k] = fmaf(dv[j], win[j + k], dw[k]);
+                    }
+                }
+            } else {
+                #pragma unroll
+                for (int j = 0; j < M; ++j) {
+                    const bool in = t + j >= 0 && t + j < end;
+                    dv[j] = in ? dv[j] : 0.f;
+                    if (!in || !mine) continue;
                     db += dv[j];
                     #pragma unroll
                     for (int k = 0; k < K; ++k) dw[k] = fmaf(dv[j], win[j + k], dw[k]);
@@ -311,7 +365,6 @@ __global__ void __launch_bounds__(kCausalThreads, 5) causal_bwd_kernel(const __g
         }
         if (on && mine && t < a.L) {
             float dx[M];
-            const T *more = a.dstate_out ? static_cast<const T *>(a.dstate_out) + ((int64_t)n * a.C + c) * H : nullptr;
             #pragma unroll
             for (int j = 0; j < M; ++j) {
                 float v = 0.f;
@@ -319,7 +372,7 @@ __global__ void __launch_bounds__(kCausalThreads, 5) causal_bwd_kernel(const __g
                 for (int k = 0; k < K; ++k) v = fmaf(w[k], dv[j + H - k], v);
                 dx[j] = v;
             }
-            if (t + M > end - H) {                   // near the end, or behind it
+            if (!whole && t + M > end - H) {         // near the end, or behind it
                 #pragma unroll
                 for (int j = 0; j < M; ++j) {
                     const int from = t + j - (end - H);
@@ -327,8 +380,8 @@ __global__ void __launch_bounds__(kCausalThreads, 5) causal_bwd_kernel(const __g
                     dx[j] = t + j < end ? dx[j] : 0.f;
                 }
             }
-            store_pieces<T, M, VEC>(static_cast<T *>(a.out) + n * a.sdx + (int64_t)c * a.L, t, a.L, dx);
-            if (H && a.dstate && seg == 0 && tx == 0) {
+            store_pieces<T, M, VEC>(out, t, a.L, whole, dx);
+            if (H && a.dstate && at.seg == 0 && tx == 0) {
                 #pragma unroll
                 for (int j = 0; j < H; ++j) {
                     float v = 0.f;
@@ -395,18 +448,27 @@ struct CausalShape { int TX, segs, splits; int64_t grid; };
 CausalShape causal_shape(const gconv_causal &s, gconv_dtype dt, bool back, bool whole)
 {
     const int V = 16 / esize(dt), M = back ? kCausalBack : 2 * V;
-    const int64_t runs = ((int64_t)s.L + V - 1 + M - 1) / M, real = whole ? ((int64_t)s.L + M - 1) / M : runs;
+    // lanes of a worker and pieces of a row of `n` runs: as few lanes idle as may be, then the most lanes
+    auto cut = [&](int64_t n, int64_t *segs) {
+        int best = 1;
+        int64_t least = 0;
+        for (int TX = 32; TX >= 1; TX /= 2) {
+            const int64_t each = back && n > TX ? TX - 1 : TX;
+            if (each < 1 || (n > TX && TX < 8)) continue;
+            const int64_t pieces = (n + each - 1) / each;
+            if (least == 0 || pieces * TX < least) { least = pieces * TX; best = TX; *segs = pieces; }
+        }
+        return best;
+    };
+    int64_t segs = 1, usual = 1;
     CausalShape p{};
-    p.TX = 1;
-    while (p.TX < 32 && p.TX < real) p.TX *= 2;
-    const int64_t each = back && real > 32 ? 31 : p.TX;
-    p.segs = (int)((real + each - 1) / each);
-    // workers that share a channel: warps for the whole GPU about twice over; the workspace's size, which does not
-    // know the alignment, goes by the longer rows
-    int TX = 1;
-    while (TX < 32 && TX < runs) TX *= 2;
-    const int64_t most = (int64_t)s.N * ((runs + 30) / (TX < 32 ? runs + 30 : 31)), want = (int64_t)num_sms() * 64 * (32 / TX);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, (want + s.C - 1) / s.C));
+    p.TX = cut(((int64_t)s.L + (whole ? 0 : V - 1) + M - 1) / M, &segs);
+    p.segs = (int)segs;
+    // workers that share a channel: warps for the whole GPU; the workspace's size does not know the alignment, so they go by
+    // rows that begin anywhere
+    const int lanes = cut(((int64_t)s.L + V - 1 + M - 1) / M, &usual);
+    const int64_t want = (int64_t)num_sms() * 64 * (32 / lanes);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)s.N * usual, (want + s.C - 1) / s.C));
     p.grid = ((int64_t)s.C * p.splits + kCausalThreads / p.TX - 1) / (kCausalThreads / p.TX);
     return p;
 }
@@ -448,7 +510,7 @@ void causal_start(int K_, int kind, bool vec, const CausalArgs &a, int64_t grid,
 
 size_t causal_ws(const gconv_causal &s, gconv_dtype dt)
 {
-    return s.N ? (size_t)causal_shape(s, dt, true, true).splits * s.C * (s.taps + 1) * sizeof(float) : 0;
+    return s.N ? (size_t)causal_shape(s, dt, true, false).splits * s.C * (s.taps + 1) * sizeof(float) : 0;
 }
 
 gconv_status done() { return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA; }

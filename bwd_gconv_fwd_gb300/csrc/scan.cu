@@ -14,50 +14,83 @@ constexpr int kTokenMost = 8;     // positions of the short form
 // ---- short sequences ----------------------------------------------------------------
 //
 // What a single new position has to move is its state, 8 bytes a state and channel.  Four lanes share a channel, four
-// neighbouring states each, so that a warp's reads are whole lines; sums over states are two shuffles.
-template <typename T, int LT>
-__global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs a)
+// neighbouring states each (one 16-byte access where FOUR: states in fours, on 16 bytes), so that a warp's accesses are
+// whole lines; sums over states are two shuffles.
+template <typename T, int LT, bool FOUR>
+__global__ void __launch_bounds__(128) scan_token_kernel(const __grid_constant__ ScanArgs a)
 {
-    int64_t id = blockIdx.x;
-    const int cb = (int)(id % a.ncb); id /= a.ncb;
-    const int g = (int)(id % a.G), n = (int)(id / a.G);
-    const int q = threadIdx.x & 3, ch = cb * 32 + (threadIdx.x >> 2);
+    const unsigned ng = blockIdx.x / (unsigned)a.ncb, cb = blockIdx.x - ng * a.ncb;
+    const int n = (int)(ng / (unsigned)a.G), g = (int)(ng - (unsigned)n * a.G);
+    const int q = threadIdx.x & 3, ch = (int)cb * 32 + (threadIdx.x >> 2);
     const bool there = ch < a.Cg;
-    const int c = g * a.Cg + (there ? ch : 0);
+    const int c = g * a.Cg + (there ? ch : 0), S = a.S;
     ptx::griddep_wait();
     const int end = sequence_end(a, n);
     const T *u = static_cast<const T *>(a.u) + n * a.su + (int64_t)c * a.L;
     const T *dl = static_cast<const T *>(a.delta) + n * a.sdelta + (int64_t)c * a.L;
-    const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * a.S * a.L;
-    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * a.S * a.L;
+    const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * S * a.L;
+    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * S * a.L;
+    const int64_t at = ((int64_t)n * a.C + c) * S;
+    const float *rates = a.A + (int64_t)c * S;
+    // a thread's four states from s0 + 4 q, and their rates: the first four are asked for before anything is waited for
+    Pack<float, 4> h, rate;
+    auto load = [&](int s0) {
+        const int s = s0 + 4 * q;
+        if constexpr (FOUR) {
+            const bool on = s < S;
+            const Pack<float, 4> none{};
+            rate = on ? *reinterpret_cast<const Pack<float, 4> *>(rates + s) : none;
+            h = on && a.state ? *reinterpret_cast<const Pack<float, 4> *>(a.state + at + s) : none;
+        } else {
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                rate.v[j] = s + j < S ? rates[s + j] : 0.f;
+                h.v[j] = s + j < S && a.state ? a.state[at + s + j] : 0.f;
+            }
+        }
+    };
+    load(0);
     const float bias = a.bias ? a.bias[c] : 0.f, skip = a.D ? a.D[c] : 0.f;
-    float d[LT], du[LT], out[LT];
+    float d[LT], du[LT], out[LT], z[LT];
     #pragma unroll
     for (int t = 0; t < LT; ++t) {
-        const bool on = t < end;
-        float v = on ? to_f(dl[t]) + bias : 0.f;
-        if (a.softplus) v = scan_softplus(v);
-        const float x = on ? to_f(u[t]) : 0.f;
-        d[t] = on ? v : 0.f;
-        du[t] = d[t] * x;
-        out[t] = q == 0 ? skip * x : 0.f;
+        d[t] = t < end ? to_f(dl[t]) : 0.f;
+        du[t] = t < end ? to_f(u[t]) : 0.f;
+        z[t] = a.z && t < end ? to_f(static_cast<const T *>(a.z)[n * a.sz + (int64_t)c * a.L + t]) : 0.f;
     }
-    const int64_t at = ((int64_t)n * a.C + c) * a.S;
-    for (int s0 = 0; s0 < a.S; s0 += 16) {
+    #pragma unroll
+    for (int t = 0; t < LT; ++t) {
+        float v = d[t] + bias;
+        if (a.softplus) v = scan_softplus(v);
+        d[t] = t < end ? v : 0.f;
+        out[t] = q == 0 ? skip * du[t] : 0.f;
+        du[t] *= d[t];
+    }
+    for (int s0 = 0; s0 < S; s0 += 16) {
+        const int s = s0 + 4 * q;
+        if (s0) load(s0);
+        Pack<float, 4> now = h;
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int s = s0 + q * 4 + j;
-            if (s >= a.S || !there) continue;
-            const float rate = decay_rate(a.A[(int64_t)c * a.S + s]);
-            float h = a.state ? a.state[at + s] : 0.f;
-            if (a.mark) a.mark[((int64_t)n * a.S + s) * a.C + c] = h;
+            if (s + j >= S) continue;
+            const float r = decay_rate(rate.v[j]);
+            float v = h.v[j];
+            if (a.mark && there) a.mark[((int64_t)n * S + s + j) * a.C + c] = v;
             #pragma unroll
             for (int t = 0; t < LT; ++t) {
                 if (t >= end) continue;
-                h = fmaf(ex2(d[t] * rate), h, du[t] * to_f(B[(int64_t)s * a.L + t]));
-                out[t] = fmaf(to_f(Cm[(int64_t)s * a.L + t]), h, out[t]);
+                v = fmaf(ex2(d[t] * r), v, du[t] * to_f(B[(int64_t)(s + j) * a.L + t]));
+                out[t] = fmaf(to_f(Cm[(int64_t)(s + j) * a.L + t]), v, out[t]);
             }
-            if (a.state_out) a.state_out[at + s] = h;
+            now.v[j] = v;
+        }
+        if (!a.state_out || !there) continue;
+        if constexpr (FOUR) {
+            if (s < S) *reinterpret_cast<Pack<float, 4> *>(a.state_out + at + s) = now;
+        } else {
+            #pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (s + j < S) a.state_out[at + s + j] = now.v[j];
         }
     }
     #pragma unroll
@@ -67,10 +100,9 @@ __global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs a)
         if ((t & 3) != q || t >= a.L || !there) continue;
         const int64_t row = (int64_t)c * a.L + t;
         float v = out[t];
-        if (a.z && t < end) {
-            if (a.pre) static_cast<T *>(a.pre)[(int64_t)n * a.C * a.L + row] = from_f<T>(v);
-            const float z = to_f(static_cast<const T *>(a.z)[n * a.sz + row]);
-            v *= z * scan_sigmoid(z);
+        if (a.z) {
+            if (a.pre && t < end) static_cast<T *>(a.pre)[(int64_t)n * a.C * a.L + row] = from_f<T>(v);
+            v *= z[t] * scan_sigmoid(z[t]);
         }
         static_cast<T *>(a.y)[n * a.sy + row] = from_f<T>(t < end ? v : 0.f);
     }
@@ -357,8 +389,14 @@ gconv_status gconv_scan_fwd(const gconv_scan *scan, gconv_dtype dtype, const voi
     a.mark = static_cast<float *>(saved);
     a.pre = saved && z ? static_cast<char *>(saved) + saved_marks(*scan) : nullptr;
     if (p.token) {
-        auto *kernel = dtype == GCONV_BF16 ? (scan->L == 1 ? scan_token_kernel<__nv_bfloat16, 1> : scan_token_kernel<__nv_bfloat16, kTokenMost>)
-                                           : (scan->L == 1 ? scan_token_kernel<float, 1> : scan_token_kernel<float, kTokenMost>);
+        const bool four = scan->states % 4 == 0 && on(A, 16) && on(state, 16) && on(state_out, 16);
+        auto pick = [&](auto one, auto few) { return scan->L == 1 ? one : few; };
+        using H = __nv_bfloat16;
+        auto *kernel = dtype == GCONV_BF16
+            ? (four ? pick(scan_token_kernel<H, 1, true>, scan_token_kernel<H, kTokenMost, true>)
+                    : pick(scan_token_kernel<H, 1, false>, scan_token_kernel<H, kTokenMost, false>))
+            : (four ? pick(scan_token_kernel<float, 1, true>, scan_token_kernel<float, kTokenMost, true>)
+                    : pick(scan_token_kernel<float, 1, false>, scan_token_kernel<float, kTokenMost, false>));
         launch_dependent(kernel, p.shape.grid, 128u, 0, st, a);
         return done();
     }

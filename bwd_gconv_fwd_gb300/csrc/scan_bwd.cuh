@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
                     const bool fresh = !(set | round);
                     const float *rowB = sB + begin * ROW + run, *rowC = sC + begin * ROW + run;
                     float *toB = accB + (begin * CL + cl) * ROW + run, *toC = accC + (begin * CL + cl) * ROW + run;
-                    #pragma unroll 1
+                    // two states side by side: a scan's shuffles wait less ([8,2048,2048] 986 -> 939 us)
+                    #pragma unroll 2
                     for (int s = begin; s < stop; ++s, rowB += ROW, rowC += ROW, toB += CL * ROW, toC += CL * ROW) {
                         float Bv[K], Cv[K], aB[K], aC[K];
                         float2 e[K], q[K], h = both(0.f), w = both(0.f);
