@@ -788,14 +788,14 @@ def _positions(shape):
     return count
 
 
-def _sequences(t, shape, dtype, name):
+def _sequences(t, shape, dtype, device, name):
     """(address, elements between sequences or 0 for dense) of an activation tensor; (0, 0) for None."""
     if t is None:
         return 0, 0
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} and dtype {dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, on the device of the others")
     if t.is_contiguous():
         return t.data_ptr(), 0
     if t.stride(0) <= 0 or not t[0].is_contiguous():
@@ -803,8 +803,29 @@ def _sequences(t, shape, dtype, name):
     return t.data_ptr(), t.stride(0)
 
 
-def _lengths(lengths, n):
-    return 0 if lengths is None else _like(lengths, torch.Size((n,)), torch.int32, "lengths")
+def _array(t, shape, dtype, device, name):
+    """Address of a contiguous tensor of this shape and dtype on the device (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} and dtype {dtype}")
+    if t.get_device() != device or device < 0 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor, on the device of the others")
+    return t.data_ptr()
+
+
+def _lengths(lengths, n, device):
+    return 0 if lengths is None else _array(lengths, torch.Size((n,)), torch.int32, device, "lengths")
+
+
+def _stream_on(stream, device):
+    """The stream's handle; the tensors have to be on the current device, which the kernels run on."""
+    now = torch._C._cuda_getDevice()
+    if now != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{now}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(now)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=1024)
@@ -831,12 +852,12 @@ def gconv_causal_fwd(x, w, bias, y, *, act="none", state=None, state_out=None, l
     """y[t] <- act(bias + sum_k w[k] x[t - K + 1 + k]) for every channel; w: fp32 [C, K], bias: fp32 [C] or
     None, act: "none" or "silu".  state [N, C, K-1] holds the positions before the first (None: zeros), state_out, which
     may be state, gets the last ones.  lengths: int32 [N] or None; results behind a sequence's length are zero."""
-    s, d, ws, f = x.shape, x.dtype, w.shape, torch.float32
+    s, d, ws, f, dev = x.shape, x.dtype, w.shape, torch.float32, x.get_device()
     dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
-    (xp, xs), (yp, ys) = _sequences(x, s, d, "x"), _sequences(y, s, d, "y")
-    _, ref, _, c, held = _causal_record(s, ws, act, (xs, ys, 0, 0), dt, x.get_device())
-    st = lib().gconv_causal_fwd(ref, dt, xp, _like(w, ws, f, "w"), _like(bias, c, f, "bias"), _like(state, held, d, "state"),
-                                _lengths(lengths, s[0]), yp, _like(state_out, held, d, "state_out"), _raw_stream(stream))
+    (xp, xs), (yp, ys) = _sequences(x, s, d, dev, "x"), _sequences(y, s, d, dev, "y")
+    _, ref, _, c, held = _causal_record(s, ws, act, (xs, ys, 0, 0), dt, dev)
+    st = lib().gconv_causal_fwd(ref, dt, xp, _array(w, ws, f, dev, "w"), _array(bias, c, f, dev, "bias"), _array(state, held, d, dev, "state"),
+                                _lengths(lengths, s[0], dev), yp, _array(state_out, held, d, dev, "state_out"), _stream_on(stream, dev))
     if st:
         _check(st, "gconv_causal_fwd")
     return y
@@ -846,14 +867,14 @@ def gconv_causal_bwd(x, w, bias, dy, dx, dw, dbias=None, *, act="none", state=No
                      workspace=None, stream=None):
     """Gradients of gconv_causal_fwd: dx like x, dw and dbias fp32; dstate gets the gradient of state, dstate_out is that of
     state_out (None: none)."""
-    s, d, ws, f = x.shape, x.dtype, w.shape, torch.float32
+    s, d, ws, f, dev = x.shape, x.dtype, w.shape, torch.float32, x.get_device()
     dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
-    (xp, xs), (yp, ys), (dp, ds) = _sequences(x, s, d, "x"), _sequences(dy, s, d, "dy"), _sequences(dx, s, d, "dx")
-    _, ref, need, c, held = _causal_record(s, ws, act, (xs, 0, ys, ds), dt, x.get_device())
+    (xp, xs), (yp, ys), (dp, ds) = _sequences(x, s, d, dev, "x"), _sequences(dy, s, d, dev, "dy"), _sequences(dx, s, d, dev, "dx")
+    _, ref, need, c, held = _causal_record(s, ws, act, (xs, 0, ys, ds), dt, dev)
     hold, sp, sb = _orth_workspace(need, workspace, x.device, stream)
-    st = lib().gconv_causal_bwd(ref, dt, xp, _like(w, ws, f, "w"), _like(bias, c, f, "bias"), _like(state, held, d, "state"),
-                                _lengths(lengths, s[0]), yp, _like(dstate_out, held, d, "dstate_out"), dp, _like(dw, ws, f, "dw"),
-                                _like(dbias, c, f, "dbias"), _like(dstate, held, d, "dstate"), sp, sb, _raw_stream(stream))
+    st = lib().gconv_causal_bwd(ref, dt, xp, _array(w, ws, f, dev, "w"), _array(bias, c, f, dev, "bias"), _array(state, held, d, dev, "state"),
+                                _lengths(lengths, s[0], dev), yp, _array(dstate_out, held, d, dev, "dstate_out"), dp, _array(dw, ws, f, dev, "dw"),
+                                _array(dbias, c, f, dev, "dbias"), _array(dstate, held, d, dev, "dstate"), sp, sb, _stream_on(stream, dev))
     if st:
         _check(st, "gconv_causal_bwd")
     return dx, dw, dbias
@@ -891,8 +912,8 @@ def gconv_scan_workspace_size(x_shape, states: int, dtype: int, groups: int = 1,
     return _scan_record(s, B, int(states), int(groups), 0, (0,) * 12, int(dtype), _device_index())[3 if backward else 2]
 
 
-def _scan_saved(saved, need):
-    if not (saved.is_cuda and saved.is_contiguous()) or saved.numel() * saved.element_size() < need:
+def _scan_saved(saved, need, dev):
+    if saved.get_device() != dev or not saved.is_contiguous() or saved.numel() * saved.element_size() < need:
         raise ValueError(f"saved is a contiguous CUDA tensor of at least {need} bytes (gconv_scan_saved_size)")
     return saved.data_ptr()
 
@@ -903,21 +924,21 @@ def gconv_scan_fwd(u, delta, A, B, C, y, *, D=None, z=None, delta_bias=None, sof
     y <- (sum over the states of C[t] h[t] + D u) silu(z).  A: fp32 [C, states]; B, C: [N, groups * states, positions];
     D, delta_bias: fp32 [C]; state, state_out (which may be state): fp32 [N, C, states]; lengths: int32 [N].
     saved (gconv_scan_saved_size bytes) keeps what gconv_scan_bwd needs."""
-    s, d, bs, f = u.shape, u.dtype, B.shape, torch.float32
+    s, d, bs, f, dev = u.shape, u.dtype, B.shape, torch.float32, u.get_device()
     dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
-    up, us = _sequences(u, s, d, "u")
-    dp, ds = _sequences(delta, s, d, "delta")
-    zp, zs = _sequences(z, s, d, "z")
-    yp, ys = _sequences(y, s, d, "y")
-    Bp, Bs = _sequences(B, bs, d, "B")
-    Cp, Cs = _sequences(C, bs, d, "C")
+    up, us = _sequences(u, s, d, dev, "u")
+    dp, ds = _sequences(delta, s, d, dev, "delta")
+    zp, zs = _sequences(z, s, d, dev, "z")
+    yp, ys = _sequences(y, s, d, dev, "y")
+    Bp, Bs = _sequences(B, bs, d, dev, "B")
+    Cp, Cs = _sequences(C, bs, d, dev, "C")
     _, ref, need, _, plain, gated, c, cs, full = _scan_record(s, bs, A.shape[-1], int(groups), 1 if softplus else 0,
-                                                              (us, ds, zs, Bs, Cs, ys, 0, 0, 0, 0, 0, 0), dt, u.get_device())
+                                                              (us, ds, zs, Bs, Cs, ys, 0, 0, 0, 0, 0, 0), dt, dev)
     hold, wp, wb = _orth_workspace(need, workspace, u.device, stream)
-    st = lib().gconv_scan_fwd(ref, dt, up, dp, _like(A, cs, f, "A"), Bp, Cp, _like(D, c, f, "D"), zp,
-                              _like(delta_bias, c, f, "delta_bias"), _like(state, full, f, "state"), _lengths(lengths, s[0]), yp,
-                              _like(state_out, full, f, "state_out"),
-                              0 if saved is None else _scan_saved(saved, plain if z is None else gated), wp, wb, _raw_stream(stream))
+    st = lib().gconv_scan_fwd(ref, dt, up, dp, _array(A, cs, f, dev, "A"), Bp, Cp, _array(D, c, f, dev, "D"), zp,
+                              _array(delta_bias, c, f, dev, "delta_bias"), _array(state, full, f, dev, "state"), _lengths(lengths, s[0], dev), yp,
+                              _array(state_out, full, f, dev, "state_out"),
+                              0 if saved is None else _scan_saved(saved, plain if z is None else gated, dev), wp, wb, _stream_on(stream, dev))
     if st:
         _check(st, "gconv_scan_fwd")
     return y
@@ -928,21 +949,21 @@ def gconv_scan_bwd(u, delta, A, B, C, dy, saved, du, ddelta, dA, dB, dC, *, D=No
                    stream=None):
     """Gradients of gconv_scan_fwd from its inputs and what it saved.  du, ddelta, dz like u, dB and dC like B; dA, dD,
     ddelta_bias fp32; dstate (fp32) gets the gradient of state, dstate_out is that of state_out (None: none)."""
-    s, d, bs, f = u.shape, u.dtype, B.shape, torch.float32
+    s, d, bs, f, dev = u.shape, u.dtype, B.shape, torch.float32, u.get_device()
     dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
-    t = [_sequences(v, shape, d, name) for name, v, shape in
+    t = [_sequences(v, shape, d, dev, name) for name, v, shape in
          (("u", u, s), ("delta", delta, s), ("z", z, s), ("B", B, bs), ("C", C, bs), ("dy", dy, s), ("du", du, s),
           ("ddelta", ddelta, s), ("dz", dz, s), ("dB", dB, bs), ("dC", dC, bs))]
     (up, us), (dp, ds), (zp, zs), (Bp, Bs), (Cp, Cs), (gp, gs), (dup, dus), (ddp, dds), (dzp, dzs), (dBp, dBs), (dCp, dCs) = t
     _, ref, _, need, plain, gated, c, cs, full = _scan_record(s, bs, A.shape[-1], int(groups), 1 if softplus else 0,
                                                               (us, ds, zs, Bs, Cs, 0, gs, dus, dds, dzs, dBs, dCs), dt,
-                                                              u.get_device())
+                                                              dev)
     hold, wp, wb = _orth_workspace(need, workspace, u.device, stream)
-    st = lib().gconv_scan_bwd(ref, dt, up, dp, _like(A, cs, f, "A"), Bp, Cp, _like(D, c, f, "D"), zp,
-                              _like(delta_bias, c, f, "delta_bias"), _lengths(lengths, s[0]),
-                              _scan_saved(saved, plain if z is None else gated), gp, _like(dstate_out, full, f, "dstate_out"), dup,
-                              ddp, _like(dA, cs, f, "dA"), dBp, dCp, _like(dD, c, f, "dD"), dzp,
-                              _like(ddelta_bias, c, f, "ddelta_bias"), _like(dstate, full, f, "dstate"), wp, wb, _raw_stream(stream))
+    st = lib().gconv_scan_bwd(ref, dt, up, dp, _array(A, cs, f, dev, "A"), Bp, Cp, _array(D, c, f, dev, "D"), zp,
+                              _array(delta_bias, c, f, dev, "delta_bias"), _lengths(lengths, s[0], dev),
+                              _scan_saved(saved, plain if z is None else gated, dev), gp, _array(dstate_out, full, f, dev, "dstate_out"), dup,
+                              ddp, _array(dA, cs, f, dev, "dA"), dBp, dCp, _array(dD, c, f, dev, "dD"), dzp,
+                              _array(ddelta_bias, c, f, dev, "ddelta_bias"), _array(dstate, full, f, dev, "dstate"), wp, wb, _stream_on(stream, dev))
     if st:
         _check(st, "gconv_scan_bwd")
     return du, ddelta
@@ -950,16 +971,16 @@ def gconv_scan_bwd(u, delta, A, B, C, dy, saved, du, ddelta, dA, dB, dC, *, D=No
 
 # ---- dropout -----------------------------------------------------------------------
 
-def _rng(rng):
-    return _like(rng, torch.Size((2,)), torch.int64, "rng")
+def _rng(rng, dev):
+    return _array(rng, torch.Size((2,)), torch.int64, dev, "rng")
 
 
 def gconv_dropout_fwd(x, y, rng, p, *, res=None, stream=None):
     """y <- x / (1 - p) where kept, else 0, plus res.  rng: int64 CUDA tensor (seed, step), which the mask follows from;
     use another pair for every tensor and step, and the same for the gradient.  y may be x or res."""
-    s, d = x.shape, x.dtype
-    st = lib().gconv_dropout_fwd(x.numel(), dtype_code(d), _like(x, s, d, "x"), _like(res, s, d, "res"), _rng(rng), p,
-                                 _like(y, s, d, "y"), _raw_stream(stream))
+    s, d, dev = x.shape, x.dtype, x.get_device()
+    st = lib().gconv_dropout_fwd(x.numel(), dtype_code(d), _array(x, s, d, dev, "x"), _array(res, s, d, dev, "res"), _rng(rng, dev), p,
+                                 _array(y, s, d, dev, "y"), _stream_on(stream, dev))
     if st:
         _check(st, "gconv_dropout_fwd")
     return y
@@ -967,9 +988,9 @@ def gconv_dropout_fwd(x, y, rng, p, *, res=None, stream=None):
 
 def gconv_dropout_bwd(dy, dx, rng, p, *, stream=None):
     """dx <- dy / (1 - p) where the forward call with this rng kept the element, else 0 (the gradient of res is dy)."""
-    s, d = dy.shape, dy.dtype
-    st = lib().gconv_dropout_bwd(dy.numel(), dtype_code(d), _like(dy, s, d, "dy"), _rng(rng), p, _like(dx, s, d, "dx"),
-                                 _raw_stream(stream))
+    s, d, dev = dy.shape, dy.dtype, dy.get_device()
+    st = lib().gconv_dropout_bwd(dy.numel(), dtype_code(d), _array(dy, s, d, dev, "dy"), _rng(rng, dev), p, _array(dx, s, d, dev, "dx"),
+                                 _stream_on(stream, dev))
     if st:
         _check(st, "gconv_dropout_bwd")
     return dx

@@ -67,6 +67,23 @@ __device__ __forceinline__ void philox(const uint64_t (&block)[B], uint32_t s0, 
     }
 }
 
+// Elements e .. e + 3, one by one.
+template <typename T>
+__device__ __forceinline__ void drop_four(const DropArgs &a, int64_t e, uint32_t s0, uint32_t s1, uint32_t k0, uint32_t k1)
+{
+    const uint64_t block[1] = {(uint64_t)e / 4};
+    uint32_t w[1][4];
+    philox<1>(block, s0, s1, k0, k1, w);
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (e + j >= a.count) continue;
+        const bool keep = w[0][j] >= a.bound && !a.none;
+        const float z = keep ? to_f(static_cast<const T *>(a.x)[e + j]) : 0.f;
+        const float f = a.res ? fmaf(z, a.scale, to_f(static_cast<const T *>(a.res)[e + j])) : z * a.scale;
+        static_cast<T *>(a.y)[e + j] = rounded<T>(f);
+    }
+}
+
 // A tile is two runs of 16 bytes a thread, a block's width apart.  Blocks stay for all their tiles and ask for the next one's
 // elements before they make this one's numbers: the products of ten rounds take 30 us for 51 million elements, about as long as
 // their bytes, and without that (a block a tile) the two times add up: 61 us for the 52 measured, 68 for 64 with res.
@@ -123,26 +140,22 @@ __global__ void __launch_bounds__(kDropThreads, kDropBlocks) dropout_kernel(cons
         y += ahead;
         e += ahead;
     }
+    // what is behind the last whole tile
+    for (e = tiles * TILE + ((int64_t)blockIdx.x * kDropThreads + threadIdx.x) * 4; e < a.count; e += (int64_t)gridDim.x * kDropThreads * 4)
+        drop_four<T>(a, e, s0, s1, k0, k1);
 }
 
-// Four elements a thread from `from` on, one by one: what is behind the last whole tile, and tensors off 16 bytes.
+// Tensors off 16 bytes, and small ones: four elements a thread.
 template <typename T>
-__global__ void __launch_bounds__(kDropThreads) dropout_rest_kernel(const __grid_constant__ DropArgs a, int64_t from)
+__global__ void __launch_bounds__(kDropThreads) dropout_few_kernel(const __grid_constant__ DropArgs a)
 {
-    const int64_t e = from + ((int64_t)blockIdx.x * kDropThreads + threadIdx.x) * 4;
+    const int64_t e = ((int64_t)blockIdx.x * kDropThreads + threadIdx.x) * 4;
+    if (e >= a.count) return;
     ptx::griddep_wait();
-    const uint64_t seed = a.rng[0], step = a.rng[1], block[1] = {(uint64_t)e / 4};
-    uint32_t w[1][4];
-    philox<1>(block, (uint32_t)step, (uint32_t)(step >> 32), (uint32_t)seed, (uint32_t)(seed >> 32), w);
-    #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (e + j >= a.count) continue;
-        const bool keep = w[0][j] >= a.bound && !a.none;
-        const float z = keep ? to_f(static_cast<const T *>(a.x)[e + j]) : 0.f;
-        const float f = a.res ? fmaf(z, a.scale, to_f(static_cast<const T *>(a.res)[e + j])) : z * a.scale;
-        static_cast<T *>(a.y)[e + j] = rounded<T>(f);
-    }
+    const uint64_t seed = a.rng[0], step = a.rng[1];
+    drop_four<T>(a, e, (uint32_t)step, (uint32_t)(step >> 32), (uint32_t)seed, (uint32_t)(seed >> 32));
 }
+
 
 bool on(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -162,19 +175,17 @@ gconv_status dropout(long long count, gconv_dtype dtype, const void *x, const vo
         a.scale = (float)(4294967296.0 / (4294967296.0 - a.bound));
     }
     const bool vec = on(x, 16) && on(y, 16) && on(res, 16);
-    const int64_t tile = 2 * kDropThreads * (int64_t)(16 / es), tiles = vec ? count / tile : 0;
-    // fewer tiles than SMs take longer in a second launch for the rest than the rest alone
-    const int64_t whole = tiles >= num_sms() / 4 ? tiles * tile : 0, rest = (count - whole + 4 * kDropThreads - 1) / (4 * kDropThreads);
-    if (rest > INT_MAX) return GCONV_ERR_INVALID_ARG;
+    const int64_t tile = 2 * kDropThreads * (int64_t)(16 / es), tiles = count / tile;
+    const int64_t few = (count + 4 * kDropThreads - 1) / (4 * kDropThreads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (whole) {
+    if (vec && tiles >= num_sms()) {
         auto *kernel = dtype == GCONV_BF16 ? (res ? dropout_kernel<__nv_bfloat16, true> : dropout_kernel<__nv_bfloat16, false>)
                                            : (res ? dropout_kernel<float, true> : dropout_kernel<float, false>);
         launch_dependent(kernel, (unsigned)std::min<int64_t>(tiles, (int64_t)num_sms() * kDropBlocks), (unsigned)kDropThreads, 0, st, a);
-    }
-    if (rest) {
-        auto *kernel = dtype == GCONV_BF16 ? dropout_rest_kernel<__nv_bfloat16> : dropout_rest_kernel<float>;
-        launch_dependent(kernel, (unsigned)rest, (unsigned)kDropThreads, 0, st, a, whole);
+    } else {
+        if (few > INT_MAX) return GCONV_ERR_INVALID_ARG;
+        launch_dependent(dtype == GCONV_BF16 ? dropout_few_kernel<__nv_bfloat16> : dropout_few_kernel<float>, (unsigned)few,
+                         (unsigned)kDropThreads, 0, st, a);
     }
     return cudaGetLastError() == cudaSuccess ? GCONV_OK : GCONV_ERR_CUDA;
 }

@@ -9,102 +9,146 @@ namespace gconv {
 
 namespace {
 
-constexpr int kTokenMost = 8;     // positions of the short form
+constexpr int kTokenMost = 8, kTokenMany = 2;     // positions of the short form; sequences a thread of it
 
 // ---- short sequences ----------------------------------------------------------------
 //
 // What a single new position has to move is its state, 8 bytes a state and channel.  Four lanes share a channel, four
 // neighbouring states each (one 16-byte access where FOUR: states in fours, on 16 bytes), so that a warp's accesses are
-// whole lines; sums over states are two shuffles.
-template <typename T, int LT, bool FOUR>
-__global__ void __launch_bounds__(128) scan_token_kernel(const __grid_constant__ ScanArgs a)
+// whole lines; sums over states are two shuffles.  NB: sequences a thread takes, all of whose states are on their way
+// before the first is used; the channel's rates are read once for them.
+template <typename T, int LT, int NB, bool FOUR>
+__global__ void __launch_bounds__(128, LT > 1 ? 4 : NB > 1 ? 8 : 10) scan_token_kernel(const __grid_constant__ ScanArgs a)
 {
     const unsigned ng = blockIdx.x / (unsigned)a.ncb, cb = blockIdx.x - ng * a.ncb;
-    const int n = (int)(ng / (unsigned)a.G), g = (int)(ng - (unsigned)n * a.G);
+    const int n0 = (int)(ng / (unsigned)a.G) * NB, g = (int)(ng % (unsigned)a.G);
     const int q = threadIdx.x & 3, ch = (int)cb * 32 + (threadIdx.x >> 2);
     const bool there = ch < a.Cg;
     const int c = g * a.Cg + (there ? ch : 0), S = a.S;
     ptx::griddep_wait();
-    const int end = sequence_end(a, n);
-    const T *u = static_cast<const T *>(a.u) + n * a.su + (int64_t)c * a.L;
-    const T *dl = static_cast<const T *>(a.delta) + n * a.sdelta + (int64_t)c * a.L;
-    const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * S * a.L;
-    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * S * a.L;
-    const int64_t at = ((int64_t)n * a.C + c) * S;
+    // the last block's missing sequences stand for the first one of it, and are not written
+    int n[NB], end[NB];
+    #pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        n[i] = n0 + i < a.N ? n0 + i : n0;
+        end[i] = sequence_end(a, n[i]);
+    }
     const float *rates = a.A + (int64_t)c * S;
-    // a thread's four states from s0 + 4 q, and their rates: the first four are asked for before anything is waited for
-    Pack<float, 4> h, rate;
+    Pack<float, 4> h[NB], rate;
+    Pack<T, 4> Bv[NB], Cv[NB];          // of the one position (LT 1)
     auto load = [&](int s0) {
         const int s = s0 + 4 * q;
+        const Pack<float, 4> none{};
         if constexpr (FOUR) {
-            const bool on = s < S;
-            const Pack<float, 4> none{};
-            rate = on ? *reinterpret_cast<const Pack<float, 4> *>(rates + s) : none;
-            h = on && a.state ? *reinterpret_cast<const Pack<float, 4> *>(a.state + at + s) : none;
+            rate = s < S ? *reinterpret_cast<const Pack<float, 4> *>(rates + s) : none;
+            #pragma unroll
+            for (int i = 0; i < NB; ++i)
+                h[i] = s < S && a.state ? *reinterpret_cast<const Pack<float, 4> *>(a.state + ((int64_t)n[i] * a.C + c) * S + s) : none;
         } else {
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 rate.v[j] = s + j < S ? rates[s + j] : 0.f;
-                h.v[j] = s + j < S && a.state ? a.state[at + s + j] : 0.f;
+                #pragma unroll
+                for (int i = 0; i < NB; ++i) h[i].v[j] = s + j < S && a.state ? a.state[((int64_t)n[i] * a.C + c) * S + s + j] : 0.f;
+            }
+        }
+        if constexpr (LT == 1) {
+            #pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const T *B = static_cast<const T *>(a.B) + n[i] * a.sB + g * S + s;
+                const T *Cm = static_cast<const T *>(a.Cm) + n[i] * a.sC + g * S + s;
+                Bv[i] = Cv[i] = Pack<T, 4>{};
+                if constexpr (FOUR) {
+                    if (s < S) {
+                        Bv[i] = *reinterpret_cast<const Pack<T, 4> *>(B);
+                        Cv[i] = *reinterpret_cast<const Pack<T, 4> *>(Cm);
+                    }
+                } else {
+                    #pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (s + j < S) {
+                            Bv[i].v[j] = B[j];
+                            Cv[i].v[j] = Cm[j];
+                        }
+                }
             }
         }
     };
     load(0);
     const float bias = a.bias ? a.bias[c] : 0.f, skip = a.D ? a.D[c] : 0.f;
-    float d[LT], du[LT], out[LT], z[LT];
+    float d[NB][LT], du[NB][LT], out[NB][LT], z[NB][LT];
     #pragma unroll
-    for (int t = 0; t < LT; ++t) {
-        d[t] = t < end ? to_f(dl[t]) : 0.f;
-        du[t] = t < end ? to_f(u[t]) : 0.f;
-        z[t] = a.z && t < end ? to_f(static_cast<const T *>(a.z)[n * a.sz + (int64_t)c * a.L + t]) : 0.f;
+    for (int i = 0; i < NB; ++i) {
+        const T *dl = static_cast<const T *>(a.delta) + n[i] * a.sdelta + (int64_t)c * a.L;
+        const T *u = static_cast<const T *>(a.u) + n[i] * a.su + (int64_t)c * a.L;
+        const T *zr = static_cast<const T *>(a.z) + n[i] * a.sz + (int64_t)c * a.L;
+        #pragma unroll
+        for (int t = 0; t < LT; ++t) {
+            d[i][t] = t < end[i] ? to_f(dl[t]) : 0.f;
+            du[i][t] = t < end[i] ? to_f(u[t]) : 0.f;
+            z[i][t] = a.z && t < end[i] ? to_f(zr[t]) : 0.f;
+        }
     }
     #pragma unroll
-    for (int t = 0; t < LT; ++t) {
-        float v = d[t] + bias;
-        if (a.softplus) v = scan_softplus(v);
-        d[t] = t < end ? v : 0.f;
-        out[t] = q == 0 ? skip * du[t] : 0.f;
-        du[t] *= d[t];
+    for (int i = 0; i < NB; ++i) {
+        #pragma unroll
+        for (int t = 0; t < LT; ++t) {
+            float v = d[i][t] + bias;
+            if (a.softplus) v = scan_softplus(v);
+            d[i][t] = t < end[i] ? v : 0.f;
+            out[i][t] = q == 0 ? skip * du[i][t] : 0.f;
+            du[i][t] *= d[i][t];
+        }
     }
     for (int s0 = 0; s0 < S; s0 += 16) {
         const int s = s0 + 4 * q;
         if (s0) load(s0);
-        Pack<float, 4> now = h;
         #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (s + j >= S) continue;
-            const float r = decay_rate(rate.v[j]);
-            float v = h.v[j];
-            if (a.mark && there) a.mark[((int64_t)n * S + s + j) * a.C + c] = v;
+        for (int i = 0; i < NB; ++i) {
+            const bool real = there && n0 + i < a.N;
+            const T *B = static_cast<const T *>(a.B) + n[i] * a.sB + ((int64_t)g * S + s) * a.L;
+            const T *Cm = static_cast<const T *>(a.Cm) + n[i] * a.sC + ((int64_t)g * S + s) * a.L;
+            const int64_t at = ((int64_t)n[i] * a.C + c) * S + s;
+            Pack<float, 4> now = h[i];
             #pragma unroll
-            for (int t = 0; t < LT; ++t) {
-                if (t >= end) continue;
-                v = fmaf(ex2(d[t] * r), v, du[t] * to_f(B[(int64_t)(s + j) * a.L + t]));
-                out[t] = fmaf(to_f(Cm[(int64_t)(s + j) * a.L + t]), v, out[t]);
+            for (int j = 0; j < 4; ++j) {
+                if (s + j >= S) continue;
+                const float r = decay_rate(rate.v[j]);
+                float v = h[i].v[j];
+                if (a.mark && real) a.mark[((int64_t)n[i] * S + s + j) * a.C + c] = v;
+                #pragma unroll
+                for (int t = 0; t < LT; ++t) {
+                    if (t >= end[i]) continue;
+                    v = fmaf(ex2(d[i][t] * r), v, du[i][t] * to_f(LT == 1 ? Bv[i].v[j] : B[(int64_t)j * a.L + t]));
+                    out[i][t] = fmaf(to_f(LT == 1 ? Cv[i].v[j] : Cm[(int64_t)j * a.L + t]), v, out[i][t]);
+                }
+                now.v[j] = v;
             }
-            now.v[j] = v;
-        }
-        if (!a.state_out || !there) continue;
-        if constexpr (FOUR) {
-            if (s < S) *reinterpret_cast<Pack<float, 4> *>(a.state_out + at + s) = now;
-        } else {
-            #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (s + j < S) a.state_out[at + s + j] = now.v[j];
+            if (!a.state_out || !real) continue;
+            if constexpr (FOUR) {
+                if (s < S) *reinterpret_cast<Pack<float, 4> *>(a.state_out + at) = now;
+            } else {
+                #pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (s + j < S) a.state_out[at + j] = now.v[j];
+            }
         }
     }
     #pragma unroll
-    for (int t = 0; t < LT; ++t) {
-        out[t] += __shfl_xor_sync(~0u, out[t], 1);
-        out[t] += __shfl_xor_sync(~0u, out[t], 2);
-        if ((t & 3) != q || t >= a.L || !there) continue;
-        const int64_t row = (int64_t)c * a.L + t;
-        float v = out[t];
-        if (a.z) {
-            if (a.pre && t < end) static_cast<T *>(a.pre)[(int64_t)n * a.C * a.L + row] = from_f<T>(v);
-            v *= z[t] * scan_sigmoid(z[t]);
+    for (int i = 0; i < NB; ++i) {
+        #pragma unroll
+        for (int t = 0; t < LT; ++t) {
+            out[i][t] += __shfl_xor_sync(~0u, out[i][t], 1);
+            out[i][t] += __shfl_xor_sync(~0u, out[i][t], 2);
+            if (((LT > 1 ? t : i) & 3) != q || t >= a.L || !there || n0 + i >= a.N) continue;
+            const int64_t row = (int64_t)c * a.L + t;
+            float v = out[i][t];
+            if (a.z) {
+                if (a.pre && t < end[i]) static_cast<T *>(a.pre)[(int64_t)n[i] * a.C * a.L + row] = from_f<T>(v);
+                v *= z[i][t] * scan_sigmoid(z[i][t]);
+            }
+            static_cast<T *>(a.y)[n[i] * a.sy + row] = from_f<T>(t < end[i] ? v : 0.f);
         }
-        static_cast<T *>(a.y)[n * a.sy + row] = from_f<T>(t < end ? v : 0.f);
     }
 }
 
@@ -249,7 +293,11 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
     if (!back && s.L <= kTokenMost) {
         p->token = 1;
         p->ncb = (Cg + 31) / 32;
-        const int64_t grid = (int64_t)s.N * s.groups * p->ncb;
+        // two sequences a thread once the blocks of one go round more than once: [64,2048,1], 16 states 6.9 us, 7.5 with
+        // one a thread and 8.1 with four
+        int64_t grid = (int64_t)s.N * s.groups * p->ncb;
+        p->token = s.L == 1 && grid > (int64_t)num_sms() * 10 ? kTokenMany : 1;
+        grid = (int64_t)((s.N + p->token - 1) / p->token) * s.groups * p->ncb;
         p->shape.grid = (unsigned)grid;
         return grid <= INT_MAX;
     }
@@ -281,6 +329,7 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
     const int64_t grid = (int64_t)s.N * s.groups * p->ncb * p->chunks;
     const int64_t ends_grid = back ? (int64_t)s.N * s.groups * ((Cg + warps * own - 1) / (warps * own)) * p->chunks : grid;
     if (grid > INT_MAX || ends_grid > INT_MAX) return false;
+    if (p->chunks > 1 && (int64_t)s.N * S > ((int64_t)INT_MAX * 128 - 127) / s.C) return false;      // scan_join_kernel's threads
     const int row = spots(TT);
     const int SP = S | 1;
     auto floats = [&](bool ends) -> size_t {
@@ -389,14 +438,16 @@ gconv_status gconv_scan_fwd(const gconv_scan *scan, gconv_dtype dtype, const voi
     a.mark = static_cast<float *>(saved);
     a.pre = saved && z ? static_cast<char *>(saved) + saved_marks(*scan) : nullptr;
     if (p.token) {
-        const bool four = scan->states % 4 == 0 && on(A, 16) && on(state, 16) && on(state_out, 16);
-        auto pick = [&](auto one, auto few) { return scan->L == 1 ? one : few; };
+        const bool four = scan->states % 4 == 0 && on(A, 16) && on(state, 16) && on(state_out, 16) && on(B, 4 * esize(dtype)) &&
+                          on(C, 4 * esize(dtype)) && (scan->N == 1 || (a.sB % 4 == 0 && a.sC % 4 == 0));
         using H = __nv_bfloat16;
+        auto pick = [&](auto few, auto one, auto many) { return scan->L > 1 ? few : p.token == 1 ? one : many; };
+        constexpr int M = kTokenMost, K = kTokenMany;
         auto *kernel = dtype == GCONV_BF16
-            ? (four ? pick(scan_token_kernel<H, 1, true>, scan_token_kernel<H, kTokenMost, true>)
-                    : pick(scan_token_kernel<H, 1, false>, scan_token_kernel<H, kTokenMost, false>))
-            : (four ? pick(scan_token_kernel<float, 1, true>, scan_token_kernel<float, kTokenMost, true>)
-                    : pick(scan_token_kernel<float, 1, false>, scan_token_kernel<float, kTokenMost, false>));
+            ? (four ? pick(scan_token_kernel<H, M, 1, true>, scan_token_kernel<H, 1, 1, true>, scan_token_kernel<H, 1, K, true>)
+                    : pick(scan_token_kernel<H, M, 1, false>, scan_token_kernel<H, 1, 1, false>, scan_token_kernel<H, 1, K, false>))
+            : (four ? pick(scan_token_kernel<float, M, 1, true>, scan_token_kernel<float, 1, 1, true>, scan_token_kernel<float, 1, K, true>)
+                    : pick(scan_token_kernel<float, M, 1, false>, scan_token_kernel<float, 1, 1, false>, scan_token_kernel<float, 1, K, false>));
         launch_dependent(kernel, p.shape.grid, 128u, 0, st, a);
         return done();
     }

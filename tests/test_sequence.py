@@ -217,6 +217,28 @@ def test_scan(dev, i, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(131, 480, 1, 16, 1), (2051, 6, 1, 5, 2), (67, 990, 1, 20, 3)])
+def test_scan_one_position_of_many(dev, shape, dtype):
+    """Enough sequences that a thread takes several, some of them without a position; the state in place."""
+    n, c, _, S, _ = shape
+    d = scan_inputs(shape, dtype, dev, n)
+    d["lengths"] = torch.tensor([0 if i % 5 == 3 else 1 for i in range(n)], dtype=torch.int32, device=dev)
+    ref, mag = scan_ref(d), scan_ref(d, size=True)
+    new = Guarded(dev)
+    y, state, saved = new((n, c, 1), dtype), new((n, c, S), F32), kept(d, dtype)
+    state.copy_(d["state"])
+    forward(dict(d, state=state), y, state_out=state, saved=saved)
+    tol = 2.0 ** -20 * (2 * mag["M"] + 8)
+    near("y", y, ref["y"], mag["y"], tol, dtype)
+    near("state", state, ref["state"], mag["state"], tol)
+    assert torch.equal(state[3], d["state"][3]) and bool((y[3] == 0).all())
+    marks = saved.view(torch.float32)[:n * S * c].view(n, S, c) if saved.numel() % 4 == 0 else None
+    if marks is not None:
+        assert torch.equal(marks.transpose(1, 2), d["state"])
+    new.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_scan_slices_in_place(dev, dtype):
     """Inputs and gradients as channel slices of larger tensors, at offsets on and off 16 bytes."""
     n, c, l, S = 3, 24, 136, 16
@@ -449,6 +471,46 @@ def test_causal_slices_and_planes(dev, l, dtype):
     if dtype == F32:
         gc.gconv_fwd(line, w, None, same, padding=(0, 0, k - 1, 0), groups=6)
         near("depthwise", y.reshape(same.shape), same.double(), same.double().abs() + 1, 2.0 ** -20)
+
+
+def test_empty_batches(dev):
+    """No sequences: nothing runs, and the parameters' gradients are zero."""
+    e = lambda *s: torch.empty(s, device=dev)  # noqa: E731
+    w, b, dw, db = torch.randn((6, 4), device=dev), e(6), torch.full((6, 4), 5.0, device=dev), torch.full((6,), 5.0, device=dev)
+    gc.gconv_causal_fwd(e(0, 6, 9), w, b, e(0, 6, 9), state=e(0, 6, 3), state_out=e(0, 6, 3))
+    gc.gconv_causal_bwd(e(0, 6, 9), w, b, e(0, 6, 9), e(0, 6, 9), dw, db)
+    assert not bool(dw.any()) and not bool(db.any())
+    for l in (1, 80):
+        d = scan_inputs((0, 6, l, 8, 2), F32, dev, 1)
+        saved = kept(d, F32)
+        forward(d, e(0, 6, l), saved=saved)
+        got = backward(d, e(0, 6, l), saved, lambda s, t: torch.full(s, 5.0, dtype=t, device=dev), F32)
+        assert not any(bool(got[k].any()) for k in ("dA", "dD", "ddelta_bias"))
+    gc.gconv_dropout_fwd(e(0), e(0), torch.zeros(2, dtype=torch.int64, device=dev), 0.5)
+
+
+def test_tensors_elsewhere_are_refused(dev):
+    """A tensor of the host among the device's, for each argument."""
+    d = scan_inputs((2, 6, 20, 8, 1), F32, dev, 1)
+    y = torch.empty_like(d["u"])
+    for k in ("u", "delta", "A", "B", "C", "D", "z", "delta_bias", "state"):
+        with pytest.raises(ValueError):
+            forward(dict(d, **{k: d[k].cpu()}), y)
+    with pytest.raises(ValueError):
+        forward(d, y.cpu())
+    with pytest.raises(ValueError):
+        forward(dict(d, lengths=torch.tensor([1, 2], dtype=torch.int32)), y)
+    with pytest.raises(ValueError):
+        forward(dict(d, lengths=torch.tensor([1, 2], device=dev)), y)
+    with pytest.raises(ValueError):
+        forward(d, y, saved=torch.empty(8, device=dev))
+    w = torch.randn((6, 4), device=dev)
+    for args in ((d["u"].cpu(), w, None, y), (d["u"], w.cpu(), None, y), (d["u"], w, None, y.cpu()), (d["u"], w.bfloat16(), None, y),
+                 (d["u"], w, torch.zeros(5, device=dev), y), (d["u"].transpose(1, 2), w, None, y), (d["u"][:1].expand(2, 6, 20), w, None, y)):
+        with pytest.raises(ValueError):
+            gc.gconv_causal_fwd(*args)
+    with pytest.raises(ValueError):
+        gc.gconv_dropout_fwd(y, y, torch.zeros(2, dtype=torch.int64), 0.5)
 
 
 # ---- together, captured, on another stream ------------------------------------------
