@@ -134,11 +134,30 @@ struct Run {
 
     __device__ __forceinline__ void load(const T *base, const Place<T, K, VEC> &at)
     {
-        #pragma unroll
-        for (int i = 0; i < K / E; ++i) {
-            const int64_t o = VEC ? at.x[VEC ? i : 0] : at.x[0] + min(at.t + i, at.L - 1);
-            x[i] = *reinterpret_cast<const Pack<T, E> *>(base + o);
-            y[i] = *reinterpret_cast<const Pack<T, E> *>(base + o + at.step);
+        if constexpr (VEC) {
+            #pragma unroll
+            for (int i = 0; i < K / E; ++i) {
+                x[i] = *reinterpret_cast<const Pack<T, E> *>(base + at.x[i]);
+                y[i] = *reinterpret_cast<const Pack<T, E> *>(base + at.x[i] + at.step);
+            }
+        } else {
+            const T *p = base + at.x[0];
+            const bool whole = at.t + K <= at.L;    // no element needs a place of its own
+            if (whole) {
+                p += at.t;
+                #pragma unroll
+                for (int i = 0; i < K; ++i) {
+                    x[i].v[0] = p[i];
+                    y[i].v[0] = p[at.step + i];
+                }
+            } else {
+                #pragma unroll
+                for (int i = 0; i < K; ++i) {
+                    const int o = min(at.t + i, at.L - 1);
+                    x[i].v[0] = p[o];
+                    y[i].v[0] = p[at.step + o];
+                }
+            }
         }
     }
     __device__ __forceinline__ float2 at(int k) const { return make_float2(to_f(x[k / E].v[k % E]), to_f(y[k / E].v[k % E])); }
@@ -185,11 +204,22 @@ __device__ __forceinline__ void store_run(T *row, int64_t L, int t, bool there0,
             if (there1) *reinterpret_cast<Pack<T, E> *>(row + L + t + i) = y;
         }
     } else {
-        #pragma unroll
-        for (int i = 0; i < K; ++i) {
-            if (t + i >= L) continue;
-            if (there0) row[t + i] = from_f<T>(v[i].x);
-            if (there1) row[L + t + i] = from_f<T>(v[i].y);
+        if (t + K <= L) {
+            if (there0) {
+                #pragma unroll
+                for (int i = 0; i < K; ++i) row[t + i] = from_f<T>(v[i].x);
+            }
+            if (there1) {
+                #pragma unroll
+                for (int i = 0; i < K; ++i) row[L + t + i] = from_f<T>(v[i].y);
+            }
+        } else {
+            #pragma unroll
+            for (int i = 0; i < K; ++i) {
+                if (t + i >= L) continue;
+                if (there0) row[t + i] = from_f<T>(v[i].x);
+                if (there1) row[L + t + i] = from_f<T>(v[i].y);
+            }
         }
     }
 }
