@@ -1,5 +1,6 @@
 """GB300-native grouped 2D convolution (NCHW): forward, backward-data,
-backward-weight and bias gradient, as hand-written sm_103a CUDA kernels behind a
+backward-weight and bias gradient, with the norms, joins, sequence layers, dropout and
+weight updates around them, as hand-written sm_103a CUDA kernels behind a
 C ABI (include/gconv.h, libgconv.so).  This package is the thin Python binding;
 it loads the library on first use and has no fallback path.
 """

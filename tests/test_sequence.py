@@ -513,6 +513,30 @@ def test_tensors_elsewhere_are_refused(dev):
         gc.gconv_dropout_fwd(y, y, torch.zeros(2, dtype=torch.int64), 0.5)
 
 
+def test_beyond_32_bits(dev):
+    """Tensors of more than 2^31 elements: the last channels of the last sequence against a call on them alone."""
+    n, c, l, S = 2, 17000, 65535, 4
+    if torch.cuda.get_device_properties(dev).total_memory < 60e9:
+        pytest.skip("needs 40 GB")
+    gen = torch.Generator(device=dev).manual_seed(3)
+    x = torch.empty((n, c, l), dtype=BF16, device=dev).normal_(generator=gen)
+    delta = torch.empty_like(x).normal_(generator=gen)
+    y = torch.empty_like(x)
+    w, b = torch.randn((c, 4), device=dev), torch.randn(c, device=dev)
+    last = lambda t: t[n - 1:, c - 3:].contiguous()  # noqa: E731
+    want = torch.empty((1, 3, l), dtype=BF16, device=dev)
+    gc.gconv_causal_fwd(x, w, b, y, act="silu")
+    gc.gconv_causal_fwd(last(x), w[c - 3:].contiguous(), b[c - 3:].contiguous(), want, act="silu")
+    assert torch.equal(last(y), want)
+    B, C = (torch.randn((n, S, l), device=dev).to(BF16) for _ in range(2))
+    A, D = -0.2 - torch.rand((c, S), device=dev), torch.randn(c, device=dev)
+    gc.gconv_scan_fwd(x, delta, A, B, C, y, D=D)
+    gc.gconv_scan_fwd(last(x), last(delta), A[c - 3:].contiguous(), B[1:].contiguous(), C[1:].contiguous(), want, D=D[c - 3:].contiguous())
+    # the sequences are cut in other pieces: fp32 sums of some tens of terms that matter, then bf16
+    got = last(y).double()
+    assert bool(((got - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 2.0 ** -12).all())
+
+
 # ---- together, captured, on another stream ------------------------------------------
 
 
