@@ -239,6 +239,48 @@ def test_scan_one_position_of_many(dev, shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("l", [70, 72])
+def test_scan_channels_in_turn(dev, l, dtype):
+    """So many blocks of channels that a block of the gradient takes two sets of them in turn."""
+    n, c, S = 33, 510, 4
+    d = scan_inputs((n, c, l, S, 1), dtype, dev, l, ragged=True)
+    y, last, saved = torch.empty_like(d["u"]), torch.empty_like(d["state"]), kept(d, dtype)
+    forward(d, y, state_out=last, saved=saved)
+    dy = torch.randn((n, c, l), generator=torch.Generator().manual_seed(l)).to(dtype).to(dev)
+    new = Guarded(dev)
+    got = backward(d, dy, saved, new, dtype)
+    ref, mag = scan_ref(d, dy), scan_ref(d, dy, size=True)
+    tol = 2.0 ** -20 * (2 * mag["M"] + 8)
+    near("y", y, ref["y"], mag["y"], tol, dtype)
+    for k, v in got.items():
+        # dB and dC add 510 channels, at most 2^7 of them one after the other
+        more = 2.0 ** -15 if k in ("dA", "dD", "ddelta_bias") else 2.0 ** -17
+        near(k, v, ref[k].reshape(v.shape), mag[k].reshape(v.shape), tol + more, v.dtype, 2 if k == "dz" else 1)
+    new.check()
+
+
+def test_positions_without_an_axis(dev):
+    """[N, C] for one position and [N, C, H, W] for a plane are the same calls as [N, C, L]."""
+    d = scan_inputs((3, 10, 1, 8, 2), F32, dev, 2)
+    want, got = torch.empty((3, 10, 1), device=dev), torch.empty((3, 10), device=dev)
+    forward(d, want)
+    forward(dict(d, **{k: d[k][..., 0] for k in ("u", "delta", "B", "C", "z")}), got)
+    assert torch.equal(got, want[..., 0])
+    d = scan_inputs((2, 10, 35, 8, 2), F32, dev, 2)
+    want, got = torch.empty((2, 10, 35), device=dev), torch.empty((2, 10, 5, 7), device=dev)
+    forward(d, want)
+    e = dict(d, **{k: d[k].view(2, 10, 5, 7) for k in ("u", "delta", "z")}, **{k: d[k].view(2, 2, 8, 5, 7) for k in "BC"})
+    forward(e, got)
+    assert torch.equal(got.view(2, 10, 35), want)
+    x, w = torch.randn((3, 10), device=dev), torch.randn((10, 4), device=dev)
+    state = torch.randn((3, 10, 3), device=dev)
+    y, z = torch.empty((3, 10), device=dev), torch.empty((3, 10, 1), device=dev)
+    gc.gconv_causal_fwd(x, w, None, y, state=state)
+    gc.gconv_causal_fwd(x[..., None], w, None, z, state=state)
+    assert torch.equal(y, z[..., 0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_scan_slices_in_place(dev, dtype):
     """Inputs and gradients as channel slices of larger tensors, at offsets on and off 16 bytes."""
     n, c, l, S = 3, 24, 136, 16
