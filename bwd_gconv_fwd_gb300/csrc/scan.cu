@@ -16,7 +16,7 @@ constexpr int kTokenMost = 8, kTokenMany = 2;     // positions of the short form
 // What a single new position has to move is its state, 8 bytes a state and channel.  Four lanes share a channel, four
 // neighbouring states each (one 16-byte access where FOUR: states in fours, on 16 bytes), so that a warp's accesses are
 // whole lines; sums over states are two shuffles.  NB: sequences a thread takes, all of whose states are on their way
-// before the first is used; the channel's rates are read once for them.
+// before the first is used; the channel's rates are read once for them.  [64,2048,1], 16 states: 6.9 us in a graph (2.6 by its bytes).
 template <typename T, int LT, int NB, bool FOUR>
 __global__ void __launch_bounds__(128, LT > 1 ? 4 : NB > 1 ? 8 : 10) scan_token_kernel(const __grid_constant__ ScanArgs a)
 {
@@ -288,14 +288,15 @@ struct ScanPlan {
     size_t o_init, o_dsum, o_part, o_pA, o_pD, o_pb, bytes;
 };
 
-// Time of a launch, in units of a tile of one block alone on an SM.  A tile's time with k blocks on each SM is about 1, 1.2,
-// 1.4, 1.6 (forward; 7.5 us with 16 states alone, 12 us four at a time) or 1, 1.35 (gradient; 13 and 17 us, two fit).
-// A block's start is another half tile.
+// Time of a launch, in units of a tile of one block alone on an SM.  A tile's time with k blocks on each SM counts as 1, 1.2,
+// 1.4, 1.6 (forward; 7.5 us with 16 states alone, 12 us four at a time) or 1, 1.5 (gradient; 13 and 17 us, two fit) and a
+// block's start as a quarter tile.  These and the factors of a cut were fitted together to the times of ten shapes at some
+// twenty cuts each: what they pick is 0.3% (forward) and 2.5% (gradient) above the best of those, 2 and 12% at worst.
 double scan_cost(bool back, int64_t blocks, double tiles)
 {
-    tiles += 0.5;
+    tiles += 0.25;
     const int most = back ? 2 : 4;
-    const double more = back ? 0.35 : 0.2;
+    const double more = back ? 0.5 : 0.2;
     const int64_t slots = (int64_t)num_sms() * most, last = blocks % slots;
     return tiles * (blocks / slots * (1 + more * (most - 1)) + (last ? 1 + more * ((last + num_sms() - 1) / num_sms() - 1) : 0));
 }
@@ -320,18 +321,18 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
     const int units = (Cg + own - 1) / own, tiles = (s.L + TT - 1) / TT;      // a warp's channels, tiles of a sequence
     // Warps a block, channel sets that a block of the gradient takes in turn (fewer partial sums of dB and dC; where B and C
     // of all the states fit), and pieces that a sequence is cut into: the cheapest.  A cut takes a pass over the
-    // pieces before (0.45 of the forward pass, 0.3 of the gradient) and two launches.  Measured in us, uncut and cut:
-    // forward [1,2048,4096] 482 and 147 (16 pieces), [1,256,65536] 6987 and 292 (64), [8,2048,2048] 373 and 400 (2);
-    // gradient [1,2048,4096] 822 and 342 (8), [8,2048,2048] 1023, 985 in two sets, 1115 in 4 pieces.
+    // pieces before (0.3 of the forward pass, 0.15 of the gradient) and two launches.  Measured in us, uncut and cut:
+    // forward [1,2048,4096] 457 and 131 (16 pieces), [1,256,65536] 6566 and 237 (147), [8,2048,2048] 341 and 434 (8);
+    // gradient [1,2048,4096] 751 and 294 (32), [8,2048,2048] 957, 929 in two sets, 991 in 8 pieces.
     double best = 0;
     int warps = 1;
     for (int sets = 1; sets <= (back && S <= kScanStates ? 2 : 1); ++sets) {
         const int ncb = (units + 4 * sets - 1) / (4 * sets), w = (units + ncb * sets - 1) / (ncb * sets);
         const int64_t blocks = (int64_t)s.N * s.groups * ncb;
-        for (int chunks = 1; chunks <= tiles; chunks += chunks < 8 ? 1 : chunks / 8) {
+        for (int chunks = 1; chunks <= tiles; chunks = std::max(chunks + 1, std::min(chunks + chunks / 8, tiles))) {
             const int each = (tiles + chunks - 1) / chunks, real = (tiles + each - 1) / each;
             double cost = scan_cost(back, blocks * real, (double)each * sets);
-            if (real > 1) cost = cost * (back ? 1.3 : 1.45) + 1.0;
+            if (real > 1) cost = cost * (back ? 1.15 : 1.3) + 1.0;
             if (sets == 1) cost *= 1.02;             // twice the partial sums
             if (best == 0 || cost < best) {
                 best = cost;
@@ -348,8 +349,8 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
     const int row = spots(TT);
     const int SP = S | 1;
     auto floats = [&](bool ends) -> size_t {
-        if (!back) return (size_t)(ends ? 1 : 2) * kScanStates * row + 3 * (size_t)warps * own * SP;
-        if (ends) return (size_t)kScanStates * row + 3 * (size_t)warps * own * SP;
+        if (ends) return (size_t)kScanStates * row + (size_t)warps * (own * SP + 64 * kScanStates);
+        if (!back) return (size_t)2 * kScanStates * row + 3 * (size_t)warps * own * SP;
         return (size_t)(2 + 2 * CL) * kScanStates * row + (size_t)warps * (own * (kScanStates + 1) + 64 * kScanStates) +
                4 * (size_t)per * SP + 4 * per;
     };

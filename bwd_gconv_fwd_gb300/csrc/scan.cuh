@@ -229,18 +229,23 @@ __device__ __forceinline__ void store_run(T *row, int64_t L, int t, bool there0,
 __device__ __forceinline__ int spot(int t) { return t + ((t >> 5) << 2); }
 constexpr int spots(int TT) { return TT + (TT / 32) * 4; }
 
-// B or C of up to kScanStates states from s0 and TT positions from t0, in fp32, zeros from `end` on: loaded first,
-// stored to shared memory later.
-template <typename T, int TT, bool VEC>
+// B or C of up to kScanStates states, in fp32, zeros from `end` on: loaded first, stored to shared memory later.  The positions
+// are those of the lanes' runs, kScanLanes of kScanRun each, the first at t0 and each `each` further (kScanRun: 64 neighbours).
+template <typename T, bool VEC>
 struct States {
-    static constexpr int E = VEC ? 16 / (int)sizeof(T) : 1, PER = TT / E;
+    static constexpr int E = VEC ? 16 / (int)sizeof(T) : 1, PER = kScanTile / E;
     static constexpr int ALL = kScanStates * PER / 128, HELD = ALL < 1 ? 1 : ALL < 8 ? ALL : 8;   // pieces a thread holds; more are stored as they come
     Pack<T, E> x[HELD];
 
-    __device__ __forceinline__ static void put(float *sh, int i, int t0, int end, const Pack<T, E> &v)
+    __device__ __forceinline__ static int place(int i, int t0, int each)
     {
-        const int t = (i % PER) * E, left = end - t0 - t;
-        float *to = sh + (i / PER) * spots(TT) + spot(t);
+        const int t = (i % PER) * E;
+        return t0 + t / kScanRun * each + t % kScanRun;
+    }
+    __device__ __forceinline__ static void put(float *sh, int i, int t0, int each, int end, const Pack<T, E> &v)
+    {
+        const int left = end - place(i, t0, each);
+        float *to = sh + (i / PER) * spots(kScanTile) + spot((i % PER) * E);
         if constexpr (VEC) {
             float f[E];
             #pragma unroll
@@ -255,29 +260,30 @@ struct States {
             *to = to_f(v.v[0]);
         }
     }
-    __device__ __forceinline__ static Pack<T, E> get(const T *base, int64_t L, int i, int t0, int end)
+    __device__ __forceinline__ static Pack<T, E> get(const T *base, int64_t L, int i, int t0, int each, int end)
     {
         Pack<T, E> v{};
-        const int t = t0 + (i % PER) * E;
+        const int t = place(i, t0, each);
         if (t < end) v = *reinterpret_cast<const Pack<T, E> *>(base + (i / PER) * L + t);
         return v;
     }
-    __device__ __forceinline__ void load(const T *base, int64_t L, int count, int t0, int end)
+    __device__ __forceinline__ void load(const T *base, int64_t L, int count, int t0, int each, int end)
     {
         #pragma unroll
         for (int j = 0; j < HELD; ++j) {
             const int i = threadIdx.x + j * blockDim.x;
-            x[j] = i < count * PER ? get(base, L, i, t0, end) : Pack<T, E>{};
+            x[j] = i < count * PER ? get(base, L, i, t0, each, end) : Pack<T, E>{};
         }
     }
-    __device__ __forceinline__ void store(const T *base, int64_t L, int count, int t0, int end, float *sh) const
+    __device__ __forceinline__ void store(const T *base, int64_t L, int count, int t0, int each, int end, float *sh) const
     {
         #pragma unroll
         for (int j = 0; j < HELD; ++j) {
             const int i = threadIdx.x + j * blockDim.x;
-            if (i < count * PER) put(sh, i, t0, end, x[j]);
+            if (i < count * PER) put(sh, i, t0, each, end, x[j]);
         }
-        for (int i = threadIdx.x + HELD * blockDim.x; i < count * PER; i += blockDim.x) put(sh, i, t0, end, get(base, L, i, t0, end));
+        for (int i = threadIdx.x + HELD * blockDim.x; i < count * PER; i += blockDim.x)
+            put(sh, i, t0, each, end, get(base, L, i, t0, each, end));
     }
 };
 

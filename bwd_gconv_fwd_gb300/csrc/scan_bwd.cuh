@@ -9,6 +9,9 @@
 // thread adds its pair of channels and then into a place of its own channel lane in shared memory; the warps of a
 // block take different quarters of the states at a time, so that nothing is added by two of them at once and the order
 // is fixed.
+//
+// [8,2048,2048] bf16 with 16 states and a gate: 910 us, where bytes would take 89 and the fp32 pipe 250.  248 registers leave 8 warps
+// an SM, whose waits for shuffles and shared memory bound it (issue slots, fp32 pipe and shared memory 0.33 to 0.38 each).
 #pragma once
 
 #include "scan.cuh"
@@ -109,14 +112,14 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
                     fetch(pb + o + at.step);
                 }
             }
-            States<T, TT, VEC> fB, fC;
+            States<T, VEC> fB, fC;
             constexpr int M = OWN * kScanStates / 32;
             float marks[M];
             auto ask = [&](int s0) {                // for what the next round of states needs from memory
                 const int count = min(kScanStates, S - s0);
                 if (set == 0) {
-                    fB.load(B + (int64_t)s0 * a.L, a.L, count, t0, end);
-                    fC.load(Cm + (int64_t)s0 * a.L, a.L, count, t0, end);
+                    fB.load(B + (int64_t)s0 * a.L, a.L, count, t0, K, end);
+                    fC.load(Cm + (int64_t)s0 * a.L, a.L, count, t0, K, end);
                 }
                 #pragma unroll
                 for (int j = 0; j < M; ++j) {
@@ -157,8 +160,8 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
                     __syncthreads();
                 }
                 if (set == 0) {
-                    fB.store(B + (int64_t)s0 * a.L, a.L, count, t0, end, sB);
-                    fC.store(Cm + (int64_t)s0 * a.L, a.L, count, t0, end, sC);
+                    fB.store(B + (int64_t)s0 * a.L, a.L, count, t0, K, end, sB);
+                    fC.store(Cm + (int64_t)s0 * a.L, a.L, count, t0, K, end, sC);
                 }
                 #pragma unroll
                 for (int j = 0; j < M; ++j) {
@@ -338,100 +341,6 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
         a.pD[base + i] = sdD[i];
         a.pb[base + i] = sdb[i];
     }
-}
-
-// What leaves a piece of a sequence backwards when nothing enters it, and its sum of d.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(128) scan_bwd_ends_kernel(const __grid_constant__ ScanArgs a)
-{
-    constexpr int TL = kScanLanes, K = kScanRun, CL = 32 / TL, TT = kScanTile, ROW = spots(TT);
-    extern __shared__ __align__(16) float smem[];
-    const int CB = (blockDim.x >> 5) * CL * 2, S = a.S, SP = S | 1;
-    float *sC = smem, *sA = sC + kScanStates * ROW, *carry = sA + CB * SP;
-    int64_t id = blockIdx.x;
-    const int blocks = (a.Cg + CB - 1) / CB;
-    const int cb = (int)(id % blocks); id /= blocks;
-    const int g = (int)(id % a.G); id /= a.G;
-    const int chunk = (int)(id % a.chunks), n = (int)(id / a.chunks);
-    const int lane = threadIdx.x & 31, tl = lane % TL;
-    const int pair = (threadIdx.x >> 5) * CL + lane / TL, mine = 2 * pair;
-    const int c0 = g * a.Cg + cb * CB, left = min(CB, a.Cg - cb * CB);
-    ptx::griddep_wait();
-    const int end = sequence_end(a, n);
-    for (int i = threadIdx.x; i < CB * S; i += blockDim.x) {
-        const int ch = i / S, s = i % S;
-        sA[(ch >> 1) * 2 * SP + 2 * s + (ch & 1)] = ch < left ? decay_rate(a.A[(int64_t)c0 * S + i]) : 0.f;
-    }
-    for (int i = threadIdx.x; i < CB * SP; i += blockDim.x) carry[i] = 0.f;
-    const bool there0 = mine < left, there1 = mine + 1 < left;
-    const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;
-    const int64_t row = (int64_t)(c0 + mine) * a.L;
-    const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * S * a.L;
-    const float2 bias = make_float2(a.bias && there0 ? a.bias[c0 + mine] : 0.f, a.bias && there1 ? a.bias[c0 + mine + 1] : 0.f);
-    float2 total = both(0.f);
-    int turn = 0;
-    const int first = chunk * a.chunk_tiles, last = min(first + a.chunk_tiles, (a.L + TT - 1) / TT);
-    for (int tile = last - 1; tile >= first; --tile) {
-        const int t0 = tile * TT, t = t0 + tl * K;
-        if (t0 >= end) continue;
-        Run<T, K, VEC> rd, ry, rz;
-        const Place<T, K, VEC> at(row, t, a.L, there0, there1);
-        rd.load(static_cast<const T *>(a.delta) + n * a.sdelta, at);
-        ry.load(static_cast<const T *>(a.dy) + n * a.sdy, at);
-        if (a.z) rz.load(static_cast<const T *>(a.z) + n * a.sz, at);
-        float2 d[K], dy[K], sum = both(0.f);
-        #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            d[k] = rd.at(k) + bias;
-            if (a.softplus) d[k] = scan_softplus(d[k]);
-            dy[k] = ry.at(k);
-            if (a.z) dy[k] = dy[k] * (rz.at(k) * scan_sigmoid(rz.at(k)));
-        }
-        clear_run<K>(t, end0, end1, d);
-        clear_run<K>(t, end0, end1, dy);
-        #pragma unroll
-        for (int k = 0; k < K; ++k) sum = sum + d[k];
-        total = total + sum;
-        for (int s0 = 0; s0 < S; s0 += kScanStates) {
-            const int count = min(kScanStates, S - s0);
-            States<T, TT, VEC> fC;
-            fC.load(Cm + (int64_t)s0 * a.L, a.L, count, t0, end);
-            __syncthreads();
-            fC.store(Cm + (int64_t)s0 * a.L, a.L, count, t0, end, sC);
-            __syncthreads();
-            const float2 *rates = reinterpret_cast<const float2 *>(sA) + pair * SP + s0;
-            const float2 *in = reinterpret_cast<const float2 *>(carry + turn * CB * SP) + pair * SP + s0;
-            float2 *next = reinterpret_cast<float2 *>(carry + (turn ^ 1) * CB * SP) + pair * SP + s0;
-            #pragma unroll 1
-            for (int s = 0; s < count; ++s) {
-                float Cv[K];
-                read_run<K>(sC + s * ROW + spot(tl * K), Cv);
-                const float2 rate = rates[s];
-                float2 w = both(0.f), q = ex2(sum * rate);
-                #pragma unroll
-                for (int k = K - 1; k >= 0; --k) w = ex2(d[k] * rate) * fma2(both(Cv[k]), dy[k], w);
-                w = pick(tl == TL - 1, fma2(q, in[s], w), w);
-                #pragma unroll
-                for (int o = 1; o < TL; o <<= 1) {
-                    w = pick(tl + o < TL, fma2(q, shift_down(w, o, TL), w), w);
-                    if (2 * o < TL) q = q * shift_down(q, o, TL);
-                }
-                if (tl == 0) next[s] = w;
-            }
-        }
-        turn ^= 1;
-    }
-    __syncthreads();
-    const float *fin = carry + turn * CB * SP;
-    for (int i = threadIdx.x; i < left * S; i += blockDim.x) {
-        const int s = i / left, ch = i % left;
-        a.init[(((int64_t)n * a.chunks + chunk) * S + s) * a.C + c0 + ch] = fin[(ch >> 1) * 2 * SP + 2 * s + (ch & 1)];
-    }
-    #pragma unroll
-    for (int o = TL / 2; o > 0; o >>= 1) total = total + shift_down(total, o, TL);
-    float *to = a.dsum + ((int64_t)n * a.chunks + chunk) * a.C + c0 + mine;
-    if (tl == 0 && there0) to[0] = total.x;
-    if (tl == 0 && there1) to[1] = total.y;
 }
 
 }  // namespace gconv

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "scan_bwd.cuh"
+#include "scan_ends.cuh"
 #include "scan_fwd.cuh"
 #include "scan_internal.h"
 
@@ -19,15 +20,15 @@ void scan_start(F *kernel, const ScanShape &s, const ScanArgs &a, cudaStream_t s
 template <typename T>
 void scan_fwd_start(const ScanShape &s, bool ends, const ScanArgs &a, cudaStream_t st)
 {
-    if (s.vec) scan_start(ends ? scan_fwd_kernel<T, true, true> : scan_fwd_kernel<T, true, false>, s, a, st);
-    else scan_start(ends ? scan_fwd_kernel<T, false, true> : scan_fwd_kernel<T, false, false>, s, a, st);
+    if (s.vec) scan_start(ends ? scan_ends_kernel<T, true, false> : scan_fwd_kernel<T, true>, s, a, st);
+    else scan_start(ends ? scan_ends_kernel<T, false, false> : scan_fwd_kernel<T, false>, s, a, st);
 }
 
 template <typename T>
 void scan_bwd_start(const ScanShape &s, bool ends, const ScanArgs &a, cudaStream_t st)
 {
-    if (s.vec) scan_start(ends ? scan_bwd_ends_kernel<T, true> : scan_bwd_kernel<T, true>, s, a, st);
-    else scan_start(ends ? scan_bwd_ends_kernel<T, false> : scan_bwd_kernel<T, false>, s, a, st);
+    if (s.vec) scan_start(ends ? scan_ends_kernel<T, true, true> : scan_bwd_kernel<T, true>, s, a, st);
+    else scan_start(ends ? scan_ends_kernel<T, false, true> : scan_bwd_kernel<T, false>, s, a, st);
 }
 
 }  // namespace gconv
