@@ -885,8 +885,14 @@ def _scan_record(shape, B_shape, states, groups, softplus, strides, dt, device):
     """(record, its reference, workspace bytes forward and backward, bytes saved without and with a gate, [C], [C, states],
     [N, C, states])."""
     N, C, L = shape[0], shape[1], _positions(shape)
-    if len(B_shape) < 2 or B_shape[0] != N or B_shape.numel() != N * groups * states * L:
-        raise ValueError("B and C are [N, groups * states, ...] with A [C, states]")
+    if B_shape[:2] == (N, groups * states):
+        own = B_shape[2:]
+    elif B_shape[:3] == (N, groups, states):
+        own = B_shape[3:]
+    else:
+        raise ValueError("B and C are [N, groups * states, ...] or [N, groups, states, ...] with A [C, states]")
+    if torch.Size(own).numel() != L:
+        raise ValueError("B and C have the positions of u")
     rec = Scan(N, C, L, groups, states, softplus, *strides)
     ref = ctypes.byref(rec)
     need = [lib().gconv_scan_workspace_size(ref, dt, back) for back in (0, 1)] + \
@@ -921,8 +927,8 @@ def _scan_saved(saved, need, dev):
 def gconv_scan_fwd(u, delta, A, B, C, y, *, D=None, z=None, delta_bias=None, softplus=True, groups=1, state=None,
                    state_out=None, lengths=None, saved=None, workspace=None, stream=None):
     """The selective scan: with d = softplus(delta + delta_bias), h[t] = exp(d A) h[t-1] + d B[t] u[t] and
-    y <- (sum over the states of C[t] h[t] + D u) silu(z).  A: fp32 [C, states]; B, C: [N, groups * states, positions];
-    D, delta_bias: fp32 [C]; state, state_out (which may be state): fp32 [N, C, states]; lengths: int32 [N].
+    y <- (sum over the states of C[t] h[t] + D u) silu(z).  A: fp32 [C, states]; B, C: [N, groups * states, positions]
+    or [N, groups, states, positions]; D, delta_bias: fp32 [C]; state, state_out (which may be state): fp32 [N, C, states]; lengths: int32 [N].
     saved (gconv_scan_saved_size bytes) keeps what gconv_scan_bwd needs."""
     s, d, bs, f, dev = u.shape, u.dtype, B.shape, torch.float32, u.get_device()
     dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)

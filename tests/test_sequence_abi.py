@@ -132,3 +132,16 @@ def test_binding_refusals():
         gc.gconv_scan_fwd(x, x, A, torch.zeros(2, 15, 30), Bm, x)
     with pytest.raises(B.GconvError):
         gc.gconv_scan_saved_size((2, 8, 30), 300, 0)
+
+
+@pytest.mark.parametrize("n", [0, 2])
+def test_shapes_of_B(L, n):
+    def look(shape, x=(n, 8, 5, 6), states=16, groups=2):
+        return B._scan_record(torch.Size(x), torch.Size(shape), states, groups, 1, (0,) * 12, 0, 0)
+    for shape in ((n, 32, 30), (n, 32, 5, 6), (n, 2, 16, 30), (n, 2, 16, 5, 6)):
+        assert look(shape)[0].states == 16
+    assert look((n, 32), (n, 8))[0].L == 1 and look((n, 2, 16), (n, 8))[0].L == 1
+    # as many elements, but not a channel's positions one behind the other
+    for shape in ((n, 30, 32), (n, 16, 2, 30), (n, 30, 2, 16), (n, 32, 29), (n, 32), (n, 960), (32, n, 30), (n,)):
+        with pytest.raises(ValueError):
+            look(shape)
