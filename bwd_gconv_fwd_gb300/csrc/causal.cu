@@ -134,6 +134,12 @@ __device__ __forceinline__ int phase_of(const T *row)
 template <typename T>
 __device__ __forceinline__ int first_place(int phase) { return phase ? 16 / (int)sizeof(T) - phase : 0; }
 
+// The worker that a thread belongs to.  There may be 2^36 threads, but no more than 2^32 workers (TX divides a block).
+__host__ __device__ __forceinline__ unsigned worker_of(unsigned block, unsigned thread, unsigned TX)
+{
+    return block * (kCausalThreads / TX) + thread / TX;
+}
+
 // A worker's way through its share of a channel's rows: pieces in order, row after row.
 struct Walk {
     unsigned made, all, left;            // left: pieces that are still its own
@@ -175,7 +181,7 @@ template <typename T, int K, bool VEC>
 __global__ void __launch_bounds__(kCausalThreads) causal_fwd_kernel(const __grid_constant__ CausalArgs a)
 {
     constexpr int V = 16 / (int)sizeof(T), M = 2 * V, H = K - 1;
-    const unsigned worker = (blockIdx.x * (unsigned)kCausalThreads + threadIdx.x) / (unsigned)a.TX, tx = threadIdx.x % a.TX;
+    const unsigned worker = worker_of(blockIdx.x, threadIdx.x, (unsigned)a.TX), tx = threadIdx.x % a.TX;
     const int c = (int)(worker / (unsigned)a.splits);
     const unsigned split = worker % (unsigned)a.splits;
     const bool there = c < a.C;
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(kCausalThreads, 6) causal_bwd_kernel(const __g
 {
     constexpr int M = kCausalBack, H = K - 1;
     static_assert(H <= M, "what a lane needs from the next one is in that one's run");
-    const unsigned worker = (blockIdx.x * (unsigned)kCausalThreads + threadIdx.x) / (unsigned)a.TX, tx = threadIdx.x % a.TX;
+    const unsigned worker = worker_of(blockIdx.x, threadIdx.x, (unsigned)a.TX), tx = threadIdx.x % a.TX;
     const int c = (int)(worker / (unsigned)a.splits), runs = a.segs > 1 ? a.TX - 1 : a.TX;
     const unsigned split = worker % (unsigned)a.splits;
     const bool there = c < a.C;
