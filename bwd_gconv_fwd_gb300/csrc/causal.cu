@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kCausalThreads, 6) causal_bwd_kernel(const __g
         const int64_t t_ = at.t + (int64_t)tx * M - phase;
         const int t = on && t_ < a.L ? (int)t_ : a.L;
         const T *more = a.dstate_out && on ? static_cast<const T *>(a.dstate_out) + ((int64_t)n * a.C + c) * H : nullptr;
-        const bool whole = VEC && !a.dstate_out && whole_run<T, M, H>(t, end, a.L, state != nullptr);
+        const bool whole = VEC && (!more || t + M <= end - H) && whole_run<T, M, H>(t, end, a.L, state != nullptr);
         if (VEC && on) {                            // the next round's lines, on their way to L2
             if (t_ + runs * M < a.L) {
                 fetch(row + t_ + runs * M);
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kCausalThreads, 6) causal_bwd_kernel(const __g
                 for (int k = 0; k < K; ++k) v = fmaf(w[k], dv[j + H - k], v);
                 dx[j] = v;
             }
-            if (!whole && t + M > end - H) {         // near the end, or behind it
+            if (t + M > end - H) {                   // near the end, or behind it
                 #pragma unroll
                 for (int j = 0; j < M; ++j) {
                     const int from = t + j - (end - H);

@@ -670,3 +670,16 @@ def test_captured_and_streams(dev):
         d["u"].mul_(scale)
         graph.replay()
         assert all(torch.equal(p, q) for p, q in zip(step(), held))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_zeros_behind_a_length_whatever_the_weights_are(dev, dtype, act):
+    x, w = torch.randn(2, 3, 512, device=dev).to(dtype), torch.randn(3, 4, device=dev)
+    w[1, 0], w[2, 3] = float("inf"), float("nan")
+    lengths = torch.tensor([100, 0], dtype=torch.int32, device=dev)
+    y, dx, dw = torch.full_like(x, 7), torch.full_like(x, 7), torch.empty_like(w)
+    gc.gconv_causal_fwd(x, w, None, y, act=act, lengths=lengths)
+    gc.gconv_causal_bwd(x, w, None, x, dx, dw, act=act, lengths=lengths)
+    for out in (y, dx):
+        assert (out[0, :, 100:] == 0).all() and (out[1] == 0).all()
