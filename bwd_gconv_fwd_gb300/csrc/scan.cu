@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(32 * kScanColumn) scan_join_kernel(const __gri
     const int64_t i = on ? at : 0;
     const int n = (int)(i / sc), s = (int)(i % sc / a.C), c = (int)(i % a.C);
     ptx::griddep_wait();
-    const float rate = decay_rate(a.A[(int64_t)c * a.S + s]);
+    const float rate = sequence_end(a, n) > 0 ? decay_rate(a.A[(int64_t)c * a.S + s]) : 0.f;
     const float *first = back ? a.dstate_out : a.state;
     float h = first ? first[((int64_t)n * a.C + c) * a.S + s] : 0.f;
     const int64_t step = back ? -1 : 1, begin = (int64_t)n * a.chunks + (back ? a.chunks - 1 : 0);

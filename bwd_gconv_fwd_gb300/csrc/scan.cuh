@@ -310,7 +310,8 @@ __device__ __forceinline__ float2 shift_down(float2 v, int o, int width)
 }
 __device__ __forceinline__ float2 pick(bool c, float2 a, float2 b) { return make_float2(c ? a.x : b.x, c ? a.y : b.y); }
 
-// A log2 e, finite, so that a step of zero leaves a state as it was whatever A is.
+// A log2 e, finite, so that a step of zero leaves a state as it was even where A is not (where A is NaN, a sequence without
+// positions takes 0 in its place).
 __device__ __forceinline__ float decay_rate(float a)
 {
     const float v = a * kLog2e;

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
     const int end = sequence_end(a, n);
     for (int i = threadIdx.x; i < all * S; i += blockDim.x) {
         const int ch = i / S, s = i % S, to = (ch >> 1) * 2 * SP + 2 * s + (ch & 1);
-        sA[to] = ch < left ? decay_rate(a.A[(int64_t)c0 * S + i]) : 0.f;
+        sA[to] = ch < left && end > 0 ? decay_rate(a.A[(int64_t)c0 * S + i]) : 0.f;
         accA[to] = 0.f;
         float w = 0.f;
         if (ch < left) {

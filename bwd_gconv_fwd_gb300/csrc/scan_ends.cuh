@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(128, 5) scan_ends_kernel(const __grid_constant
     const int end = sequence_end(a, n);
     for (int i = threadIdx.x; i < CB * S; i += blockDim.x) {
         const int ch = i / S, s = i % S;
-        sA[(ch >> 1) * 2 * SP + 2 * s + (ch & 1)] = ch < left ? decay_rate(a.A[(int64_t)c0 * S + i]) : 0.f;
+        sA[(ch >> 1) * 2 * SP + 2 * s + (ch & 1)] = ch < left && end > 0 ? decay_rate(a.A[(int64_t)c0 * S + i]) : 0.f;
     }
     const bool there0 = mine < left, there1 = mine + 1 < left;
     const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;

@@ -683,3 +683,27 @@ def test_zeros_behind_a_length_whatever_the_weights_are(dev, dtype, act):
     gc.gconv_causal_bwd(x, w, None, x, dx, dw, act=act, lengths=lengths)
     for out in (y, dx):
         assert (out[0, :, 100:] == 0).all() and (out[1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("l", [6, 255, 512, 4096])
+def test_scan_zeros_behind_a_length_whatever_the_parameters_are(dev, dtype, l):
+    n, c, S = 2, 10, 16
+    x, bc = torch.randn(n, c, l, device=dev).to(dtype), torch.randn(n, S, l, device=dev).to(dtype)
+    A, D, bias = -torch.rand(c, S, device=dev), torch.randn(c, device=dev), torch.randn(c, device=dev)
+    A[1, 0], D[2], bias[3] = float("nan"), float("inf"), float("nan")
+    state = torch.full((n, c, S), float("inf"), device=dev)
+    state[0] = 1
+    half = l // 2
+    lengths = torch.tensor([half, 0], dtype=torch.int32, device=dev)
+    new = lambda like: torch.full_like(like, 7)  # noqa: E731
+    y, du, dd, dz, dB, dC, dA, dstate = new(x), new(x), new(x), new(x), new(bc), new(bc), new(A), new(state)
+    saved = torch.empty(gc.gconv_scan_saved_size((n, c, l), S, 1 if dtype is BF16 else 0, gated=True), dtype=torch.uint8, device=dev)
+    out = torch.empty_like(state)
+    gc.gconv_scan_fwd(x, x, A, bc, bc, y, D=D, z=x, delta_bias=bias, state=state, state_out=out, lengths=lengths, saved=saved)
+    gc.gconv_scan_bwd(x, x, A, bc, bc, x, saved, du, dd, dA, dB, dC, D=D, z=x, delta_bias=bias, lengths=lengths, dz=dz,
+                      dstate_out=state, dstate=dstate)
+    for o in (y, du, dd, dz, dB, dC):
+        assert (o[0, :, half:] == 0).all() and (o[1] == 0).all()
+    assert (out[1] == float("inf")).all() and (dstate[1] == float("inf")).all()
+    assert torch.isfinite(dA[4:]).all() and torch.isfinite(y[0, 4:]).all()
