@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(128) causal_short_kernel(const __grid_constant
 // Gradients.  dv of the next lane's first positions comes by shuffles.  Where a row has more pieces than one, a worker's last
 // lane makes its dv for the lane before alone, and its run is the first of the next piece: 31 of 32 lanes' work counts.
 // (Exchanging through shared memory by the whole block instead took a barrier a piece: 132 us against 99 then.)  Now 70 us for
-// [8,2048,2048] bf16, 4 taps: issue slots 0.69, 2.9 TB/s.
+// [8,2048,2048] bf16, 4 taps: issue slots 0.67, 2.9 TB/s.
 template <typename T, int K, bool VEC>
 __global__ void __launch_bounds__(kCausalThreads, 6) causal_bwd_kernel(const __grid_constant__ CausalArgs a)
 {
