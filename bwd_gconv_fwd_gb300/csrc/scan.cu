@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(128, LT > 1 ? 4 : NB > 1 ? 8 : 10) scan_token_
             const int64_t row = (int64_t)c * a.L + t;
             float v = out[i][t];
             if (a.z) {
-                if (a.pre && t < end[i]) static_cast<T *>(a.pre)[(int64_t)n[i] * a.C * a.L + row] = from_f<T>(v);
+                if (scan_keeps<T> && a.pre && t < end[i]) a.pre[(int64_t)n[i] * a.C * a.L + row] = v;
                 v *= z[i][t] * scan_sigmoid(z[i][t]);
             }
             static_cast<T *>(a.y)[n[i] * a.sy + row] = from_f<T>(t < end[i] ? v : 0.f);
@@ -478,7 +478,7 @@ gconv_status gconv_scan_fwd(const gconv_scan *scan, gconv_dtype dtype, const voi
     a.u = u; a.delta = delta; a.A = A; a.B = B; a.Cm = C; a.D = D; a.z = z; a.bias = delta_bias; a.state = state;
     a.lengths = lengths; a.y = y; a.state_out = state_out;
     a.mark = static_cast<float *>(saved);
-    a.pre = saved && z ? static_cast<char *>(saved) + saved_marks(*scan) : nullptr;
+    a.pre = saved && z && dtype == GCONV_F32 ? a.mark + saved_marks(*scan) / sizeof(float) : nullptr;
     if (p.token) {
         const bool four = scan->states % 4 == 0 && on(A, 16) && on(state, 16) && on(state_out, 16) && on(B, 4 * esize(dtype)) &&
                           on(C, 4 * esize(dtype)) && (scan->N == 1 || (a.sB % 4 == 0 && a.sC % 4 == 0));
@@ -534,7 +534,7 @@ gconv_status gconv_scan_bwd(const gconv_scan *scan, gconv_dtype dtype, const voi
     scan_args(*scan, p, workspace, &a);
     a.u = u; a.delta = delta; a.A = A; a.B = B; a.Cm = C; a.D = D; a.z = z; a.bias = delta_bias; a.lengths = lengths;
     a.mark = const_cast<float *>(static_cast<const float *>(saved));
-    a.pre = z ? const_cast<char *>(static_cast<const char *>(saved)) + saved_marks(*scan) : nullptr;
+    a.pre = z && dtype == GCONV_F32 ? a.mark + saved_marks(*scan) / sizeof(float) : nullptr;
     a.dy = dy; a.dstate_out = dstate_out; a.du = du; a.ddelta = ddelta; a.dB = dB; a.dC = dC; a.dz = dz; a.dstate = dstate;
     p.shape.vec = p.ends.vec = vectors(*scan, dtype, {{u, a.su}, {delta, a.sdelta}, {z, a.sz}, {B, a.sB}, {C, a.sC}, {dy, a.sdy},
                                                       {du, a.sdu}, {ddelta, a.sddelta}, {dz, a.sdz},

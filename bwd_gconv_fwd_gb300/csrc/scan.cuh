@@ -25,6 +25,10 @@ constexpr int kScanMaxStates = 256;
 constexpr int kScanLanes = 8, kScanRun = 8, kScanTile = kScanLanes * kScanRun;
 constexpr int kScanOwn = 32 / kScanLanes * 2;      // channels a warp
 
+// Whether the forward pass keeps the sums before the gate for the gradient.  In fp32 it does; in bf16 the room that `saved` has for
+// them would round a sum to 16 bits, and the gradient makes them again from its states.
+template <typename T> constexpr bool scan_keeps = sizeof(T) == sizeof(float);
+
 struct ScanArgs {
     int N, C, L, G, S, Cg;
     int softplus;
@@ -39,7 +43,7 @@ struct ScanArgs {
     const int *lengths;
     void *y;
     float *mark;                // [N][marks][S][C]
-    void *pre;                  // [N][C][L], y before the gate
+    float *pre;                 // [N][C][L], y before the gate (fp32 activations)
     float *init;                // [N][chunks][S][C]: what enters a piece (chunks > 1)
     float *dsum;                // [N][chunks][C]: sum of d over a piece
     // gradient

@@ -18,11 +18,14 @@
 
 namespace gconv {
 
-template <typename T, bool VEC>
+// SUMS: y before the gate is made again, for dz, one more multiply-add a state element (see scan_keeps; [8,2048,2048] bf16 899 us,
+// 921 with the sums read from what the forward pass kept in bf16).
+template <typename T, bool VEC, bool SUMS>
 __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant__ ScanArgs a)
 {
     constexpr int TL = kScanLanes, K = kScanRun, CL = 32 / TL, TT = kScanTile, ROW = spots(TT), OWN = kScanOwn;
     static_assert(TT % kScanMark == 0 && TL == 8, "a tile begins at a kept state; three steps a scan");
+    const bool gated = scan_keeps<T> ? a.z != nullptr : SUMS;
     extern __shared__ __align__(16) float smem[];
     const int warps = blockDim.x >> 5, CB = warps * OWN, all = CB * a.sets, S = a.S, SP = S | 1;
     float *sB = smem, *sC = sB + kScanStates * ROW, *accB = sC + kScanStates * ROW, *accC = accB + kScanStates * CL * ROW;
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
                 const bool more = ch + 1 < left;
                 store_run<T, K, VEC>(static_cast<T *>(a.du) + n * a.sdu + row, a.L, t, true, more, zero);
                 store_run<T, K, VEC>(static_cast<T *>(a.ddelta) + n * a.sddelta + row, a.L, t, true, more, zero);
-                if (a.z) store_run<T, K, VEC>(static_cast<T *>(a.dz) + n * a.sdz + row, a.L, t, true, more, zero);
+                if (gated) store_run<T, K, VEC>(static_cast<T *>(a.dz) + n * a.sdz + row, a.L, t, true, more, zero);
             }
             if (a.ncb == 1)
                 for (int i = threadIdx.x; i < 2 * S * TT; i += blockDim.x) {
@@ -91,12 +94,12 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
             const Place<T, K, VEC> at(row, t, a.L, there0, there1);
             const T *ub = static_cast<const T *>(a.u) + n * a.su, *db = static_cast<const T *>(a.delta) + n * a.sdelta;
             const T *yb = static_cast<const T *>(a.dy) + n * a.sdy, *zb = static_cast<const T *>(a.z) + n * a.sz;
-            const T *pb = static_cast<const T *>(a.pre) + (int64_t)n * a.C * a.L;
+            const float *pb = a.pre + (int64_t)n * a.C * a.L;
             Run<T, K, VEC> ru, rd, ry, rz;
             ru.load(ub, at);
             rd.load(db, at);
             ry.load(yb, at);
-            if (a.z) rz.load(zb, at);
+            if (gated) rz.load(zb, at);
             if (VEC && tile > first && t < a.L && there0) {        // the next tile's lines
                 const int64_t o = at.x[0] - TT;
                 fetch(ub + o);
@@ -105,11 +108,13 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
                 fetch(db + o + at.step);
                 fetch(yb + o);
                 fetch(yb + o + at.step);
-                if (a.z) {
+                if (gated) {
                     fetch(zb + o);
                     fetch(zb + o + at.step);
-                    fetch(pb + o);
-                    fetch(pb + o + at.step);
+                    if (scan_keeps<T>) {
+                        fetch(pb + o);
+                        fetch(pb + o + at.step);
+                    }
                 }
             }
             States<T, VEC> fB, fC;
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
             };
             ask(0);
             __syncthreads();                        // sbias, the first time; the tile or set before is done with what is staged
-            float2 d[K], du[K], dy[K], sb[K], aq[K], sum = both(0.f);
+            float2 d[K], du[K], dy[K], sb[K], aq[K], pre[SUMS ? K : 1], sum = both(0.f);
             const float2 bias = *reinterpret_cast<const float2 *>(sbias + mine);
             #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -138,7 +143,7 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
                 if (a.softplus) d[k] = scan_softplus(d[k]);
                 du[k] = ru.at(k);
                 dy[k] = ry.at(k);
-                if (a.z) dy[k] = dy[k] * (rz.at(k) * scan_sigmoid(rz.at(k)));
+                if (gated) dy[k] = dy[k] * (rz.at(k) * scan_sigmoid(rz.at(k)));
             }
             clear_run<K>(t, end0, end1, d);
             clear_run<K>(t, end0, end1, du);
@@ -148,6 +153,7 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
                 sum = sum + d[k];
                 du[k] = du[k] * d[k];
                 sb[k] = aq[k] = both(0.f);
+                if (SUMS) pre[k] = both(0.f);
             }
             // steps of two and of four runs from here back and ahead: the scans' decays are exponentials of these instead of
             // more shuffles for every state (947 -> 928 us for [8,2048,2048])
@@ -217,6 +223,7 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
                             h = fma2(du[k], both(Bv[k]), q[k]);
                             const float2 x = dy[k] * h;
                             aC[k] = x.x + x.y;
+                            if (SUMS) pre[k] = fma2(both(Cv[k]), h, pre[k]);
                         }
                         float2 dA = both(0.f);
                         #pragma unroll
@@ -287,15 +294,16 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
             #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const float2 x = ru.at(k);
+                if (SUMS) pre[k] = fma2(x, skip, pre[k]);
                 aq[k] = fma2(x, sb[k], aq[k] * both(kLn2));
                 if (a.softplus) aq[k] = aq[k] * scan_sigmoid(rd.at(k) + bias);
                 sb[k] = fma2(d[k], sb[k], skip * dy[k]);
                 dy[k] = dy[k] * x;
             }
-            if (a.z) {
+            if (gated) {
                 rz.load(zb, at);
                 ry.load(yb, at);
-                ru.load(pb, at);
+                if constexpr (scan_keeps<T>) ru.load(pb, at);
             }
             clear_run<K>(t, end0, end1, aq);
             clear_run<K>(t, end0, end1, sb);
@@ -307,12 +315,12 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
             }
             store_run<T, K, VEC>(static_cast<T *>(a.du) + n * a.sdu + row, a.L, t, there0, there1, sb);
             store_run<T, K, VEC>(static_cast<T *>(a.ddelta) + n * a.sddelta + row, a.L, t, there0, there1, aq);
-            if (a.z) {
+            if (gated) {
                 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const float2 z = rz.at(k), sg = scan_sigmoid(z);
                     const float2 rest = fma2(sg, both(-1.f), both(1.f));
-                    sb[k] = ry.at(k) * ru.at(k) * (sg * fma2(z, rest, both(1.f)));
+                    sb[k] = ry.at(k) * (SUMS ? pre[SUMS ? k : 0] : ru.at(k)) * (sg * fma2(z, rest, both(1.f)));
                 }
                 clear_run<K>(t, end0, end1, sb);
                 store_run<T, K, VEC>(static_cast<T *>(a.dz) + n * a.sdz + row, a.L, t, there0, there1, sb);

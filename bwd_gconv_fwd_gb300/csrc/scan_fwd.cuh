@@ -40,7 +40,6 @@ __global__ void __launch_bounds__(128, 4) scan_fwd_kernel(const __grid_constant_
     const bool there0 = mine < left, there1 = mine + 1 < left;
     const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;
     const int64_t row = (int64_t)(c0 + mine) * a.L;
-    const T *u = static_cast<const T *>(a.u) + n * a.su, *dl = static_cast<const T *>(a.delta) + n * a.sdelta;
     const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * S * a.L;
     const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * S * a.L;
     const float2 bias = make_float2(a.bias && there0 ? a.bias[c0 + mine] : 0.f, a.bias && there1 ? a.bias[c0 + mine + 1] : 0.f);
@@ -57,6 +56,7 @@ __global__ void __launch_bounds__(128, 4) scan_fwd_kernel(const __grid_constant_
             store_run<T, K, VEC>(static_cast<T *>(a.y) + n * a.sy + row, a.L, t, there0, there1, zero);
             continue;
         }
+        const T *u = static_cast<const T *>(a.u) + n * a.su, *dl = static_cast<const T *>(a.delta) + n * a.sdelta;
         const Place<T, K, VEC> at(row, t, a.L, there0, there1);
         Run<T, K, VEC> ru, rd;
         ru.load(u, at);
@@ -147,7 +147,9 @@ __global__ void __launch_bounds__(128, 4) scan_fwd_kernel(const __grid_constant_
         if (a.z) {
             Run<T, K, VEC> rz;
             rz.load(static_cast<const T *>(a.z) + n * a.sz, at);
-            if (a.pre) store_run<T, K, VEC>(static_cast<T *>(a.pre) + (int64_t)n * a.C * a.L + row, a.L, t, there0, there1, out);
+            if constexpr (scan_keeps<T>) {
+                if (a.pre) store_run<T, K, VEC>(a.pre + (int64_t)n * a.C * a.L + row, a.L, t, there0, there1, out);
+            }
             #pragma unroll
             for (int k = 0; k < K; ++k) out[k] = out[k] * (rz.at(k) * scan_sigmoid(rz.at(k)));
         }

@@ -404,8 +404,9 @@ typedef struct {
     long long dy_batch, du_batch, ddelta_batch, dz_batch, dB_batch, dC_batch;   /* read by gconv_scan_bwd only */
 } gconv_scan;
 
-/* Bytes that gconv_scan_fwd keeps for gconv_scan_bwd (states at intervals and, with a gate, the sums before it, in
- * dtype: the one value of the gradient dz that is rounded twice), and workspace bytes of either call ((size_t)-1: invalid). */
+/* Bytes of what gconv_scan_fwd keeps for gconv_scan_bwd, and workspace bytes of either call ((size_t)-1: invalid).  Kept are states
+ * at intervals and, with a gate, the sums before it where dtype is fp32.  In bf16 the N C L elements for them are counted too
+ * but not used: the gradient makes the sums again in fp32, so that dz is rounded once like every other result. */
 size_t gconv_scan_saved_size(const gconv_scan *scan, gconv_dtype dtype, int gated);
 size_t gconv_scan_workspace_size(const gconv_scan *scan, gconv_dtype dtype, int backward);
 
