@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(128, 4) scan_fwd_kernel(const __grid_constant_
     const bool there0 = mine < left, there1 = mine + 1 < left;
     const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;
     const int64_t row = (int64_t)(c0 + mine) * a.L;
-    const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * S * a.L;
+    const T *u = static_cast<const T *>(a.u) + n * a.su;
     const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * S * a.L;
     const float2 bias = make_float2(a.bias && there0 ? a.bias[c0 + mine] : 0.f, a.bias && there1 ? a.bias[c0 + mine + 1] : 0.f);
     const float2 skip = make_float2(a.D && there0 ? a.D[c0 + mine] : 0.f, a.D && there1 ? a.D[c0 + mine + 1] : 0.f);
@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(128, 4) scan_fwd_kernel(const __grid_constant_
             store_run<T, K, VEC>(static_cast<T *>(a.y) + n * a.sy + row, a.L, t, there0, there1, zero);
             continue;
         }
-        const T *u = static_cast<const T *>(a.u) + n * a.su, *dl = static_cast<const T *>(a.delta) + n * a.sdelta;
+        const T *dl = static_cast<const T *>(a.delta) + n * a.sdelta;
+        const T *B = static_cast<const T *>(a.B) + n * a.sB + (int64_t)g * S * a.L;
         const Place<T, K, VEC> at(row, t, a.L, there0, there1);
         Run<T, K, VEC> ru, rd;
         ru.load(u, at);
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(128, 4) scan_fwd_kernel(const __grid_constant_
             du[k] = du[k] * d[k];
         }
         const bool marks = a.mark && t % kScanMark == 0 && t < a.L;
-        float *mark = a.mark + (((int64_t)n * a.marks + t / kScanMark) * S) * a.C + c0 + mine;
+        float *mark = marks ? a.mark + (((int64_t)n * a.marks + t / kScanMark) * S) * a.C + c0 + mine : nullptr;
         for (int s0 = 0; s0 < S; s0 += kScanStates) {
             const int count = min(kScanStates, S - s0);
             if (s0) {
