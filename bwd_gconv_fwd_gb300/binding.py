@@ -728,8 +728,8 @@ def _orth_workspace(need, workspace, device, stream):
         if need == 0:
             return None, 0, 0
         workspace = _scratch(need, device, stream)
-    elif not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif not (workspace.device == device and workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor, on the device of the others")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -819,7 +819,8 @@ def _lengths(lengths, n, device):
 
 
 def _stream_on(stream, device):
-    """The stream's handle; the tensors have to be on the current device, which the kernels run on."""
+    """The stream's handle; the tensors have to be on the current device, which the kernels run on.  Asked for before the records
+    below, whose sizes are the current device's."""
     now = torch._C._cuda_getDevice()
     if now != device:
         raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{now}")
@@ -855,9 +856,10 @@ def gconv_causal_fwd(x, w, bias, y, *, act="none", state=None, state_out=None, l
     s, d, ws, f, dev = x.shape, x.dtype, w.shape, torch.float32, x.get_device()
     dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
     (xp, xs), (yp, ys) = _sequences(x, s, d, dev, "x"), _sequences(y, s, d, dev, "y")
+    on = _stream_on(stream, dev)
     _, ref, _, c, held = _causal_record(s, ws, act, (xs, ys, 0, 0), dt, dev)
     st = lib().gconv_causal_fwd(ref, dt, xp, _array(w, ws, f, dev, "w"), _array(bias, c, f, dev, "bias"), _array(state, held, d, dev, "state"),
-                                _lengths(lengths, s[0], dev), yp, _array(state_out, held, d, dev, "state_out"), _stream_on(stream, dev))
+                                _lengths(lengths, s[0], dev), yp, _array(state_out, held, d, dev, "state_out"), on)
     if st:
         _check(st, "gconv_causal_fwd")
     return y
@@ -870,11 +872,12 @@ def gconv_causal_bwd(x, w, bias, dy, dx, dw, dbias=None, *, act="none", state=No
     s, d, ws, f, dev = x.shape, x.dtype, w.shape, torch.float32, x.get_device()
     dt = GCONV_BF16 if d is torch.bfloat16 else dtype_code(d)
     (xp, xs), (yp, ys), (dp, ds) = _sequences(x, s, d, dev, "x"), _sequences(dy, s, d, dev, "dy"), _sequences(dx, s, d, dev, "dx")
+    on = _stream_on(stream, dev)
     _, ref, need, c, held = _causal_record(s, ws, act, (xs, 0, ys, ds), dt, dev)
     hold, sp, sb = _orth_workspace(need, workspace, x.device, stream)
     st = lib().gconv_causal_bwd(ref, dt, xp, _array(w, ws, f, dev, "w"), _array(bias, c, f, dev, "bias"), _array(state, held, d, dev, "state"),
                                 _lengths(lengths, s[0], dev), yp, _array(dstate_out, held, d, dev, "dstate_out"), dp, _array(dw, ws, f, dev, "dw"),
-                                _array(dbias, c, f, dev, "dbias"), _array(dstate, held, d, dev, "dstate"), sp, sb, _stream_on(stream, dev))
+                                _array(dbias, c, f, dev, "dbias"), _array(dstate, held, d, dev, "dstate"), sp, sb, on)
     if st:
         _check(st, "gconv_causal_bwd")
     return dx, dw, dbias
@@ -938,13 +941,14 @@ def gconv_scan_fwd(u, delta, A, B, C, y, *, D=None, z=None, delta_bias=None, sof
     yp, ys = _sequences(y, s, d, dev, "y")
     Bp, Bs = _sequences(B, bs, d, dev, "B")
     Cp, Cs = _sequences(C, bs, d, dev, "C")
+    on = _stream_on(stream, dev)
     _, ref, need, _, plain, gated, c, cs, full = _scan_record(s, bs, A.shape[-1], int(groups), 1 if softplus else 0,
                                                               (us, ds, zs, Bs, Cs, ys, 0, 0, 0, 0, 0, 0), dt, dev)
     hold, wp, wb = _orth_workspace(need, workspace, u.device, stream)
     st = lib().gconv_scan_fwd(ref, dt, up, dp, _array(A, cs, f, dev, "A"), Bp, Cp, _array(D, c, f, dev, "D"), zp,
                               _array(delta_bias, c, f, dev, "delta_bias"), _array(state, full, f, dev, "state"), _lengths(lengths, s[0], dev), yp,
                               _array(state_out, full, f, dev, "state_out"),
-                              0 if saved is None else _scan_saved(saved, plain if z is None else gated, dev), wp, wb, _stream_on(stream, dev))
+                              0 if saved is None else _scan_saved(saved, plain if z is None else gated, dev), wp, wb, on)
     if st:
         _check(st, "gconv_scan_fwd")
     return y
@@ -961,6 +965,7 @@ def gconv_scan_bwd(u, delta, A, B, C, dy, saved, du, ddelta, dA, dB, dC, *, D=No
          (("u", u, s), ("delta", delta, s), ("z", z, s), ("B", B, bs), ("C", C, bs), ("dy", dy, s), ("du", du, s),
           ("ddelta", ddelta, s), ("dz", dz, s), ("dB", dB, bs), ("dC", dC, bs))]
     (up, us), (dp, ds), (zp, zs), (Bp, Bs), (Cp, Cs), (gp, gs), (dup, dus), (ddp, dds), (dzp, dzs), (dBp, dBs), (dCp, dCs) = t
+    on = _stream_on(stream, dev)
     _, ref, _, need, plain, gated, c, cs, full = _scan_record(s, bs, A.shape[-1], int(groups), 1 if softplus else 0,
                                                               (us, ds, zs, Bs, Cs, 0, gs, dus, dds, dzs, dBs, dCs), dt,
                                                               dev)
@@ -969,7 +974,7 @@ def gconv_scan_bwd(u, delta, A, B, C, dy, saved, du, ddelta, dA, dB, dC, *, D=No
                               _array(delta_bias, c, f, dev, "delta_bias"), _lengths(lengths, s[0], dev),
                               _scan_saved(saved, plain if z is None else gated, dev), gp, _array(dstate_out, full, f, dev, "dstate_out"), dup,
                               ddp, _array(dA, cs, f, dev, "dA"), dBp, dCp, _array(dD, c, f, dev, "dD"), dzp,
-                              _array(ddelta_bias, c, f, dev, "ddelta_bias"), _array(dstate, full, f, dev, "dstate"), wp, wb, _stream_on(stream, dev))
+                              _array(ddelta_bias, c, f, dev, "ddelta_bias"), _array(dstate, full, f, dev, "dstate"), wp, wb, on)
     if st:
         _check(st, "gconv_scan_bwd")
     return du, ddelta
