@@ -328,7 +328,7 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
     p->sets = p->chunks = 1;
     if (!back && s.L <= kTokenMost) {
         p->token = 1;
-        p->ncb = (Cg + 31) / 32;
+        p->ncb = (Cg - 1) / 32 + 1;
         // two sequences a thread once the blocks of one go round more than once: [64,2048,1], 16 states 6.9 us, 7.5 with
         // one a thread and 8.1 with four
         int64_t grid = (int64_t)s.N * s.groups * p->ncb;
@@ -338,7 +338,7 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
         return grid <= INT_MAX;
     }
     const int own = kScanOwn, CL = 32 / kScanLanes, TT = kScanTile;
-    const int units = (Cg + own - 1) / own, tiles = (s.L + TT - 1) / TT;      // a warp's channels, tiles of a sequence
+    const int units = (Cg - 1) / own + 1, tiles = (s.L + TT - 1) / TT;      // a warp's channels, tiles of a sequence
     // Warps a block, channel sets that a block of the gradient takes in turn (fewer partial sums of dB and dC; where B and C
     // of all the states fit), and pieces that a sequence is cut into: the cheapest.  A cut takes a pass over the
     // pieces before (0.3 of the forward pass, 0.15 of the gradient) and two launches.  Measured in us, uncut and cut:
@@ -363,7 +363,7 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
     }
     const int per = warps * own * p->sets;
     const int64_t grid = (int64_t)s.N * s.groups * p->ncb * p->chunks;
-    const int64_t ends_grid = back ? (int64_t)s.N * s.groups * ((Cg + warps * own - 1) / (warps * own)) * p->chunks : grid;
+    const int64_t ends_grid = back ? (int64_t)s.N * s.groups * ((Cg - 1) / (warps * own) + 1) * p->chunks : grid;
     if (grid > INT_MAX || ends_grid > INT_MAX) return false;
     if (p->chunks > 1 && (int64_t)s.N * S > ((int64_t)INT_MAX * 32 - 31) / s.C) return false;        // scan_join_kernel's blocks
     const int row = spots(TT);

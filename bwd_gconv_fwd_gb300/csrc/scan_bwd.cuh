@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const __grid_constant_
             const int mine = set * CB + 2 * (warp * CL + cl), pair = mine >> 1;
             const bool there0 = mine < left, there1 = mine + 1 < left;
             const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;
-            const int64_t row = (int64_t)(c0 + mine) * a.L;
+            const int64_t row = ((int64_t)c0 + mine) * a.L;
             const Place<T, K, VEC> at(row, t, a.L, there0, there1);
             const T *ub = static_cast<const T *>(a.u) + n * a.su, *db = static_cast<const T *>(a.delta) + n * a.sdelta;
             const T *yb = static_cast<const T *>(a.dy) + n * a.sdy, *zb = static_cast<const T *>(a.z) + n * a.sz;

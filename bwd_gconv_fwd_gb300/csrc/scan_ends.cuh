@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(128, 5) scan_ends_kernel(const __grid_constant
     float *sB = smem, *sA = sB + kScanStates * ROW;               // B or C; rates [pairs][SP][2]
     float2 *held = reinterpret_cast<float2 *>(sA + CB * SP);      // [kScanStates][threads]
     int64_t id = blockIdx.x;
-    const int blocks = (a.Cg + CB - 1) / CB;
+    const int blocks = (a.Cg - 1) / CB + 1;
     const int cb = (int)(id % blocks); id /= blocks;
     const int g = (int)(id % a.G); id /= a.G;
     const int chunk = (int)(id % a.chunks), n = (int)(id / a.chunks);
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(128, 5) scan_ends_kernel(const __grid_constant
     }
     const bool there0 = mine < left, there1 = mine + 1 < left;
     const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;
-    const int64_t row = (int64_t)(c0 + mine) * a.L;
+    const int64_t row = ((int64_t)c0 + mine) * a.L;
     const T *from = static_cast<const T *>(BACK ? a.Cm : a.B) + n * (BACK ? a.sC : a.sB) + (int64_t)g * S * a.L;
     const T *db = static_cast<const T *>(a.delta) + n * a.sdelta;
     const T *xb = static_cast<const T *>(BACK ? a.dy : a.u) + n * (BACK ? a.sdy : a.su), *zb = static_cast<const T *>(a.z) + n * a.sz;

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(128, 4) scan_fwd_kernel(const __grid_constant_
     }
     const bool there0 = mine < left, there1 = mine + 1 < left;
     const int end0 = there0 ? end : 0, end1 = there1 ? end : 0;
-    const int64_t row = (int64_t)(c0 + mine) * a.L;
+    const int64_t row = ((int64_t)c0 + mine) * a.L;
     const T *u = static_cast<const T *>(a.u) + n * a.su;
     const T *Cm = static_cast<const T *>(a.Cm) + n * a.sC + (int64_t)g * S * a.L;
     const float2 bias = make_float2(a.bias && there0 ? a.bias[c0 + mine] : 0.f, a.bias && there1 ? a.bias[c0 + mine + 1] : 0.f);
