@@ -39,7 +39,7 @@ struct CausalArgs {
     float *part;                        // [splits][C][K + 1]
 };
 
-__device__ __forceinline__ int causal_end(const CausalArgs &a, int n)
+__host__ __device__ __forceinline__ int causal_end(const CausalArgs &a, int n)
 {
     if (!a.lengths) return a.L;
     const int v = a.lengths[n];
@@ -147,7 +147,7 @@ struct Walk {
     int64_t t;                          // of the piece's first run, were the row on 16 bytes
     bool on;
 
-    __device__ __forceinline__ Walk(const CausalArgs &a, unsigned split, int c, bool there) : made(0), t(0)
+    __host__ __device__ __forceinline__ Walk(const CausalArgs &a, unsigned split, int c, bool there) : made(0), t(0)
     {
         const unsigned items = (unsigned)a.N * (unsigned)a.segs;
         all = (items + a.splits - 1) / a.splits;
@@ -159,7 +159,7 @@ struct Walk {
         end = on ? causal_end(a, n) : 0;
     }
     template <typename F>
-    __device__ __forceinline__ void step(const CausalArgs &a, int width, F next_row)
+    __host__ __device__ __forceinline__ void step(const CausalArgs &a, int width, F next_row)
     {
         ++made;
         ++seg;
