@@ -4,8 +4,8 @@
 //   dv = dy act'(v),   dx[t] = sum_k w[k] dv[t + K - 1 - k],   dw[k] = sum dv[t] x[t - K + 1 + k],   db = sum dv
 //
 // Two or three tensors go through once, at 2 K + 8 operations an element (6 K + 12 for the gradients); with what it takes to
-// unpack, shift and round them issue slots bound it (0.72) beside memory (4.2 TB/s, 32 us for [8,2048,2048] bf16, 4 taps).
-// Every access is 16 bytes.  A lane takes the elements of one row (channel of a sequence) that lie in one or two
+// unpack, shift and round them issue slots bound it (0.62 of the launch) beside memory (4.2 TB/s, 32 us for [8,2048,2048] bf16, 4 taps).
+// Accesses are 16 bytes where the tensors' rows begin at the same place of 16 bytes (element by element otherwise).  A lane takes the elements of one row (channel of a sequence) that lie in one or two
 // neighbouring 16-byte pieces of memory, so rows of odd length, which begin anywhere, are read in whole pieces too; only a row's
 // two ends go element by element.  What the window needs from the piece before is read again (from L1).
 // TX lanes (a power of two, a warp where rows are long) are a worker: it keeps a channel's weights, and its sums for their
@@ -20,7 +20,10 @@ namespace gconv {
 namespace {
 
 constexpr int kCausalMost = 8;          // taps
-constexpr int kCausalShort = 4;         // positions of the form with one thread a row
+// Positions of the form with one thread a row, for one new position of a sequence and few more.  [64,2048,L] bf16, 4 taps: 4
+// positions 2.1 us, 8.5 by workers; 5 by workers 11.1.  With room for sixteen a thread 5 take 2.6, 8 4.7 (15 by workers), 16 14
+// (27, in fp32 12 and 5.4), so that the border could lie at 8.
+constexpr int kCausalShort = 4;
 constexpr int kCausalThreads = 128;
 constexpr int kCausalBack = 8;          // elements a lane of the gradient
 
@@ -327,7 +330,8 @@ __device__ __noinline__ void causal_ends_again(const CausalArgs &a, int K, int c
 // Gradients.  dv of the next lane's first positions comes by shuffles.  Where a row has more pieces than one, a worker's last
 // lane makes its dv for the lane before alone, and its run is the first of the next piece: 31 of 32 lanes' work counts.
 // (Exchanging through shared memory by the whole block instead took a barrier a piece: 132 us against 99 then.)  Now 70 us for
-// [8,2048,2048] bf16, 4 taps: issue slots 0.67, 2.9 TB/s.
+// [8,2048,2048] bf16, 4 taps: issue slots 0.68, 2.9 TB/s.  Six blocks an SM leave 80 registers: from 5 taps on rows that take 16-byte
+// accesses spill (24 to 128 bytes stored).
 template <typename T, int K, bool VEC>
 __global__ void __launch_bounds__(kCausalThreads, 6) causal_bwd_kernel(const __grid_constant__ CausalArgs a)
 {
@@ -517,8 +521,10 @@ CausalShape causal_shape(const gconv_causal &s, gconv_dtype dt, bool back, bool 
     CausalShape p{};
     p.TX = cut(((int64_t)s.L + (whole ? 0 : V - 1) + M - 1) / M, &segs);
     p.segs = (int)segs;
-    // workers that share a channel: warps for the whole GPU; the workspace's size does not know the alignment, so they go by
-    // rows that begin anywhere
+    // workers that share a channel: 64 warps an SM; the workspace's size does not know the alignment, so they go by rows that begin
+    // anywhere.  Forward and gradient in us with 32, 64 and 128, 4 taps: [8,2048,2048] bf16 30 and 71, 32 and 70, 37 and 77;
+    // [1,2048,4096] bf16 10 and 20, 14 and 22, 20 and 26; [64,2048,64] bf16 9.7 and 24, 9.0 and 24, 9.4 and 25; [7,512,1023] fp32 8.3
+    // and 17.5, 8.2 and 17.5, 8.1 and 19
     const int lanes = cut(((int64_t)s.L + V - 1 + M - 1) / M, &usual);
     const int64_t want = (int64_t)num_sms() * 64 * (32 / lanes);
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)s.N * usual, (want + s.C - 1) / s.C));

@@ -174,6 +174,8 @@ gconv_status dropout(long long count, gconv_dtype dtype, const void *x, const vo
         a.bound = (unsigned int)bound;
         a.scale = (float)(4294967296.0 / (4294967296.0 - a.bound));
     }
+    // From a tile an SM on, blocks that stay: 1.6 us at 622592 elements in bf16 (1.8 with res), 2.2 by four elements a thread; at a
+    // quarter of that 1.5 (1.7) and 1.4.  In fp32 1.3 and 1.9 at 311296, 1.2 and 1.5 at a quarter: it would pay there earlier.
     const bool vec = on(x, 16) && on(y, 16) && on(res, 16);
     const int64_t tile = 2 * kDropThreads * (int64_t)(16 / es), tiles = count / tile;
     const int64_t few = (count + 4 * kDropThreads - 1) / (4 * kDropThreads);

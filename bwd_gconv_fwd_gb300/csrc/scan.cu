@@ -9,7 +9,10 @@ namespace gconv {
 
 namespace {
 
-constexpr int kTokenMost = 8, kTokenMany = 2;     // positions of the short form; sequences a thread of it
+// Positions of the short form; sequences a thread of it.  [64,2048,L] bf16, 16 states and a gate: 8 positions 24 us, 76 as a tile
+// of which seven eighths are empty; 9 as a tile 90.  With room for sixteen positions a thread 9 take 38 us and 16 52 (76), but 2
+// take 32 for 20 and 8 36 for 24.
+constexpr int kTokenMost = 8, kTokenMany = 2;
 
 // ---- short sequences ----------------------------------------------------------------
 //
@@ -342,8 +345,8 @@ bool plan_scan(const gconv_scan &s, bool back, ScanPlan *p)
     // Warps a block, channel sets that a block of the gradient takes in turn (fewer partial sums of dB and dC; where B and C
     // of all the states fit), and pieces that a sequence is cut into: the cheapest.  A cut takes a pass over the
     // pieces before (0.3 of the forward pass, 0.15 of the gradient) and two launches.  Measured in us, uncut and cut:
-    // forward [1,2048,4096] 457 and 131 (16 pieces), [1,256,65536] 6566 and 237 (147), [8,2048,2048] 341 and 434 (8);
-    // gradient [1,2048,4096] 751 and 294 (32), [8,2048,2048] 957, 929 in two sets, 991 in 8 pieces.
+    // forward [1,2048,4096] 370 and 112 (16 pieces), [1,256,65536] 5997 and 205 (147), [8,2048,2048] 319 and 409 (8);
+    // gradient [1,2048,4096] 687 and 275 (32), [8,2048,2048] 919, 898 in two sets, 962 in 8 pieces.
     double best = 0;
     int warps = 1;
     for (int sets = 1; sets <= (back && S <= kScanStates ? 2 : 1); ++sets) {

@@ -10,8 +10,9 @@
 // block take different quarters of the states at a time, so that nothing is added by two of them at once and the order
 // is fixed.
 //
-// [8,2048,2048] bf16 with 16 states and a gate: 910 us, where bytes would take 89 and the fp32 pipe 250.  248 registers leave 8 warps
-// an SM, whose waits for shuffles and shared memory bound it (issue slots, fp32 pipe and shared memory 0.33 to 0.38 each).
+// [8,2048,2048] bf16 with 16 states and a gate: 899 us, where bytes would take 78 and the fp32 pipe 270.  248 registers leave 8 warps
+// an SM, whose waits for shuffles and shared memory bound it (issue slots 0.37, fp32 pipe 0.40, shared memory 0.34).  Rows off 16
+// bytes sit at the limit of 255 and spill: 264 bytes stored and 152 read in fp32, 48 and 68 in bf16 with a gate, none without one.
 #pragma once
 
 #include "scan.cuh"
