@@ -42,6 +42,14 @@ def test_weights_of_results_that_are_not_there(dev, l, taps, dtype):  # noqa: F8
         same("dx", dx, ref["dx"], mag["dx"], dtype)
         same("dstate", first, ref["dstate"], mag["dstate"], dtype)
         new.check()
+    # rows of dy that begin at another place of 16 bytes than those of x, so that no access is 16 bytes
+    wide = torch.full((n, c + 1, l + 1), 3.0, dtype=dtype, device=dev).view(n, -1)[:, 1:1 + c * l].unflatten(1, (c, l))
+    wide.copy_(dy)
+    other, last = torch.empty_like(dx), torch.empty_like(first)
+    gc.gconv_causal_bwd(x, w, None, wide, other, dw, state=state, lengths=lengths, dstate_out=more, dstate=last)
+    gc.gconv_causal_bwd(x, w, None, dy, dx, dw, state=state, lengths=lengths, dstate_out=more, dstate=first)
+    for p, q in ((other, dx), (last, first)):
+        assert torch.equal(torch.isnan(p), torch.isnan(q)) and torch.equal(torch.nan_to_num(p), torch.nan_to_num(q))
     # of a sequence without positions the state goes on as it is, and so does its gradient, through silu too
     i = ends.index(0)
     for act in ("none", "silu"):
