@@ -395,7 +395,8 @@ gconv_status gconv_causal_bwd(const gconv_causal *causal, gconv_dtype dtype, con
  * meant to be negative or zero (-Inf: a state that forgets at every step of 2^-120 or more).  Where d A is positive (a positive A,
  * or without softplus a negative step) the exponentials of its sums over any run of a sequence's positions have to stay within fp32.
  * Requirements: C, L, groups, states >= 1, N >= 0, C divisible by groups, L at most 2^30, states <= 256,
- * C states below 2^31, tensors of at most 2^40 elements, pointers aligned to their elements (those of saved and workspace
+ * C states below 2^31, tensors of at most 2^40 elements, N groups ceil(C / (32 groups)) below 2^31,
+ * pointers aligned to their elements (those of saved and workspace
  * to 16 bytes; rows of a multiple of 16 bytes on 16-byte boundaries are faster).  The record is read during the
  * call only.  N == 0 is a no-op (the gradients of A, D and delta_bias are set to zero). */
 typedef struct {
